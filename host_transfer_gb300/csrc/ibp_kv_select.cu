@@ -1,0 +1,429 @@
+// ibp_kv_select.cu - 8-bit bounds of a page's keys, and the selection of pages
+// by the score of those bounds for each query.
+//
+// The score is an upper estimate of q . k over the page: each dimension takes
+// the bound that its query's sign asks for.  With codes of 8 bits on both
+// sides the sum is whole-number arithmetic, so every split, order and GPU
+// selects the same pages.  The sum over a group's heads needs no loop over
+// them: total = (sum_g max(c, 0)) . max + (sum_g min(c, 0)) . min, so one pair
+// of 16-bit vectors per query and kv head meets the page's 8-bit codes.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "ibp_kv_internal.cuh"
+
+namespace ibp {
+
+constexpr int kSumThreads = 256;
+constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
+
+__device__ __forceinline__ float2 pair_f32(uint32_t v, bool f16) {
+  return f16 ? __half22float2(*reinterpret_cast<__half2*>(&v))
+             : __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v));
+}
+
+// NaN if either is, so that a page with one shows it.
+template <bool F16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (F16)
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (F16)
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 127 * (1 / a), each operation rounded: the codes are the same wherever they
+// are computed in this order.
+__device__ __forceinline__ float code_factor(float a) { return __fmul_rn(__frcp_rn(a), 127.f); }
+
+__device__ __forceinline__ bool finite_f(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// A warp takes one head of one page: each lane holds the minima and maxima of
+// eight dimensions over every (32 / (dim / 8))-th token and the lanes of a
+// dimension meet at the end.  Bound by DRAM: the keys are read once, 16 bytes a
+// lane with eight loads in flight.
+template <bool F16>
+__global__ void __launch_bounds__(kSumThreads)
+    k_kv_summarize(const KvView k, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
+                   const int32_t* __restrict__ first, uint32_t max_pages, uint32_t n_pages, uint32_t page_tokens,
+                   uint32_t heads, uint32_t dim, int8_t* __restrict__ codes, float* __restrict__ scales,
+                   uint32_t* status) {
+  pdl_begin();
+  const uint32_t b = blockIdx.y, lane = threadIdx.x & 31u;
+  const int32_t raw = lens[b], len = clamp_len(raw, page_tokens, max_pages);
+  if (raw != len && blockIdx.x == 0 && threadIdx.x == 0) kv_status(status, IBP_ERANGE);
+  int32_t f = first ? first[b] : 0;
+  f = f < 0 ? 0 : f;
+  const uint32_t p0 = static_cast<uint32_t>(f) / page_tokens, p1 = held_pages(len, page_tokens, max_pages);
+  if (f >= len || p0 >= p1) return;
+  const uint64_t units = static_cast<uint64_t>(p1 - p0) * heads;
+  const uint32_t cpr = dim / 8, rows = 32 / cpr;
+  const uint32_t col = lane % cpr, row0 = lane / cpr;
+  constexpr uint32_t kFly = 8;
+  for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * (kSumThreads / 32) + (threadIdx.x >> 5); u < units;
+       u += static_cast<uint64_t>(gridDim.x) * (kSumThreads / 32)) {
+    const uint32_t h = static_cast<uint32_t>(u % heads), p = p0 + static_cast<uint32_t>(u / heads);
+    const uint32_t pg = static_cast<uint32_t>(table[static_cast<uint64_t>(b) * max_pages + p]);
+    if (pg >= n_pages) {
+      if (lane == 0) kv_status(status, IBP_ERANGE);
+      continue;
+    }
+    const uint32_t left = static_cast<uint32_t>(len) - p * page_tokens;
+    const uint32_t n = left < page_tokens ? left : page_tokens;
+    const char* src = k.data + static_cast<int64_t>(pg) * k.page_stride + static_cast<int64_t>(h) * k.head_stride +
+                      col * 16;
+    const uint32_t pinf = F16 ? 0x7C007C00u : 0x7F807F80u, ninf = pinf | 0x80008000u;
+    uint4 lo = make_uint4(pinf, pinf, pinf, pinf), hi = make_uint4(ninf, ninf, ninf, ninf);
+    if (row0 < rows) {
+      for (uint32_t r = row0; r < n; r += rows * kFly) {
+        uint4 x[kFly];
+#pragma unroll
+        for (uint32_t i = 0; i < kFly; ++i) {
+          // a row past the end repeats the first one: it changes no bound
+          const uint32_t rr = r + i * rows < n ? r + i * rows : r;
+          x[i] = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(rr) * k.token_stride));
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kFly; ++i) {
+          lo.x = min2<F16>(lo.x, x[i].x), lo.y = min2<F16>(lo.y, x[i].y);
+          lo.z = min2<F16>(lo.z, x[i].z), lo.w = min2<F16>(lo.w, x[i].w);
+          hi.x = max2<F16>(hi.x, x[i].x), hi.y = max2<F16>(hi.y, x[i].y);
+          hi.z = max2<F16>(hi.z, x[i].z), hi.w = max2<F16>(hi.w, x[i].w);
+        }
+      }
+    }
+    for (uint32_t i = 1; i < rows; ++i) {  // lanes of row group 0 collect the others
+      const uint32_t from = col + i * cpr;
+      uint4 a, c;
+      a.x = __shfl_sync(0xFFFFFFFFu, lo.x, from), a.y = __shfl_sync(0xFFFFFFFFu, lo.y, from);
+      a.z = __shfl_sync(0xFFFFFFFFu, lo.z, from), a.w = __shfl_sync(0xFFFFFFFFu, lo.w, from);
+      c.x = __shfl_sync(0xFFFFFFFFu, hi.x, from), c.y = __shfl_sync(0xFFFFFFFFu, hi.y, from);
+      c.z = __shfl_sync(0xFFFFFFFFu, hi.z, from), c.w = __shfl_sync(0xFFFFFFFFu, hi.w, from);
+      if (row0 == 0) {
+        lo.x = min2<F16>(lo.x, a.x), lo.y = min2<F16>(lo.y, a.y), lo.z = min2<F16>(lo.z, a.z);
+        lo.w = min2<F16>(lo.w, a.w);
+        hi.x = max2<F16>(hi.x, c.x), hi.y = max2<F16>(hi.y, c.y), hi.z = max2<F16>(hi.z, c.z);
+        hi.w = max2<F16>(hi.w, c.w);
+      }
+    }
+    float l8[8], h8[8], amax = 0.f;
+    bool bad = false;
+    const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = pair_f32(lw[i], F16), c = pair_f32(hw[i], F16);
+      l8[2 * i] = a.x, l8[2 * i + 1] = a.y, h8[2 * i] = c.x, h8[2 * i + 1] = c.y;
+    }
+    if (row0 == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        bad = bad || !finite_f(l8[i]) || !finite_f(h8[i]);
+        amax = fmaxf(amax, fmaxf(fabsf(l8[i]), fabsf(h8[i])));
+      }
+    }
+    bad = __any_sync(0xFFFFFFFFu, bad);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    const bool fine = !bad && amax >= kTiny;
+    const float inv = fine ? code_factor(amax) : 0.f;
+    const uint64_t at = static_cast<uint64_t>(pg) * heads + h;
+    if (row0 == 0) {
+      uint32_t w[4] = {0, 0, 0, 0};  // minima then maxima, four codes a word
+      if (fine) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int cl = max(-127, min(127, __float2int_rn(__fmul_rn(l8[i], inv))));
+          const int ch = max(-127, min(127, __float2int_rn(__fmul_rn(h8[i], inv))));
+          w[i / 4] |= static_cast<uint32_t>(cl & 0xFF) << (8 * (i % 4));
+          w[2 + i / 4] |= static_cast<uint32_t>(ch & 0xFF) << (8 * (i % 4));
+        }
+      }
+      uint32_t* dst = reinterpret_cast<uint32_t*>(codes + at * 2 * dim);
+      dst[2 * col] = w[0], dst[2 * col + 1] = w[1];
+      dst[dim / 4 + 2 * col] = w[2], dst[dim / 4 + 2 * col + 1] = w[3];
+    }
+    if (lane == 0) scales[at] = bad ? __int_as_float(0x7F800000) : (fine ? __fmul_rn(amax, 1.f / 127.f) : 0.f);
+  }
+}
+
+int launch_kv_summarize(const KvView& k, const int32_t* table, const int32_t* lens, const int32_t* first,
+                        uint32_t n_seqs, uint32_t max_pages, uint32_t n_pages, uint32_t page_tokens, uint32_t heads,
+                        uint32_t dim, uint32_t f16, int8_t* codes, float* scales, uint32_t* status, int device,
+                        cudaStream_t stream) {
+  // Two units a warp fill the longest sequence; at most 32 CTAs per SM in all,
+  // so that a step that touches one page each does not launch empty CTAs by the
+  // ten thousand.
+  const uint64_t units = static_cast<uint64_t>(max_pages) * heads;
+  const uint64_t want = (units + 2 * (kSumThreads / 32) - 1) / (2 * (kSumThreads / 32));
+  const uint64_t cap = (32ull * sm_count(device) + n_seqs - 1) / n_seqs;
+  const dim3 grid(static_cast<unsigned>(want < cap ? want : cap), n_seqs);
+  auto go = [&](auto kern) {
+    return kv_launch("k_kv_summarize", kern, grid, kSumThreads, 0, 1, stream, k, table, lens, first, max_pages,
+                     n_pages, page_tokens, heads, dim, codes, scales, status);
+  };
+  return f16 ? go(k_kv_summarize<true>) : go(k_kv_summarize<false>);
+}
+
+// ---------------------------------------------------------------------------
+// Scores
+
+constexpr int kScThreads = 256;
+constexpr uint32_t kScQueries = 8;  // queries a CTA holds
+
+__device__ __forceinline__ int dp2a(uint32_t a16, uint32_t b8, int c, bool high) {
+  int d;
+  if (high)
+    asm("dp2a.hi.s32.s32 %0, %1, %2, %3;" : "=r"(d) : "r"(a16), "r"(b8), "r"(c));
+  else
+    asm("dp2a.lo.s32.s32 %0, %1, %2, %3;" : "=r"(d) : "r"(a16), "r"(b8), "r"(c));
+  return d;
+}
+
+// Position of query t of sequence b, or -1 where there is no such query.
+__device__ __forceinline__ int32_t query_place(const SelectArgs& a, uint32_t b, uint32_t t, int32_t len) {
+  const int32_t n = a.n_live ? a.n_live[b] : static_cast<int32_t>(a.T);
+  if (static_cast<int32_t>(t) >= n) return -1;
+  const int32_t p = len - n + static_cast<int32_t>(t);
+  return p < 0 ? -1 : p;
+}
+
+// CTA (sequence, block of kScQueries queries and share of the pages; kv head): quantises its
+// queries into shared memory, then scores its share of the pages.  lanes of
+// dim / 8 (16 codes each: minima of the lower half, maxima of the upper) hold
+// a page and are summed by shuffles.  Bound by the codes' bytes for single tokens
+// (each code is read once per kScQueries queries), by dp2a issue for chunks.
+__global__ void __launch_bounds__(kScThreads) k_kv_score(const SelectArgs a, uint32_t q_blocks,
+                                                         uint32_t shares) {
+  extern __shared__ uint32_t sq[];  // kScQueries x dim words of two 16-bit sums: min part, max part
+  __shared__ int32_t place[kScQueries];
+  __shared__ uint32_t most;
+  pdl_begin();
+  const uint32_t h = blockIdx.y, share = blockIdx.x % shares, bq = blockIdx.x / shares;
+  const uint32_t b = bq / q_blocks, t0 = bq % q_blocks * kScQueries;
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  const int32_t len = clamp_len(a.lens[b], a.page_tokens, a.max_pages);
+  if (threadIdx.x == 0) most = 0;
+  __syncthreads();
+  if (threadIdx.x < kScQueries) {
+    const uint32_t t = t0 + threadIdx.x;
+    const int32_t p = t < a.T ? query_place(a, b, t, len) : -1;
+    // a query that sees no more pages than its budget takes them all unscored
+    const uint32_t n = p < 0 ? 0 : static_cast<uint32_t>(p) / a.page_tokens + 1;
+    place[threadIdx.x] = n > a.budget ? p : -1;
+    if (n > a.budget) atomicMax(&most, n);
+  }
+  __syncthreads();
+  const uint32_t n_pages = most;
+  if (n_pages == 0) return;
+  const uint32_t nd = a.dim / 2;  // words of two elements
+  for (uint32_t i = warp; i < kScQueries; i += kScThreads / 32) {
+    if (place[i] < 0) continue;
+    const char* q = a.q + static_cast<int64_t>(b) * a.q_seq + static_cast<int64_t>(t0 + i) * a.q_token +
+                    static_cast<int64_t>(h) * a.group * a.q_head;
+    float amax = 0.f;
+    bool bad = false;
+    for (uint32_t g = 0; g < a.group; ++g)
+      for (uint32_t w = lane; w < nd; w += 32) {
+        const float2 v = pair_f32(*reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(g) * a.q_head + 4 * w), a.f16);
+        bad = bad || !finite_f(v.x) || !finite_f(v.y);
+        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+      }
+    bad = __any_sync(0xFFFFFFFFu, bad);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    const float inv = !bad && amax >= kTiny ? code_factor(amax) : 0.f;
+    for (uint32_t w = lane; w < nd; w += 32) {
+      int lx = 0, ly = 0, hx = 0, hy = 0;
+      if (inv != 0.f)
+        for (uint32_t g = 0; g < a.group; ++g) {
+          const float2 v = pair_f32(*reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(g) * a.q_head + 4 * w), a.f16);
+          const int x = max(-127, min(127, __float2int_rn(__fmul_rn(v.x, inv))));
+          const int y = max(-127, min(127, __float2int_rn(__fmul_rn(v.y, inv))));
+          lx += min(x, 0), ly += min(y, 0), hx += max(x, 0), hy += max(y, 0);
+        }
+      sq[i * a.dim + w] = (lx & 0xFFFF) | (static_cast<uint32_t>(ly) << 16);
+      sq[i * a.dim + nd + w] = (hx & 0xFFFF) | (static_cast<uint32_t>(hy) << 16);
+    }
+  }
+  __syncthreads();
+  // lanes per page: dim / 8 of them when that is a power of two, else the next one
+  uint32_t lpp = 1;
+  while (lpp * 8 < a.dim) lpp <<= 1;
+  const uint32_t per = 32 / lpp, sub = lane % lpp;
+  const bool on = sub * 8 < a.dim;
+  const uint32_t step = kScThreads / 32 * per * shares;
+  for (uint32_t p0 = (share * (kScThreads / 32) + warp) * per; p0 < n_pages; p0 += step) {
+    const uint32_t p = p0 + lane / lpp;
+    uint4 c = make_uint4(0, 0, 0, 0);
+    float scale = 0.f;
+    if (p < n_pages) {
+      const uint32_t pg = static_cast<uint32_t>(a.table[static_cast<uint64_t>(b) * a.max_pages + p]);
+      if (pg < a.n_pages) {
+        const uint64_t at = static_cast<uint64_t>(pg) * a.kv_heads + h;
+        if (on) {
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(a.codes + at * 2 * a.dim) + sub * 4;
+          c = make_uint4(src[0], src[1], src[2], src[3]);
+        }
+        scale = a.scales[at];
+      } else if (sub == 0) {
+        kv_status(a.status, IBP_ERANGE);
+      }
+    }
+    for (uint32_t i = 0; i < kScQueries; ++i) {
+      if (place[i] < 0) continue;
+      int s = 0;
+      if (on) {
+        const uint32_t* qw = sq + i * a.dim + sub * 8;
+        const uint4 q0 = *reinterpret_cast<const uint4*>(qw), q1 = *reinterpret_cast<const uint4*>(qw + 4);
+        s = dp2a(q0.x, c.x, s, false), s = dp2a(q0.y, c.x, s, true);
+        s = dp2a(q0.z, c.y, s, false), s = dp2a(q0.w, c.y, s, true);
+        s = dp2a(q1.x, c.z, s, false), s = dp2a(q1.y, c.z, s, true);
+        s = dp2a(q1.z, c.w, s, false), s = dp2a(q1.w, c.w, s, true);
+      }
+      for (uint32_t o = lpp >> 1; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      if (sub == 0 && p < n_pages)
+        a.scores[((static_cast<uint64_t>(b) * a.T + t0 + i) * a.kv_heads + h) * a.max_pages + p] =
+            finite_f(scale) ? __fmul_rn(__int2float_rn(s), scale) : __int_as_float(0x7F800000);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Selection
+
+constexpr int kSelThreads = 128;
+constexpr uint32_t kSelShared = 8192;  // scores held in shared memory; more are read from L2 on every pass
+
+// Whole-number key in the order of the score; +0 and -0 are equal.
+__device__ __forceinline__ uint32_t order_key(float s) {
+  const uint32_t u = __float_as_uint(s == 0.f ? 0.f : s);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ uint32_t sel_rank(bool flag, uint32_t* sums, uint32_t* total) {
+  const uint32_t lane = threadIdx.x & 31u, w = threadIdx.x >> 5;
+  const uint32_t m = __ballot_sync(0xFFFFFFFFu, flag);
+  __syncthreads();
+  if (lane == 0) sums[w] = __popc(m);
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+#pragma unroll
+  for (uint32_t i = 0; i < kSelThreads / 32; ++i) {
+    before += i < w ? sums[i] : 0;
+    all += sums[i];
+  }
+  *total = all;
+  return before + __popc(m & lanemask_lt());
+}
+
+// One CTA per query and kv head: the threshold key by four passes of an 8-bit
+// histogram over the scores that are neither forced nor hidden, then the pages
+// in ascending order by prefix counts.  Bound by the latency of its passes.
+__global__ void __launch_bounds__(kSelThreads) k_kv_select(const SelectArgs a, uint32_t key_cap) {
+  extern __shared__ uint32_t keys[];
+  __shared__ uint32_t hist[256], sums[kSelThreads / 32], sh_digit, sh_left;
+  pdl_begin();
+  const uint64_t row = blockIdx.x;
+  const uint64_t bt = row / a.kv_heads;
+  const uint32_t t = static_cast<uint32_t>(bt % a.T), b = static_cast<uint32_t>(bt / a.T), tid = threadIdx.x;
+  const int32_t raw = a.lens[b], len = clamp_len(raw, a.page_tokens, a.max_pages);
+  const int32_t place = query_place(a, b, t, len);
+  if (tid == 0) {
+    const int32_t nl = a.n_live ? a.n_live[b] : static_cast<int32_t>(a.T);
+    if (raw != len || nl > len || nl < 0) kv_status(a.status, IBP_ERANGE);
+  }
+  int32_t* out = a.picks + row * a.budget;
+  const uint32_t n = place < 0 ? 0 : static_cast<uint32_t>(place) / a.page_tokens + 1;
+  if (n <= a.budget) {
+    for (uint32_t i = tid; i < a.budget; i += kSelThreads) out[i] = i < n ? static_cast<int32_t>(i) : -1;
+    return;
+  }
+  // here keep_first + keep_last <= budget < n: the two forced ranges are apart
+  const uint32_t f0 = a.keep_first, f1 = n - a.keep_last;
+  const float* scores = a.scores + row * a.max_pages;
+  const bool held = n <= key_cap;
+  if (held)
+    for (uint32_t i = f0 + tid; i < f1; i += kSelThreads) keys[i] = order_key(scores[i]);
+  auto key = [&](uint32_t i) { return held ? keys[i] : order_key(scores[i]); };
+  uint32_t left = a.budget - a.keep_first - a.keep_last;  // to be taken by score
+  uint32_t prefix = 0;
+  if (left > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (uint32_t i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      const uint32_t high = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+      for (uint32_t i = f0 + tid; i < f1; i += kSelThreads) {
+        const uint32_t k = key(i);
+        if ((k & high) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      }
+      __syncthreads();
+      if (tid < 32) {  // lane l holds the digits 8l .. 8l+7; counts from the top
+        uint32_t mine = 0;
+        for (uint32_t i = 0; i < 8; ++i) mine += hist[8 * tid + i];
+        uint32_t above = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t v = __shfl_down_sync(0xFFFFFFFFu, above, o);
+          if (tid + o < 32) above += v;
+        }
+        above -= mine;  // keys of higher lanes
+        if (above < left && above + mine >= left) {
+          uint32_t d = 8 * tid + 7, acc = above;
+          while (acc + hist[d] < left) acc += hist[d--];
+          sh_digit = d;
+          sh_left = left - acc;
+        }
+      }
+      __syncthreads();
+      prefix |= sh_digit << shift;
+      left = sh_left;
+    }
+  }
+  // keys above `prefix` are taken, and the first `left` equal to it
+  const bool any = a.budget > a.keep_first + a.keep_last;
+  uint32_t done = 0, ties = 0, total;
+  for (uint32_t i0 = 0; i0 < n; i0 += kSelThreads) {
+    const uint32_t i = i0 + tid;
+    const bool forced = i < n && (i < f0 || i >= f1), open = any && i < n && !forced;
+    const uint32_t k = open ? key(i) : 0;
+    const bool tie = open && k == prefix;
+    const uint32_t nth = ties + sel_rank(tie, sums, &total);
+    ties += total;
+    const bool take = forced || (open && k > prefix) || (tie && nth < left);
+    const uint32_t at = done + sel_rank(take, sums, &total);
+    if (take && at < a.budget) out[at] = static_cast<int32_t>(i);
+    done += total;
+  }
+}
+
+int launch_kv_select(const SelectArgs& a, int device, cudaStream_t stream) {
+  const uint32_t q_blocks = (a.T + kScQueries - 1) / kScQueries;
+  uint32_t lpp = 1;
+  while (lpp * 8 < a.dim) lpp <<= 1;
+  const uint32_t per_cta = kScThreads / 32 * (32 / lpp);
+  const uint64_t want = (a.max_pages + 2 * per_cta - 1) / (2 * per_cta);
+  const uint64_t rows = static_cast<uint64_t>(a.kv_heads) * a.n_seqs * q_blocks;
+  const uint64_t cap = (16ull * sm_count(device) + rows - 1) / rows;
+  int rc = IBP_OK;
+  if (a.max_pages > a.budget) {
+    const uint32_t shares = static_cast<uint32_t>(want < cap ? want : cap);
+    const dim3 grid(a.n_seqs * q_blocks * shares, a.kv_heads);
+    rc = kv_launch("k_kv_score", k_kv_score, grid, kScThreads, kScQueries * a.dim * 4, 1, stream, a, q_blocks, shares);
+  }
+  if (rc != IBP_OK) return rc;
+  const uint32_t cap_keys = a.max_pages < kSelShared ? a.max_pages : kSelShared;
+  return kv_launch("k_kv_select", k_kv_select, dim3(a.n_seqs * a.T * a.kv_heads), kSelThreads, 4ull * cap_keys, 1,
+                   stream, a, cap_keys);
+}
+
+}  // namespace ibp

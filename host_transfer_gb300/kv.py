@@ -1,0 +1,439 @@
+"""Python binding of libibp's paged key/value cache operators (ctypes).
+
+Argument marshalling only, as in ``host_transfer_gb300.ibp``: every step runs
+in the library's CUDA kernels.  Names and formulas follow include/ibp.h:
+
+    table, lens, refs, moves, count = ibp_kv_fork(table, lens, refs, parents, page_tokens)
+    table, lens, refs = ibp_kv_free(table, lens, refs, seqs, page_tokens)
+    table, refs, moves, count = ibp_kv_compact(table, refs, page_tokens)
+    ibp_kv_copy(pages, moves, count)                        # in place
+    table, lens, refs = ibp_kv_accept(pages, table, lens, refs, n_draft, path, n_accept)
+    out, lse = ibp_tree_attention(q, k, v, table, lens, mask=mask)
+    ibp_kv_summarize(k, table, lens, codes, scales)         # in place
+    out, lse, picked = ibp_sparse_attention(q, k, v, table, lens, codes, scales, budget)
+    ibp_kv_get_status()                                     # raises on a data error
+
+Keys and values of a layer are tensors ``[n_pages, heads, page_tokens, dim]``
+(bfloat16 or float16) of any strides whose last is 1: tokens-first pages are a
+transposed view.  The page copies also take ``[n_pools, n_pages, heads,
+page_tokens, dim]``, every layer's K and V at once.  ``table`` is int32
+``[n_seqs, max_pages]``, ``lens`` int32 ``[n_seqs]``, ``refs`` int32
+``[n_pages]``, all on the device.
+
+``stream`` is a torch stream or a raw handle (default: the current stream);
+results and scratch are allocated for that stream.  Data errors go to a status
+word: the caller's own (``status``, an int32 device tensor) or the device's,
+read by ``ibp_kv_get_status``.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+
+import torch
+
+from . import ibp
+from .ibp import IBP_OK, IbpError
+
+IBP_KV_BF16 = 0
+IBP_KV_F16 = 1
+IBP_KV_MAX_DIM = 256
+IBP_SPARSE_MAX_BUDGET = 4096
+
+_DTYPES = {torch.bfloat16: IBP_KV_BF16, torch.float16: IBP_KV_F16}
+
+
+class _Pages(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n_pools", ctypes.c_uint64), ("pool_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_uint64), ("page_stride", ctypes.c_int64), ("heads", ctypes.c_uint32),
+                ("head_stride", ctypes.c_int64), ("page_tokens", ctypes.c_uint32),
+                ("token_stride", ctypes.c_int64), ("dim", ctypes.c_uint32), ("elem_bytes", ctypes.c_uint32)]
+
+
+class _Seqs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("n_seqs", ctypes.c_uint32),
+                ("max_pages", ctypes.c_uint32)]
+
+
+_bound = None
+
+
+def _load():
+    global _bound
+    lib = ibp.load()
+    if _bound is lib:
+        return lib
+    vp, u64, i64, u32, i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int64, ctypes.c_uint32, ctypes.c_int
+    size, f32 = ctypes.c_size_t, ctypes.c_float
+    pages, seqs = ctypes.POINTER(_Pages), ctypes.POINTER(_Seqs)
+    sigs = {
+        "ibp_kv_fork": ([seqs, u32, vp, u64, vp, u32, vp, vp, vp, vp, vp, vp, size, vp, vp], i32),
+        "ibp_kv_free": ([seqs, u32, vp, u64, vp, u32, vp, vp, vp, vp, vp], i32),
+        "ibp_kv_compact": ([seqs, u32, vp, u64, vp, vp, vp, vp, vp, size, vp, vp], i32),
+        "ibp_kv_pages_workspace": ([u64, u32], size),
+        "ibp_kv_copy": ([pages, vp, vp, u32, vp, vp], i32),
+        "ibp_kv_accept": ([pages, seqs, vp, vp, vp, vp, u32, vp, vp, vp, vp, vp], i32),
+        "ibp_tree_attention": ([pages, pages, u32, seqs, vp, i64, i64, i64, u32, u32, vp, vp, f32, vp, vp, vp, size,
+                                vp, vp], i32),
+        "ibp_tree_attention_workspace": ([u32, u32, u32, u32, u32], size),
+        "ibp_kv_summarize": ([pages, u32, seqs, vp, vp, vp, vp, vp], i32),
+        "ibp_sparse_attention": ([pages, pages, u32, seqs, vp, vp, vp, i64, i64, i64, u32, u32, vp, u32, u32, u32,
+                                  f32, vp, vp, vp, vp, size, vp, vp], i32),
+        "ibp_sparse_attention_workspace": ([u32] * 7, size),
+    }
+    for name, (args, res) in sigs.items():
+        f = getattr(lib, name)
+        f.argtypes = args
+        f.restype = res
+    _bound = lib
+    return lib
+
+
+# ---------------------------------------------------------------------------
+# Arguments
+
+
+def _ints(name: str, t: torch.Tensor, dim: int, device: torch.device | None = None) -> torch.Tensor:
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != dim:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension(s)")
+    if device is not None and t.is_cuda and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t
+
+
+def _sequences(table: torch.Tensor, lens: torch.Tensor) -> _Seqs:
+    _ints("table", table, 2)
+    _ints("lens", lens, 1, table.device)
+    if table.shape[0] != lens.shape[0]:
+        raise ValueError(f"table has {table.shape[0]} rows, lens {lens.shape[0]}")
+    return _Seqs(table.data_ptr(), lens.data_ptr(), table.shape[0], table.shape[1])
+
+
+def _as_pages(name: str, t: torch.Tensor, pools: bool = False) -> _Pages:
+    if pools and t.dim() == 5:
+        n_pools, shape, strides = t.shape[0], t.shape[1:], t.stride()
+        pool_stride, strides = strides[0], strides[1:]
+    elif t.dim() == 4:
+        n_pools, pool_stride, shape, strides = 1, 0, t.shape, t.stride()
+    else:
+        raise ValueError(f"{name} must have the dimensions {'[pools,] ' if pools else ''}pages, heads, tokens, dim")
+    if shape[3] > 1 and strides[3] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return _Pages(t.data_ptr(), n_pools, pool_stride, shape[0], strides[0], shape[1], strides[1], shape[2], strides[2],
+                  shape[3], t.element_size())
+
+
+def _dtype(q: torch.Tensor | None, *pages: torch.Tensor) -> int:
+    dt = pages[0].dtype
+    if dt not in _DTYPES or any(p.dtype != dt for p in pages) or (q is not None and q.dtype != dt):
+        raise ValueError("queries, keys and values must all be bfloat16 or all float16")
+    return _DTYPES[dt]
+
+
+def _same_device(device: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _out(name: str, t: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+def _for(stream, device: torch.device):
+    """(stream handle, context in which results of that stream are allocated)."""
+    if stream is None:
+        handle = ibp._stream(None, device)
+        if device.index == torch.cuda.current_device():
+            return handle, contextlib.nullcontext()
+        return handle, torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _device(t: torch.Tensor) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError("the page tensors must be on a CUDA device")
+    return t.device
+
+
+# ---------------------------------------------------------------------------
+# Status
+
+_status_words: dict[int, torch.Tensor] = {}
+
+
+def _status(status: torch.Tensor | None, device: torch.device) -> int:
+    if status is None:
+        word = _status_words.get(device.index)
+        if word is None:
+            word = torch.zeros(1, dtype=torch.int32, device=device)
+            torch.cuda.synchronize(device)  # made once: every stream may use it
+            _status_words[device.index] = word
+        return word.data_ptr()
+    if status.element_size() != 4 or status.numel() < 1:
+        raise ValueError("status must be a 32-bit word")
+    return status.data_ptr()
+
+
+def ibp_kv_get_status(device: int | None = None, raise_on_error: bool = True) -> int:
+    """Waits for the device, returns the first data error of the calls that
+    named no status word of their own since the last call, and clears it."""
+    device = torch.cuda.current_device() if device is None else int(device)
+    word = _status_words.get(device)
+    if word is None:
+        return IBP_OK
+    torch.cuda.synchronize(device)
+    code = int(word.item())
+    if code != IBP_OK:
+        word.zero_()
+        torch.cuda.synchronize(device)
+        if raise_on_error:
+            raise IbpError(code, "ibp_kv_get_status")
+    return code
+
+
+def _check(code: int, where: str):
+    if code != IBP_OK:
+        raise IbpError(code, where)
+
+
+# ---------------------------------------------------------------------------
+# Pages
+
+
+def ibp_kv_fork(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, parents: torch.Tensor,
+                page_tokens: int, status: torch.Tensor | None = None, stream=None):
+    """The next batch: row i continues row parents[i].  Returns new (table,
+    lens, refs) and the page copies to make, (moves, count) for ibp_kv_copy."""
+    lib, seqs = _load(), _sequences(table, lens)
+    device = _device(table)
+    _ints("refs", refs, 1, device)
+    _ints("parents", parents, 1, device)
+    n_out, n_pages = parents.shape[0], refs.shape[0]
+    handle, where = _for(stream, device)
+    with where:
+        table_out = torch.empty((n_out, table.shape[1]), dtype=torch.int32, device=device)
+        lens_out = torch.empty(n_out, dtype=torch.int32, device=device)
+        refs_out = torch.empty_like(refs)
+        moves = torch.empty((n_out, 3), dtype=torch.int32, device=device)
+        count = torch.empty(1, dtype=torch.int32, device=device)
+        size = lib.ibp_kv_pages_workspace(n_pages, n_out)
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        _check(lib.ibp_kv_fork(seqs, page_tokens, refs.data_ptr(), n_pages, parents.data_ptr(), n_out,
+                               table_out.data_ptr(), lens_out.data_ptr(), refs_out.data_ptr(), moves.data_ptr(),
+                               count.data_ptr(), ws.data_ptr(), size, _status(status, device), handle),
+               "ibp_kv_fork")
+    return table_out, lens_out, refs_out, moves, count
+
+
+def ibp_kv_free(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seqs: torch.Tensor, page_tokens: int,
+                inplace: bool = False, status: torch.Tensor | None = None, stream=None):
+    """Frees the listed sequences; returns (table, lens, refs), the arguments
+    themselves with `inplace`."""
+    lib, s = _load(), _sequences(table, lens)
+    device = _device(table)
+    _ints("refs", refs, 1, device)
+    _ints("seqs", seqs, 1, device)
+    handle, where = _for(stream, device)
+    with where:
+        out = (table, lens, refs) if inplace else tuple(torch.empty_like(t) for t in (table, lens, refs))
+        _check(lib.ibp_kv_free(s, page_tokens, refs.data_ptr(), refs.shape[0], seqs.data_ptr(), seqs.shape[0],
+                               out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _status(status, device),
+                               handle), "ibp_kv_free")
+    return out
+
+
+def ibp_kv_compact(table: torch.Tensor, refs: torch.Tensor, page_tokens: int, inplace: bool = False,
+                   status: torch.Tensor | None = None, stream=None):
+    """Live pages to the front of the pool; returns (table, refs, moves, count),
+    the first two the arguments themselves with `inplace`."""
+    lib = _load()
+    _ints("table", table, 2)
+    device = _device(table)
+    _ints("refs", refs, 1, device)
+    n_pages = refs.shape[0]
+    handle, where = _for(stream, device)
+    with where:
+        out = (table, refs) if inplace else (torch.empty_like(table), torch.empty_like(refs))
+        moves = torch.empty((n_pages, 3), dtype=torch.int32, device=device)
+        count = torch.empty(1, dtype=torch.int32, device=device)
+        size = lib.ibp_kv_pages_workspace(n_pages, 0)
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        # the lengths are not used: the references say which pages live
+        seqs = _Seqs(table.data_ptr(), refs.data_ptr(), table.shape[0], table.shape[1])
+        _check(lib.ibp_kv_compact(seqs, page_tokens, refs.data_ptr(), n_pages, out[0].data_ptr(), out[1].data_ptr(),
+                                  moves.data_ptr(), count.data_ptr(), ws.data_ptr(), size, _status(status, device),
+                                  handle), "ibp_kv_compact")
+    return *out, moves, count
+
+
+def ibp_kv_copy(pages: torch.Tensor, moves: torch.Tensor, count: torch.Tensor, status: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Copies pages as `moves` lists them, in place and in every pool."""
+    lib, p = _load(), _as_pages("pages", pages, pools=True)
+    device = _device(pages)
+    _ints("moves", moves, 2, device)
+    _ints("count", count, 1, device)
+    if moves.shape[1] != 3:
+        raise ValueError("moves must have three columns: from, to, tokens")
+    handle, where = _for(stream, device)
+    with where:
+        _check(lib.ibp_kv_copy(p, moves.data_ptr(), count.data_ptr(), moves.shape[0], _status(status, device),
+                               handle), "ibp_kv_copy")
+    return pages
+
+
+def ibp_kv_accept(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                  n_draft: torch.Tensor, path: torch.Tensor, n_accept: torch.Tensor, inplace: bool = False,
+                  status: torch.Tensor | None = None, stream=None):
+    """Keeps the accepted tokens of each sequence's draft (its last n_draft[b]
+    tokens): path[b][: n_accept[b]] move to the draft's front in every pool.
+    Returns (table, lens, refs)."""
+    lib, p, seqs = _load(), _as_pages("pages", pages, pools=True), _sequences(table, lens)
+    device = _device(pages)
+    for name, t, dim in (("refs", refs, 1), ("n_draft", n_draft, 1), ("path", path, 2), ("n_accept", n_accept, 1)):
+        _ints(name, t, dim, device)
+    n = table.shape[0]
+    if refs.shape[0] != p.n_pages or n_draft.shape[0] != n or path.shape[0] != n or n_accept.shape[0] != n:
+        raise ValueError("refs, n_draft, path or n_accept does not fit the pages or the sequences")
+    handle, where = _for(stream, device)
+    with where:
+        out = (table, lens, refs) if inplace else tuple(torch.empty_like(t) for t in (table, lens, refs))
+        if n == 0:
+            return (table, lens, refs) if inplace else (table.clone(), lens.clone(), refs.clone())
+        _check(lib.ibp_kv_accept(p, seqs, refs.data_ptr(), n_draft.data_ptr(), path.data_ptr(), n_accept.data_ptr(),
+                                 path.shape[1], out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
+                                 _status(status, device), handle), "ibp_kv_accept")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Attention
+
+
+def _queries(q: torch.Tensor, k: torch.Tensor, n_seqs: int):
+    if q.dim() != 4 or q.shape[0] != n_seqs or q.shape[3] != k.shape[3]:
+        raise ValueError("q must be [n_seqs, T, q_heads, dim] with the table's sequences and the pages' dim")
+    if q.shape[3] > 1 and q.stride(3) != 1:
+        raise ValueError("the last dimension of q must be contiguous")
+    return q.shape[1], q.shape[2]
+
+
+def _workspace(workspace: torch.Tensor | None, size: int, device):
+    if workspace is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    if workspace.numel() * workspace.element_size() < size or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and hold {size} bytes")
+    return workspace
+
+
+def ibp_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                       mask: torch.Tensor | None = None, n_draft: torch.Tensor | None = None,
+                       scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """Attention of each sequence's draft, its last T (or n_draft[b]) tokens.
+
+    mask   int32 [n_seqs, T, ceil(T / 32)]: bit i of row t lets drafted token t
+           see drafted token i; None: a chain (i <= t).
+    scale  default 1 / sqrt(dim).
+    Returns (out [n_seqs, T, q_heads, dim], lse [n_seqs, T, q_heads])."""
+    lib, seqs = _load(), _sequences(table, lens)
+    device = _device(k)
+    kp, vp = _as_pages("k", k), _as_pages("v", v)
+    T, heads = _queries(q, k, seqs.n_seqs)
+    dt = _dtype(q, k, v)
+    _same_device(device, q=q, v=v, table=table)
+    if mask is not None:
+        _ints("mask", mask, 3, device)
+        if tuple(mask.shape) != (seqs.n_seqs, T, (T + 31) // 32):
+            raise ValueError("mask must be [n_seqs, T, ceil(T / 32)]")
+    if n_draft is not None and _ints("n_draft", n_draft, 1, device).shape[0] != seqs.n_seqs:
+        raise ValueError("n_draft must hold one number per sequence")
+    handle, where = _for(stream, device)
+    with where:
+        out = _out("out", out, q.shape, q.dtype, device)
+        lse = _out("lse", lse, q.shape[:3], torch.float32, device)
+        size = lib.ibp_tree_attention_workspace(seqs.n_seqs, T, heads, kp.heads, kp.dim)
+        ws = _workspace(workspace, size, device)
+        _check(lib.ibp_tree_attention(kp, vp, dt, seqs, q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), T, heads,
+                                      ibp._ptr(n_draft), ibp._ptr(mask),
+                                      1.0 / math.sqrt(kp.dim) if scale is None else scale, out.data_ptr(),
+                                      lse.data_ptr(), ws.data_ptr(), size, _status(status, device), handle),
+               "ibp_tree_attention")
+    return out, lse
+
+
+def ibp_kv_summarize(k: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, codes: torch.Tensor,
+                     scales: torch.Tensor, first: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                     stream=None):
+    """8-bit bounds of the keys of every page that holds a position from
+    first[b] on (None: every page), into codes [n_pages, heads, 2, dim] int8
+    and scales [n_pages, heads] float32.  Returns (codes, scales)."""
+    lib, seqs = _load(), _sequences(table, lens)
+    device = _device(k)
+    kp, dt = _as_pages("k", k), _dtype(None, k)
+    _same_device(device, table=table)
+    _bounds(k, codes, scales)
+    if first is not None and _ints("first", first, 1, device).shape[0] != seqs.n_seqs:
+        raise ValueError("first must hold one position per sequence")
+    handle, where = _for(stream, device)
+    with where:
+        _check(lib.ibp_kv_summarize(kp, dt, seqs, ibp._ptr(first), codes.data_ptr(), scales.data_ptr(),
+                                    _status(status, device), handle), "ibp_kv_summarize")
+    return codes, scales
+
+
+def _bounds(k: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
+    n_pages, heads, _, dim = k.shape
+    if codes.dtype != torch.int8 or tuple(codes.shape) != (n_pages, heads, 2, dim) or not codes.is_contiguous():
+        raise ValueError("codes must be a contiguous int8 tensor [n_pages, heads, 2, dim]")
+    if scales.dtype != torch.float32 or tuple(scales.shape) != (n_pages, heads) or not scales.is_contiguous():
+        raise ValueError("scales must be a contiguous float32 tensor [n_pages, heads]")
+    _same_device(k.device, codes=codes, scales=scales)
+
+
+def ibp_sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                         codes: torch.Tensor, scales: torch.Tensor, budget: int, keep_first: int = 1,
+                         keep_last: int = 1, n_query: torch.Tensor | None = None, scale: float | None = None,
+                         out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                         pages: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         status: torch.Tensor | None = None, stream=None):
+    """Attention of each sequence's last T (or n_query[b]) tokens over `budget`
+    pages per query and kv head, selected by the bounds of ibp_kv_summarize;
+    the first keep_first and the last keep_last pages are always among them.
+
+    Returns (out, lse, pages): pages int32 [n_seqs, T, kv_heads, budget], the
+    selected places in the table row ascending, then -1."""
+    lib, seqs = _load(), _sequences(table, lens)
+    device = _device(k)
+    kp, vp = _as_pages("k", k), _as_pages("v", v)
+    T, heads = _queries(q, k, seqs.n_seqs)
+    dt = _dtype(q, k, v)
+    _same_device(device, q=q, v=v, table=table)
+    _bounds(k, codes, scales)
+    if not 1 <= budget <= IBP_SPARSE_MAX_BUDGET or keep_first < 0 or keep_last < 1 or keep_first + keep_last > budget:
+        raise ValueError("budget must hold keep_first >= 0 and keep_last >= 1 pages and be at most "
+                         f"{IBP_SPARSE_MAX_BUDGET}")
+    if n_query is not None and _ints("n_query", n_query, 1, device).shape[0] != seqs.n_seqs:
+        raise ValueError("n_query must hold one number per sequence")
+    handle, where = _for(stream, device)
+    with where:
+        out = _out("out", out, q.shape, q.dtype, device)
+        lse = _out("lse", lse, q.shape[:3], torch.float32, device)
+        pages = _out("pages", pages, (seqs.n_seqs, T, kp.heads, budget), torch.int32, device)
+        size = lib.ibp_sparse_attention_workspace(seqs.n_seqs, seqs.max_pages, T, heads, kp.heads, kp.dim, budget)
+        ws = _workspace(workspace, size, device)
+        _check(lib.ibp_sparse_attention(kp, vp, dt, seqs, codes.data_ptr(), scales.data_ptr(), q.data_ptr(),
+                                        q.stride(0), q.stride(1), q.stride(2), T, heads, ibp._ptr(n_query), budget,
+                                        keep_first, keep_last, 1.0 / math.sqrt(kp.dim) if scale is None else scale,
+                                        out.data_ptr(), lse.data_ptr(), pages.data_ptr(), ws.data_ptr(), size,
+                                        _status(status, device), handle), "ibp_sparse_attention")
+    return out, lse, pages

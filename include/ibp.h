@@ -66,8 +66,10 @@
 extern "C" {
 #endif
 
-/* 3: ibp_plan_info.short_rows, ibp_get_status_async, IBP_HINT_EARLY_FETCH */
-#define IBP_VERSION 3
+/* 3: ibp_plan_info.short_rows, ibp_get_status_async, IBP_HINT_EARLY_FETCH
+ * 4: the paged key/value cache entry points (ibp_kv_*, ibp_tree_attention,
+ *    ibp_sparse_attention) */
+#define IBP_VERSION 4
 #define IBP_MAX_W 8192u
 #define IBP_NOALLOC_MAX_W 4096u
 
@@ -499,6 +501,217 @@ int ibp_row_lengths(const ibp_plan* plan, const uint32_t* slots, uint64_t n_rows
  */
 int ibp_gather_raw(const uint32_t* rows, uint64_t n_rows, uint32_t W, const int64_t* row_ids,
                    uint64_t n_ids, uint32_t* out, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Paged key/value caches
+ * ---------------------------------------------------------------------------
+ * The keys and values of a layer live in pages of page_tokens tokens each; a
+ * sequence is a row of page ids (its table row) and a length.  Position p of
+ * sequence b is token p % page_tokens of page table[b][p / page_tokens].
+ * Pages decoded by the entry points above, copied, or written by a model all
+ * serve: a page is plain memory.  These operators have no counterpart on the
+ * pages this library follows; the formulas below define them.
+ *
+ * Conventions beyond those at the top of this file:
+ * - Every pointer is memory of the current device (tables and status words may
+ *   also be mapped pinned host memory); calls are asynchronous on `stream`,
+ *   launched as programmatic dependents and ordered on it.
+ * - `status` is a device-accessible uint32 word of the caller, or NULL: data
+ *   errors a kernel meets (a page or sequence id out of range: IBP_ERANGE; no
+ *   free page: IBP_ENOMEM; a reference count below zero: IBP_ECORRUPT; a wait
+ *   that ran out: IBP_ETIMEOUT) are stored there when it holds 0 (first error
+ *   wins).  No data error makes a kernel read or write out of range.
+ * - `ws` is scratch of at least the stated number of bytes, 16-byte aligned,
+ *   owned by the caller and free for reuse when the stream has passed the
+ *   call.  It needs no initial value.  No entry point allocates.
+ * - Strides are in elements; the dim elements of one token of one head are
+ *   contiguous.  Heads-first and tokens-first pages differ in strides only.
+ * - Offsets are 64-bit: pools may be larger than 2^32 bytes or elements.
+ */
+#define IBP_KV_BF16 0u
+#define IBP_KV_F16 1u
+#define IBP_KV_MAX_DIM 256u
+
+/* Pages of one pool (K or V of one layer), or of n_pools alike pools that share
+ * their page ids (K and V of every layer). */
+typedef struct ibp_kv_pages {
+  void* data;            /* token 0 of head 0 of page 0 of pool 0 */
+  uint64_t n_pools;      /* pools; the attention calls read pool 0 */
+  int64_t pool_stride;
+  uint64_t n_pages;      /* pages per pool, < 2^31 */
+  int64_t page_stride;
+  uint32_t heads;
+  int64_t head_stride;
+  uint32_t page_tokens;
+  int64_t token_stride;
+  uint32_t dim;          /* elements of one token of one head */
+  uint32_t elem_bytes;   /* 1, 2, 4 or 8 (the attention calls: 2) */
+} ibp_kv_pages;
+
+/* Sequences: rows of page ids and lengths in tokens.  Entries past a
+ * sequence's last page are not read. */
+typedef struct ibp_kv_seqs {
+  const int32_t* table;  /* n_seqs x max_pages, row-major */
+  const int32_t* lens;   /* n_seqs, each in [0, max_pages * page_tokens] */
+  uint32_t n_seqs;
+  uint32_t max_pages;
+} ibp_kv_seqs;
+
+/*
+ * Next batch of sequences from their parents (a beam step; a fork of one
+ * sequence into several drafts; a drop or a reorder of sequences): row i of
+ * the result continues row parents[i].  Full pages are shared (one reference
+ * each).  A partly filled last page stays with the lowest row that holds it;
+ * every other row gets the lowest free page in its place, in row order, and an
+ * entry of `moves`: (from, to, tokens to copy), for ibp_kv_copy.  The
+ * references of the old rows are dropped first, so pages that no result row
+ * holds are free for the copies.  When no page is left a row keeps its full
+ * pages alone (its new length says so) and the status is IBP_ENOMEM.
+ *
+ * seqs, refs  the present rows, and the references of n_pages pages.
+ * parents     n_out row numbers (out of range: an empty row, IBP_ERANGE).
+ * table_out, lens_out  n_out rows; must not overlap the present ones.
+ * refs_out    n_pages counts; may be refs.
+ * moves       n_out x 3 int32, unused entries -1; count  one int32.
+ * ws          ibp_kv_pages_workspace(n_pages, n_out) bytes.
+ * Errors: IBP_EINVAL, IBP_ECUDA.
+ */
+int ibp_kv_fork(const ibp_kv_seqs* seqs, uint32_t page_tokens, const int32_t* refs, uint64_t n_pages,
+                const int32_t* parents, uint32_t n_out, int32_t* table_out, int32_t* lens_out,
+                int32_t* refs_out, int32_t* moves, int32_t* count, void* ws, size_t ws_bytes,
+                uint32_t* status, void* stream);
+
+/*
+ * Frees sequences: drops one reference of each page of the listed rows and
+ * empties them (length 0, table row -1).  A row listed twice is freed once.
+ * The outputs may be the inputs.  A count that would fall below zero stays and
+ * records IBP_ECORRUPT.
+ */
+int ibp_kv_free(const ibp_kv_seqs* seqs, uint32_t page_tokens, const int32_t* refs, uint64_t n_pages,
+                const int32_t* rows, uint32_t n_rows, int32_t* table_out, int32_t* lens_out,
+                int32_t* refs_out, uint32_t* status, void* stream);
+
+/*
+ * Compacts the pool: with n_live pages of positive reference count, the live
+ * pages numbered n_live or more move, in order, to the free pages below n_live,
+ * in order.  Tables and references follow; `moves` (n_pages x 3, unused
+ * entries -1) and `count` list the copies for ibp_kv_copy, whole pages each.
+ * The outputs may be the inputs.  ws: ibp_kv_pages_workspace(n_pages, 0).
+ * Negative table entries give -1, entries of n_pages or more -1 and IBP_ERANGE.
+ */
+int ibp_kv_compact(const ibp_kv_seqs* seqs, uint32_t page_tokens, const int32_t* refs, uint64_t n_pages,
+                   int32_t* table_out, int32_t* refs_out, int32_t* moves, int32_t* count, void* ws,
+                   size_t ws_bytes, uint32_t* status, void* stream);
+
+/* Scratch bytes of ibp_kv_fork and ibp_kv_compact. */
+size_t ibp_kv_pages_workspace(uint64_t n_pages, uint32_t n_out);
+
+/*
+ * Copies pages within pools: for each of the first *count entries (from, to,
+ * tokens) of `moves` (at most max_moves), the first min(tokens, page_tokens)
+ * tokens of page `from` onto page `to`, in every pool.  No page may be both
+ * read and written by one call, nor written twice (the lists of ibp_kv_fork
+ * and ibp_kv_compact satisfy this).  Ids out of range are skipped and record
+ * IBP_ERANGE.  Any data indexed by page can follow a list, e.g. the codes and
+ * scales of ibp_kv_summarize as pages of one token.
+ */
+int ibp_kv_copy(const ibp_kv_pages* pages, const int32_t* moves, const int32_t* count, uint32_t max_moves,
+                uint32_t* status, void* stream);
+
+/*
+ * Keeps the accepted tokens of each sequence's draft, the last n_draft[b]
+ * tokens: draft token path[b][j] moves to place j of the draft for
+ * j < n_accept[b], in every pool, the length becomes that of the kept tokens,
+ * and pages behind it lose a reference.  path[b] ascends; at its first entry
+ * that does not, or that is not below n_draft[b], the sequence's list ends and
+ * IBP_ERANGE is recorded.  The draft's pages must not be shared.
+ *
+ * pages    every pool; seqs, refs, table_out, lens_out, refs_out as for
+ *          ibp_kv_free (the outputs may be the inputs).
+ * n_draft, n_accept  int32 per sequence; path  n_seqs x max_accept int32.
+ */
+int ibp_kv_accept(const ibp_kv_pages* pages, const ibp_kv_seqs* seqs, const int32_t* refs,
+                  const int32_t* n_draft, const int32_t* path, const int32_t* n_accept, uint32_t max_accept,
+                  int32_t* table_out, int32_t* lens_out, int32_t* refs_out, uint32_t* status, void* stream);
+
+/*
+ * Attention of drafted tokens over a paged cache.  The last n = n_draft[b]
+ * tokens of sequence b (n_draft NULL: T) are a draft: its keys and values are
+ * in the cache already.  Query t < n of sequence b sees every position before
+ * the draft and the drafted tokens i whose bit i % 32 of word
+ * mask[b][t][i / 32] is set (mask NULL: i <= t, a chain).  With the visible
+ * positions' scores s_j = scale * q . k_j:  out = sum exp(s_j - m) v_j / l,
+ * lse = m + ln l, m = max s_j, l = sum exp(s_j - m); a query that sees nothing,
+ * and queries t >= n, give zeros and -infinity.  One drafted token is ordinary
+ * decoding.  What a query does not see has no influence on it, whatever its
+ * bits (infinities and NaN included).  A position whose page id is out of
+ * range reads as a zero key and value and records IBP_ERANGE, as does a length
+ * below n (positions before the first do not exist).
+ *
+ * dtype    IBP_KV_BF16 or IBP_KV_F16: queries, pages and output.
+ * q        n_seqs x T x q_heads x dim by strides; dim contiguous.
+ * k, v     pages of one layer: dim a multiple of 8, at most IBP_KV_MAX_DIM; base
+ *          and strides multiples of 16 bytes; kv heads divide q_heads.
+ * mask     n_seqs x T x ceil(T / 32) words, or NULL.
+ * out      n_seqs x T x q_heads x dim, contiguous; lse  n_seqs x T x q_heads
+ *          floats, or NULL.
+ * ws       ibp_tree_attention_workspace bytes.
+ * Errors: IBP_EINVAL, IBP_ECUDA.
+ */
+int ibp_tree_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t dtype, const ibp_kv_seqs* seqs,
+                       const void* q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
+                       uint32_t T, uint32_t q_heads, const int32_t* n_draft, const uint32_t* mask, float scale,
+                       void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* status, void* stream);
+size_t ibp_tree_attention_workspace(uint32_t n_seqs, uint32_t T, uint32_t q_heads, uint32_t kv_heads,
+                                    uint32_t dim);
+
+/*
+ * Bounds of a page's keys in 8 bits, the cheap stand-in that
+ * ibp_sparse_attention scores pages by.  Over the valid tokens of a page and a
+ * head: a = max |k|, scale = a * (1 / 127), codes = rint(min_d * f) and
+ * rint(max_d * f) clamped to +-127, f = (1 / a) * 127, every operation rounded to
+ * single precision (so the codes do not depend on who computes them).
+ * a < 2^-100 gives zero codes and scale 0; a key that is not finite gives zero
+ * codes and scale +infinity.  Pages holding a position in [first[b], lens[b]) are computed anew
+ * (first NULL: every page); the others are left alone.
+ *
+ * codes   n_pages x heads x 2 (min, max) x dim int8; scales  n_pages x heads
+ *         float32, both contiguous; codes 4-byte aligned, k as above.
+ */
+int ibp_kv_summarize(const ibp_kv_pages* k, uint32_t dtype, const ibp_kv_seqs* seqs, const int32_t* first,
+                     int8_t* codes, float* scales, uint32_t* status, void* stream);
+
+/*
+ * Attention over the pages that a cheap score selects for each query.  The T
+ * queries of sequence b are its last n = n_query[b] tokens (NULL: T; queries
+ * t >= n give zeros, -infinity and no pages); query t sits at position
+ * p = lens[b] - n + t and sees positions up to p.  Per query and kv head, with
+ * c = rint(q * ((1 / a) * 127)), a = max |q| over the head's group (zeros when a
+ * is below 2^-100 or not finite): total = sum over the group's heads and dims
+ * of max(c, 0) * max_d + min(c, 0) * min_d, in whole numbers, and
+ * score = float(total) * scale (+infinity where the scale is).  The pages below
+ * keep_first and the keep_last pages up to p's own are selected; the highest
+ * scores among the rest, the lower page first when equal, fill up to `budget`.
+ * The whole-number totals make the choice the same on every run and split.
+ * Attention over the selected pages' positions up to p as in
+ * ibp_tree_attention.
+ *
+ * budget   pages per query and kv head, keep_first + keep_last <= budget,
+ *          keep_last >= 1, budget <= IBP_SPARSE_MAX_BUDGET.
+ * pages_out  n_seqs x T x kv_heads x budget int32, or NULL: the selected pages
+ *          (places in the table row) ascending, then -1.
+ * q_heads / kv_heads * dim <= 65536.  The rest as for ibp_tree_attention.
+ */
+#define IBP_SPARSE_MAX_BUDGET 4096u
+int ibp_sparse_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t dtype, const ibp_kv_seqs* seqs,
+                         const int8_t* codes, const float* scales, const void* q, int64_t q_seq_stride,
+                         int64_t q_token_stride, int64_t q_head_stride, uint32_t T, uint32_t q_heads,
+                         const int32_t* n_query, uint32_t budget, uint32_t keep_first, uint32_t keep_last,
+                         float scale, void* out, float* lse, int32_t* pages_out, void* ws, size_t ws_bytes,
+                         uint32_t* status, void* stream);
+size_t ibp_sparse_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t T, uint32_t q_heads,
+                                      uint32_t kv_heads, uint32_t dim, uint32_t budget);
 
 #ifdef __cplusplus
 }
