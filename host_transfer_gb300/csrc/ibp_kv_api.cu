@@ -276,7 +276,12 @@ int ibp_kv_accept(const ibp_kv_pages* pages, const ibp_kv_seqs* seqs, const int3
 
 size_t ibp_tree_attention_workspace(uint32_t n_seqs, uint32_t T, uint32_t q_heads, uint32_t kv_heads, uint32_t dim) {
   if (kv_heads == 0 || q_heads % kv_heads || dim == 0 || dim > IBP_KV_MAX_DIM) return 0;
-  return kv_attend_workspace(static_cast<uint64_t>(n_seqs) * kv_heads, T * (q_heads / kv_heads), dim);
+  const uint64_t rows = static_cast<uint64_t>(T) * (q_heads / kv_heads);
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) cudaGetLastError();
+  const size_t few = kv_attend_workspace(static_cast<uint64_t>(n_seqs) * kv_heads, rows, dim);
+  const size_t many = kv_tree_workspace(rows, dim, device);
+  return few > many ? few : many;
 }
 
 int ibp_tree_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t dtype, const ibp_kv_seqs* seqs,
@@ -296,6 +301,9 @@ int ibp_tree_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t dt
   if (!resolve(a.mask, device, true)) return refuse("mask is not device-accessible");
   if (ws_bytes < ibp_tree_attention_workspace(seqs->n_seqs, T, q_heads, k->heads, k->dim) || (ws_bytes && !ws))
     return refuse("ws is smaller than ibp_tree_attention_workspace");
+  bool done = false;
+  rc = launch_kv_tree(a, device, ws_bytes, static_cast<cudaStream_t>(stream), &done);
+  if (rc || done) return rc;
   return launch_kv_attend(a, device, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 

@@ -544,10 +544,10 @@ constexpr uint32_t kMaxUnits = 2048;  // CTAs up to which items are split
 
 static uint32_t padded_dim(uint32_t dim) { return dim <= 64 ? 64 : (dim <= 128 ? 128 : 256); }
 // 16 rows a CTA where there are more than 8 and the registers allow it.
-static uint32_t tile_rows(uint32_t rows, uint32_t dp) { return rows > 8 && dp < 256 ? 16 : 8; }
+static uint32_t tile_rows(uint64_t rows, uint32_t dp) { return rows > 8 && dp < 256 ? 16 : 8; }
 
 // items: (sequence[, query], kv head) triples; rows of each.
-size_t kv_attend_workspace(uint64_t items, uint32_t rows, uint32_t dim) {
+size_t kv_attend_workspace(uint64_t items, uint64_t rows, uint32_t dim) {
   const uint32_t dp = padded_dim(dim), tr = tile_rows(rows, dp);
   const uint64_t tiles = items * ((rows + tr - 1) / tr);
   return tiles >= kMaxUnits ? 0 : 2ull * kMaxUnits * tr * (dp + 2) * 4;

@@ -121,7 +121,12 @@ struct AttendArgs {
 // Tree attention by rows of at most 16 queries per CTA, and sparse attention
 // (ibp_kv_attend.cu).
 int launch_kv_attend(AttendArgs& a, int device, size_t ws_bytes, cudaStream_t stream);
-size_t kv_attend_workspace(uint64_t items, uint32_t rows, uint32_t dim);
+size_t kv_attend_workspace(uint64_t items, uint64_t rows, uint32_t dim);
+
+// Tree attention on the tensor cores (ibp_kv_tree.cu); *done is set when the
+// call's shape is one it takes.
+int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_t stream, bool* done);
+size_t kv_tree_workspace(uint64_t rows, uint32_t dim, int device);
 
 struct SelectArgs {
   const char* q;
