@@ -146,9 +146,12 @@ int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_
   const uint64_t longest = (static_cast<uint64_t>(a.max_pages) * a.page_tokens + kTcTile - 1) / kTcTile;
   const uint64_t tiles = longest * a.n_seqs * a.kv_heads * t.row_pairs;
   const uint64_t want = (tiles + kTcMinTiles - 1) / kTcMinTiles, sms = sm_count(device);
-  t.n_ctas = static_cast<uint32_t>(want < sms ? want : sms);
+  const uint64_t n = sms;
+  uint64_t ctas = want < sms ? want : sms;
+  if (ctas > t.row_pairs) ctas -= ctas % t.row_pairs;
+  t.n_ctas = static_cast<uint32_t>(ctas);
   char* w = reinterpret_cast<char*>(a.part);
-  const size_t n = sms, per = mt * kTcTile;
+  const size_t per = mt * kTcTile;
   t.first = reinterpret_cast<int4*>(w);
   w += align256((n + 1) * sizeof(int4));
   t.ml_part = reinterpret_cast<float2*>(w);

@@ -24,7 +24,9 @@
 // Work is split evenly over the CTAs, one per SM, by tiles of all items in a
 // row: a CTA's range may end inside an item, whose parts are then joined by
 // k_kv_tree_join in a fixed order.  Ragged lengths thus cost nothing and the
-// scratch is two slots per CTA.
+// scratch is two slots per CTA.  The row blocks of a kv head are furthest apart
+// in that order and the number of CTAs is a multiple of theirs, so the CTAs that
+// read the same cache tiles do so at the same time and DRAM is read once.
 //
 // Every wait has an iteration limit: a CTA that runs into it raises a flag all
 // its waits heed, records IBP_ETIMEOUT, waits for its copies and returns.
@@ -116,6 +118,11 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"(add)
       : "memory");
 }
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -153,6 +160,25 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two single-precision lanes in one register pair.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
@@ -183,9 +209,8 @@ struct TcShared {
   uint32_t tmem;
   uint32_t stop;
   uint32_t odd;       // 1 + the last segment whose draft holds infinities or NaN among its values
-  uint32_t b0;        // first sequence of this CTA's range
-  uint64_t before;    // tiles of the sequences before it
-  uint64_t total;     // tiles of all
+  uint32_t pair0, b0; // row block and sequence in which this CTA's range begins
+  uint64_t in0;       // tiles of that sequence before the range
   uint32_t sums[12];
 };
 
@@ -206,21 +231,24 @@ __device__ __forceinline__ uint32_t tiles_of(const AttendArgs& a, uint32_t b) {
 // Walks the segments of [at, end): every role of the CTA does so by itself.
 struct TcWalk {
   const TcArgs& t;
-  uint32_t b, per;      // present sequence, its items
-  uint32_t tiles;       // of each item
+  uint32_t pair, b;     // present row block and sequence
+  uint32_t tiles;       // of each of its items
   uint64_t in;          // position inside the sequence's tiles
   uint64_t left;
   __device__ TcWalk(const TcArgs& t_, const TcShared& sh, uint64_t at, uint64_t end) : t(t_) {
+    pair = sh.pair0;
     b = sh.b0;
-    per = t.a.kv_heads * t.row_pairs;
     tiles = at < end ? tiles_of(t.a, b) : 1;
-    in = at - sh.before;
+    in = sh.in0;
     left = end - at;
   }
   __device__ bool next(TcSeg* s) {
     if (left == 0) return false;
-    if (in == static_cast<uint64_t>(tiles) * per) {
-      ++b;
+    if (in == static_cast<uint64_t>(tiles) * t.a.kv_heads) {
+      if (++b == t.a.n_seqs) {
+        b = 0;
+        ++pair;
+      }
       in = 0;
       tiles = tiles_of(t.a, b);
     }
@@ -230,8 +258,8 @@ struct TcWalk {
     s->tiles = static_cast<uint32_t>(rest < left ? rest : left);
     s->all = tiles;
     s->b = b;
-    s->pair = item % t.row_pairs;
-    s->h = item / t.row_pairs;
+    s->pair = pair;
+    s->h = item;
     const int32_t len = clamp_len(t.a.lens[b], t.a.page_tokens, t.a.max_pages);
     const int32_t n = t.a.n_live ? t.a.n_live[b] : static_cast<int32_t>(t.a.T);
     s->len = len;
@@ -316,7 +344,6 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
 
   // Where this CTA's range begins: the tiles of all sequences, and the first
   // sequence that reaches past the start.
-  const uint64_t per_tile = static_cast<uint64_t>(a.kv_heads) * t.row_pairs;
   {
     uint32_t n = 0;
     for (uint32_t b = tid; b < a.n_seqs; b += S::kThreads) n += tiles_of(a, b);
@@ -330,26 +357,30 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
   uint64_t total = 0;
 #pragma unroll
   for (uint32_t i = 0; i < S::kThreads / 32; ++i) total += sh.sums[i];
-  total *= per_tile;
+  const uint64_t block = total * a.kv_heads;  // tiles of a row block
+  total = block * t.row_pairs;
   uint64_t share = (total + t.n_ctas - 1) / t.n_ctas;
   if (share < kTcMinTiles) share = kTcMinTiles;
   const uint64_t at = blockIdx.x * share < total ? blockIdx.x * share : total;
   const uint64_t end = total - at < share ? total : at + share;
   if (warp == 0 && at < end) {
+    const uint32_t pair = static_cast<uint32_t>(at / block);
+    const uint64_t in = at - pair * block;
     uint64_t seen = 0;
     for (uint32_t c = 0; c < a.n_seqs; c += 32) {
       const uint32_t b = c + lane;
-      uint64_t n = b < a.n_seqs ? tiles_of(a, b) * per_tile : 0, incl = n;
+      uint64_t n = b < a.n_seqs ? static_cast<uint64_t>(tiles_of(a, b)) * a.kv_heads : 0, incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += v;
       }
-      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, seen + incl > at);
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, seen + incl > in);
       if (hit) {
         if (lane == __ffs(hit) - 1) {
+          sh.pair0 = pair;
           sh.b0 = b;
-          sh.before = seen + incl - n;
+          sh.in0 = in - (seen + incl - n);
         }
         break;
       }
@@ -433,24 +464,32 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
     TcSeg s;
     uint32_t g = 0, segs = 0;
     bool ok = true;
+    // One elected thread issues.  The descriptors of a group differ from its
+    // first by constants, so that eight products are little more than eight
+    // instructions: built one by one from addresses, beside two busy softmax warps
+    // on the scheduler, each took 110 cycles instead of the 64 it runs for.
+    const uint64_t qd = tc::operand(q_sm, 16), kd = tc::operand(k_at(0), 16), vd = tc::operand(v_at(0), S::kPanel);
+    constexpr uint32_t kTileStep = S::kTileBytes >> 4;
     auto qk = [&](uint32_t tile, uint32_t slot, uint32_t st) {
-      if (lane == 0) {
-        const uint32_t qa = q_sm + tile * S::kTileBytes;
+      if (tc::elect()) {
+        const uint64_t qa = qd + tile * kTileStep, ka = kd + st * (2 * kTileStep);
+        const uint32_t d = tmem + slot * 128;
 #pragma unroll
         for (uint32_t kk = 0; kk < DP / 16; ++kk) {
-          const uint32_t off = (kk / 4) * S::kPanel + (kk % 4) * 32;
-          tc::mma_ss(tmem + slot * 128, tc::operand(qa + off, 16), tc::operand(k_at(st) + off, 16), id_qk, kk > 0);
+          const uint32_t off = ((kk / 4) * S::kPanel + (kk % 4) * 32) >> 4;
+          tc::mma_ss(d, qa + off, ka + off, id_qk, kk > 0);
         }
         tc::commit(tc::s32(&sh.s_full[slot]));
       }
       __syncwarp();
     };
     auto pv = [&](uint32_t tile, uint32_t slot, uint32_t st, bool add) {
-      if (lane == 0) {
+      if (tc::elect()) {
+        const uint64_t va = vd + st * (2 * kTileStep);
+        const uint32_t d = tmem + S::kOCol + tile * DP, p = tmem + slot * 128;
+        tc::mma_ts(d, p, va, id_pv, add);
 #pragma unroll
-        for (uint32_t kk = 0; kk < kTcTile / 16; ++kk)
-          tc::mma_ts(tmem + S::kOCol + tile * DP, tmem + slot * 128 + kk * 8,
-                     tc::operand(v_at(st) + kk * 16 * 128, S::kPanel), id_pv, add || kk > 0);
+        for (uint32_t kk = 1; kk < kTcTile / 16; ++kk) tc::mma_ts(d, p + kk * 8, va + kk * (2048 >> 4), id_pv, 1);
         tc::commit(tc::s32(&sh.pv_done[tile]));
       }
       __syncwarp();
@@ -460,7 +499,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       return __all_sync(0xFFFFFFFFu, r) != 0;
     };
     auto release = [&](uint64_t* bar) {
-      if (lane == 0) tc::commit(tc::s32(bar));
+      if (tc::elect()) tc::commit(tc::s32(bar));
       __syncwarp();
     };
     // V of the item's last tiles: tokens past the length become zeros (what the
@@ -599,26 +638,34 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc::fence_after();
-        float x[kTcTile];
         const uint32_t s_col = tmem + lanes + slot * 128;
-#pragma unroll
-        for (uint32_t c = 0; c < 4; ++c) tc::ld32(x + 32 * c, s_col + 32 * c);
-        tc::ld_wait();
         const int32_t p0 = static_cast<int32_t>((s.tile0 + j) * kTcTile);
-        if (p0 + static_cast<int32_t>(kTcTile) > s.ctx) {
+        const bool partly = p0 + static_cast<int32_t>(kTcTile) > s.ctx;  // some row may not see it all
+        // The scores are read twice, 32 at a time: for the maximum, and for the
+        // exponentials.  All 128 in registers would spill at 168 a thread.
+        float y[2][32];
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (partly)
 #pragma unroll
-          for (uint32_t c = 0; c < 4; ++c) {
-            const uint32_t bits = live ? seen_bits(a, s, words, tok, p0 + 32 * static_cast<int32_t>(c)) : 0u;
+          for (uint32_t c = 0; c < 4; ++c)
+            bits[c] = live ? seen_bits(a, s, words, tok, p0 + 32 * static_cast<int32_t>(c)) : 0u;
+        tc::ld32(y[0], s_col);
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c) {
+          float(&x)[32] = y[c & 1u];
+          tc::ld_wait();
+          if (c < 3) tc::ld32(y[(c + 1) & 1u], s_col + 32 * (c + 1));
+          if (partly)
 #pragma unroll
             for (uint32_t i = 0; i < 32; ++i)
-              if (!((bits >> i) & 1u)) x[32 * c + i] = -INFINITY;
-          }
+              if (!((bits[c] >> i) & 1u)) x[i] = -INFINITY;
+#pragma unroll
+          for (uint32_t i = 0; i < 32; i += 8)
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(x[i + e], x[i + e + 4]));
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (uint32_t i = 0; i < kTcTile; i += 4)
-#pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[i + e]);
+        tc::ld32(y[0], s_col);
         const float tile_top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
         const bool grow = tile_top > top + 8.f || (top == -INFINITY && tile_top > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -643,21 +690,31 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
           }
         }
         const float off = top == -INFINITY ? 0.f : -top;
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t part[2] = {0, 0};  // two sums of two lanes
+        const uint64_t scale2 = tc::two(a.scale_log2, a.scale_log2), off2 = tc::two(off, off);
+        float w[32];
 #pragma unroll
-        for (uint32_t c = 0; c < 2; ++c) {
-          float w[32];
+        for (uint32_t c = 0; c < 4; ++c) {
+          float(&x)[32] = y[c & 1u];
+          tc::ld_wait();
+          if (c < 3) tc::ld32(y[(c + 1) & 1u], s_col + 32 * (c + 1));
+          if (partly)
 #pragma unroll
-          for (uint32_t i = 0; i < 32; ++i) {
-            const float p = tc::ex2(fmaf(x[64 * c + 2 * i], a.scale_log2, off));
-            const float q = tc::ex2(fmaf(x[64 * c + 2 * i + 1], a.scale_log2, off));
-            part[(2 * i) & 3u] += p;
-            part[(2 * i + 1) & 3u] += q;
-            w[i] = __uint_as_float(tc::pack2<F16>(p, q));
+            for (uint32_t i = 0; i < 32; ++i)
+              if (!((bits[c] >> i) & 1u)) x[i] = -INFINITY;
+#pragma unroll
+          for (uint32_t i = 0; i < 16; ++i) {
+            float p, q;
+            tc::split(tc::fma2(tc::two(x[2 * i], x[2 * i + 1]), scale2, off2), p, q);
+            p = tc::ex2(p), q = tc::ex2(q);
+            part[i & 1u] = tc::add2(part[i & 1u], tc::two(p, q));
+            w[(c & 1u) * 16 + i] = __uint_as_float(tc::pack2<F16>(p, q));
           }
-          tc::st32(s_col + 32 * c, w);
+          if (c & 1u) tc::st32(s_col + 32 * (c / 2), w);
         }
-        sum += (part[0] + part[1]) + (part[2] + part[3]);
+        float s0, s1;
+        tc::split(tc::add2(part[0], part[1]), s0, s1);
+        sum += s0 + s1;
         tc::st_wait();
         tc::fence_before();
         tc::bar_arrive(tc::s32(&sh.p_full[slot]));
