@@ -149,7 +149,15 @@ __device__ __forceinline__ void st32(uint32_t addr, const float* r) {
       "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
       : "memory");
 }
-__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loaded registers pass through the wait, so that no use of them can be
+// moved before it.
+__device__ __forceinline__ void ld_wait32(float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]), "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15]), "+r"(u[16]), "+r"(u[17]), "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]), "+r"(u[22]), "+r"(u[23]), "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]), "+r"(u[29]), "+r"(u[30]), "+r"(u[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -205,7 +213,7 @@ struct TcShape {
 
 struct TcShared {
   uint64_t k_full[6], v_full[6], k_empty[6], v_empty[6];
-  uint64_t s_full[2], p_full[2], pv_done[2], q_full[2];
+  uint64_t s_full[2], p_full[2][2], pv_done[2], q_full[2];  // p_full: per slot and half
   uint32_t tmem;
   uint32_t stop;
   uint32_t odd;       // 1 + the last segment whose draft holds infinities or NaN among its values
@@ -326,7 +334,8 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
     }
     for (uint32_t i = 0; i < 2; ++i) {
       tc::bar_init(tc::s32(&sh.s_full[i]), 1);
-      tc::bar_init(tc::s32(&sh.p_full[i]), 128);
+      tc::bar_init(tc::s32(&sh.p_full[i][0]), 128);
+      tc::bar_init(tc::s32(&sh.p_full[i][1]), 128);
       tc::bar_init(tc::s32(&sh.pv_done[i]), 1);
       tc::bar_init(tc::s32(&sh.q_full[i]), 128);
     }
@@ -483,14 +492,15 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       }
       __syncwarp();
     };
-    auto pv = [&](uint32_t tile, uint32_t slot, uint32_t st, bool add) {
+    // Half hf of P V: 64 tokens.
+    auto pv = [&](uint32_t tile, uint32_t slot, uint32_t st, uint32_t hf, bool add) {
       if (tc::elect()) {
-        const uint64_t va = vd + st * (2 * kTileStep);
-        const uint32_t d = tmem + S::kOCol + tile * DP, p = tmem + slot * 128;
+        const uint64_t va = vd + st * (2 * kTileStep) + hf * (8192 >> 4);
+        const uint32_t d = tmem + S::kOCol + tile * DP, p = tmem + slot * 128 + hf * 32;
         tc::mma_ts(d, p, va, id_pv, add);
 #pragma unroll
-        for (uint32_t kk = 1; kk < kTcTile / 16; ++kk) tc::mma_ts(d, p + kk * 8, va + kk * (2048 >> 4), id_pv, 1);
-        tc::commit(tc::s32(&sh.pv_done[tile]));
+        for (uint32_t kk = 1; kk < kTcTile / 32; ++kk) tc::mma_ts(d, p + kk * 8, va + kk * (2048 >> 4), id_pv, 1);
+        if (hf) tc::commit(tc::s32(&sh.pv_done[tile]));
       }
       __syncwarp();
     };
@@ -556,16 +566,22 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
         for (uint32_t j = 0; j < n; ++j) {
           if (!(ok = wait(&sh.v_full[stage(j)], phase(j)))) break;
           clean(s, j, stage(j));
-          if (!(ok = wait(&sh.p_full[0], (g + j) & 1u))) break;
+          if (!(ok = wait(&sh.p_full[0][0], (g + j) & 1u))) break;
           tc::fence_after();
-          pv(0, 0, stage(j), j > 0);
+          pv(0, 0, stage(j), 0, j > 0);
+          if (!(ok = wait(&sh.p_full[0][1], (g + j) & 1u))) break;
+          tc::fence_after();
+          pv(0, 0, stage(j), 1, true);
           if (j + 1 < n) {
             if (!(ok = wait(&sh.k_full[stage(j + 1)], phase(j + 1)))) break;
             qk(0, 0, stage(j + 1));
           }
-          if (!(ok = wait(&sh.p_full[1], (g + j) & 1u))) break;
+          if (!(ok = wait(&sh.p_full[1][0], (g + j) & 1u))) break;
           tc::fence_after();
-          pv(1, 1, stage(j), j > 0);
+          pv(1, 1, stage(j), 0, j > 0);
+          if (!(ok = wait(&sh.p_full[1][1], (g + j) & 1u))) break;
+          tc::fence_after();
+          pv(1, 1, stage(j), 1, true);
           release(&sh.v_empty[stage(j)]);
           if (j + 1 < n) {
             qk(1, 1, stage(j + 1));
@@ -581,9 +597,13 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
         for (uint32_t j = 0; j < n && ok; ++j) {
           if (!(ok = wait(&sh.v_full[stage(j)], phase(j)))) break;
           clean(s, j, stage(j));
-          if (!(ok = wait(&sh.p_full[(g + j) & 1u], ((g + j) >> 1) & 1u))) break;
+          const uint32_t slot = (g + j) & 1u, ph = ((g + j) >> 1) & 1u;
+          if (!(ok = wait(&sh.p_full[slot][0], ph))) break;
           tc::fence_after();
-          pv(0, (g + j) & 1u, stage(j), j > 0);
+          pv(0, slot, stage(j), 0, j > 0);
+          if (!(ok = wait(&sh.p_full[slot][1], ph))) break;
+          tc::fence_after();
+          pv(0, slot, stage(j), 1, true);
           release(&sh.v_empty[stage(j)]);
           if (j + 2 < n) {
             if (!(ok = wait(&sh.k_full[stage(j + 2)], phase(j + 2)))) break;
@@ -641,31 +661,35 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
         const uint32_t s_col = tmem + lanes + slot * 128;
         const int32_t p0 = static_cast<int32_t>((s.tile0 + j) * kTcTile);
         const bool partly = p0 + static_cast<int32_t>(kTcTile) > s.ctx;  // some row may not see it all
+        if (partly) {  // what the row does not see becomes -infinity, in place
+#pragma unroll 1
+          for (uint32_t c = 0; c < 4; ++c) {
+            const uint32_t bits = live ? seen_bits(a, s, words, tok, p0 + 32 * static_cast<int32_t>(c)) : 0u;
+            float x[32];
+            tc::ld32(x, s_col + 32 * c);
+            tc::ld_wait32(x);
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i)
+              if (!((bits >> i) & 1u)) x[i] = -INFINITY;
+            tc::st32(s_col + 32 * c, x);
+          }
+          tc::st_wait();
+        }
         // The scores are read twice, 32 at a time: for the maximum, and for the
         // exponentials.  All 128 in registers would spill at 168 a thread.
         float y[2][32];
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (partly)
-#pragma unroll
-          for (uint32_t c = 0; c < 4; ++c)
-            bits[c] = live ? seen_bits(a, s, words, tok, p0 + 32 * static_cast<int32_t>(c)) : 0u;
         tc::ld32(y[0], s_col);
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {
           float(&x)[32] = y[c & 1u];
-          tc::ld_wait();
-          if (c < 3) tc::ld32(y[(c + 1) & 1u], s_col + 32 * (c + 1));
-          if (partly)
-#pragma unroll
-            for (uint32_t i = 0; i < 32; ++i)
-              if (!((bits[c] >> i) & 1u)) x[i] = -INFINITY;
+          tc::ld_wait32(x);
+          tc::ld32(y[(c + 1) & 1u], s_col + 32 * ((c + 1) & 3u));
 #pragma unroll
           for (uint32_t i = 0; i < 32; i += 8)
 #pragma unroll
             for (uint32_t e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(x[i + e], x[i + e + 4]));
         }
-        tc::ld32(y[0], s_col);
         const float tile_top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
         const bool grow = tile_top > top + 8.f || (top == -INFINITY && tile_top > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -682,7 +706,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
             for (uint32_t c = 0; c < DP / 32; ++c) {
               float o[32];
               tc::ld32(o, o_col + 32 * c);
-              tc::ld_wait();
+              tc::ld_wait32(o);
 #pragma unroll
               for (uint32_t i = 0; i < 32; ++i) o[i] *= f;
               tc::st32(o_col + 32 * c, o);
@@ -696,12 +720,8 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {
           float(&x)[32] = y[c & 1u];
-          tc::ld_wait();
+          tc::ld_wait32(x);
           if (c < 3) tc::ld32(y[(c + 1) & 1u], s_col + 32 * (c + 1));
-          if (partly)
-#pragma unroll
-            for (uint32_t i = 0; i < 32; ++i)
-              if (!((bits[c] >> i) & 1u)) x[i] = -INFINITY;
 #pragma unroll
           for (uint32_t i = 0; i < 16; ++i) {
             float p, q;
@@ -710,14 +730,16 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
             part[i & 1u] = tc::add2(part[i & 1u], tc::two(p, q));
             w[(c & 1u) * 16 + i] = __uint_as_float(tc::pack2<F16>(p, q));
           }
-          if (c & 1u) tc::st32(s_col + 32 * (c / 2), w);
+          if (c & 1u) {  // half of P: its product may begin
+            tc::st32(s_col + 32 * (c / 2), w);
+            tc::st_wait();
+            tc::fence_before();
+            tc::bar_arrive(tc::s32(&sh.p_full[slot][c / 2]));
+          }
         }
         float s0, s1;
         tc::split(tc::add2(part[0], part[1]), s0, s1);
         sum += s0 + s1;
-        tc::st_wait();
-        tc::fence_before();
-        tc::bar_arrive(tc::s32(&sh.p_full[slot]));
       }
       if (!ok) break;
       // ---- this segment's sums.  A wait by parity must not be two phases behind:
@@ -737,7 +759,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       for (uint32_t c = 0; c < DP / 32; ++c) {
         float o[32];
         tc::ld32(o, o_col + 32 * c);
-        tc::ld_wait();
+        tc::ld_wait32(o);
         if (odd && live) {
           // infinities and NaN of the drafted tokens of this segment that the row sees
           for (int32_t p = max(s.ctx, static_cast<int32_t>(s.tile0 * kTcTile));
