@@ -31,6 +31,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import threading
 
 import torch
 
@@ -93,25 +94,60 @@ def _load():
 
 # ---------------------------------------------------------------------------
 # Arguments
+#
+# A call's checks depend on its tensors' shapes, strides and types alone.  They
+# run once for each combination of these; what they yield (the C structures
+# without their addresses, sizes of results and scratch) is kept per thread under
+# that combination, and a call fills in its addresses.  Nothing of a call's
+# data or addresses is kept.
 
 
-def _ints(name: str, t: torch.Tensor, dim: int, device: torch.device | None = None) -> torch.Tensor:
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != dim:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension(s)")
-    if device is not None and t.is_cuda and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return t
+class _Checked(threading.local):
+    def __init__(self):
+        self.calls = {}
+
+
+_checked = _Checked()
+_MOST_CHECKED = 1024
+
+
+def _form(t: torch.Tensor | None):
+    """What the checks look at."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.is_cuda)
+
+
+def _once(key, check):
+    calls = _checked.calls
+    found = calls.get(key)
+    if found is None:
+        found = check()
+        if len(calls) >= _MOST_CHECKED:
+            calls.clear()
+        calls[key] = found
+    return found
+
+
+def _ints(name: str, t: torch.Tensor, *shape):
+    """shape: the wanted sizes, None where any will do."""
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {len(shape)} dimension(s)")
+    if any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} is {list(t.shape)}, not {[w if w is not None else 'any' for w in shape]}")
+
+
+def _on_device(name: str, t: torch.Tensor):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
 
 
 def _sequences(table: torch.Tensor, lens: torch.Tensor) -> _Seqs:
-    _ints("table", table, 2)
-    _ints("lens", lens, 1, table.device)
-    if table.shape[0] != lens.shape[0]:
-        raise ValueError(f"table has {table.shape[0]} rows, lens {lens.shape[0]}")
-    return _Seqs(table.data_ptr(), lens.data_ptr(), table.shape[0], table.shape[1])
+    _ints("table", table, None, None)
+    _ints("lens", lens, table.shape[0])
+    return _Seqs(0, 0, table.shape[0], table.shape[1])
 
 
 def _as_pages(name: str, t: torch.Tensor, pools: bool = False) -> _Pages:
+    _on_device(name, t)
     if pools and t.dim() == 5:
         n_pools, shape, strides = t.shape[0], t.shape[1:], t.stride()
         pool_stride, strides = strides[0], strides[1:]
@@ -121,47 +157,44 @@ def _as_pages(name: str, t: torch.Tensor, pools: bool = False) -> _Pages:
         raise ValueError(f"{name} must have the dimensions {'[pools,] ' if pools else ''}pages, heads, tokens, dim")
     if shape[3] > 1 and strides[3] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return _Pages(t.data_ptr(), n_pools, pool_stride, shape[0], strides[0], shape[1], strides[1], shape[2], strides[2],
+    return _Pages(0, n_pools, pool_stride, shape[0], strides[0], shape[1], strides[1], shape[2], strides[2],
                   shape[3], t.element_size())
 
 
-def _dtype(q: torch.Tensor | None, *pages: torch.Tensor) -> int:
-    dt = pages[0].dtype
-    if dt not in _DTYPES or any(p.dtype != dt for p in pages) or (q is not None and q.dtype != dt):
+def _dtype(*tensors: torch.Tensor) -> int:
+    dt = tensors[0].dtype
+    if dt not in _DTYPES or any(t.dtype != dt for t in tensors):
         raise ValueError("queries, keys and values must all be bfloat16 or all float16")
     return _DTYPES[dt]
 
 
-def _same_device(device: torch.device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-
-
-def _out(name: str, t: torch.Tensor | None, shape, dtype, device) -> torch.Tensor:
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+def _given(name: str, t: torch.Tensor, shape, dtype) -> torch.Tensor:
+    """A result tensor of the caller's."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
     return t
+
+
+def _scratch(workspace: torch.Tensor | None, size: int, device: torch.device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    if workspace.numel() * workspace.element_size() < size or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and hold {size} bytes")
+    return workspace
+
+
+_as_is = contextlib.nullcontext()
 
 
 def _for(stream, device: torch.device):
     """(stream handle, context in which results of that stream are allocated)."""
     if stream is None:
-        handle = ibp._stream(None, device)
-        if device.index == torch.cuda.current_device():
-            return handle, contextlib.nullcontext()
-        return handle, torch.cuda.device(device)
+        index = device.index
+        handle = ibp._raw_stream(index) if ibp._raw_stream is not None else ibp._stream(None, device)
+        return handle, _as_is if index == torch.cuda.current_device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return stream.cuda_stream, torch.cuda.stream(stream)
-
-
-def _device(t: torch.Tensor) -> torch.device:
-    if not t.is_cuda:
-        raise ValueError("the page tensors must be on a CUDA device")
-    return t.device
 
 
 # ---------------------------------------------------------------------------
@@ -176,7 +209,7 @@ def _status(status: torch.Tensor | None, device: torch.device) -> int:
         if word is None:
             word = torch.zeros(1, dtype=torch.int32, device=device)
             torch.cuda.synchronize(device)  # made once: every stream may use it
-            _status_words[device.index] = word
+            word = _status_words.setdefault(device.index, word)
         return word.data_ptr()
     if status.element_size() != 4 or status.numel() < 1:
         raise ValueError("status must be a 32-bit word")
@@ -213,20 +246,27 @@ def ibp_kv_fork(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, par
                 page_tokens: int, status: torch.Tensor | None = None, stream=None):
     """The next batch: row i continues row parents[i].  Returns new (table,
     lens, refs) and the page copies to make, (moves, count) for ibp_kv_copy."""
-    lib, seqs = _load(), _sequences(table, lens)
-    device = _device(table)
-    _ints("refs", refs, 1, device)
-    _ints("parents", parents, 1, device)
-    n_out, n_pages = parents.shape[0], refs.shape[0]
+    lib = _load()
+
+    def check():
+        _on_device("table", table)
+        _ints("refs", refs, None)
+        _ints("parents", parents, None)
+        n_pages, n_out = refs.shape[0], parents.shape[0]
+        return _sequences(table, lens), n_pages, n_out, lib.ibp_kv_pages_workspace(n_pages, n_out)
+
+    key = ("fork", _form(table), _form(lens), _form(refs), _form(parents))
+    seqs, n_pages, n_out, size = _once(key, check)
+    device = table.device
     handle, where = _for(stream, device)
     with where:
         table_out = torch.empty((n_out, table.shape[1]), dtype=torch.int32, device=device)
         lens_out = torch.empty(n_out, dtype=torch.int32, device=device)
-        refs_out = torch.empty_like(refs)
+        refs_out = torch.empty(n_pages, dtype=torch.int32, device=device)
         moves = torch.empty((n_out, 3), dtype=torch.int32, device=device)
         count = torch.empty(1, dtype=torch.int32, device=device)
-        size = lib.ibp_kv_pages_workspace(n_pages, n_out)
         ws = torch.empty(size, dtype=torch.uint8, device=device)
+        seqs.table, seqs.lens = table.data_ptr(), lens.data_ptr()
         _check(lib.ibp_kv_fork(seqs, page_tokens, refs.data_ptr(), n_pages, parents.data_ptr(), n_out,
                                table_out.data_ptr(), lens_out.data_ptr(), refs_out.data_ptr(), moves.data_ptr(),
                                count.data_ptr(), ws.data_ptr(), size, _status(status, device), handle),
@@ -238,14 +278,23 @@ def ibp_kv_free(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seq
                 inplace: bool = False, status: torch.Tensor | None = None, stream=None):
     """Frees the listed sequences; returns (table, lens, refs), the arguments
     themselves with `inplace`."""
-    lib, s = _load(), _sequences(table, lens)
-    device = _device(table)
-    _ints("refs", refs, 1, device)
-    _ints("seqs", seqs, 1, device)
+    lib = _load()
+
+    def check():
+        _on_device("table", table)
+        _ints("refs", refs, None)
+        _ints("seqs", seqs, None)
+        return _sequences(table, lens), refs.shape[0], seqs.shape[0]
+
+    s, n_pages, n_rows = _once(("free", _form(table), _form(lens), _form(refs), _form(seqs)), check)
+    device = table.device
     handle, where = _for(stream, device)
     with where:
-        out = (table, lens, refs) if inplace else tuple(torch.empty_like(t) for t in (table, lens, refs))
-        _check(lib.ibp_kv_free(s, page_tokens, refs.data_ptr(), refs.shape[0], seqs.data_ptr(), seqs.shape[0],
+        out = (table, lens, refs)
+        if not inplace:
+            out = torch.empty_like(table), torch.empty_like(lens), torch.empty_like(refs)
+        s.table, s.lens = table.data_ptr(), lens.data_ptr()
+        _check(lib.ibp_kv_free(s, page_tokens, refs.data_ptr(), n_pages, seqs.data_ptr(), n_rows,
                                out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _status(status, device),
                                handle), "ibp_kv_free")
     return out
@@ -256,19 +305,24 @@ def ibp_kv_compact(table: torch.Tensor, refs: torch.Tensor, page_tokens: int, in
     """Live pages to the front of the pool; returns (table, refs, moves, count),
     the first two the arguments themselves with `inplace`."""
     lib = _load()
-    _ints("table", table, 2)
-    device = _device(table)
-    _ints("refs", refs, 1, device)
-    n_pages = refs.shape[0]
+
+    def check():
+        _on_device("table", table)
+        _ints("table", table, None, None)
+        _ints("refs", refs, None)
+        n_pages = refs.shape[0]
+        return _Seqs(0, 0, *table.shape), n_pages, lib.ibp_kv_pages_workspace(n_pages, 0)
+
+    seqs, n_pages, size = _once(("compact", _form(table), _form(refs)), check)
+    device = table.device
     handle, where = _for(stream, device)
     with where:
         out = (table, refs) if inplace else (torch.empty_like(table), torch.empty_like(refs))
         moves = torch.empty((n_pages, 3), dtype=torch.int32, device=device)
         count = torch.empty(1, dtype=torch.int32, device=device)
-        size = lib.ibp_kv_pages_workspace(n_pages, 0)
         ws = torch.empty(size, dtype=torch.uint8, device=device)
         # the lengths are not used: the references say which pages live
-        seqs = _Seqs(table.data_ptr(), refs.data_ptr(), table.shape[0], table.shape[1])
+        seqs.table = seqs.lens = table.data_ptr()
         _check(lib.ibp_kv_compact(seqs, page_tokens, refs.data_ptr(), n_pages, out[0].data_ptr(), out[1].data_ptr(),
                                   moves.data_ptr(), count.data_ptr(), ws.data_ptr(), size, _status(status, device),
                                   handle), "ibp_kv_compact")
@@ -278,16 +332,20 @@ def ibp_kv_compact(table: torch.Tensor, refs: torch.Tensor, page_tokens: int, in
 def ibp_kv_copy(pages: torch.Tensor, moves: torch.Tensor, count: torch.Tensor, status: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     """Copies pages as `moves` lists them, in place and in every pool."""
-    lib, p = _load(), _as_pages("pages", pages, pools=True)
-    device = _device(pages)
-    _ints("moves", moves, 2, device)
-    _ints("count", count, 1, device)
-    if moves.shape[1] != 3:
-        raise ValueError("moves must have three columns: from, to, tokens")
+    lib = _load()
+
+    def check():
+        _ints("moves", moves, None, 3)
+        _ints("count", count, 1)
+        return _as_pages("pages", pages, pools=True), moves.shape[0]
+
+    p, most = _once(("copy", _form(pages), _form(moves), _form(count)), check)
+    device = pages.device
     handle, where = _for(stream, device)
     with where:
-        _check(lib.ibp_kv_copy(p, moves.data_ptr(), count.data_ptr(), moves.shape[0], _status(status, device),
-                               handle), "ibp_kv_copy")
+        p.data = pages.data_ptr()
+        _check(lib.ibp_kv_copy(p, moves.data_ptr(), count.data_ptr(), most, _status(status, device), handle),
+               "ibp_kv_copy")
     return pages
 
 
@@ -297,20 +355,31 @@ def ibp_kv_accept(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, 
     """Keeps the accepted tokens of each sequence's draft (its last n_draft[b]
     tokens): path[b][: n_accept[b]] move to the draft's front in every pool.
     Returns (table, lens, refs)."""
-    lib, p, seqs = _load(), _as_pages("pages", pages, pools=True), _sequences(table, lens)
-    device = _device(pages)
-    for name, t, dim in (("refs", refs, 1), ("n_draft", n_draft, 1), ("path", path, 2), ("n_accept", n_accept, 1)):
-        _ints(name, t, dim, device)
-    n = table.shape[0]
-    if refs.shape[0] != p.n_pages or n_draft.shape[0] != n or path.shape[0] != n or n_accept.shape[0] != n:
-        raise ValueError("refs, n_draft, path or n_accept does not fit the pages or the sequences")
+    lib = _load()
+
+    def check():
+        p, n = _as_pages("pages", pages, pools=True), table.shape[0]
+        _ints("refs", refs, p.n_pages)
+        _ints("n_draft", n_draft, n)
+        _ints("path", path, n, None)
+        _ints("n_accept", n_accept, n)
+        return p, _sequences(table, lens), path.shape[1]
+
+    key = ("accept", _form(pages), _form(table), _form(lens), _form(refs), _form(n_draft), _form(path),
+           _form(n_accept))
+    p, seqs, most = _once(key, check)
+    device = pages.device
     handle, where = _for(stream, device)
     with where:
-        out = (table, lens, refs) if inplace else tuple(torch.empty_like(t) for t in (table, lens, refs))
-        if n == 0:
-            return (table, lens, refs) if inplace else (table.clone(), lens.clone(), refs.clone())
+        out = (table, lens, refs)
+        if seqs.n_seqs == 0:
+            return out if inplace else (table.clone(), lens.clone(), refs.clone())
+        if not inplace:
+            out = torch.empty_like(table), torch.empty_like(lens), torch.empty_like(refs)
+        p.data = pages.data_ptr()
+        seqs.table, seqs.lens = table.data_ptr(), lens.data_ptr()
         _check(lib.ibp_kv_accept(p, seqs, refs.data_ptr(), n_draft.data_ptr(), path.data_ptr(), n_accept.data_ptr(),
-                                 path.shape[1], out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
+                                 most, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
                                  _status(status, device), handle), "ibp_kv_accept")
     return out
 
@@ -319,20 +388,16 @@ def ibp_kv_accept(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, 
 # Attention
 
 
-def _queries(q: torch.Tensor, k: torch.Tensor, n_seqs: int):
-    if q.dim() != 4 or q.shape[0] != n_seqs or q.shape[3] != k.shape[3]:
+def _heads(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
+    """(k pages, v pages, dtype, sequences) of an attention call."""
+    kp, vp = _as_pages("k", k), _as_pages("v", v)
+    seqs = _sequences(table, lens)
+    _on_device("q", q)
+    if q.dim() != 4 or q.shape[0] != seqs.n_seqs or q.shape[3] != kp.dim:
         raise ValueError("q must be [n_seqs, T, q_heads, dim] with the table's sequences and the pages' dim")
     if q.shape[3] > 1 and q.stride(3) != 1:
         raise ValueError("the last dimension of q must be contiguous")
-    return q.shape[1], q.shape[2]
-
-
-def _workspace(workspace: torch.Tensor | None, size: int, device):
-    if workspace is None:
-        return torch.empty(size, dtype=torch.uint8, device=device)
-    if workspace.numel() * workspace.element_size() < size or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and hold {size} bytes")
-    return workspace
+    return kp, vp, _dtype(k, v, q), seqs
 
 
 def ibp_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -345,30 +410,43 @@ def ibp_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table:
            see drafted token i; None: a chain (i <= t).
     scale  default 1 / sqrt(dim).
     Returns (out [n_seqs, T, q_heads, dim], lse [n_seqs, T, q_heads])."""
-    lib, seqs = _load(), _sequences(table, lens)
-    device = _device(k)
-    kp, vp = _as_pages("k", k), _as_pages("v", v)
-    T, heads = _queries(q, k, seqs.n_seqs)
-    dt = _dtype(q, k, v)
-    _same_device(device, q=q, v=v, table=table)
-    if mask is not None:
-        _ints("mask", mask, 3, device)
-        if tuple(mask.shape) != (seqs.n_seqs, T, (T + 31) // 32):
-            raise ValueError("mask must be [n_seqs, T, ceil(T / 32)]")
-    if n_draft is not None and _ints("n_draft", n_draft, 1, device).shape[0] != seqs.n_seqs:
-        raise ValueError("n_draft must hold one number per sequence")
+    lib = _load()
+
+    def check():
+        kp, vp, dt, seqs = _heads(q, k, v, table, lens)
+        T, heads = q.shape[1], q.shape[2]
+        if mask is not None:
+            _ints("mask", mask, seqs.n_seqs, T, (T + 31) // 32)
+        if n_draft is not None:
+            _ints("n_draft", n_draft, seqs.n_seqs)
+        size = lib.ibp_tree_attention_workspace(seqs.n_seqs, T, heads, kp.heads, kp.dim)
+        return kp, vp, dt, seqs, (*q.stride()[:3], T, heads), size, 1.0 / math.sqrt(kp.dim)
+
+    key = ("tree", _form(q), _form(k), _form(v), _form(table), _form(lens), _form(mask), _form(n_draft))
+    kp, vp, dt, seqs, rows, size, usual = _once(key, check)
+    device = k.device
     handle, where = _for(stream, device)
     with where:
-        out = _out("out", out, q.shape, q.dtype, device)
-        lse = _out("lse", lse, q.shape[:3], torch.float32, device)
-        size = lib.ibp_tree_attention_workspace(seqs.n_seqs, T, heads, kp.heads, kp.dim)
-        ws = _workspace(workspace, size, device)
-        _check(lib.ibp_tree_attention(kp, vp, dt, seqs, q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), T, heads,
-                                      ibp._ptr(n_draft), ibp._ptr(mask),
-                                      1.0 / math.sqrt(kp.dim) if scale is None else scale, out.data_ptr(),
-                                      lse.data_ptr(), ws.data_ptr(), size, _status(status, device), handle),
-               "ibp_tree_attention")
+        out = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else _given("out", out, q.shape, q.dtype)
+        if lse is None:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=device)
+        else:
+            _given("lse", lse, q.shape[:3], torch.float32)
+        ws = _scratch(workspace, size, device)
+        kp.data, vp.data = k.data_ptr(), v.data_ptr()
+        seqs.table, seqs.lens = table.data_ptr(), lens.data_ptr()
+        _check(lib.ibp_tree_attention(kp, vp, dt, seqs, q.data_ptr(), *rows,
+                                      None if n_draft is None else n_draft.data_ptr(),
+                                      None if mask is None else mask.data_ptr(), usual if scale is None else scale,
+                                      out.data_ptr(), lse.data_ptr(), ws.data_ptr(), size, _status(status, device),
+                                      handle), "ibp_tree_attention")
     return out, lse
+
+
+def _bounds(k: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
+    n_pages, heads, _, dim = k.shape
+    _given("codes", codes, (n_pages, heads, 2, dim), torch.int8)
+    _given("scales", scales, (n_pages, heads), torch.float32)
 
 
 def ibp_kv_summarize(k: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, codes: torch.Tensor,
@@ -377,27 +455,25 @@ def ibp_kv_summarize(k: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, c
     """8-bit bounds of the keys of every page that holds a position from
     first[b] on (None: every page), into codes [n_pages, heads, 2, dim] int8
     and scales [n_pages, heads] float32.  Returns (codes, scales)."""
-    lib, seqs = _load(), _sequences(table, lens)
-    device = _device(k)
-    kp, dt = _as_pages("k", k), _dtype(None, k)
-    _same_device(device, table=table)
-    _bounds(k, codes, scales)
-    if first is not None and _ints("first", first, 1, device).shape[0] != seqs.n_seqs:
-        raise ValueError("first must hold one position per sequence")
+    lib = _load()
+
+    def check():
+        kp, seqs = _as_pages("k", k), _sequences(table, lens)
+        _bounds(k, codes, scales)
+        if first is not None:
+            _ints("first", first, seqs.n_seqs)
+        return kp, seqs, _dtype(k)
+
+    key = ("summarize", _form(k), _form(table), _form(lens), _form(codes), _form(scales), _form(first))
+    kp, seqs, dt = _once(key, check)
+    device = k.device
     handle, where = _for(stream, device)
     with where:
-        _check(lib.ibp_kv_summarize(kp, dt, seqs, ibp._ptr(first), codes.data_ptr(), scales.data_ptr(),
-                                    _status(status, device), handle), "ibp_kv_summarize")
+        kp.data = k.data_ptr()
+        seqs.table, seqs.lens = table.data_ptr(), lens.data_ptr()
+        _check(lib.ibp_kv_summarize(kp, dt, seqs, None if first is None else first.data_ptr(), codes.data_ptr(),
+                                    scales.data_ptr(), _status(status, device), handle), "ibp_kv_summarize")
     return codes, scales
-
-
-def _bounds(k: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
-    n_pages, heads, _, dim = k.shape
-    if codes.dtype != torch.int8 or tuple(codes.shape) != (n_pages, heads, 2, dim) or not codes.is_contiguous():
-        raise ValueError("codes must be a contiguous int8 tensor [n_pages, heads, 2, dim]")
-    if scales.dtype != torch.float32 or tuple(scales.shape) != (n_pages, heads) or not scales.is_contiguous():
-        raise ValueError("scales must be a contiguous float32 tensor [n_pages, heads]")
-    _same_device(k.device, codes=codes, scales=scales)
 
 
 def ibp_sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -412,28 +488,42 @@ def ibp_sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tabl
 
     Returns (out, lse, pages): pages int32 [n_seqs, T, kv_heads, budget], the
     selected places in the table row ascending, then -1."""
-    lib, seqs = _load(), _sequences(table, lens)
-    device = _device(k)
-    kp, vp = _as_pages("k", k), _as_pages("v", v)
-    T, heads = _queries(q, k, seqs.n_seqs)
-    dt = _dtype(q, k, v)
-    _same_device(device, q=q, v=v, table=table)
-    _bounds(k, codes, scales)
-    if not 1 <= budget <= IBP_SPARSE_MAX_BUDGET or keep_first < 0 or keep_last < 1 or keep_first + keep_last > budget:
-        raise ValueError("budget must hold keep_first >= 0 and keep_last >= 1 pages and be at most "
-                         f"{IBP_SPARSE_MAX_BUDGET}")
-    if n_query is not None and _ints("n_query", n_query, 1, device).shape[0] != seqs.n_seqs:
-        raise ValueError("n_query must hold one number per sequence")
+    lib = _load()
+
+    def check():
+        kp, vp, dt, seqs = _heads(q, k, v, table, lens)
+        T, heads = q.shape[1], q.shape[2]
+        _bounds(k, codes, scales)
+        if not 1 <= budget <= IBP_SPARSE_MAX_BUDGET or keep_first < 0 or keep_last < 1 or keep_first + keep_last > budget:
+            raise ValueError("budget must hold keep_first >= 0 and keep_last >= 1 pages and be at most "
+                             f"{IBP_SPARSE_MAX_BUDGET}")
+        if n_query is not None:
+            _ints("n_query", n_query, seqs.n_seqs)
+        size = lib.ibp_sparse_attention_workspace(seqs.n_seqs, seqs.max_pages, T, heads, kp.heads, kp.dim, budget)
+        return kp, vp, dt, seqs, (*q.stride()[:3], T, heads), size, 1.0 / math.sqrt(kp.dim)
+
+    key = ("sparse", _form(q), _form(k), _form(v), _form(table), _form(lens), _form(codes), _form(scales),
+           _form(n_query), budget, keep_first, keep_last)
+    kp, vp, dt, seqs, rows, size, usual = _once(key, check)
+    device = k.device
     handle, where = _for(stream, device)
     with where:
-        out = _out("out", out, q.shape, q.dtype, device)
-        lse = _out("lse", lse, q.shape[:3], torch.float32, device)
-        pages = _out("pages", pages, (seqs.n_seqs, T, kp.heads, budget), torch.int32, device)
-        size = lib.ibp_sparse_attention_workspace(seqs.n_seqs, seqs.max_pages, T, heads, kp.heads, kp.dim, budget)
-        ws = _workspace(workspace, size, device)
-        _check(lib.ibp_sparse_attention(kp, vp, dt, seqs, codes.data_ptr(), scales.data_ptr(), q.data_ptr(),
-                                        q.stride(0), q.stride(1), q.stride(2), T, heads, ibp._ptr(n_query), budget,
-                                        keep_first, keep_last, 1.0 / math.sqrt(kp.dim) if scale is None else scale,
-                                        out.data_ptr(), lse.data_ptr(), pages.data_ptr(), ws.data_ptr(), size,
-                                        _status(status, device), handle), "ibp_sparse_attention")
+        out = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else _given("out", out, q.shape, q.dtype)
+        if lse is None:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=device)
+        else:
+            _given("lse", lse, q.shape[:3], torch.float32)
+        wanted = (seqs.n_seqs, rows[3], kp.heads, budget)
+        if pages is None:
+            pages = torch.empty(wanted, dtype=torch.int32, device=device)
+        else:
+            _given("pages", pages, wanted, torch.int32)
+        ws = _scratch(workspace, size, device)
+        kp.data, vp.data = k.data_ptr(), v.data_ptr()
+        seqs.table, seqs.lens = table.data_ptr(), lens.data_ptr()
+        _check(lib.ibp_sparse_attention(kp, vp, dt, seqs, codes.data_ptr(), scales.data_ptr(), q.data_ptr(), *rows,
+                                        None if n_query is None else n_query.data_ptr(), budget, keep_first,
+                                        keep_last, usual if scale is None else scale, out.data_ptr(), lse.data_ptr(),
+                                        pages.data_ptr(), ws.data_ptr(), size, _status(status, device), handle),
+               "ibp_sparse_attention")
     return out, lse, pages

@@ -563,7 +563,7 @@ def test_refusals():
     with pytest.raises(ValueError):
         kv.ibp_kv_summarize(k, table, lens, codes.int(), scales)
     lib = kv._load()
-    seqs = kv._sequences(table, lens)
+    seqs = kv._Seqs(table.data_ptr(), lens.data_ptr(), 1, 2)
     # overlapping tables, a scratch that is too small, pageable memory
     one = torch.zeros(8, dtype=torch.int32, device="cuda")
     args = lambda t, size: (seqs, 16, refs.data_ptr(), 4, rows.data_ptr(), 1, t, one.data_ptr(), refs.data_ptr(),  # noqa: E731
