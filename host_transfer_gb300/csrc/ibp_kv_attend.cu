@@ -6,7 +6,8 @@
 // the cache's bytes are what counts, so the layout serves the loads: each of
 // the four warps has its own ring of 16-token stages, filled by 16-byte
 // asynchronous copies, and its own running maximum and sum; no barrier is met
-// until the warps are joined at the end.
+// until the warps are joined at the end.  Where there are items enough for every
+// warp (a chunk of sparse queries), each warp takes an item of its own.
 //
 // The products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so that the
 // 16-row side of mma.m16n8k16 is filled by tokens and dimensions and the 8-wide
@@ -103,7 +104,8 @@ struct Attend {
   static constexpr uint32_t kWarpBytes = kStages * 2 * kTile;
   static constexpr uint32_t kBytes = kAtWarps * kWarpBytes;
   static constexpr uint32_t kRows = 8 * NT;
-  static_assert(kAtWarps * (kRows * DP + 2 * kRows) * 4 <= kBytes, "the join fits the stages");
+  static_assert((kRows * DP + 2 * kRows) * 4 <= kWarpBytes, "the join fits the stages");
+  static_assert((kAtWarps + 1) * kRows * (DP + 2) * 4 <= kBytes, "a cluster's part fits beside it");
 
   // Row of the flat (token, group head) order: the query token of row r.
   static __device__ __forceinline__ uint32_t token_of(const AttendArgs& a, const Item& it, uint32_t r) {
@@ -181,15 +183,24 @@ __device__ __forceinline__ void load_stage(const AttendArgs& a, const Item& it, 
   }
 }
 
-template <uint32_t DP, uint32_t NT, bool F16, bool PICK>
-__global__ void __launch_bounds__(kAtWarps * 32) k_kv_attend(const AttendArgs a, uint32_t row_tiles, uint32_t one_page) {
+template <uint32_t DP, uint32_t NT, bool F16, bool PICK, uint32_t WPI>
+__global__ void __launch_bounds__(kAtWarps * 32)
+    k_kv_attend(const AttendArgs a, uint32_t row_tiles, uint32_t one_page, uint32_t items) {
   using A = Attend<DP, NT, F16, PICK>;
   extern __shared__ __align__(128) unsigned char sm[];
   pdl_begin();
-  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  // WPI warps share an item: all four of a CTA, or one each.
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x / 32 % WPI, group = threadIdx.x / 32 / WPI;
+  auto sync = [] {
+    if (WPI == 1)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
   const uint32_t split = blockIdx.x % a.splits;
-  uint32_t x = blockIdx.x / a.splits;
+  uint32_t x = blockIdx.x / a.splits * (kAtWarps / WPI) + group;
   const uint32_t item = x;
+  if (item >= items) return;
   Item it;
   const uint32_t tile = x % row_tiles;
   x /= row_tiles;
@@ -200,7 +211,7 @@ __global__ void __launch_bounds__(kAtWarps * 32) k_kv_attend(const AttendArgs a,
   it.row0 = tile * A::kRows;
   const int32_t raw = a.lens[it.b], len = clamp_len(raw, a.page_tokens, a.max_pages);
   const int32_t live = a.n_live ? a.n_live[it.b] : static_cast<int32_t>(a.T);
-  if ((raw != len || live > len || live < 0 || live > static_cast<int32_t>(a.T)) && threadIdx.x == 0)
+  if ((raw != len || live > len || live < 0 || live > static_cast<int32_t>(a.T)) && warp == 0 && lane == 0)
     kv_status(a.status, IBP_ERANGE);
   const int32_t n_live = live < 0 ? 0 : (live > static_cast<int32_t>(a.T) ? static_cast<int32_t>(a.T) : live);
   it.ctx = len - n_live;  // below 0: the draft's first tokens do not exist
@@ -213,23 +224,14 @@ __global__ void __launch_bounds__(kAtWarps * 32) k_kv_attend(const AttendArgs a,
     const int32_t* pk =
         a.picks + ((static_cast<uint64_t>(it.b) * a.T + it.t0) * a.kv_heads + it.h) * a.budget;
     it.picks = pk;
-    uint32_t n = 0;
-    if (it.seen > 0) {  // entries before the first -1
-      uint32_t lo = 0, hi = a.budget;
-      while (lo < hi) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (pk[mid] >= 0)
-          lo = mid + 1;
-        else
-          hi = mid;
-      }
-      n = lo;
-    }
-    it.n_tok = n * a.page_tokens;
-    // the last page ends at the query's own position
-    if (n > 0) {
-      const int32_t end = it.seen - pk[n - 1] * static_cast<int32_t>(a.page_tokens);
-      if (end < static_cast<int32_t>(a.page_tokens)) it.n_tok -= a.page_tokens - (end > 0 ? end : 0);
+    // All pages the query sees, or `budget` of them; the last is the query's own
+    // and ends at its position.
+    if (it.seen > 0) {
+      const uint32_t own = static_cast<uint32_t>(p) / a.page_tokens;
+      const uint32_t n = own + 1 < a.budget ? own + 1 : a.budget;
+      it.n_tok = (n - 1) * a.page_tokens + static_cast<uint32_t>(p) % a.page_tokens + 1;
+    } else {
+      it.n_tok = 0;
     }
   } else {
     it.seen = len;
@@ -270,25 +272,26 @@ __global__ void __launch_bounds__(kAtWarps * 32) k_kv_attend(const AttendArgs a,
     for (uint32_t d = 0; d < DP / 16; ++d) o[d][n][0] = o[d][n][1] = o[d][n][2] = o[d][n][3] = 0.f;
   }
 
-  const uint32_t ring = smem_u32(sm) + warp * A::kWarpBytes;
+  unsigned char* const mine = sm + group * WPI * A::kWarpBytes;
+  const uint32_t ring = smem_u32(mine) + warp * A::kWarpBytes;
   int32_t pos_ring[A::kStages];  // this lane's token of each stage in flight
 #pragma unroll
   for (uint32_t i = 0; i < A::kStages - 1; ++i) {
-    const uint32_t s = s0 + warp + i * kAtWarps;
+    const uint32_t s = s0 + warp + i * WPI;
     if (s < s1)
       load_stage<DP, NT, F16, PICK>(a, it, s, it.n_tok, ring + i * 2 * A::kTile, one_page, &pos_ring[i]);
     cp_commit();
   }
-  for (uint32_t sb = s0 + warp; sb < s1; sb += kAtWarps * A::kStages) {
+  for (uint32_t sb = s0 + warp; sb < s1; sb += WPI * A::kStages) {
 #pragma unroll
     for (uint32_t u = 0; u < A::kStages; ++u) {
-      const uint32_t s = sb + u * kAtWarps;
+      const uint32_t s = sb + u * WPI;
       if (s >= s1) break;
       constexpr uint32_t kAhead = A::kStages - 1;
       const uint32_t un = (u + kAhead) % A::kStages;
       __syncwarp();  // every lane is done with the stage that is filled next
-      if (s + kAhead * kAtWarps < s1)
-        load_stage<DP, NT, F16, PICK>(a, it, s + kAhead * kAtWarps, it.n_tok, ring + un * 2 * A::kTile, one_page,
+      if (s + kAhead * WPI < s1)
+        load_stage<DP, NT, F16, PICK>(a, it, s + kAhead * WPI, it.n_tok, ring + un * 2 * A::kTile, one_page,
                                       &pos_ring[un]);
       cp_commit();
       cp_wait<kAhead>();
@@ -417,16 +420,17 @@ __global__ void __launch_bounds__(kAtWarps * 32) k_kv_attend(const AttendArgs a,
   }
   cp_wait<0>();
 
-  // Join the warps: sums of a lane's tokens first, then the four warps'.
+  // Join the warps: sums of a lane's tokens first, then the item's warps'.
 #pragma unroll
   for (uint32_t n = 0; n < NT; ++n)
 #pragma unroll
     for (uint32_t e = 0; e < 2; ++e)
 #pragma unroll
       for (uint32_t w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], w);
-  __syncthreads();
-  float* so = reinterpret_cast<float*>(sm);                     // [warp][row][DP]
-  float* sml = so + kAtWarps * A::kRows * DP;                   // [warp][row][2]
+  sync();
+  float* so = reinterpret_cast<float*>(mine);                     // [warp][row][DP]
+  float* sml = so + WPI * A::kRows * DP;                          // [warp][row][2]
+  float* sp = sml + WPI * A::kRows * 2;                           // [row][2 + DP]: this CTA's part in a cluster
 #pragma unroll
   for (uint32_t n = 0; n < NT; ++n)
 #pragma unroll
@@ -440,17 +444,17 @@ __global__ void __launch_bounds__(kAtWarps * 32) k_kv_attend(const AttendArgs a,
         sml[(warp * A::kRows + r) * 2 + 1] = l[n][e];
       }
     }
-  __syncthreads();
-  for (uint32_t r = warp; r < it.rows; r += kAtWarps) {
-    float mw[kAtWarps], top = -INFINITY, sum = 0.f;
+  sync();
+  for (uint32_t r = warp; r < it.rows; r += WPI) {
+    float mw[WPI], top = -INFINITY, sum = 0.f;
     const bool live_row = r < live_rows;
 #pragma unroll
-    for (uint32_t w = 0; w < kAtWarps; ++w) {
+    for (uint32_t w = 0; w < WPI; ++w) {
       mw[w] = live_row ? sml[(w * A::kRows + r) * 2] : -INFINITY;
       top = fmaxf(top, mw[w]);
     }
 #pragma unroll
-    for (uint32_t w = 0; w < kAtWarps; ++w) {
+    for (uint32_t w = 0; w < WPI; ++w) {
       const float s = live_row ? sml[(w * A::kRows + r) * 2 + 1] : 0.f;
       // a NaN sum stays one: only an empty warp is left out
       mw[w] = mw[w] == -INFINITY ? (s == 0.f ? 0.f : 1.f) : exp2f(mw[w] - top);
@@ -460,11 +464,12 @@ __global__ void __launch_bounds__(kAtWarps * 32) k_kv_attend(const AttendArgs a,
     const uint64_t orow = (static_cast<uint64_t>(it.b) * a.T + t) * a.kv_heads * a.group + it.h * a.group + g;
     const bool whole = a.splits == 1;
     const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-    float* part = a.part + (static_cast<uint64_t>(item) * a.splits + split) * A::kRows * (DP + 2) + r * (DP + 2);
+    float* part = a.cluster ? sp + r * (DP + 2)
+                            : a.part + (static_cast<uint64_t>(item) * a.splits + split) * A::kRows * (DP + 2) + r * (DP + 2);
     for (uint32_t d = lane * 2; d < a.dim; d += 64) {
       float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-      for (uint32_t w = 0; w < kAtWarps; ++w) {
+      for (uint32_t w = 0; w < WPI; ++w) {
         const float2 y = *reinterpret_cast<const float2*>(so + (w * A::kRows + r) * DP + d);
         if (live_row) v0 += mw[w] * y.x, v1 += mw[w] * y.y;
       }
@@ -482,6 +487,52 @@ __global__ void __launch_bounds__(kAtWarps * 32) k_kv_attend(const AttendArgs a,
       }
     }
   }
+  if (!a.cluster) return;
+  // The splits of an item are a cluster: each CTA joins every a.splits-th row out
+  // of the others' shared memory.
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (uint32_t r = split + a.splits * warp; r < it.rows; r += a.splits * WPI) {
+    auto remote = [&](uint32_t rank, uint32_t at) {
+      uint32_t addr = smem_u32(sp + r * (DP + 2) + at);
+      asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(rank));
+      return addr;
+    };
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < a.splits)
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml.x), "=f"(ml.y) : "r"(remote(lane, 0)) : "memory");
+    float top = ml.x;
+#pragma unroll
+    for (int w = 4; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
+    top = __shfl_sync(0xFFFFFFFFu, top, 0);
+    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - top);
+    float sum = 0.f;
+    float2 acc[DP / 64];
+#pragma unroll
+    for (uint32_t i = 0; i < DP / 64; ++i) acc[i] = make_float2(0.f, 0.f);
+    for (uint32_t c = 0; c < a.splits; ++c) {
+      const float fc = __shfl_sync(0xFFFFFFFFu, f, c);
+      sum += fc * __shfl_sync(0xFFFFFFFFu, ml.y, c);
+#pragma unroll
+      for (uint32_t i = 0; i < DP / 64; ++i) {
+        float2 y;
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(y.x), "=f"(y.y) : "r"(remote(c, 2 + lane * 2 + i * 64)) : "memory");
+        if (lane * 2 + i * 64 < a.dim) acc[i].x += fc * y.x, acc[i].y += fc * y.y;
+      }
+    }
+    const uint32_t gr = it.row0 + r, t = A::token_of(a, it, gr), g = gr % a.group;
+    const uint64_t orow = (static_cast<uint64_t>(it.b) * a.T + t) * a.kv_heads * a.group + it.h * a.group + g;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (uint32_t i = 0; i < DP / 64; ++i) {
+      const uint32_t d = lane * 2 + i * 64;
+      if (d < a.dim)
+        *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) =
+            pack2<F16>(acc[i].x * inv, acc[i].y * inv);
+    }
+    if (lane == 0 && a.lse) a.lse[orow] = (top + log2f(sum)) * 0.6931471805599453f;
+  }
+  // no CTA leaves while another reads its shared memory
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Joins the partial sums of split items: a warp per row.
@@ -541,6 +592,7 @@ __global__ void __launch_bounds__(128) k_kv_join(const AttendArgs a, uint32_t ro
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kMaxUnits = 2048;  // CTAs up to which items are split
+constexpr uint32_t kLeast = 2 * kAtWarps * kSub;  // tokens of a share
 
 static uint32_t padded_dim(uint32_t dim) { return dim <= 64 ? 64 : (dim <= 128 ? 128 : 256); }
 // 16 rows a CTA where there are more than 8 and the registers allow it.
@@ -553,10 +605,10 @@ size_t kv_attend_workspace(uint64_t items, uint64_t rows, uint32_t dim) {
   return tiles >= kMaxUnits ? 0 : 2ull * kMaxUnits * tr * (dp + 2) * 4;
 }
 
-template <uint32_t DP, uint32_t NT, bool F16, bool PICK>
-static int launch_attend(AttendArgs& a, int device, size_t ws_bytes, cudaStream_t stream) {
+template <uint32_t DP, uint32_t NT, bool F16, bool PICK, uint32_t WPI>
+static int launch_items(const AttendArgs& a, uint32_t tiles, uint64_t items, int device, cudaStream_t stream) {
   using A = Attend<DP, NT, F16, PICK>;
-  auto kern = k_kv_attend<DP, NT, F16, PICK>;
+  auto kern = k_kv_attend<DP, NT, F16, PICK, WPI>;
   static std::atomic<int> ready[64];
   if (device < 0 || device >= 64 || !ready[device].load(std::memory_order_acquire)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, A::kBytes);
@@ -567,23 +619,40 @@ static int launch_attend(AttendArgs& a, int device, size_t ws_bytes, cudaStream_
     }
     if (device >= 0 && device < 64) ready[device].store(1, std::memory_order_release);
   }
+  const uint64_t per = kAtWarps / WPI;
+  return kv_launch("k_kv_attend", kern, dim3(static_cast<unsigned>((items + per - 1) / per * a.splits)), kAtWarps * 32,
+                   A::kBytes, a.cluster ? a.splits : 1, stream, a, tiles, a.page_tokens % kSub == 0 ? 1u : 0u, static_cast<uint32_t>(items));
+}
+
+template <uint32_t DP, uint32_t NT, bool F16, bool PICK>
+static int launch_attend(AttendArgs& a, int device, size_t ws_bytes, cudaStream_t stream) {
+  using A = Attend<DP, NT, F16, PICK>;
   const uint32_t rows = (PICK ? 1u : a.T) * a.group, tiles = (rows + A::kRows - 1) / A::kRows;
   const uint64_t items = static_cast<uint64_t>(a.n_seqs) * (PICK ? a.T : 1u) * a.kv_heads * tiles;
-  // Items are split so that about two rounds of CTAs fill the GPU, down to two
-  // steps a warp; lengths are on the device, so the longest possible counts.
-  const uint64_t pages = PICK && a.budget < a.max_pages ? a.budget : a.max_pages;
-  const uint64_t most = (pages * a.page_tokens + 2 * kAtWarps * kSub - 1) / (2 * kAtWarps * kSub);
+  if (items > 0x7FFFFFFFull) return IBP_EINVAL;
   const uint64_t resident = static_cast<uint64_t>(sm_count(device)) * (232448 / (A::kBytes + 1024));
-  uint64_t target = 2 * resident < kMaxUnits ? 2 * resident : kMaxUnits;
+  a.splits = 1;
+  a.cluster = 0;
+  if (PICK && items >= 2 * resident * kAtWarps)
+    return launch_items<DP, NT, F16, PICK, PICK ? 1 : kAtWarps>(a, tiles, items, device, stream);
+  // Items are split so that about two rounds of CTAs fill the GPU, down to two
+  // steps a warp; lengths are on the device, so the longest possible counts.  Up
+  // to eight splits are a cluster and join in place; more write their parts for
+  // a second kernel.
+  const uint64_t pages = PICK && a.budget < a.max_pages ? a.budget : a.max_pages;
+  const uint64_t most = pages * a.page_tokens / kLeast;
+  const uint64_t target = 2 * resident < kMaxUnits ? 2 * resident : kMaxUnits;
   uint64_t splits = items >= target ? 1 : (target + items - 1) / items;
   splits = splits < most ? splits : most;
   if (splits < 1) splits = 1;
+  if (splits > 1 && splits <= 8) {
+    a.cluster = 1;
+    while (splits & (splits - 1)) ++splits;  // 2, 4 or 8
+  }
   a.splits = static_cast<uint32_t>(splits);
-  if (splits > 1 && ws_bytes < items * splits * A::kRows * (DP + 2) * 4) return IBP_EINVAL;
-  const bool one_page = a.page_tokens % kSub == 0;
-  int rc = kv_launch("k_kv_attend", kern, dim3(static_cast<unsigned>(items * splits)), kAtWarps * 32, A::kBytes, 1,
-                     stream, a, tiles, one_page ? 1u : 0u);
-  if (rc != IBP_OK || splits == 1) return rc;
+  if (splits > 8 && ws_bytes < items * splits * A::kRows * (DP + 2) * 4) return IBP_EINVAL;
+  const int rc = launch_items<DP, NT, F16, PICK, kAtWarps>(a, tiles, items, device, stream);
+  if (rc != IBP_OK || splits <= 8) return rc;
   const uint64_t warps = items * A::kRows;
   return kv_launch("k_kv_join", k_kv_join<DP, F16, PICK>, dim3(static_cast<unsigned>((warps + 3) / 4)), 128, 0, 1,
                    stream, a, tiles, A::kRows, rows);

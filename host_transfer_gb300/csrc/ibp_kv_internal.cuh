@@ -114,6 +114,7 @@ struct AttendArgs {
   float* lse;               // n_seqs x T x heads, or nullptr
   float* part;              // partial sums of split items (workspace)
   uint32_t splits;
+  uint32_t cluster;         // the splits of an item are a cluster
   uint32_t* status;
   uint32_t f16;
 };

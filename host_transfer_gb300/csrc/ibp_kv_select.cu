@@ -179,7 +179,7 @@ int launch_kv_summarize(const KvView& k, const int32_t* table, const int32_t* le
 // Scores
 
 constexpr int kScThreads = 256;
-constexpr uint32_t kScQueries = 8;  // queries a CTA holds
+constexpr uint32_t kScFly = 4;  // pages a lane group has in flight
 
 __device__ __forceinline__ int dp2a(uint32_t a16, uint32_t b8, int c, bool high) {
   int d;
@@ -198,24 +198,27 @@ __device__ __forceinline__ int32_t query_place(const SelectArgs& a, uint32_t b, 
   return p < 0 ? -1 : p;
 }
 
-// CTA (sequence, block of kScQueries queries and share of the pages; kv head): quantises its
-// queries into shared memory, then scores its share of the pages.  lanes of
-// dim / 8 (16 codes each: minima of the lower half, maxima of the upper) hold
-// a page and are summed by shuffles.  Bound by the codes' bytes for single tokens
-// (each code is read once per kScQueries queries), by dp2a issue for chunks.
-__global__ void __launch_bounds__(kScThreads) k_kv_score(const SelectArgs a, uint32_t q_blocks,
-                                                         uint32_t shares) {
-  extern __shared__ uint32_t sq[];  // kScQueries x dim words of two 16-bit sums: min part, max part
-  __shared__ int32_t place[kScQueries];
+// CTA (sequence, block of NQ queries and share of the pages; kv head):
+// quantises its queries into shared memory, then scores its share of the pages.
+// LPP lanes hold a page's codes, 16 each (minima in the lower lanes, maxima in
+// the upper), four pages a lane group in flight, and the queries' 16 sums for the
+// same dimensions stay in registers.  One query is summed over its lanes by a
+// butterfly; eight are by a halving exchange that leaves each lane one query's
+// total, 7 to 9 shuffles for the eight.  Single tokens are bound by the codes'
+// bytes and the latency of two dependent loads, chunks by dp2a issue.
+template <int NQ, int LPP>
+__global__ void __launch_bounds__(kScThreads) k_kv_score(const SelectArgs a, uint32_t q_blocks, uint32_t shares) {
+  extern __shared__ uint32_t sq[];  // NQ x dim words of two 16-bit sums: min part, max part
+  __shared__ int32_t place[NQ];
   __shared__ uint32_t most;
   pdl_begin();
   const uint32_t h = blockIdx.y, share = blockIdx.x % shares, bq = blockIdx.x / shares;
-  const uint32_t b = bq / q_blocks, t0 = bq % q_blocks * kScQueries;
+  const uint32_t b = bq / q_blocks, t0 = bq % q_blocks * NQ;
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const int32_t len = clamp_len(a.lens[b], a.page_tokens, a.max_pages);
   if (threadIdx.x == 0) most = 0;
   __syncthreads();
-  if (threadIdx.x < kScQueries) {
+  if (threadIdx.x < NQ) {
     const uint32_t t = t0 + threadIdx.x;
     const int32_t p = t < a.T ? query_place(a, b, t, len) : -1;
     // a query that sees no more pages than its budget takes them all unscored
@@ -227,18 +230,18 @@ __global__ void __launch_bounds__(kScThreads) k_kv_score(const SelectArgs a, uin
   const uint32_t n_pages = most;
   if (n_pages == 0) return;
   const uint32_t nd = a.dim / 2;  // words of two elements
-  for (uint32_t i = warp; i < kScQueries; i += kScThreads / 32) {
-    if (place[i] < 0) continue;
+  for (uint32_t i = warp; i < NQ; i += kScThreads / 32) {
     const char* q = a.q + static_cast<int64_t>(b) * a.q_seq + static_cast<int64_t>(t0 + i) * a.q_token +
                     static_cast<int64_t>(h) * a.group * a.q_head;
     float amax = 0.f;
-    bool bad = false;
-    for (uint32_t g = 0; g < a.group; ++g)
-      for (uint32_t w = lane; w < nd; w += 32) {
-        const float2 v = pair_f32(*reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(g) * a.q_head + 4 * w), a.f16);
-        bad = bad || !finite_f(v.x) || !finite_f(v.y);
-        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
-      }
+    bool bad = place[i] < 0;
+    if (!bad)
+      for (uint32_t g = 0; g < a.group; ++g)
+        for (uint32_t w = lane; w < nd; w += 32) {
+          const float2 v = pair_f32(*reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(g) * a.q_head + 4 * w), a.f16);
+          bad = bad || !finite_f(v.x) || !finite_f(v.y);
+          amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+        }
     bad = __any_sync(0xFFFFFFFFu, bad);
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
@@ -257,44 +260,82 @@ __global__ void __launch_bounds__(kScThreads) k_kv_score(const SelectArgs a, uin
     }
   }
   __syncthreads();
-  // lanes per page: dim / 8 of them when that is a power of two, else the next one
-  uint32_t lpp = 1;
-  while (lpp * 8 < a.dim) lpp <<= 1;
-  const uint32_t per = 32 / lpp, sub = lane % lpp;
-  const bool on = sub * 8 < a.dim;
-  const uint32_t step = kScThreads / 32 * per * shares;
-  for (uint32_t p0 = (share * (kScThreads / 32) + warp) * per; p0 < n_pages; p0 += step) {
-    const uint32_t p = p0 + lane / lpp;
-    uint4 c = make_uint4(0, 0, 0, 0);
-    float scale = 0.f;
-    if (p < n_pages) {
-      const uint32_t pg = static_cast<uint32_t>(a.table[static_cast<uint64_t>(b) * a.max_pages + p]);
-      if (pg < a.n_pages) {
-        const uint64_t at = static_cast<uint64_t>(pg) * a.kv_heads + h;
-        if (on) {
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(a.codes + at * 2 * a.dim) + sub * 4;
-          c = make_uint4(src[0], src[1], src[2], src[3]);
-        }
-        scale = a.scales[at];
-      } else if (sub == 0) {
+  constexpr uint32_t kPer = 32 / LPP;  // pages a warp step
+  const uint32_t sub = lane % LPP;
+  const bool on = sub * 8 < a.dim;     // lanes past a dimension that is no power of two idle
+  uint32_t qw[NQ][8];
+#pragma unroll
+  for (int i = 0; i < NQ; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) qw[i][e] = on ? sq[i * a.dim + sub * 8 + e] : 0u;
+  const bool wide = (reinterpret_cast<uintptr_t>(a.codes) & 15u) == 0;
+  const int32_t* row = a.table + static_cast<uint64_t>(b) * a.max_pages;
+  const uint32_t step = kScThreads / 32 * kPer * kScFly * shares;
+  for (uint32_t p0 = (share * (kScThreads / 32) + warp) * kPer * kScFly; p0 < n_pages; p0 += step) {
+    uint4 c[kScFly];
+    float scale[kScFly];
+    uint32_t pg[kScFly];
+#pragma unroll
+    for (uint32_t u = 0; u < kScFly; ++u) {
+      const uint32_t p = p0 + u * kPer + lane / LPP;
+      pg[u] = p < n_pages ? static_cast<uint32_t>(row[p]) : 0u;
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < kScFly; ++u) {
+      const uint32_t p = p0 + u * kPer + lane / LPP;
+      c[u] = make_uint4(0, 0, 0, 0);
+      scale[u] = 0.f;
+      if (p < n_pages && pg[u] < a.n_pages) {
+        const uint64_t at = static_cast<uint64_t>(pg[u]) * a.kv_heads + h;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(a.codes + at * 2 * a.dim) + sub * 4;
+        if (on) c[u] = wide ? *reinterpret_cast<const uint4*>(src) : make_uint4(src[0], src[1], src[2], src[3]);
+        scale[u] = a.scales[at];
+      } else if (p < n_pages && sub == 0) {
         kv_status(a.status, IBP_ERANGE);
       }
     }
-    for (uint32_t i = 0; i < kScQueries; ++i) {
-      if (place[i] < 0) continue;
-      int s = 0;
-      if (on) {
-        const uint32_t* qw = sq + i * a.dim + sub * 8;
-        const uint4 q0 = *reinterpret_cast<const uint4*>(qw), q1 = *reinterpret_cast<const uint4*>(qw + 4);
-        s = dp2a(q0.x, c.x, s, false), s = dp2a(q0.y, c.x, s, true);
-        s = dp2a(q0.z, c.y, s, false), s = dp2a(q0.w, c.y, s, true);
-        s = dp2a(q1.x, c.z, s, false), s = dp2a(q1.y, c.z, s, true);
-        s = dp2a(q1.z, c.w, s, false), s = dp2a(q1.w, c.w, s, true);
+#pragma unroll
+    for (uint32_t u = 0; u < kScFly; ++u) {
+      const uint32_t p = p0 + u * kPer + lane / LPP;
+      int s[NQ];
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        int x = 0;
+        x = dp2a(qw[i][0], c[u].x, x, false), x = dp2a(qw[i][1], c[u].x, x, true);
+        x = dp2a(qw[i][2], c[u].y, x, false), x = dp2a(qw[i][3], c[u].y, x, true);
+        x = dp2a(qw[i][4], c[u].z, x, false), x = dp2a(qw[i][5], c[u].z, x, true);
+        x = dp2a(qw[i][6], c[u].w, x, false), x = dp2a(qw[i][7], c[u].w, x, true);
+        s[i] = x;
       }
-      for (uint32_t o = lpp >> 1; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      if (sub == 0 && p < n_pages)
-        a.scores[((static_cast<uint64_t>(b) * a.T + t0 + i) * a.kv_heads + h) * a.max_pages + p] =
-            finite_f(scale) ? __fmul_rn(__int2float_rn(s), scale) : __int_as_float(0x7F800000);
+      // After the exchanges over lane bits LPP/2, LPP/4, ... a lane holds the
+      // query whose number its bits spell (as many bits as queries need).
+      uint32_t mine = 0;
+      int left = NQ;
+#pragma unroll
+      for (uint32_t o = LPP / 2; o; o >>= 1) {
+        if (left > 1) {
+          const bool up = lane & o;
+#pragma unroll
+          for (int i = 0; i < NQ / 2; ++i)
+            if (i < left / 2) {
+              const int give = up ? s[i] : s[i + left / 2], keep = up ? s[i + left / 2] : s[i];
+              s[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+            }
+          left /= 2;
+          mine += up ? left : 0;
+        } else {
+          s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], o);
+        }
+      }
+      // lanes that still hold `left` queries each (fewer lanes than queries), and
+      // one lane of those that hold the same
+      const bool writes = LPP >= NQ ? (sub % (LPP / (LPP < NQ ? LPP : NQ))) == 0 : true;
+      if (writes && p < n_pages)
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+          if (i < left && place[mine + i] >= 0)
+            a.scores[((static_cast<uint64_t>(b) * a.T + t0 + mine + i) * a.kv_heads + h) * a.max_pages + p] =
+                finite_f(scale[u]) ? __fmul_rn(__int2float_rn(s[i]), scale[u]) : __int_as_float(0x7F800000);
     }
   }
 }
@@ -302,7 +343,6 @@ __global__ void __launch_bounds__(kScThreads) k_kv_score(const SelectArgs a, uin
 // ---------------------------------------------------------------------------
 // Selection
 
-constexpr int kSelThreads = 128;
 constexpr uint32_t kSelShared = 8192;  // scores held in shared memory; more are read from L2 on every pass
 
 // Whole-number key in the order of the score; +0 and -0 are equal.
@@ -311,32 +351,20 @@ __device__ __forceinline__ uint32_t order_key(float s) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ uint32_t sel_rank(bool flag, uint32_t* sums, uint32_t* total) {
-  const uint32_t lane = threadIdx.x & 31u, w = threadIdx.x >> 5;
-  const uint32_t m = __ballot_sync(0xFFFFFFFFu, flag);
-  __syncthreads();
-  if (lane == 0) sums[w] = __popc(m);
-  __syncthreads();
-  uint32_t before = 0, all = 0;
-#pragma unroll
-  for (uint32_t i = 0; i < kSelThreads / 32; ++i) {
-    before += i < w ? sums[i] : 0;
-    all += sums[i];
-  }
-  *total = all;
-  return before + __popc(m & lanemask_lt());
-}
-
-// One CTA per query and kv head: the threshold key by four passes of an 8-bit
-// histogram over the scores that are neither forced nor hidden, then the pages
-// in ascending order by prefix counts.  Bound by the latency of its passes.
-__global__ void __launch_bounds__(kSelThreads) k_kv_select(const SelectArgs a, uint32_t key_cap) {
+// One CTA per query and kv head.  The threshold key comes from passes of an
+// 8-bit histogram over the scores that are neither forced nor hidden, and ends
+// early when a digit's keys are all wanted (two passes, as a rule); then each
+// warp counts what it takes in its own stretch of pages and writes it, ascending,
+// behind the warps before it.  Bound by the latency of its passes.
+template <int NT>
+__global__ void __launch_bounds__(NT) k_kv_select(const SelectArgs a, uint32_t key_cap) {
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[256], sums[kSelThreads / 32], sh_digit, sh_left;
+  __shared__ uint32_t hist[256], sums[2][NT / 32], sh_digit, sh_left, sh_all;
   pdl_begin();
   const uint64_t row = blockIdx.x;
   const uint64_t bt = row / a.kv_heads;
   const uint32_t t = static_cast<uint32_t>(bt % a.T), b = static_cast<uint32_t>(bt / a.T), tid = threadIdx.x;
+  const uint32_t lane = tid & 31u, warp = tid >> 5;
   const int32_t raw = a.lens[b], len = clamp_len(raw, a.page_tokens, a.max_pages);
   const int32_t place = query_place(a, b, t, len);
   if (tid == 0) {
@@ -346,84 +374,149 @@ __global__ void __launch_bounds__(kSelThreads) k_kv_select(const SelectArgs a, u
   int32_t* out = a.picks + row * a.budget;
   const uint32_t n = place < 0 ? 0 : static_cast<uint32_t>(place) / a.page_tokens + 1;
   if (n <= a.budget) {
-    for (uint32_t i = tid; i < a.budget; i += kSelThreads) out[i] = i < n ? static_cast<int32_t>(i) : -1;
+    for (uint32_t i = tid; i < a.budget; i += NT) out[i] = i < n ? static_cast<int32_t>(i) : -1;
     return;
   }
   // here keep_first + keep_last <= budget < n: the two forced ranges are apart
   const uint32_t f0 = a.keep_first, f1 = n - a.keep_last;
   const float* scores = a.scores + row * a.max_pages;
   const bool held = n <= key_cap;
-  if (held)
-    for (uint32_t i = f0 + tid; i < f1; i += kSelThreads) keys[i] = order_key(scores[i]);
-  auto key = [&](uint32_t i) { return held ? keys[i] : order_key(scores[i]); };
+  for (uint32_t i = tid; i < 256; i += NT) hist[i] = 0;
+  __syncthreads();
   uint32_t left = a.budget - a.keep_first - a.keep_last;  // to be taken by score
-  uint32_t prefix = 0;
-  if (left > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (uint32_t i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      const uint32_t high = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      for (uint32_t i = f0 + tid; i < f1; i += kSelThreads) {
-        const uint32_t k = key(i);
+  const bool any = left > 0;
+  // keys at or above `prefix` with its low bits clear: `left` of those equal in
+  // the high bits `high`
+  uint32_t prefix = 0, high = 0;
+  bool all = false;  // every key equal in the high bits is taken
+  if (any) {
+    for (int shift = 24; shift >= 0 && !all; shift -= 8) {
+      for (uint32_t i = f0 + tid; i < f1; i += NT) {
+        uint32_t k;
+        if (shift == 24) {
+          k = order_key(scores[i]);
+          if (held) keys[i] = k;
+        } else {
+          k = held ? keys[i] : order_key(scores[i]);
+        }
         if ((k & high) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
       }
       __syncthreads();
-      if (tid < 32) {  // lane l holds the digits 8l .. 8l+7; counts from the top
-        uint32_t mine = 0;
-        for (uint32_t i = 0; i < 8; ++i) mine += hist[8 * tid + i];
+      if (warp == 0) {  // lane l holds the digits 8l .. 8l+7; counts from the top
+        uint32_t d8[8], mine = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) {
+          d8[i] = hist[8 * lane + i];
+          hist[8 * lane + i] = 0;
+          mine += d8[i];
+        }
         uint32_t above = mine;
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint32_t v = __shfl_down_sync(0xFFFFFFFFu, above, o);
-          if (tid + o < 32) above += v;
+          if (lane + o < 32) above += v;
         }
         above -= mine;  // keys of higher lanes
         if (above < left && above + mine >= left) {
-          uint32_t d = 8 * tid + 7, acc = above;
-          while (acc + hist[d] < left) acc += hist[d--];
-          sh_digit = d;
-          sh_left = left - acc;
+          uint32_t acc = above;
+          bool found = false;
+#pragma unroll
+          for (int d = 7; d >= 0; --d) {
+            if (!found && acc + d8[d] >= left) {
+              found = true;
+              sh_digit = 8 * lane + d;
+              sh_left = left - acc;
+              sh_all = left - acc == d8[d];
+            }
+            acc += d8[d];
+          }
         }
       }
       __syncthreads();
       prefix |= sh_digit << shift;
+      high |= 255u << shift;
       left = sh_left;
+      all = sh_all != 0;
     }
   }
-  // keys above `prefix` are taken, and the first `left` equal to it
-  const bool any = a.budget > a.keep_first + a.keep_last;
-  uint32_t done = 0, ties = 0, total;
-  for (uint32_t i0 = 0; i0 < n; i0 += kSelThreads) {
-    const uint32_t i = i0 + tid;
-    const bool forced = i < n && (i < f0 || i >= f1), open = any && i < n && !forced;
-    const uint32_t k = open ? key(i) : 0;
-    const bool tie = open && k == prefix;
-    const uint32_t nth = ties + sel_rank(tie, sums, &total);
-    ties += total;
-    const bool take = forced || (open && k > prefix) || (tie && nth < left);
-    const uint32_t at = done + sel_rank(take, sums, &total);
-    if (take && at < a.budget) out[at] = static_cast<int32_t>(i);
-    done += total;
+  // Each warp's stretch: counts of taken pages and of ties, then their places.
+  const uint32_t per = ceil_div(ceil_div(n, NT / 32), 32) * 32;
+  const uint32_t w0 = warp * per < n ? warp * per : n, w1 = n - w0 < per ? n : w0 + per;
+  auto kind = [&](uint32_t i, bool* take, bool* tie) {
+    *take = *tie = false;
+    if (i >= w1) return;
+    if (i < f0 || i >= f1) {
+      *take = true;
+    } else if (any) {
+      const uint32_t k = held ? keys[i] : order_key(scores[i]);
+      const uint32_t kh = k & high;
+      *take = kh > prefix || (all && kh == prefix);
+      *tie = !all && kh == prefix;
+    }
+  };
+  uint32_t n_take = 0, n_tie = 0;
+  for (uint32_t i = w0; i < w1; i += 32) {
+    bool take, tie;
+    kind(i + lane, &take, &tie);
+    n_take += __popc(__ballot_sync(0xFFFFFFFFu, take));
+    n_tie += __popc(__ballot_sync(0xFFFFFFFFu, tie));
+  }
+  if (lane == 0) sums[0][warp] = n_take, sums[1][warp] = n_tie;
+  __syncthreads();
+  uint32_t at = 0, ties = 0;
+  for (uint32_t w = 0; w < warp; ++w) at += sums[0][w], ties += sums[1][w];
+  at += ties < left ? ties : left;
+  for (uint32_t i = w0; i < w1; i += 32) {
+    bool take, tie;
+    kind(i + lane, &take, &tie);
+    const uint32_t tm = __ballot_sync(0xFFFFFFFFu, tie);
+    take = take || (tie && ties + __popc(tm & lanemask_lt()) < left);
+    ties += __popc(tm);
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, take);
+    const uint32_t to = at + __popc(m & lanemask_lt());
+    if (take && to < a.budget) out[to] = static_cast<int32_t>(i + lane);
+    at += __popc(m);
+  }
+}
+
+template <int NQ>
+static int launch_score(const SelectArgs& a, int device, cudaStream_t stream) {
+  const uint32_t q_blocks = (a.T + NQ - 1) / NQ;
+  uint32_t lpp = 1;
+  while (lpp * 8 < a.dim) lpp <<= 1;
+  // Shares of at least one step, until one round of CTAs fills the GPU.
+  const uint32_t per_cta = kScThreads / 32 * (32 / lpp) * kScFly;
+  const uint64_t want = (a.max_pages + per_cta - 1) / per_cta;
+  const uint64_t rows = static_cast<uint64_t>(a.kv_heads) * a.n_seqs * q_blocks;
+  const uint64_t cap = (6ull * sm_count(device) + rows - 1) / rows;
+  const uint32_t shares = static_cast<uint32_t>(want < cap ? want : cap);
+  const dim3 grid(a.n_seqs * q_blocks * shares, a.kv_heads);
+  auto go = [&](auto kern) {
+    return kv_launch("k_kv_score", kern, grid, kScThreads, NQ * a.dim * 4, 1, stream, a, q_blocks, shares);
+  };
+  switch (lpp) {
+    case 1: return go(k_kv_score<NQ, 1>);
+    case 2: return go(k_kv_score<NQ, 2>);
+    case 4: return go(k_kv_score<NQ, 4>);
+    case 8: return go(k_kv_score<NQ, 8>);
+    case 16: return go(k_kv_score<NQ, 16>);
+    default: return go(k_kv_score<NQ, 32>);
   }
 }
 
 int launch_kv_select(const SelectArgs& a, int device, cudaStream_t stream) {
-  const uint32_t q_blocks = (a.T + kScQueries - 1) / kScQueries;
-  uint32_t lpp = 1;
-  while (lpp * 8 < a.dim) lpp <<= 1;
-  const uint32_t per_cta = kScThreads / 32 * (32 / lpp);
-  const uint64_t want = (a.max_pages + 2 * per_cta - 1) / (2 * per_cta);
-  const uint64_t rows = static_cast<uint64_t>(a.kv_heads) * a.n_seqs * q_blocks;
-  const uint64_t cap = (16ull * sm_count(device) + rows - 1) / rows;
   int rc = IBP_OK;
-  if (a.max_pages > a.budget) {
-    const uint32_t shares = static_cast<uint32_t>(want < cap ? want : cap);
-    const dim3 grid(a.n_seqs * q_blocks * shares, a.kv_heads);
-    rc = kv_launch("k_kv_score", k_kv_score, grid, kScThreads, kScQueries * a.dim * 4, 1, stream, a, q_blocks, shares);
-  }
+  // Eight queries share a CTA's reading of the codes; a single token would leave
+  // seven of the eight sums idle.
+  if (a.max_pages > a.budget) rc = a.T == 1 ? launch_score<1>(a, device, stream) : launch_score<8>(a, device, stream);
   if (rc != IBP_OK) return rc;
-  const uint32_t cap_keys = a.max_pages < kSelShared ? a.max_pages : kSelShared;
-  return kv_launch("k_kv_select", k_kv_select, dim3(a.n_seqs * a.T * a.kv_heads), kSelThreads, 4ull * cap_keys, 1,
-                   stream, a, cap_keys);
+  const uint32_t cap = a.max_pages < kSelShared ? a.max_pages : kSelShared;
+  const dim3 grid(a.n_seqs * a.T * a.kv_heads);
+  // A wide CTA shortens the passes over many pages; with more rows than the GPU
+  // holds such CTAs, narrow ones finish sooner.
+  if (a.max_pages > 512 && grid.x <= 4u * sm_count(device))
+    return kv_launch("k_kv_select", k_kv_select<512>, grid, 512, 4ull * cap, 1, stream, a, cap);
+  return kv_launch("k_kv_select", k_kv_select<128>, grid, 128, 4ull * cap, 1, stream, a, cap);
 }
 
 }  // namespace ibp
