@@ -4,7 +4,7 @@
 // A CTA holds 8 or 16 query rows of one sequence and kv head (the group's heads,
 // and the drafted tokens) and walks a share of the tokens.  With so few rows
 // the cache's bytes are what counts, so the layout serves the loads: each of
-// the four warps has its own ring of 16-token stages, filled by 16-byte
+// the four warps has its own ring of stages of 16 or 32 tokens, filled by 16-byte
 // asynchronous copies, and its own running maximum and sum; no barrier is met
 // until the warps are joined at the end.  Where there are items enough for every
 // warp (a chunk of sparse queries), each warp takes an item of its own.
@@ -28,7 +28,6 @@
 namespace ibp {
 
 constexpr uint32_t kAtWarps = 4;
-constexpr uint32_t kSub = 16;  // tokens of a stage
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -98,9 +97,13 @@ struct Item {
 
 template <uint32_t DP, uint32_t NT, bool F16, bool PICK>
 struct Attend {
+  // Tokens of a step: what a step costs besides its products (page, maxima over
+  // the lanes, bookkeeping) is halved for narrow heads, whose bytes are few.
+  static constexpr uint32_t kSub = DP == 64 ? 32 : 16;
+  static constexpr uint32_t kMma = kSub / 16;
   static constexpr uint32_t kPitch = DP * 2;                 // bytes of a token in a stage
   static constexpr uint32_t kTile = kSub * kPitch;           // bytes of K or V in a stage
-  static constexpr uint32_t kStages = DP == 64 ? 4 : (DP == 128 ? 3 : 2);
+  static constexpr uint32_t kStages = DP == 128 ? 3 : 2;
   static constexpr uint32_t kWarpBytes = kStages * 2 * kTile;
   static constexpr uint32_t kBytes = kAtWarps * kWarpBytes;
   static constexpr uint32_t kRows = 8 * NT;
@@ -121,72 +124,100 @@ struct Attend {
   }
 };
 
-// Copies the 16 tokens of step `sub` into a stage; tokens that no row may see
-// are zeros, so nothing they hold reaches a sum.
+// The page of a step, looked up one step before its tokens are asked for.
+struct Ahead {
+  uint32_t nth, page;
+};
+
+// What a lane's copies need in every step.
+struct Lane {
+  const char *k, *v;  // this lane's chunk of the first token of a step at offset 0
+  const int32_t* row; // the sequence's table row
+  int32_t shift;      // pages hold 2^shift steps; -1: some other whole number; -2: steps cross pages
+};
+
 template <uint32_t DP, uint32_t NT, bool F16, bool PICK>
-__device__ __forceinline__ void load_stage(const AttendArgs& a, const Item& it, uint32_t sub, uint32_t end,
-                                           uint32_t stage, bool one_page, int32_t* pos_out) {
+__device__ __forceinline__ Ahead look_ahead(const AttendArgs& a, const Item& it, const Lane& ln, uint32_t sub) {
+  using A = Attend<DP, NT, F16, PICK>;
+  Ahead x = {0u, 0xFFFFFFFFu};
+  if (ln.shift < -1 || sub * A::kSub >= it.n_tok) return x;
+  const uint32_t at = ln.shift >= 0 ? sub >> ln.shift : sub * A::kSub / a.page_tokens;
+  x.nth = PICK ? static_cast<uint32_t>(it.picks[at]) : at;
+  x.page = static_cast<uint32_t>(ln.row[x.nth]);
+  return x;
+}
+
+// Copies the tokens of step `sub` into a stage; tokens that no row may see
+// are zeros, so nothing they hold reaches a sum.  *pos_out: the position of this
+// lane's token (lane modulo the step).
+template <uint32_t DP, uint32_t NT, bool F16, bool PICK>
+__device__ __forceinline__ void load_stage(const AttendArgs& a, const Item& it, const Lane& ln, uint32_t sub,
+                                           uint32_t stage, const Ahead& ah, int32_t* pos_out) {
   using A = Attend<DP, NT, F16, PICK>;
   const uint32_t lane = threadIdx.x & 31u;
+  constexpr uint32_t kSub = A::kSub;
   constexpr uint32_t kChunks = DP / 8;      // 16-byte chunks of a token
-  constexpr uint32_t kPer = 32 / kChunks;   // tokens per warp step
+  constexpr uint32_t kPer = 32 / kChunks;   // tokens per warp instruction
   const uint32_t c = lane % kChunks, r0 = lane / kChunks;
   const bool col = c < a.dim / 8;
-  const char* kb = a.k.data + static_cast<int64_t>(it.h) * a.k.head_stride + c * 16;
-  const char* vb = a.v.data + static_cast<int64_t>(it.h) * a.v.head_stride + c * 16;
-  // Lane i (and i + 16) finds token i; where pages hold whole steps, all find
-  // the same page and need not tell one another.
-  const uint32_t tok = sub * kSub + (lane & 15u);
-  const uint32_t at = (one_page ? sub * kSub : tok) / a.page_tokens;
-  const uint32_t slot = tok - at * a.page_tokens;
-  uint32_t nth = at, page = 0xFFFFFFFFu;
-  int32_t pos = 0x7FFFFFFF;
-  if (tok < end) {
-    if (PICK) nth = static_cast<uint32_t>(it.picks[at]);
-    pos = static_cast<int32_t>(nth * a.page_tokens + slot);
+  const uint32_t dst0 = stage + r0 * A::kPitch;
+  const uint32_t left = it.n_tok - sub * kSub;  // tokens from this step on
+  if (ln.shift >= -1) {
+    const uint32_t at = ln.shift >= 0 ? sub >> ln.shift : sub * kSub / a.page_tokens;
+    const uint32_t s0 = sub * kSub - at * a.page_tokens;  // first token of the step in its page
+    const uint32_t mine = lane % kSub;
+    *pos_out = mine < left ? static_cast<int32_t>(ah.nth * a.page_tokens + s0 + mine) : 0x7FFFFFFF;
+    const bool good = ah.page < a.n_pages;
+    if (!good) kv_status(a.status, IBP_ERANGE);
+    const char* k = ln.k + static_cast<int64_t>(ah.page) * a.k.page_stride + static_cast<int64_t>(s0) * a.k.token_stride;
+    const char* v = ln.v + static_cast<int64_t>(ah.page) * a.v.page_stride + static_cast<int64_t>(s0) * a.v.token_stride;
+#pragma unroll
+    for (uint32_t i = 0; i < kSub / kPer; ++i) {
+      const uint32_t r = r0 + i * kPer;
+      const uint32_t dst = dst0 + i * kPer * A::kPitch + ((c ^ (r & 7u)) << 4);
+      const bool on = good && col && r < left;
+      cp16(dst, on ? k : a.k.data, on);
+      cp16(dst + A::kTile, on ? v : a.v.data, on);
+      k += kPer * a.k.token_stride;
+      v += kPer * a.v.token_stride;
+    }
+    return;
   }
-  if (one_page ? sub * kSub < end : tok < end && pos < it.seen) {
-    if (PICK && one_page) nth = static_cast<uint32_t>(it.picks[at]);
-    page = static_cast<uint32_t>(a.table[static_cast<uint64_t>(it.b) * a.max_pages + nth]);
-    if (page >= a.n_pages) {
-      kv_status(a.status, IBP_ERANGE);
-      page = 0xFFFFFFFFu;
+  // Steps cross pages: lane i finds token i and tells the others.
+  const uint32_t tok = sub * kSub + lane % kSub, at = tok / a.page_tokens, slot = tok - at * a.page_tokens;
+  uint32_t page = 0xFFFFFFFFu;
+  int32_t pos = 0x7FFFFFFF;
+  if (tok < it.n_tok) {
+    const uint32_t nth = PICK ? static_cast<uint32_t>(it.picks[at]) : at;
+    pos = static_cast<int32_t>(nth * a.page_tokens + slot);
+    if (pos < it.seen) {
+      page = static_cast<uint32_t>(ln.row[nth]);
+      if (page >= a.n_pages) {
+        kv_status(a.status, IBP_ERANGE);
+        page = 0xFFFFFFFFu;
+      }
     }
   }
   *pos_out = pos;
-  const uint32_t dst0 = stage + r0 * A::kPitch;
-  if (one_page) {
-    const uint32_t s0 = sub * kSub - at * a.page_tokens;
-    const uint32_t left = end - sub * kSub;  // tokens of this step
-    const int64_t bk = static_cast<int64_t>(page) * a.k.page_stride, bv = static_cast<int64_t>(page) * a.v.page_stride;
-    const bool have = col && page != 0xFFFFFFFFu;
+  const int64_t tk = static_cast<int64_t>(page) * a.k.page_stride + static_cast<int64_t>(slot) * a.k.token_stride;
+  const int64_t tv = static_cast<int64_t>(page) * a.v.page_stride + static_cast<int64_t>(slot) * a.v.token_stride;
+  const int64_t bk = static_cast<int64_t>(r0) * a.k.token_stride, bv = static_cast<int64_t>(r0) * a.v.token_stride;
 #pragma unroll
-    for (uint32_t i = 0; i < kSub / kPer; ++i) {
-      const uint32_t r = r0 + i * kPer;
-      const uint32_t dst = dst0 + i * kPer * A::kPitch + ((c ^ (r & 7u)) << 4);
-      const bool on = have && r < left;
-      cp16(dst, on ? kb + bk + static_cast<int64_t>(s0 + r) * a.k.token_stride : a.k.data, on);
-      cp16(dst + A::kTile, on ? vb + bv + static_cast<int64_t>(s0 + r) * a.v.token_stride : a.v.data, on);
-    }
-  } else {
-    const int64_t tk = static_cast<int64_t>(page) * a.k.page_stride + static_cast<int64_t>(slot) * a.k.token_stride;
-    const int64_t tv = static_cast<int64_t>(page) * a.v.page_stride + static_cast<int64_t>(slot) * a.v.token_stride;
-#pragma unroll
-    for (uint32_t i = 0; i < kSub / kPer; ++i) {
-      const uint32_t r = r0 + i * kPer;
-      const bool on = (__shfl_sync(0xFFFFFFFFu, page, r) != 0xFFFFFFFFu) && col;
-      const int64_t ok = __shfl_sync(0xFFFFFFFFu, tk, r), ov = __shfl_sync(0xFFFFFFFFu, tv, r);
-      const uint32_t dst = dst0 + i * kPer * A::kPitch + ((c ^ (r & 7u)) << 4);
-      cp16(dst, on ? kb + ok : a.k.data, on);
-      cp16(dst + A::kTile, on ? vb + ov : a.v.data, on);
-    }
+  for (uint32_t i = 0; i < kSub / kPer; ++i) {
+    const uint32_t r = r0 + i * kPer;
+    const bool on = (__shfl_sync(0xFFFFFFFFu, page, r) != 0xFFFFFFFFu) && col;
+    const int64_t ok = __shfl_sync(0xFFFFFFFFu, tk, r), ov = __shfl_sync(0xFFFFFFFFu, tv, r);
+    const uint32_t dst = dst0 + i * kPer * A::kPitch + ((c ^ (r & 7u)) << 4);
+    cp16(dst, on ? ln.k + (ok - bk) : a.k.data, on);
+    cp16(dst + A::kTile, on ? ln.v + (ov - bv) : a.v.data, on);
   }
 }
 
 template <uint32_t DP, uint32_t NT, bool F16, bool PICK, uint32_t WPI>
 __global__ void __launch_bounds__(kAtWarps * 32)
-    k_kv_attend(const AttendArgs a, uint32_t row_tiles, uint32_t one_page, uint32_t items) {
+    k_kv_attend(const AttendArgs a, uint32_t row_tiles, int32_t shift, uint32_t items) {
   using A = Attend<DP, NT, F16, PICK>;
+  constexpr uint32_t kSub = A::kSub, kM = A::kMma;
   extern __shared__ __align__(128) unsigned char sm[];
   pdl_begin();
   // WPI warps share an item: all four of a CTA, or one each.
@@ -239,7 +270,7 @@ __global__ void __launch_bounds__(kAtWarps * 32)
     live_rows = lr > it.row0 ? (lr - it.row0 < it.rows ? lr - it.row0 : it.rows) : 0;
     it.n_tok = live_rows ? static_cast<uint32_t>(len) : 0;
   }
-  // This CTA's share of the 16-token steps.
+  // This CTA's share of the steps.
   const uint32_t steps = ceil_div(it.n_tok, kSub);
   const uint32_t per = ceil_div(steps, a.splits);
   const uint32_t s0 = split * per < steps ? split * per : steps, s1 = steps - s0 < per ? steps : s0 + per;
@@ -274,12 +305,24 @@ __global__ void __launch_bounds__(kAtWarps * 32)
 
   unsigned char* const mine = sm + group * WPI * A::kWarpBytes;
   const uint32_t ring = smem_u32(mine) + warp * A::kWarpBytes;
-  int32_t pos_ring[A::kStages];  // this lane's token of each stage in flight
+  Lane ln;
+  {
+    constexpr uint32_t kChunks = DP / 8;
+    const uint32_t c = lane % kChunks, r0 = lane / kChunks;
+    ln.k = a.k.data + static_cast<int64_t>(it.h) * a.k.head_stride + c * 16 + static_cast<int64_t>(r0) * a.k.token_stride;
+    ln.v = a.v.data + static_cast<int64_t>(it.h) * a.v.head_stride + c * 16 + static_cast<int64_t>(r0) * a.v.token_stride;
+    ln.row = a.table + static_cast<uint64_t>(it.b) * a.max_pages;
+    ln.shift = shift;
+  }
+  int32_t pos_ring[A::kStages];  // the position of this lane's token, for each stage in flight
+  Ahead ah = look_ahead<DP, NT, F16, PICK>(a, it, ln, s0 + warp);
 #pragma unroll
   for (uint32_t i = 0; i < A::kStages - 1; ++i) {
     const uint32_t s = s0 + warp + i * WPI;
-    if (s < s1)
-      load_stage<DP, NT, F16, PICK>(a, it, s, it.n_tok, ring + i * 2 * A::kTile, one_page, &pos_ring[i]);
+    if (s < s1) {
+      load_stage<DP, NT, F16, PICK>(a, it, ln, s, ring + i * 2 * A::kTile, ah, &pos_ring[i]);
+      ah = look_ahead<DP, NT, F16, PICK>(a, it, ln, s + WPI);
+    }
     cp_commit();
   }
   for (uint32_t sb = s0 + warp; sb < s1; sb += WPI * A::kStages) {
@@ -290,73 +333,105 @@ __global__ void __launch_bounds__(kAtWarps * 32)
       constexpr uint32_t kAhead = A::kStages - 1;
       const uint32_t un = (u + kAhead) % A::kStages;
       __syncwarp();  // every lane is done with the stage that is filled next
-      if (s + kAhead * WPI < s1)
-        load_stage<DP, NT, F16, PICK>(a, it, s + kAhead * WPI, it.n_tok, ring + un * 2 * A::kTile, one_page,
-                                      &pos_ring[un]);
+      if (s + kAhead * WPI < s1) {
+        load_stage<DP, NT, F16, PICK>(a, it, ln, s + kAhead * WPI, ring + un * 2 * A::kTile, ah, &pos_ring[un]);
+        ah = look_ahead<DP, NT, F16, PICK>(a, it, ln, s + (kAhead + 1) * WPI);
+      }
       cp_commit();
       cp_wait<kAhead>();
       __syncwarp();
       const uint32_t kt = ring + u * 2 * A::kTile, vt = kt + A::kTile;
       const int32_t my_pos = pos_ring[u];
 
-      float c[NT][4];
+      float c[kM][NT][4];
 #pragma unroll
-      for (uint32_t n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
-      {
+      for (uint32_t x = 0; x < kM; ++x) {
+#pragma unroll
+        for (uint32_t n = 0; n < NT; ++n) c[x][n][0] = c[x][n][1] = c[x][n][2] = c[x][n][3] = 0.f;
         const uint32_t r = lane & 15u, hi = lane >> 4;
-        const uint32_t base = kt + r * A::kPitch;
+        const uint32_t base = kt + (16 * x + r) * A::kPitch;
 #pragma unroll
         for (uint32_t kk = 0; kk < DP / 16; ++kk) {
           uint32_t f[4];
           ldsm4(f, base + (((kk * 2 + hi) ^ (r & 7u)) << 4));
 #pragma unroll
-          for (uint32_t n = 0; n < NT; ++n) mma16816<F16>(c[n], f, qf[n][kk][0], qf[n][kk][1]);
+          for (uint32_t n = 0; n < NT; ++n) mma16816<F16>(c[x][n], f, qf[n][kk][0], qf[n][kk][1]);
         }
       }
       // Scores in powers of two; what a row does not see is -infinity.
-      const int32_t p_lo = __shfl_sync(0xFFFFFFFFu, my_pos, lane / 4);
-      const int32_t p_hi = __shfl_sync(0xFFFFFFFFu, my_pos, lane / 4 + 8);
       const int32_t edge = PICK ? it.seen : (it.ctx < it.seen ? it.ctx : it.seen);
-      const bool open = __all_sync(0xFFFFFFFFu, my_pos < edge);  // every row sees all sixteen
+      const bool open = __all_sync(0xFFFFFFFFu, my_pos < edge);  // every row sees the whole step
       float cm[NT][2];
 #pragma unroll
       for (uint32_t n = 0; n < NT; ++n) {
 #pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) c[n][e] *= a.scale_log2;
-        if (!open) {
+        for (uint32_t x = 0; x < kM; ++x) {
 #pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) {
-            const uint32_t r = n * 8 + (lane & 3u) * 2 + (e & 1u);
-            if (r >= live_rows || !A::sees(a, it, it.row0 + r, e < 2 ? p_lo : p_hi)) c[n][e] = -INFINITY;
-          }
+          for (uint32_t e = 0; e < 4; ++e) c[x][n][e] *= a.scale_log2;
         }
-        cm[n][0] = fmaxf(c[n][0], c[n][2]), cm[n][1] = fmaxf(c[n][1], c[n][3]);
+      }
+      if (!open) {
+#pragma unroll
+        for (uint32_t x = 0; x < kM; ++x) {
+          const int32_t p_lo = __shfl_sync(0xFFFFFFFFu, my_pos, 16 * x + lane / 4);
+          const int32_t p_hi = __shfl_sync(0xFFFFFFFFu, my_pos, 16 * x + lane / 4 + 8);
+#pragma unroll
+          for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) {
+              const uint32_t r = n * 8 + (lane & 3u) * 2 + (e & 1u);
+              if (r >= live_rows || !A::sees(a, it, it.row0 + r, e < 2 ? p_lo : p_hi)) c[x][n][e] = -INFINITY;
+            }
+        }
+      }
+#pragma unroll
+      for (uint32_t n = 0; n < NT; ++n) {
+#pragma unroll
+        for (uint32_t e = 0; e < 2; ++e) {
+          cm[n][e] = fmaxf(c[0][n][e], c[0][n][2 + e]);
+#pragma unroll
+          for (uint32_t x = 1; x < kM; ++x) cm[n][e] = fmaxf(cm[n][e], fmaxf(c[x][n][e], c[x][n][2 + e]));
+        }
 #pragma unroll
         for (uint32_t w = 4; w < 32; w <<= 1) {
           cm[n][0] = fmaxf(cm[n][0], __shfl_xor_sync(0xFFFFFFFFu, cm[n][0], w));
           cm[n][1] = fmaxf(cm[n][1], __shfl_xor_sync(0xFFFFFFFFu, cm[n][1], w));
         }
       }
-      uint32_t pf[NT][2];
+      // The maximum that the sums are taken under follows when it has been
+      // passed by 2^8: until then the probabilities stay within the type's range.
+      bool grow = false;
+#pragma unroll
+      for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+        for (uint32_t e = 0; e < 2; ++e)
+          grow = grow || cm[n][e] > m[n][e] + 8.f || (m[n][e] == -INFINITY && cm[n][e] > -INFINITY);
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+        for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+          for (uint32_t e = 0; e < 2; ++e)
+            if (cm[n][e] > m[n][e]) {
+              const float f = ex2(m[n][e] - cm[n][e]);
+              m[n][e] = cm[n][e];
+              l[n][e] *= f;
+#pragma unroll
+              for (uint32_t d = 0; d < DP / 16; ++d) o[d][n][e] *= f, o[d][n][2 + e] *= f;
+            }
+      }
+      uint32_t pf[kM][NT][2];
 #pragma unroll
       for (uint32_t n = 0; n < NT; ++n) {
-#pragma unroll
-        for (uint32_t e = 0; e < 2; ++e) {
-          if (cm[n][e] > m[n][e]) {  // rescale what was summed under the lower maximum
-            const float f = ex2(m[n][e] - cm[n][e]);
-            m[n][e] = cm[n][e];
-            l[n][e] *= f;
-#pragma unroll
-            for (uint32_t d = 0; d < DP / 16; ++d) o[d][n][e] *= f, o[d][n][2 + e] *= f;
-          }
-        }
         const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-        const float p0 = ex2(c[n][0] - m0), p1 = ex2(c[n][1] - m1);
-        const float p2 = ex2(c[n][2] - m0), p3 = ex2(c[n][3] - m1);
-        l[n][0] += p0 + p2;
-        l[n][1] += p1 + p3;
-        pf[n][0] = transpose8(pack2<F16>(p0, p1));
-        pf[n][1] = transpose8(pack2<F16>(p2, p3));
+#pragma unroll
+        for (uint32_t x = 0; x < kM; ++x) {
+          const float p0 = ex2(c[x][n][0] - m0), p1 = ex2(c[x][n][1] - m1);
+          const float p2 = ex2(c[x][n][2] - m0), p3 = ex2(c[x][n][3] - m1);
+          l[n][0] += p0 + p2;
+          l[n][1] += p1 + p3;
+          pf[x][n][0] = transpose8(pack2<F16>(p0, p1));
+          pf[x][n][1] = transpose8(pack2<F16>(p2, p3));
+        }
       }
       if (!PICK && !open) {
         // Infinities and NaN among the draft's values: a row that does not see
@@ -404,16 +479,17 @@ __global__ void __launch_bounds__(kAtWarps * 32)
           __syncwarp();
         }
       }
-      {
+#pragma unroll
+      for (uint32_t x = 0; x < kM; ++x) {
         const uint32_t r = lane & 7u, quad = lane >> 3;
-        const uint32_t tok = r + (quad >> 1) * 8;
+        const uint32_t tok = 16 * x + r + (quad >> 1) * 8;
         const uint32_t base = vt + tok * A::kPitch;
 #pragma unroll
         for (uint32_t d = 0; d < DP / 16; ++d) {
           uint32_t f[4];
           ldsm4t(f, base + (((d * 2 + (quad & 1u)) ^ (tok & 7u)) << 4));
 #pragma unroll
-          for (uint32_t n = 0; n < NT; ++n) mma16816<F16>(o[d][n], f, pf[n][0], pf[n][1]);
+          for (uint32_t n = 0; n < NT; ++n) mma16816<F16>(o[d][n], f, pf[x][n][0], pf[x][n][1]);
         }
       }
     }
@@ -592,7 +668,7 @@ __global__ void __launch_bounds__(128) k_kv_join(const AttendArgs a, uint32_t ro
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kMaxUnits = 2048;  // CTAs up to which items are split
-constexpr uint32_t kLeast = 2 * kAtWarps * kSub;  // tokens of a share
+constexpr uint32_t kLeast = 128;      // tokens of a share
 
 static uint32_t padded_dim(uint32_t dim) { return dim <= 64 ? 64 : (dim <= 128 ? 128 : 256); }
 // 16 rows a CTA where there are more than 8 and the registers allow it.
@@ -620,8 +696,14 @@ static int launch_items(const AttendArgs& a, uint32_t tiles, uint64_t items, int
     if (device >= 0 && device < 64) ready[device].store(1, std::memory_order_release);
   }
   const uint64_t per = kAtWarps / WPI;
+  int32_t shift = -2;
+  if (a.page_tokens % A::kSub == 0) {
+    const uint32_t steps = a.page_tokens / A::kSub;
+    shift = steps & (steps - 1) ? -1 : 0;
+    while (shift >= 0 && (1u << shift) < steps) ++shift;
+  }
   return kv_launch("k_kv_attend", kern, dim3(static_cast<unsigned>((items + per - 1) / per * a.splits)), kAtWarps * 32,
-                   A::kBytes, a.cluster ? a.splits : 1, stream, a, tiles, a.page_tokens % kSub == 0 ? 1u : 0u, static_cast<uint32_t>(items));
+                   A::kBytes, a.cluster ? a.splits : 1, stream, a, tiles, shift, static_cast<uint32_t>(items));
 }
 
 template <uint32_t DP, uint32_t NT, bool F16, bool PICK>

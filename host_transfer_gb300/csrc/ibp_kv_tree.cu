@@ -5,7 +5,7 @@
 namespace ibp {
 
 constexpr int kJoinThreads = 256;
-constexpr uint32_t kJoinRows = 32;  // rows of a CTA, a warp each at a time
+constexpr uint32_t kJoinRows = kJoinThreads / 32;  // rows of a CTA, a warp each
 
 // CTA (j, rows): joins the item that crosses the start of range j, if j is the
 // first range boundary inside it.  The range before holds its first part (slot
@@ -23,49 +23,71 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_tree_join(const __grid_cons
   const uint64_t start = j * share - before, end = start + tiles_of(a, b);
   const uint32_t last = static_cast<uint32_t>((end - 1) / share);
   constexpr uint32_t kRows = MT * kTcTile;
-  for (uint32_t i = warp; i < kJoinRows; i += kJoinThreads / 32) {
-    const uint32_t r = blockIdx.y * kJoinRows + i, gr = f.z * kRows + r;
-    const uint32_t tok = gr / a.group, head = gr - tok * a.group;
-    if (tok >= a.T) return;
-    auto row_of = [&](uint32_t c) { return (2ull * c + (c < j ? 1 : 0)) * kRows + r; };
-    float top = -INFINITY;
-    for (uint32_t c = j - 1; c <= last; ++c) top = fmaxf(top, t.ml_part[row_of(c)].x);
-    float sum = 0.f;
-    float2 acc[DP / 64];
+  const uint32_t r = blockIdx.y * kJoinRows + warp, gr = f.z * kRows + r;
+  const uint32_t tok = gr / a.group, head = gr - tok * a.group;
+  if (tok >= a.T) return;
+  auto row_of = [&](uint32_t c) { return (2ull * c + (c < j ? 1 : 0)) * kRows + r; };
+  // Weights of up to 32 parts at a time, a part a lane; their rows follow with
+  // four loads in flight.  The running maximum makes room for any number.
+  float top = -INFINITY, sum = 0.f;
+  float2 acc[DP / 64];
 #pragma unroll
-    for (uint32_t e = 0; e < DP / 64; ++e) acc[e] = make_float2(0.f, 0.f);
-    for (uint32_t c = j - 1; c <= last; ++c) {
-      const float2 ml = t.ml_part[row_of(c)];
-      const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : tc::ex2(ml.x - top);
-      sum += w * ml.y;
+  for (uint32_t e = 0; e < DP / 64; ++e) acc[e] = make_float2(0.f, 0.f);
+  for (uint32_t c0 = j - 1; c0 <= last; c0 += 32) {
+    const uint32_t n = last - c0 + 1 < 32 ? last - c0 + 1 : 32;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) ml = t.ml_part[row_of(c0 + lane)];
+    float m = ml.x;
 #pragma unroll
-      for (uint32_t e = 0; e < DP / 64; ++e) {
-        const float2 o = *reinterpret_cast<const float2*>(t.o_part + row_of(c) * DP + e * 64 + lane * 2);
-        if (w != 0.f) acc[e].x += w * o.x, acc[e].y += w * o.y;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    m = fmaxf(m, top);
+    const float was = top == -INFINITY ? (sum == 0.f ? 0.f : 1.f) : tc::ex2(top - m);
+    top = m;
+    const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : tc::ex2(ml.x - top);
+    float s = w * ml.y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    sum = was * sum + s;
+#pragma unroll
+    for (uint32_t e = 0; e < DP / 64; ++e) acc[e].x *= was, acc[e].y *= was;
+    for (uint32_t c = 0; c < n; c += 4) {
+      float2 o[4][DP / 64];
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u)
+#pragma unroll
+        for (uint32_t e = 0; e < DP / 64; ++e)
+          o[u][e] = c + u < n ? *reinterpret_cast<const float2*>(t.o_part + row_of(c0 + c + u) * DP + e * 64 + lane * 2)
+                              : make_float2(0.f, 0.f);
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u) {
+        const float wc = __shfl_sync(0xFFFFFFFFu, w, c + u);
+#pragma unroll
+        for (uint32_t e = 0; e < DP / 64; ++e)
+          if (wc != 0.f) acc[e].x += wc * o[u][e].x, acc[e].y += wc * o[u][e].y;
       }
     }
-    const uint64_t orow = (static_cast<uint64_t>(b) * a.T + tok) * a.kv_heads * a.group + h * a.group + head;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (uint32_t e = 0; e < DP / 64; ++e) {
-      const uint32_t d = e * 64 + lane * 2;
-      if (d < a.dim)
-        *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) =
-            tc::pack2<F16>(acc[e].x * inv, acc[e].y * inv);
-    }
-    if (lane == 0 && a.lse) a.lse[orow] = (top + log2f(sum)) * 0.6931471805599453f;
   }
+  const uint64_t orow = (static_cast<uint64_t>(b) * a.T + tok) * a.kv_heads * a.group + h * a.group + head;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (uint32_t e = 0; e < DP / 64; ++e) {
+    const uint32_t d = e * 64 + lane * 2;
+    if (d < a.dim)
+      *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) =
+          tc::pack2<F16>(acc[e].x * inv, acc[e].y * inv);
+  }
+  if (lane == 0 && a.lse) a.lse[orow] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 static size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// More rows than the few-row kernel holds at once, and heads that fit TMEM.
-static bool tc_shape(uint64_t rows, uint32_t dim) { return rows > 16 && dim <= 128; }
+// Heads that fit TMEM beside the scores.
+static bool tc_shape(uint32_t dim) { return dim <= 128; }
 static uint32_t tc_dim(uint32_t dim) { return dim <= 64 ? 64 : 128; }
 static uint32_t tc_tiles(uint64_t rows) { return rows > kTcTile ? 2 : 1; }
 
 size_t kv_tree_workspace(uint64_t rows, uint32_t dim, int device) {
-  if (!tc_shape(rows, dim)) return 0;
+  if (!tc_shape(dim)) return 0;
   const size_t n = sm_count(device), per = tc_tiles(rows) * kTcTile;
   return align256((n + 1) * sizeof(int4)) + align256(2 * n * per * sizeof(float2)) + 2 * n * per * tc_dim(dim) * 4;
 }
@@ -128,7 +150,13 @@ int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_
   // Boxes are whole 8-row swizzle groups of a page; the softmax takes the
   // maximum before it scales, so the scale has to be positive; and the device
   // reads pages by TMA, which takes device memory only.
-  if (!tc_shape(rows, a.dim) || a.page_tokens % 8 || !(a.scale_log2 > 0.f) || a.max_pages == 0) return IBP_OK;
+  if (!tc_shape(a.dim) || a.page_tokens % 8 || !(a.scale_log2 > 0.f) || a.max_pages == 0) return IBP_OK;
+  // Little work is done sooner by the few-row kernel, which has less to set up:
+  // counted in 16-row x 128-token pieces, below two to a SM.  Measured (us, few-row /
+  // this): 40 tiles of 4 rows 7.0 / 16, of 64 rows 11 / 18, of 128 rows 22 / 19; 256
+  // tiles of 16 rows 16 / 18, of 32 rows 23 / 18; 1024 of 16 rows 28 / 22, of 128 79 / 26.
+  const uint64_t sms = sm_count(device), longest = (static_cast<uint64_t>(a.max_pages) * a.page_tokens + kTcTile - 1) / kTcTile;
+  if (longest * a.n_seqs * a.kv_heads * ((rows + 15) / 16) < 2 * sms) return IBP_OK;
   uint32_t box = 8;
   while (box < kTcTile && a.page_tokens % (2 * box) == 0) box *= 2;
   CUtensorMap mk, mv;
@@ -143,9 +171,8 @@ int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_
   t.row_pairs = static_cast<uint32_t>((rows + mt * kTcTile - 1) / (mt * kTcTile));
   t.q16 = ((reinterpret_cast<uintptr_t>(a.q) | static_cast<uint64_t>(a.q_seq) | static_cast<uint64_t>(a.q_token) |
             static_cast<uint64_t>(a.q_head)) & 15u) == 0;
-  const uint64_t longest = (static_cast<uint64_t>(a.max_pages) * a.page_tokens + kTcTile - 1) / kTcTile;
   const uint64_t tiles = longest * a.n_seqs * a.kv_heads * t.row_pairs;
-  const uint64_t want = (tiles + kTcMinTiles - 1) / kTcMinTiles, sms = sm_count(device);
+  const uint64_t want = (tiles + kTcMinTiles - 1) / kTcMinTiles;
   const uint64_t n = sms;
   uint64_t ctas = want < sms ? want : sms;
   if (ctas > t.row_pairs) ctas -= ctas % t.row_pairs;
