@@ -674,6 +674,23 @@ static uint32_t padded_dim(uint32_t dim) { return dim <= 64 ? 64 : (dim <= 128 ?
 // 16 rows a CTA where there are more than 8 and the registers allow it.
 static uint32_t tile_rows(uint64_t rows, uint32_t dp) { return rows > 8 && dp < 256 ? 16 : 8; }
 
+// Splits of an item: as many CTAs as the GPU holds at once, by powers of two up
+// to a cluster of eight, which joins in place, and down to two steps a warp.
+// Lengths are on the device, so the longest possible counts.  One round of CTAs
+// beats two: 256 items of 4096 tokens took 113 us unsplit, 126 us in quarters; 64
+// items 52, 45 and 49 us in 2, 4 and 8.  Only a handful of long items is split
+// further, with a second kernel for the join.
+static uint32_t splits_of(uint64_t items, uint64_t tokens, uint64_t resident) {
+  uint64_t s = 1;
+  while (s < 8 && 2 * s * items <= resident && tokens >= 2 * s * kLeast) s *= 2;
+  if (s == 8 && 4 * s * items <= resident && tokens >= 32 * s * kLeast) {
+    const uint64_t most = tokens / (8 * kLeast);
+    s = resident / items < most ? resident / items : most;
+    if (s * items > kMaxUnits) s = kMaxUnits / items;
+  }
+  return static_cast<uint32_t>(s);
+}
+
 // items: (sequence[, query], kv head) triples; rows of each.
 size_t kv_attend_workspace(uint64_t items, uint64_t rows, uint32_t dim) {
   const uint32_t dp = padded_dim(dim), tr = tile_rows(rows, dp);
@@ -717,24 +734,12 @@ static int launch_attend(AttendArgs& a, int device, size_t ws_bytes, cudaStream_
   a.cluster = 0;
   if (PICK && items >= 2 * resident * kAtWarps)
     return launch_items<DP, NT, F16, PICK, PICK ? 1 : kAtWarps>(a, tiles, items, device, stream);
-  // Items are split so that about two rounds of CTAs fill the GPU, down to two
-  // steps a warp; lengths are on the device, so the longest possible counts.  Up
-  // to eight splits are a cluster and join in place; more write their parts for
-  // a second kernel.
-  const uint64_t pages = PICK && a.budget < a.max_pages ? a.budget : a.max_pages;
-  const uint64_t most = pages * a.page_tokens / kLeast;
-  const uint64_t target = 2 * resident < kMaxUnits ? 2 * resident : kMaxUnits;
-  uint64_t splits = items >= target ? 1 : (target + items - 1) / items;
-  splits = splits < most ? splits : most;
-  if (splits < 1) splits = 1;
-  if (splits > 1 && splits <= 8) {
-    a.cluster = 1;
-    while (splits & (splits - 1)) ++splits;  // 2, 4 or 8
-  }
-  a.splits = static_cast<uint32_t>(splits);
-  if (splits > 8 && ws_bytes < items * splits * A::kRows * (DP + 2) * 4) return IBP_EINVAL;
+  a.splits = splits_of(items, (PICK && a.budget < a.max_pages ? a.budget : a.max_pages) * static_cast<uint64_t>(a.page_tokens),
+                       resident);
+  a.cluster = a.splits > 1 && a.splits <= 8;
+  if (a.splits > 8 && ws_bytes < items * a.splits * A::kRows * (DP + 2) * 4) return IBP_EINVAL;
   const int rc = launch_items<DP, NT, F16, PICK, kAtWarps>(a, tiles, items, device, stream);
-  if (rc != IBP_OK || splits <= 8) return rc;
+  if (rc != IBP_OK || a.splits <= 8) return rc;
   const uint64_t warps = items * A::kRows;
   return kv_launch("k_kv_join", k_kv_join<DP, F16, PICK>, dim3(static_cast<unsigned>((warps + 3) / 4)), 128, 0, 1,
                    stream, a, tiles, A::kRows, rows);

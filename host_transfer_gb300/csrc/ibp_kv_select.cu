@@ -179,7 +179,6 @@ int launch_kv_summarize(const KvView& k, const int32_t* table, const int32_t* le
 // Scores
 
 constexpr int kScThreads = 256;
-constexpr uint32_t kScFly = 4;  // pages a lane group has in flight
 
 __device__ __forceinline__ int dp2a(uint32_t a16, uint32_t b8, int c, bool high) {
   int d;
@@ -201,11 +200,15 @@ __device__ __forceinline__ int32_t query_place(const SelectArgs& a, uint32_t b, 
 // CTA (sequence, block of NQ queries and share of the pages; kv head):
 // quantises its queries into shared memory, then scores its share of the pages.
 // LPP lanes hold a page's codes, 16 each (minima in the lower lanes, maxima in
-// the upper), four pages a lane group in flight, and the queries' 16 sums for the
+// the upper), four or eight pages a lane group in flight, and the queries' 16 sums for the
 // same dimensions stay in registers.  One query is summed over its lanes by a
 // butterfly; eight are by a halving exchange that leaves each lane one query's
 // total, 7 to 9 shuffles for the eight.  Single tokens are bound by the codes'
 // bytes and the latency of two dependent loads, chunks by dp2a issue.
+// pages a lane group has in flight
+template <int NQ>
+constexpr uint32_t kScFly = NQ == 1 ? 8 : 4;
+
 template <int NQ, int LPP>
 __global__ void __launch_bounds__(kScThreads) k_kv_score(const SelectArgs a, uint32_t q_blocks, uint32_t shares) {
   extern __shared__ uint32_t sq[];  // NQ x dim words of two 16-bit sums: min part, max part
@@ -229,6 +232,38 @@ __global__ void __launch_bounds__(kScThreads) k_kv_score(const SelectArgs a, uin
   __syncthreads();
   const uint32_t n_pages = most;
   if (n_pages == 0) return;
+  constexpr uint32_t kPer = 32 / LPP, kFly = kScFly<NQ>;  // pages a warp instruction, and in flight
+  const uint32_t sub = lane % LPP;
+  const bool on = sub * 8 < a.dim;  // lanes past a dimension that is no power of two idle
+  const bool wide = (reinterpret_cast<uintptr_t>(a.codes) & 15u) == 0;
+  const int32_t* row = a.table + static_cast<uint64_t>(b) * a.max_pages;
+  uint4 c[kFly];
+  float scale[kFly];
+  auto fetch = [&](uint32_t p0) {
+    uint32_t pg[kFly];
+#pragma unroll
+    for (uint32_t u = 0; u < kFly; ++u) {
+      const uint32_t p = p0 + u * kPer + lane / LPP;
+      pg[u] = p < n_pages ? static_cast<uint32_t>(row[p]) : 0u;
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < kFly; ++u) {
+      const uint32_t p = p0 + u * kPer + lane / LPP;
+      c[u] = make_uint4(0, 0, 0, 0);
+      scale[u] = 0.f;
+      if (p < n_pages && pg[u] < a.n_pages) {
+        const uint64_t at = static_cast<uint64_t>(pg[u]) * a.kv_heads + h;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(a.codes + at * 2 * a.dim) + sub * 4;
+        if (on) c[u] = wide ? *reinterpret_cast<const uint4*>(src) : make_uint4(src[0], src[1], src[2], src[3]);
+        scale[u] = a.scales[at];
+      } else if (p < n_pages && sub == 0) {
+        kv_status(a.status, IBP_ERANGE);
+      }
+    }
+  };
+  const uint32_t step = kScThreads / 32 * kPer * kFly * shares;
+  const uint32_t start = (share * (kScThreads / 32) + warp) * kPer * kFly;
+  if (start < n_pages) fetch(start);  // on their way while the queries are quantised
   const uint32_t nd = a.dim / 2;  // words of two elements
   for (uint32_t i = warp; i < NQ; i += kScThreads / 32) {
     const char* q = a.q + static_cast<int64_t>(b) * a.q_seq + static_cast<int64_t>(t0 + i) * a.q_token +
@@ -260,42 +295,15 @@ __global__ void __launch_bounds__(kScThreads) k_kv_score(const SelectArgs a, uin
     }
   }
   __syncthreads();
-  constexpr uint32_t kPer = 32 / LPP;  // pages a warp step
-  const uint32_t sub = lane % LPP;
-  const bool on = sub * 8 < a.dim;     // lanes past a dimension that is no power of two idle
   uint32_t qw[NQ][8];
 #pragma unroll
   for (int i = 0; i < NQ; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) qw[i][e] = on ? sq[i * a.dim + sub * 8 + e] : 0u;
-  const bool wide = (reinterpret_cast<uintptr_t>(a.codes) & 15u) == 0;
-  const int32_t* row = a.table + static_cast<uint64_t>(b) * a.max_pages;
-  const uint32_t step = kScThreads / 32 * kPer * kScFly * shares;
-  for (uint32_t p0 = (share * (kScThreads / 32) + warp) * kPer * kScFly; p0 < n_pages; p0 += step) {
-    uint4 c[kScFly];
-    float scale[kScFly];
-    uint32_t pg[kScFly];
+  for (uint32_t p0 = start; p0 < n_pages; p0 += step) {
+    if (p0 != start) fetch(p0);
 #pragma unroll
-    for (uint32_t u = 0; u < kScFly; ++u) {
-      const uint32_t p = p0 + u * kPer + lane / LPP;
-      pg[u] = p < n_pages ? static_cast<uint32_t>(row[p]) : 0u;
-    }
-#pragma unroll
-    for (uint32_t u = 0; u < kScFly; ++u) {
-      const uint32_t p = p0 + u * kPer + lane / LPP;
-      c[u] = make_uint4(0, 0, 0, 0);
-      scale[u] = 0.f;
-      if (p < n_pages && pg[u] < a.n_pages) {
-        const uint64_t at = static_cast<uint64_t>(pg[u]) * a.kv_heads + h;
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(a.codes + at * 2 * a.dim) + sub * 4;
-        if (on) c[u] = wide ? *reinterpret_cast<const uint4*>(src) : make_uint4(src[0], src[1], src[2], src[3]);
-        scale[u] = a.scales[at];
-      } else if (p < n_pages && sub == 0) {
-        kv_status(a.status, IBP_ERANGE);
-      }
-    }
-#pragma unroll
-    for (uint32_t u = 0; u < kScFly; ++u) {
+    for (uint32_t u = 0; u < kFly; ++u) {
       const uint32_t p = p0 + u * kPer + lane / LPP;
       int s[NQ];
 #pragma unroll
@@ -485,10 +493,10 @@ static int launch_score(const SelectArgs& a, int device, cudaStream_t stream) {
   uint32_t lpp = 1;
   while (lpp * 8 < a.dim) lpp <<= 1;
   // Shares of at least one step, until one round of CTAs fills the GPU.
-  const uint32_t per_cta = kScThreads / 32 * (32 / lpp) * kScFly;
+  const uint32_t per_cta = kScThreads / 32 * (32 / lpp) * kScFly<NQ>;
   const uint64_t want = (a.max_pages + per_cta - 1) / per_cta;
   const uint64_t rows = static_cast<uint64_t>(a.kv_heads) * a.n_seqs * q_blocks;
-  const uint64_t cap = (6ull * sm_count(device) + rows - 1) / rows;
+  const uint64_t cap = ((NQ == 1 ? 8ull : 6ull) * sm_count(device) + rows - 1) / rows;
   const uint32_t shares = static_cast<uint32_t>(want < cap ? want : cap);
   const dim3 grid(a.n_seqs * q_blocks * shares, a.kv_heads);
   auto go = [&](auto kern) {
