@@ -210,10 +210,11 @@ template <int NQ>
 constexpr uint32_t kScFly = NQ == 1 ? 8 : 4;
 
 template <int NQ, int LPP>
-__global__ void __launch_bounds__(kScThreads) k_kv_score(const SelectArgs a, uint32_t q_blocks, uint32_t shares) {
+__global__ void __launch_bounds__(kScThreads, NQ == 1 ? 4 : 2) k_kv_score(const SelectArgs a, uint32_t q_blocks, uint32_t shares) {
   extern __shared__ uint32_t sq[];  // NQ x dim words of two 16-bit sums: min part, max part
   __shared__ int32_t place[NQ];
   __shared__ uint32_t most;
+  __shared__ float tops[kScThreads / 32];
   pdl_begin();
   const uint32_t h = blockIdx.y, share = blockIdx.x % shares, bq = blockIdx.x / shares;
   const uint32_t b = bq / q_blocks, t0 = bq % q_blocks * NQ;
@@ -265,25 +266,37 @@ __global__ void __launch_bounds__(kScThreads) k_kv_score(const SelectArgs a, uin
   const uint32_t start = (share * (kScThreads / 32) + warp) * kPer * kFly;
   if (start < n_pages) fetch(start);  // on their way while the queries are quantised
   const uint32_t nd = a.dim / 2;  // words of two elements
-  for (uint32_t i = warp; i < NQ; i += kScThreads / 32) {
+  // kTeam threads a query: its largest element, then the sums of its codes.
+  constexpr uint32_t kTeam = kScThreads / NQ;
+  {
+    const uint32_t i = threadIdx.x / kTeam, me = threadIdx.x % kTeam, words = a.group * nd;
     const char* q = a.q + static_cast<int64_t>(b) * a.q_seq + static_cast<int64_t>(t0 + i) * a.q_token +
                     static_cast<int64_t>(h) * a.group * a.q_head;
+    const bool is = place[i] >= 0;
     float amax = 0.f;
-    bool bad = place[i] < 0;
-    if (!bad)
-      for (uint32_t g = 0; g < a.group; ++g)
-        for (uint32_t w = lane; w < nd; w += 32) {
-          const float2 v = pair_f32(*reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(g) * a.q_head + 4 * w), a.f16);
-          bad = bad || !finite_f(v.x) || !finite_f(v.y);
-          amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
-        }
-    bad = __any_sync(0xFFFFFFFFu, bad);
+    bool bad = false;
+    if (is)
+#pragma unroll 4
+      for (uint32_t x = me; x < words; x += kTeam) {
+        const uint32_t g = x / nd;
+        const float2 v = pair_f32(*reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(g) * a.q_head + 4 * (x - g * nd)), a.f16);
+        bad = bad || !finite_f(v.x) || !finite_f(v.y);
+        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+      }
+    if (bad) amax = __int_as_float(0x7F800000);
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    const float inv = !bad && amax >= kTiny ? code_factor(amax) : 0.f;
-    for (uint32_t w = lane; w < nd; w += 32) {
+    if (kTeam > 32) {
+      if (lane == 0) tops[warp] = amax;
+      __syncthreads();
+#pragma unroll
+      for (uint32_t w = 0; w < kScThreads / 32; ++w) amax = fmaxf(amax, tops[w]);
+    }
+    const float inv = finite_f(amax) && amax >= kTiny ? code_factor(amax) : 0.f;
+    for (uint32_t w = me; w < nd; w += kTeam) {
       int lx = 0, ly = 0, hx = 0, hy = 0;
       if (inv != 0.f)
+#pragma unroll 4
         for (uint32_t g = 0; g < a.group; ++g) {
           const float2 v = pair_f32(*reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(g) * a.q_head + 4 * w), a.f16);
           const int x = max(-127, min(127, __float2int_rn(__fmul_rn(v.x, inv))));
@@ -492,12 +505,12 @@ static int launch_score(const SelectArgs& a, int device, cudaStream_t stream) {
   const uint32_t q_blocks = (a.T + NQ - 1) / NQ;
   uint32_t lpp = 1;
   while (lpp * 8 < a.dim) lpp <<= 1;
-  // Shares of at least one step, until one round of CTAs fills the GPU.
+  // Shares of at least one step, as many as the GPU holds at once.
   const uint32_t per_cta = kScThreads / 32 * (32 / lpp) * kScFly<NQ>;
   const uint64_t want = (a.max_pages + per_cta - 1) / per_cta;
   const uint64_t rows = static_cast<uint64_t>(a.kv_heads) * a.n_seqs * q_blocks;
-  const uint64_t cap = ((NQ == 1 ? 8ull : 6ull) * sm_count(device) + rows - 1) / rows;
-  const uint32_t shares = static_cast<uint32_t>(want < cap ? want : cap);
+  const uint64_t cap = (NQ == 1 ? 4ull : 2ull) * sm_count(device) / rows;
+  const uint32_t shares = static_cast<uint32_t>(cap < 1 ? 1 : (want < cap ? want : cap));
   const dim3 grid(a.n_seqs * q_blocks * shares, a.kv_heads);
   auto go = [&](auto kern) {
     return kv_launch("k_kv_score", kern, grid, kScThreads, NQ * a.dim * 4, 1, stream, a, q_blocks, shares);
@@ -520,10 +533,13 @@ int launch_kv_select(const SelectArgs& a, int device, cudaStream_t stream) {
   if (rc != IBP_OK) return rc;
   const uint32_t cap = a.max_pages < kSelShared ? a.max_pages : kSelShared;
   const dim3 grid(a.n_seqs * a.T * a.kv_heads);
-  // A wide CTA shortens the passes over many pages; with more rows than the GPU
-  // holds such CTAs, narrow ones finish sooner.
-  if (a.max_pages > 512 && grid.x <= 4u * sm_count(device))
+  // A wide CTA shortens the passes over many pages.  Rows by the thousand finish
+  // sooner a warp each, without barriers between warps.
+  const uint32_t sms = sm_count(device);
+  if (a.max_pages > 512 && grid.x <= 4 * sms)
     return kv_launch("k_kv_select", k_kv_select<512>, grid, 512, 4ull * cap, 1, stream, a, cap);
+  if (a.max_pages <= 1024 && grid.x >= 16 * sms)
+    return kv_launch("k_kv_select", k_kv_select<32>, grid, 32, 4ull * cap, 1, stream, a, cap);
   return kv_launch("k_kv_select", k_kv_select<128>, grid, 128, 4ull * cap, 1, stream, a, cap);
 }
 
