@@ -271,7 +271,7 @@ int ibp_kv_accept(const ibp_kv_pages* pages, const ibp_kv_seqs* seqs, const int3
   if (!resolve(n_draft, device) || !resolve(path, device, max_accept == 0) || !resolve(n_accept, device) ||
       !resolve(m.table_out, device, !m.max_pages) || !resolve(m.lens_out, device))
     return refuse("a pointer is NULL or not device-accessible");
-  return launch_kv_accept(r, m, n_draft, path, n_accept, max_accept, static_cast<cudaStream_t>(stream));
+  return launch_kv_accept(r, m, n_draft, path, n_accept, max_accept, device, static_cast<cudaStream_t>(stream));
 }
 
 size_t ibp_tree_attention_workspace(uint32_t n_seqs, uint32_t T, uint32_t q_heads, uint32_t kv_heads, uint32_t dim) {

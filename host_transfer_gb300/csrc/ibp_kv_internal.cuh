@@ -90,7 +90,7 @@ int launch_kv_compact(const KvMeta& m, cudaStream_t stream);
 int launch_kv_copy(const KvRuns& r, const int32_t* moves, const int32_t* count, uint32_t max_moves,
                    uint32_t* status, int device, cudaStream_t stream);
 int launch_kv_accept(const KvRuns& r, const KvMeta& m, const int32_t* n_draft, const int32_t* path,
-                     const int32_t* n_accept, uint32_t max_accept, cudaStream_t stream);
+                     const int32_t* n_accept, uint32_t max_accept, int device, cudaStream_t stream);
 
 struct KvView {  // K or V pages of one layer; strides in bytes
   const char* data;

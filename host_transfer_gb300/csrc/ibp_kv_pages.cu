@@ -2,10 +2,10 @@
 // key/value cache, and keeping the accepted tokens of a draft.
 //
 // Bookkeeping (tables, lengths, reference counts) is a few kilobytes to a few
-// megabytes of integers: each call is one cluster of eight CTAs, whose phases
-// are separated by cluster barriers instead of launches.  It is bound by the
-// latency of its four or five dependent phases (a few microseconds), not by
-// bytes.  The copies that follow from it move gigabytes and fill the GPU: they
+// megabytes of integers: each call is one CTA, or one cluster of eight for the
+// larger ones, whose phases are separated by barriers instead of launches.  It is
+// bound by the latency of its four or five dependent phases (a few
+// microseconds), not by bytes.  The copies that follow from it move gigabytes and fill the GPU: they
 // are a kernel of their own, driven by a list in device memory, so nothing
 // returns to the host in between.
 #include <cuda_runtime.h>
@@ -14,8 +14,9 @@
 
 namespace ibp {
 
-constexpr uint32_t kCl = 8;       // CTAs of a bookkeeping cluster (the portable size)
-constexpr uint32_t kMt = 512;     // threads of each
+constexpr uint32_t kClusterMax = 8;  // CTAs of a bookkeeping cluster (the portable size)
+constexpr uint32_t kMt = 512;        // threads of each
+constexpr uint64_t kOneCta = 16384;  // integers that one CTA handles by itself
 
 __device__ __forceinline__ uint32_t cl_rank() {
   uint32_t r;
@@ -25,13 +26,20 @@ __device__ __forceinline__ uint32_t cl_rank() {
 
 // All threads of the cluster; global and shared writes before it are visible
 // to the cluster after it.
+template <uint32_t kCl>
 __device__ __forceinline__ void cl_sync() {
+  if (kCl == 1) {
+    __syncthreads();
+    return;
+  }
   __threadfence();
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // *p of CTA `rank` of the cluster, p in shared memory.
+template <uint32_t kCl>
 __device__ __forceinline__ uint32_t cl_read(const uint32_t* p, uint32_t rank) {
+  if (kCl == 1) return *p;
   uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), v;
   asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(rank));
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -57,6 +65,7 @@ __device__ uint32_t block_rank(bool flag, uint32_t* warp_sums, uint32_t* total) 
 }
 
 // Pages [lo, hi) of this CTA's share of n, ascending with the rank.
+template <uint32_t kCl>
 __device__ __forceinline__ void slice(uint32_t n, uint32_t rank, uint32_t* lo, uint32_t* hi) {
   const uint32_t per = ceil_div(n, kCl);
   const uint64_t a = static_cast<uint64_t>(per) * rank;
@@ -72,6 +81,7 @@ struct MetaShared {
 };
 
 // Copies what the outputs start from; nothing to do where they are the inputs.
+template <uint32_t kCl>
 __device__ void carry(int32_t* out, const int32_t* in, uint64_t n, uint32_t gt) {
   if (out == in) return;
   for (uint64_t i = gt; i < n; i += kCl * kMt) out[i] = in[i];
@@ -80,18 +90,19 @@ __device__ void carry(int32_t* out, const int32_t* in, uint64_t n, uint32_t gt) 
 // ws: owner[n_pages] (lowest result row whose last, partly filled page it is),
 // wants[n_out] (1: the row wants a copy), list[n_out] (rows that want one, in
 // order), n_want.
+template <uint32_t kCl>
 __global__ void __launch_bounds__(kMt) k_kv_fork(const KvMeta m, const int32_t* __restrict__ parents,
                                                  uint32_t n_out) {
   __shared__ MetaShared sh;
   pdl_begin();
-  const uint32_t rank = cl_rank(), t = threadIdx.x, gt = rank * kMt + t, lane = t & 31u;
+  const uint32_t rank = kCl == 1 ? 0 : cl_rank(), t = threadIdx.x, gt = rank * kMt + t, lane = t & 31u;
   const uint32_t gw = gt >> 5, n_warps = kCl * kMt / 32, P = m.max_pages;
   int32_t *owner = m.ws, *wants = owner + m.n_pages, *list = wants + n_out, *n_want = list + n_out;
 
-  carry(m.refs_out, m.refs, m.n_pages, gt);
+  carry<kCl>(m.refs_out, m.refs, m.n_pages, gt);
   for (uint32_t i = gt; i < m.n_pages; i += kCl * kMt) owner[i] = 0x7FFFFFFF;
   for (uint64_t i = gt; i < 3ull * n_out; i += kCl * kMt) m.moves[i] = -1;
-  cl_sync();
+  cl_sync<kCl>();
 
   // The present rows give up their references; each last page finds its owner.
   for (uint32_t r = gw; r < m.n_seqs; r += n_warps) {
@@ -119,7 +130,7 @@ __global__ void __launch_bounds__(kMt) k_kv_fork(const KvMeta m, const int32_t* 
     const uint32_t pg = static_cast<uint32_t>(m.table[static_cast<uint64_t>(par) * P + len / m.page_tokens]);
     if (pg < m.n_pages) atomicMin(&owner[pg], static_cast<int32_t>(i));
   }
-  cl_sync();
+  cl_sync<kCl>();
 
   // The result rows take theirs.
   for (uint32_t i = gw; i < n_out; i += n_warps) {
@@ -148,11 +159,11 @@ __global__ void __launch_bounds__(kMt) k_kv_fork(const KvMeta m, const int32_t* 
       wants[i] = want;
     }
   }
-  cl_sync();
+  cl_sync<kCl>();
 
   // Free pages of each CTA's share; the rows that want one, in order.
   uint32_t lo, hi;
-  slice(m.n_pages, rank, &lo, &hi);
+  slice<kCl>(m.n_pages, rank, &lo, &hi);
   uint32_t mine = 0, total;
   for (uint32_t a = lo; a < hi; a += kMt) {
     block_rank(a + t < hi && ld_cg(&m.refs_out[a + t < hi ? a + t : lo]) == 0, sh.sums, &total);
@@ -169,12 +180,12 @@ __global__ void __launch_bounds__(kMt) k_kv_fork(const KvMeta m, const int32_t* 
     }
     if (t == 0) *n_want = static_cast<int32_t>(n);
   }
-  cl_sync();
+  cl_sync<kCl>();
 
   // The r-th free page goes to the r-th of them.
   uint32_t base = 0, n_free = 0;
   for (uint32_t c = 0; c < kCl; ++c) {
-    const uint32_t v = cl_read(&sh.count, c);
+    const uint32_t v = cl_read<kCl>(&sh.count, c);
     base += c < rank ? v : 0;
     n_free += v;
   }
@@ -203,17 +214,18 @@ __global__ void __launch_bounds__(kMt) k_kv_fork(const KvMeta m, const int32_t* 
     }
     if (t == 0) *m.count = static_cast<int32_t>(want_n < n_free ? want_n : n_free);
   }
-  cl_sync();  // no CTA leaves while another reads its shared memory
+  cl_sync<kCl>();  // no CTA leaves while another reads its shared memory
 }
 
+template <uint32_t kCl>
 __global__ void __launch_bounds__(kMt) k_kv_free(const KvMeta m, const int32_t* __restrict__ rows, uint32_t n_rows) {
   pdl_begin();
-  const uint32_t t = threadIdx.x, gt = cl_rank() * kMt + t, lane = t & 31u;
+  const uint32_t t = threadIdx.x, gt = (kCl == 1 ? 0 : cl_rank()) * kMt + t, lane = t & 31u;
   const uint32_t gw = gt >> 5, n_warps = kCl * kMt / 32, P = m.max_pages;
-  carry(m.refs_out, m.refs, m.n_pages, gt);
-  carry(m.lens_out, m.lens, m.n_seqs, gt);
-  carry(m.table_out, m.table, static_cast<uint64_t>(m.n_seqs) * P, gt);
-  cl_sync();
+  carry<kCl>(m.refs_out, m.refs, m.n_pages, gt);
+  carry<kCl>(m.lens_out, m.lens, m.n_seqs, gt);
+  carry<kCl>(m.table_out, m.table, static_cast<uint64_t>(m.n_seqs) * P, gt);
+  cl_sync<kCl>();
   for (uint32_t i = gw; i < n_rows; i += n_warps) {
     const uint32_t s = static_cast<uint32_t>(rows[i]);
     if (s >= m.n_seqs) {
@@ -244,13 +256,14 @@ __global__ void __launch_bounds__(kMt) k_kv_free(const KvMeta m, const int32_t* 
 
 // ws: to[n_pages] (new place of each page), from[n_pages] and into[n_pages]
 // (moving pages and holes, in order).
+template <uint32_t kCl>
 __global__ void __launch_bounds__(kMt) k_kv_compact(const KvMeta m) {
   __shared__ MetaShared sh;
   pdl_begin();
-  const uint32_t rank = cl_rank(), t = threadIdx.x, gt = rank * kMt + t;
+  const uint32_t rank = kCl == 1 ? 0 : cl_rank(), t = threadIdx.x, gt = rank * kMt + t;
   int32_t *to = m.ws, *from = to + m.n_pages, *into = from + m.n_pages;
   uint32_t lo, hi, total;
-  slice(m.n_pages, rank, &lo, &hi);
+  slice<kCl>(m.n_pages, rank, &lo, &hi);
 
   uint32_t mine = 0;
   for (uint32_t a = lo; a < hi; a += kMt) {
@@ -259,10 +272,10 @@ __global__ void __launch_bounds__(kMt) k_kv_compact(const KvMeta m) {
   }
   if (t == 0) sh.count = mine;
   for (uint64_t i = gt; i < 3ull * m.n_pages; i += kCl * kMt) m.moves[i] = -1;
-  cl_sync();
+  cl_sync<kCl>();
   uint32_t base = 0, n_live = 0;
   for (uint32_t c = 0; c < kCl; ++c) {
-    const uint32_t v = cl_read(&sh.count, c);
+    const uint32_t v = cl_read<kCl>(&sh.count, c);
     base += c < rank ? v : 0;
     n_live += v;
   }
@@ -279,10 +292,10 @@ __global__ void __launch_bounds__(kMt) k_kv_compact(const KvMeta m) {
     above += total;
   }
   if (t == 0) sh.count2 = above;
-  cl_sync();
+  cl_sync<kCl>();
   uint32_t mbase = 0, n_moves = 0;
   for (uint32_t c = 0; c < kCl; ++c) {
-    const uint32_t v = cl_read(&sh.count2, c);
+    const uint32_t v = cl_read<kCl>(&sh.count2, c);
     mbase += c < rank ? v : 0;
     n_moves += v;
   }
@@ -295,7 +308,7 @@ __global__ void __launch_bounds__(kMt) k_kv_compact(const KvMeta m) {
     if (mv) from[at] = static_cast<int32_t>(pg);
     mbase += total;
   }
-  cl_sync();
+  cl_sync<kCl>();
   for (uint32_t i = gt; i < n_moves; i += kCl * kMt) {
     m.moves[3ull * i] = ld_cg(&from[i]);
     m.moves[3ull * i + 1] = ld_cg(&into[i]);
@@ -326,7 +339,7 @@ __global__ void __launch_bounds__(kMt) k_kv_compact(const KvMeta m) {
     }
     m.table_out[i] = w;
   }
-  cl_sync();
+  cl_sync<kCl>();
 }
 
 // ---------------------------------------------------------------------------
@@ -334,6 +347,7 @@ __global__ void __launch_bounds__(kMt) k_kv_compact(const KvMeta m) {
 
 constexpr int kCpThreads = 256;
 constexpr uint32_t kCpFly = 8;  // accesses a thread has in flight
+constexpr uint32_t kAcFly = 4;  // the same where accepted tokens move: paths are short, threads many
 
 // A run (one head's tokens of a page, or all heads' where they are
 // contiguous) is copied in pieces of 8 accesses per lane by one warp; every
@@ -414,14 +428,14 @@ __device__ uint32_t valid_path(const int32_t* path, int32_t n_accept, uint32_t m
   return n;
 }
 
-// One CTA column of a sequence moves the rows of its accepted tokens.  A
-// thread owns one access-wide column of one run in one pool and takes eight
-// tokens at a time: it loads them all before it stores any.  Sources ascend and
+// The CTAs of a sequence move the rows of its accepted tokens.  A thread takes
+// one access-wide column of one run in one pool after another, four
+// tokens of it at a time: it loads them all before it stores any.  Sources ascend and
 // never lie below their targets, so a row is always read before it is
 // overwritten, and only by the thread that overwrites it.  Bound by the latency
 // of two dependent accesses for short paths, by DRAM sectors for long ones.
 template <typename V>
-__global__ void __launch_bounds__(kCpThreads) k_kv_accept_move(const KvRuns r, const KvMeta m,
+__global__ void __launch_bounds__(kCpThreads, 6) k_kv_accept_move(const KvRuns r, const KvMeta m,
                                                                const int32_t* __restrict__ n_draft,
                                                                const int32_t* __restrict__ path,
                                                                const int32_t* __restrict__ n_accept,
@@ -442,11 +456,7 @@ __global__ void __launch_bounds__(kCpThreads) k_kv_accept_move(const KvRuns r, c
   __syncthreads();
   const uint32_t n = n_sh;
   const uint32_t cols = r.row_bytes / sizeof(V);
-  const uint64_t x = static_cast<uint64_t>(blockIdx.x) * kCpThreads + t;
-  const uint32_t col = static_cast<uint32_t>(x % cols), o = static_cast<uint32_t>(x / cols % r.outer);
-  const uint64_t pool = x / cols / r.outer;
-  char* base = r.data + static_cast<int64_t>(pool) * r.pool_stride + static_cast<int64_t>(o) * r.outer_stride +
-               static_cast<int64_t>(col) * sizeof(V);
+  const uint64_t columns = r.n_pools * r.outer * cols;
   for (uint32_t a = 0; a < n; a += 32) {
     __syncthreads();
     if (t < 32 && a + t < n) {
@@ -460,28 +470,35 @@ __global__ void __launch_bounds__(kCpThreads) k_kv_accept_move(const KvRuns r, c
       into[t] = qs * r.page_stride + static_cast<int64_t>(q % m.page_tokens) * r.row_stride;
     }
     __syncthreads();
-    if (pool >= r.n_pools) continue;
     const uint32_t e = n - a < 32 ? n - a : 32;
-    for (uint32_t j = 0; j < e; j += kCpFly) {
-      V v[kCpFly];
+    for (uint64_t x = static_cast<uint64_t>(blockIdx.x) * kCpThreads + t; x < columns;
+         x += static_cast<uint64_t>(gridDim.x) * kCpThreads) {
+      const uint64_t y = x / cols;
+      const uint32_t col = static_cast<uint32_t>(x - y * cols), o = static_cast<uint32_t>(y % r.outer);
+      char* base = r.data + static_cast<int64_t>(y / r.outer) * r.pool_stride + static_cast<int64_t>(o) * r.outer_stride +
+                   static_cast<int64_t>(col) * sizeof(V);
+      for (uint32_t j = 0; j < e; j += kAcFly) {
+        V v[kAcFly];
 #pragma unroll
-      for (uint32_t i = 0; i < kCpFly; ++i)
-        if (j + i < e && from[j + i] >= 0) v[i] = *reinterpret_cast<const V*>(base + from[j + i]);
+        for (uint32_t i = 0; i < kAcFly; ++i)
+          if (j + i < e && from[j + i] >= 0) v[i] = *reinterpret_cast<const V*>(base + from[j + i]);
 #pragma unroll
-      for (uint32_t i = 0; i < kCpFly; ++i)
-        if (j + i < e && from[j + i] >= 0) *reinterpret_cast<V*>(base + into[j + i]) = v[i];
+        for (uint32_t i = 0; i < kAcFly; ++i)
+          if (j + i < e && from[j + i] >= 0) *reinterpret_cast<V*>(base + into[j + i]) = v[i];
+      }
     }
   }
 }
 
+template <uint32_t kCl>
 __global__ void __launch_bounds__(kMt) k_kv_accept_meta(const KvMeta m, const int32_t* __restrict__ n_draft,
                                                         const int32_t* __restrict__ path,
                                                         const int32_t* __restrict__ n_accept, uint32_t max_accept) {
   pdl_begin();
-  const uint32_t t = threadIdx.x, gt = cl_rank() * kMt + t, lane = t & 31u;
+  const uint32_t t = threadIdx.x, gt = (kCl == 1 ? 0 : cl_rank()) * kMt + t, lane = t & 31u;
   const uint32_t gw = gt >> 5, n_warps = kCl * kMt / 32, P = m.max_pages;
-  carry(m.refs_out, m.refs, m.n_pages, gt);
-  cl_sync();
+  carry<kCl>(m.refs_out, m.refs, m.n_pages, gt);
+  cl_sync<kCl>();
   for (uint32_t b = gw; b < m.n_seqs; b += n_warps) {
     const int32_t raw = m.lens[b], len = clamp_len(raw, m.page_tokens, P), nd = n_draft[b];
     bool bad;
@@ -512,16 +529,26 @@ __global__ void __launch_bounds__(kMt) k_kv_accept_meta(const KvMeta m, const in
 
 // ---------------------------------------------------------------------------
 
+// One CTA's barriers cost less than a cluster's; past some ten thousand integers
+// the work of one CTA costs more.
+static bool one_cta(const KvMeta& m, uint32_t n_out) {
+  return (static_cast<uint64_t>(m.n_seqs) + n_out) * m.max_pages + m.n_pages <= kOneCta;
+}
+
 int launch_kv_fork(const KvMeta& m, const int32_t* parents, uint32_t n_out, cudaStream_t stream) {
-  return kv_launch("k_kv_fork", k_kv_fork, dim3(kCl), kMt, 0, kCl, stream, m, parents, n_out);
+  if (one_cta(m, n_out))
+    return kv_launch("k_kv_fork", k_kv_fork<1>, dim3(1), kMt, 0, 1, stream, m, parents, n_out);
+  return kv_launch("k_kv_fork", k_kv_fork<kClusterMax>, dim3(kClusterMax), kMt, 0, kClusterMax, stream, m, parents, n_out);
 }
 
 int launch_kv_free(const KvMeta& m, const int32_t* rows, uint32_t n_rows, cudaStream_t stream) {
-  return kv_launch("k_kv_free", k_kv_free, dim3(kCl), kMt, 0, kCl, stream, m, rows, n_rows);
+  if (one_cta(m, n_rows)) return kv_launch("k_kv_free", k_kv_free<1>, dim3(1), kMt, 0, 1, stream, m, rows, n_rows);
+  return kv_launch("k_kv_free", k_kv_free<kClusterMax>, dim3(kClusterMax), kMt, 0, kClusterMax, stream, m, rows, n_rows);
 }
 
 int launch_kv_compact(const KvMeta& m, cudaStream_t stream) {
-  return kv_launch("k_kv_compact", k_kv_compact, dim3(kCl), kMt, 0, kCl, stream, m);
+  if (one_cta(m, 0)) return kv_launch("k_kv_compact", k_kv_compact<1>, dim3(1), kMt, 0, 1, stream, m);
+  return kv_launch("k_kv_compact", k_kv_compact<kClusterMax>, dim3(kClusterMax), kMt, 0, kClusterMax, stream, m);
 }
 
 int launch_kv_copy(const KvRuns& r, const int32_t* moves, const int32_t* count, uint32_t max_moves,
@@ -544,9 +571,13 @@ int launch_kv_copy(const KvRuns& r, const int32_t* moves, const int32_t* count, 
 }
 
 int launch_kv_accept(const KvRuns& r, const KvMeta& m, const int32_t* n_draft, const int32_t* path,
-                     const int32_t* n_accept, uint32_t max_accept, cudaStream_t stream) {
-  const uint64_t cols = r.n_pools * r.outer * (r.row_bytes / r.vec);
-  const dim3 grid(static_cast<unsigned>((cols + kCpThreads - 1) / kCpThreads), m.n_seqs);
+                     const int32_t* n_accept, uint32_t max_accept, int device, cudaStream_t stream) {
+  // Three rounds of CTAs: the lookups that a CTA begins with are four dependent
+  // loads, so not many; but sequences keep from none to all of their draft, so more
+  // than one.
+  const uint64_t cols = r.n_pools * r.outer * (r.row_bytes / r.vec), want = (cols + kCpThreads - 1) / kCpThreads;
+  const uint64_t cap = (24ull * sm_count(device) + m.n_seqs - 1) / m.n_seqs;
+  const dim3 grid(static_cast<unsigned>(want < cap ? want : cap), m.n_seqs);
   int rc = IBP_OK;
   if (max_accept > 0) {
     auto go = [&](auto kern) {
@@ -562,8 +593,11 @@ int launch_kv_accept(const KvRuns& r, const KvMeta& m, const int32_t* n_draft, c
     }
   }
   if (rc != IBP_OK) return rc;
-  return kv_launch("k_kv_accept_meta", k_kv_accept_meta, dim3(kCl), kMt, 0, kCl, stream, m, n_draft, path, n_accept,
-                   max_accept);
+  if (one_cta(m, 0) && m.n_seqs <= kMt / 32)  // a warp a sequence
+    return kv_launch("k_kv_accept_meta", k_kv_accept_meta<1>, dim3(1), kMt, 0, 1, stream, m, n_draft, path, n_accept,
+                     max_accept);
+  return kv_launch("k_kv_accept_meta", k_kv_accept_meta<kClusterMax>, dim3(kClusterMax), kMt, 0, kClusterMax, stream, m,
+                   n_draft, path, n_accept, max_accept);
 }
 
 }  // namespace ibp

@@ -52,6 +52,7 @@ def shared_state(rng, n_seqs, page, longest, n_pages):
 @pytest.mark.parametrize("n_seqs,n_out,page,longest,n_pages", [
     (1, 1, 16, 40, 8), (1, 5, 16, 40, 8), (4, 4, 16, 0, 3), (3, 40, 1, 9, 40), (7, 64, 64, 500, 120),
     (30, 700, 24, 100, 900), (64, 2000, 16, 60, 5000), (5, 0, 16, 40, 20),
+    (64, 4000, 16, 60, 20000), (300, 300, 16, 900, 30000),  # a cluster of CTAs
 ])
 def test_fork(n_seqs, n_out, page, longest, n_pages):
     rng = np.random.default_rng(n_seqs * 1000 + n_out)
@@ -94,7 +95,8 @@ def test_fork_bad_rows_are_empty():
 
 
 @pytest.mark.parametrize("inplace", [False, True])
-@pytest.mark.parametrize("n_seqs,page,longest,n_pages", [(1, 16, 40, 8), (9, 64, 300, 60), (200, 16, 90, 3000)])
+@pytest.mark.parametrize("n_seqs,page,longest,n_pages", [(1, 16, 40, 8), (9, 64, 300, 60), (200, 16, 90, 3000),
+                                                      (500, 16, 700, 40000)])
 def test_free_and_compact(n_seqs, page, longest, n_pages, inplace):
     rng = np.random.default_rng(n_seqs)
     table, lens, refs = shared_state(rng, n_seqs, page, longest, n_pages)
@@ -110,11 +112,11 @@ def test_free_and_compact(n_seqs, page, longest, n_pages, inplace):
     assert moves_of(*g2[2:]) == w2[2]
 
 
+@pytest.mark.parametrize("n", [1, 1000, 100001])
 @pytest.mark.parametrize("live", ["none", "all", "last"])
-def test_compact_extremes(live):
-    n = 1000
-    refs = {"none": np.zeros(n), "all": np.ones(n), "last": np.eye(n)[n - 1] * 3}[live].astype(np.int32)
-    table = np.array([[n - 1, -1, 5]], np.int32)
+def test_compact_extremes(live, n):
+    refs = {"none": np.zeros(n), "all": np.ones(n), "last": (np.arange(n) == n - 1) * 3}[live].astype(np.int32)
+    table = np.array([[n - 1, -1, n // 2]], np.int32)
     w = kv_ref.compact(table, refs, 8)
     g = kv.ibp_kv_compact(dev(table), dev(refs), 8)
     assert np.array_equal(host(g[0]), w[0]) and np.array_equal(host(g[1]), w[1]) and moves_of(*g[2:]) == w[2]
@@ -182,6 +184,22 @@ def test_accept(pools, heads, page, dim, longest, draft, layout, inplace):
     x = pool((pools, len(refs), heads, page, dim), torch.float16, layout, gen(2))
     want = kv_ref.accept(host(x), table, lens, refs, n_draft, path, n_accept)
     got = kv.ibp_kv_accept(x, dev(table), dev(lens), dev(refs), dev(n_draft), dev(path), dev(n_accept), inplace=inplace)
+    assert np.array_equal(host(x), want[0])
+    assert all(np.array_equal(host(a), b) for a, b in zip(got, want[1:]))
+
+
+def test_accept_of_many_sequences():
+    rng = np.random.default_rng(5)
+    n, draft, page = 70, 20, 8
+    lens = rng.integers(draft, 60, n).astype(np.int32)
+    table, refs = tables(lens, page, 700, 8, rng)
+    n_draft, n_accept = np.full(n, draft, np.int32), rng.integers(0, draft + 1, n).astype(np.int32)
+    path = np.sort(np.argsort(rng.random((n, draft)), 1).astype(np.int32), 1)
+    for b in range(n):
+        path[b, : n_accept[b]] = np.sort(rng.permutation(draft)[: n_accept[b]])
+    x = pool((6, 700, 4, page, 64), torch.bfloat16, "nhd", gen(3))
+    want = kv_ref.accept(host(x), table, lens, refs, n_draft, path, n_accept)
+    got = kv.ibp_kv_accept(x, dev(table), dev(lens), dev(refs), dev(n_draft), dev(path), dev(n_accept))
     assert np.array_equal(host(x), want[0])
     assert all(np.array_equal(host(a), b) for a, b in zip(got, want[1:]))
 
