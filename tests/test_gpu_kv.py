@@ -613,3 +613,39 @@ def test_no_sequences():
     refs = dev(np.array([1, 0, 2, 0]))
     assert host(kv.ibp_kv_fork(none, lens, refs, lens, 16)[2]).tolist() == [1, 0, 2, 0]
     assert host(kv.ibp_kv_compact(none, refs, 16)[1]).tolist() == [1, 2, 0, 0]
+
+
+def test_the_example_runs_the_operators_together():
+    """examples/kv_serving.py: compressed host cache, pages, sparse step, beams, tree, acceptance, compaction."""
+    import importlib.util
+    import os
+
+    at = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "kv_serving.py")
+    spec = importlib.util.spec_from_file_location("kv_serving", at)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    from host_transfer_gb300 import workloads
+
+    seq, heads, page = 260, 2, 32
+    r = example.run(seq=seq, heads=heads, group=4, page=page, beams=3, budget=4)
+    a, b = r["first"], r["second"]
+    # the pages hold the prompt's keys bit for bit
+    for s, n in enumerate(host(a["lens"])):
+        words = workloads.llm_kv(s, heads=heads, seq=seq, head_dim=128)
+        for pages, w in zip((a["k"], a["v"]), words):
+            bits = pages.view(torch.int16).cpu().numpy().view(np.uint32)
+            for h in range(heads):
+                got = np.concatenate([bits[p, h] for p in host(a["table"])[s][: -(-n // page)]])[:n]
+                assert np.array_equal(got, w.reshape(heads, seq, 64)[h, :n])
+    want = kv_ref.sparse_attention(host(a["q"]), host(a["k"]), host(a["v"]), host(a["table"]), host(a["lens"]),
+                                   host(a["codes"]), host(a["scales"]), a["budget"], 1, 2)
+    assert np.array_equal(host(a["pages"]), want[2])
+    check_attention(a["out"], a["lse"], want[0], want[1], want[3], want[4], "bf16")
+    check_attention(b["out"], b["lse"], *kv_ref.tree_attention(host(b["q"]), host(b["k"]), host(b["v"]), host(b["table"]),
+                                                               host(b["lens"]), host(b["mask"])), "bf16")
+    # compaction moved pages, not what sequences hold
+    refs, table, lens = host(r["refs"]), host(r["table"]), host(r["lens"])
+    assert r["moved"] > 0 and (refs[: (refs > 0).sum()] > 0).all()
+    for s, n in enumerate(lens):
+        for p in range(-(-n // page)):
+            assert torch.equal(r["pool"][:, table[s, p]], r["before"]["pool"][:, int(r["before"]["table"][s, p])])
