@@ -274,13 +274,14 @@ int ibp_kv_accept(const ibp_kv_pages* pages, const ibp_kv_seqs* seqs, const int3
   return launch_kv_accept(r, m, n_draft, path, n_accept, max_accept, device, static_cast<cudaStream_t>(stream));
 }
 
-size_t ibp_tree_attention_workspace(uint32_t n_seqs, uint32_t T, uint32_t q_heads, uint32_t kv_heads, uint32_t dim) {
-  if (kv_heads == 0 || q_heads % kv_heads || dim == 0 || dim > IBP_KV_MAX_DIM) return 0;
-  const uint64_t rows = static_cast<uint64_t>(T) * (q_heads / kv_heads);
+size_t ibp_tree_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t page_tokens, uint32_t T,
+                                    uint32_t q_heads, uint32_t kv_heads, uint32_t dim) {
+  if (kv_heads == 0 || q_heads % kv_heads || dim == 0 || dim > IBP_KV_MAX_DIM || page_tokens == 0) return 0;
+  const uint64_t rows = static_cast<uint64_t>(T) * (q_heads / kv_heads), tokens = static_cast<uint64_t>(max_pages) * page_tokens;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) cudaGetLastError();
-  const size_t few = kv_attend_workspace(static_cast<uint64_t>(n_seqs) * kv_heads, rows, dim);
-  const size_t many = kv_tree_workspace(rows, dim, device);
+  const size_t few = kv_attend_workspace(static_cast<uint64_t>(n_seqs) * kv_heads, rows, dim, tokens, false, device);
+  const size_t many = kv_tree_workspace(n_seqs, kv_heads, rows, dim, page_tokens, tokens, device);
   return few > many ? few : many;
 }
 
@@ -299,7 +300,8 @@ int ibp_tree_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t dt
   if (rc) return rc;
   a.mask = mask;
   if (!resolve(a.mask, device, true)) return refuse("mask is not device-accessible");
-  if (ws_bytes < ibp_tree_attention_workspace(seqs->n_seqs, T, q_heads, k->heads, k->dim) || (ws_bytes && !ws))
+  const size_t need = ibp_tree_attention_workspace(seqs->n_seqs, seqs->max_pages, k->page_tokens, T, q_heads, k->heads, k->dim);
+  if (need && (ws_bytes < need || !ws))
     return refuse("ws is smaller than ibp_tree_attention_workspace");
   bool done = false;
   rc = launch_kv_tree(a, device, ws_bytes, static_cast<cudaStream_t>(stream), &done);
@@ -329,12 +331,15 @@ int ibp_kv_summarize(const ibp_kv_pages* k, uint32_t dtype, const ibp_kv_seqs* s
                              static_cast<cudaStream_t>(stream));
 }
 
-size_t ibp_sparse_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t T, uint32_t q_heads,
-                                      uint32_t kv_heads, uint32_t dim, uint32_t budget) {
+size_t ibp_sparse_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t page_tokens, uint32_t T,
+                                      uint32_t q_heads, uint32_t kv_heads, uint32_t dim, uint32_t budget) {
   if (kv_heads == 0 || q_heads % kv_heads || dim == 0 || dim > IBP_KV_MAX_DIM) return 0;
   const uint64_t rows = static_cast<uint64_t>(n_seqs) * T * kv_heads;
+  const uint64_t tokens = static_cast<uint64_t>(budget < max_pages ? budget : max_pages) * page_tokens;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) cudaGetLastError();
   const size_t scores = max_pages > budget ? align256(4 * rows * max_pages) : 0;
-  return scores + align256(4 * rows * budget) + kv_attend_workspace(rows, q_heads / kv_heads, dim);
+  return scores + align256(4 * rows * budget) + kv_attend_workspace(rows, q_heads / kv_heads, dim, tokens, true, device);
 }
 
 int ibp_sparse_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t dtype, const ibp_kv_seqs* seqs,
@@ -360,7 +365,8 @@ int ibp_sparse_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t 
   if (!resolve(codes, device) || !resolve(scales, device) || !resolve(pages_out, device, true))
     return refuse("a pointer is NULL or not device-accessible");
   if (reinterpret_cast<uintptr_t>(codes) % 4) return refuse("codes is not 4-byte aligned");
-  if (!ws || ws_bytes < ibp_sparse_attention_workspace(seqs->n_seqs, seqs->max_pages, T, q_heads, k->heads, k->dim, budget))
+  if (!ws || ws_bytes < ibp_sparse_attention_workspace(seqs->n_seqs, seqs->max_pages, k->page_tokens, T, q_heads,
+                                                        k->heads, k->dim, budget))
     return refuse("ws is smaller than ibp_sparse_attention_workspace");
   const uint64_t rows = static_cast<uint64_t>(seqs->n_seqs) * T * k->heads;
   const size_t scores = seqs->max_pages > budget ? align256(4 * rows * seqs->max_pages) : 0;

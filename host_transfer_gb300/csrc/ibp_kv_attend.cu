@@ -691,11 +691,19 @@ static uint32_t splits_of(uint64_t items, uint64_t tokens, uint64_t resident) {
   return static_cast<uint32_t>(s);
 }
 
-// items: (sequence[, query], kv head) triples; rows of each.
-size_t kv_attend_workspace(uint64_t items, uint64_t rows, uint32_t dim) {
+// CTAs that the GPU holds at once.
+static uint64_t resident_ctas(uint32_t dp, int device) {
+  const uint32_t bytes = dp == 64 ? Attend<64, 1, false, false>::kBytes
+                                  : (dp == 128 ? Attend<128, 1, false, false>::kBytes : Attend<256, 1, false, false>::kBytes);
+  return static_cast<uint64_t>(sm_count(device)) * (232448 / (bytes + 1024));
+}
+
+size_t kv_attend_workspace(uint64_t items, uint64_t rows, uint32_t dim, uint64_t tokens, bool pick, int device) {
   const uint32_t dp = padded_dim(dim), tr = tile_rows(rows, dp);
-  const uint64_t tiles = items * ((rows + tr - 1) / tr);
-  return tiles >= kMaxUnits ? 0 : 2ull * kMaxUnits * tr * (dp + 2) * 4;
+  const uint64_t tiles = items * ((rows + tr - 1) / tr), resident = resident_ctas(dp, device);
+  if (pick && tiles >= 2 * resident * kAtWarps) return 0;
+  const uint32_t splits = splits_of(tiles, tokens, resident);
+  return splits <= 8 ? 0 : tiles * splits * tr * (dp + 2) * 4;
 }
 
 template <uint32_t DP, uint32_t NT, bool F16, bool PICK, uint32_t WPI>
@@ -729,7 +737,7 @@ static int launch_attend(AttendArgs& a, int device, size_t ws_bytes, cudaStream_
   const uint32_t rows = (PICK ? 1u : a.T) * a.group, tiles = (rows + A::kRows - 1) / A::kRows;
   const uint64_t items = static_cast<uint64_t>(a.n_seqs) * (PICK ? a.T : 1u) * a.kv_heads * tiles;
   if (items > 0x7FFFFFFFull) return IBP_EINVAL;
-  const uint64_t resident = static_cast<uint64_t>(sm_count(device)) * (232448 / (A::kBytes + 1024));
+  const uint64_t resident = resident_ctas(DP, device);
   a.splits = 1;
   a.cluster = 0;
   if (PICK && items >= 2 * resident * kAtWarps)

@@ -122,12 +122,15 @@ struct AttendArgs {
 // Tree attention by rows of at most 16 queries per CTA, and sparse attention
 // (ibp_kv_attend.cu).
 int launch_kv_attend(AttendArgs& a, int device, size_t ws_bytes, cudaStream_t stream);
-size_t kv_attend_workspace(uint64_t items, uint64_t rows, uint32_t dim);
+// Scratch of launch_kv_attend: `items` (sequence, kv head) pairs, or (sequence,
+// query, kv head) triples with `pick`, of `rows` rows and at most `tokens` tokens.
+size_t kv_attend_workspace(uint64_t items, uint64_t rows, uint32_t dim, uint64_t tokens, bool pick, int device);
 
 // Tree attention on the tensor cores (ibp_kv_tree.cu); *done is set when the
 // call's shape is one it takes.
 int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_t stream, bool* done);
-size_t kv_tree_workspace(uint64_t rows, uint32_t dim, int device);
+size_t kv_tree_workspace(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint32_t page_tokens,
+                         uint64_t tokens, int device);
 
 struct SelectArgs {
   const char* q;

@@ -86,8 +86,21 @@ static bool tc_shape(uint32_t dim) { return dim <= 128; }
 static uint32_t tc_dim(uint32_t dim) { return dim <= 64 ? 64 : 128; }
 static uint32_t tc_tiles(uint64_t rows) { return rows > kTcTile ? 2 : 1; }
 
-size_t kv_tree_workspace(uint64_t rows, uint32_t dim, int device) {
-  if (!tc_shape(dim)) return 0;
+// Whether the kernel takes a call.  Boxes are whole 8-row swizzle groups of a
+// page.  Little work is done sooner by the few-row kernel, which has less to set
+// up: counted in 16-row x 128-token pieces, below two to a SM.  Measured (us, few-row /
+// this): 40 tiles of 4 rows 7.0 / 16, of 64 rows 11 / 18, of 128 rows 22 / 19; 256
+// tiles of 16 rows 16 / 18, of 32 rows 23 / 18; 1024 of 16 rows 28 / 22, of 128 79 / 26.
+static bool tc_takes(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint32_t page_tokens,
+                     uint64_t tokens, int device) {
+  if (!tc_shape(dim) || page_tokens % 8 || tokens == 0) return false;
+  const uint64_t longest = (tokens + kTcTile - 1) / kTcTile;
+  return longest * n_seqs * kv_heads * ((rows + 15) / 16) >= 2ull * sm_count(device);
+}
+
+size_t kv_tree_workspace(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint32_t page_tokens,
+                         uint64_t tokens, int device) {
+  if (!tc_takes(n_seqs, kv_heads, rows, dim, page_tokens, tokens, device)) return 0;
   const size_t n = sm_count(device), per = tc_tiles(rows) * kTcTile;
   return align256((n + 1) * sizeof(int4)) + align256(2 * n * per * sizeof(float2)) + 2 * n * per * tc_dim(dim) * 4;
 }
@@ -140,23 +153,17 @@ static int launch(TcArgs& t, const CUtensorMap& mk, const CUtensorMap& mv, int d
   }
   int rc = kv_launch("k_kv_tree", kern, dim3(t.n_ctas), S::kThreads, S::kSmem, 1, stream, t, mk, mv);
   if (rc != IBP_OK || t.n_ctas == 1) return rc;
-  return kv_launch("k_kv_tree_join", k_kv_tree_join<DP, MT, F16>, dim3(t.n_ctas - 1, MT * kTcTile / kJoinRows),
-                   kJoinThreads, 0, 1, stream, t);
+  const uint64_t rows = static_cast<uint64_t>(t.a.T) * t.a.group, most = rows < MT * kTcTile ? rows : MT * kTcTile;
+  return kv_launch("k_kv_tree_join", k_kv_tree_join<DP, MT, F16>,
+                   dim3(t.n_ctas - 1, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows)), kJoinThreads, 0, 1, stream, t);
 }
 
 int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_t stream, bool* done) {
   *done = false;
   const uint64_t rows = static_cast<uint64_t>(a.T) * a.group;
-  // Boxes are whole 8-row swizzle groups of a page; the softmax takes the
-  // maximum before it scales, so the scale has to be positive; and the device
-  // reads pages by TMA, which takes device memory only.
-  if (!tc_shape(a.dim) || a.page_tokens % 8 || !(a.scale_log2 > 0.f) || a.max_pages == 0) return IBP_OK;
-  // Little work is done sooner by the few-row kernel, which has less to set up:
-  // counted in 16-row x 128-token pieces, below two to a SM.  Measured (us, few-row /
-  // this): 40 tiles of 4 rows 7.0 / 16, of 64 rows 11 / 18, of 128 rows 22 / 19; 256
-  // tiles of 16 rows 16 / 18, of 32 rows 23 / 18; 1024 of 16 rows 28 / 22, of 128 79 / 26.
-  const uint64_t sms = sm_count(device), longest = (static_cast<uint64_t>(a.max_pages) * a.page_tokens + kTcTile - 1) / kTcTile;
-  if (longest * a.n_seqs * a.kv_heads * ((rows + 15) / 16) < 2 * sms) return IBP_OK;
+  // The softmax takes the maximum before it scales, so the scale has to be positive.
+  const uint64_t tokens = static_cast<uint64_t>(a.max_pages) * a.page_tokens, sms = sm_count(device);
+  if (!(a.scale_log2 > 0.f) || !tc_takes(a.n_seqs, a.kv_heads, rows, a.dim, a.page_tokens, tokens, device)) return IBP_OK;
   uint32_t box = 8;
   while (box < kTcTile && a.page_tokens % (2 * box) == 0) box *= 2;
   CUtensorMap mk, mv;
@@ -171,7 +178,7 @@ int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_
   t.row_pairs = static_cast<uint32_t>((rows + mt * kTcTile - 1) / (mt * kTcTile));
   t.q16 = ((reinterpret_cast<uintptr_t>(a.q) | static_cast<uint64_t>(a.q_seq) | static_cast<uint64_t>(a.q_token) |
             static_cast<uint64_t>(a.q_head)) & 15u) == 0;
-  const uint64_t tiles = longest * a.n_seqs * a.kv_heads * t.row_pairs;
+  const uint64_t tiles = (tokens + kTcTile - 1) / kTcTile * a.n_seqs * a.kv_heads * t.row_pairs;
   const uint64_t want = (tiles + kTcMinTiles - 1) / kTcMinTiles;
   const uint64_t n = sms;
   uint64_t ctas = want < sms ? want : sms;
@@ -184,7 +191,8 @@ int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_
   t.ml_part = reinterpret_cast<float2*>(w);
   w += align256(2 * n * per * sizeof(float2));
   t.o_part = reinterpret_cast<float*>(w);
-  if (!a.part || ws_bytes < kv_tree_workspace(rows, a.dim, device)) return IBP_EINVAL;
+  if (!a.part || ws_bytes < kv_tree_workspace(a.n_seqs, a.kv_heads, rows, a.dim, a.page_tokens, tokens, device))
+    return IBP_EINVAL;
   *done = true;
   auto go = [&](auto f16) {
     constexpr bool F = decltype(f16)::value;

@@ -78,11 +78,11 @@ def _load():
         "ibp_kv_accept": ([pages, seqs, vp, vp, vp, vp, u32, vp, vp, vp, vp, vp], i32),
         "ibp_tree_attention": ([pages, pages, u32, seqs, vp, i64, i64, i64, u32, u32, vp, vp, f32, vp, vp, vp, size,
                                 vp, vp], i32),
-        "ibp_tree_attention_workspace": ([u32, u32, u32, u32, u32], size),
+        "ibp_tree_attention_workspace": ([u32] * 7, size),
         "ibp_kv_summarize": ([pages, u32, seqs, vp, vp, vp, vp, vp], i32),
         "ibp_sparse_attention": ([pages, pages, u32, seqs, vp, vp, vp, i64, i64, i64, u32, u32, vp, u32, u32, u32,
                                   f32, vp, vp, vp, vp, size, vp, vp], i32),
-        "ibp_sparse_attention_workspace": ([u32] * 7, size),
+        "ibp_sparse_attention_workspace": ([u32] * 8, size),
     }
     for name, (args, res) in sigs.items():
         f = getattr(lib, name)
@@ -175,9 +175,9 @@ def _given(name: str, t: torch.Tensor, shape, dtype) -> torch.Tensor:
     return t
 
 
-def _scratch(workspace: torch.Tensor | None, size: int, device: torch.device) -> torch.Tensor:
+def _scratch(workspace: torch.Tensor | None, size: int, device: torch.device) -> torch.Tensor | None:
     if workspace is None:
-        return torch.empty(size, dtype=torch.uint8, device=device)
+        return torch.empty(size, dtype=torch.uint8, device=device) if size else None
     if workspace.numel() * workspace.element_size() < size or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and hold {size} bytes")
     return workspace
@@ -419,7 +419,7 @@ def ibp_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table:
             _ints("mask", mask, seqs.n_seqs, T, (T + 31) // 32)
         if n_draft is not None:
             _ints("n_draft", n_draft, seqs.n_seqs)
-        size = lib.ibp_tree_attention_workspace(seqs.n_seqs, T, heads, kp.heads, kp.dim)
+        size = lib.ibp_tree_attention_workspace(seqs.n_seqs, seqs.max_pages, kp.page_tokens, T, heads, kp.heads, kp.dim)
         return kp, vp, dt, seqs, (*q.stride()[:3], T, heads), size, 1.0 / math.sqrt(kp.dim)
 
     key = ("tree", _form(q), _form(k), _form(v), _form(table), _form(lens), _form(mask), _form(n_draft))
@@ -438,8 +438,8 @@ def ibp_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table:
         _check(lib.ibp_tree_attention(kp, vp, dt, seqs, q.data_ptr(), *rows,
                                       None if n_draft is None else n_draft.data_ptr(),
                                       None if mask is None else mask.data_ptr(), usual if scale is None else scale,
-                                      out.data_ptr(), lse.data_ptr(), ws.data_ptr(), size, _status(status, device),
-                                      handle), "ibp_tree_attention")
+                                      out.data_ptr(), lse.data_ptr(), None if ws is None else ws.data_ptr(), size,
+                                      _status(status, device), handle), "ibp_tree_attention")
     return out, lse
 
 
@@ -499,7 +499,8 @@ def ibp_sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tabl
                              f"{IBP_SPARSE_MAX_BUDGET}")
         if n_query is not None:
             _ints("n_query", n_query, seqs.n_seqs)
-        size = lib.ibp_sparse_attention_workspace(seqs.n_seqs, seqs.max_pages, T, heads, kp.heads, kp.dim, budget)
+        size = lib.ibp_sparse_attention_workspace(seqs.n_seqs, seqs.max_pages, kp.page_tokens, T, heads, kp.heads, kp.dim,
+                                                  budget)
         return kp, vp, dt, seqs, (*q.stride()[:3], T, heads), size, 1.0 / math.sqrt(kp.dim)
 
     key = ("sparse", _form(q), _form(k), _form(v), _form(table), _form(lens), _form(codes), _form(scales),
@@ -524,6 +525,6 @@ def ibp_sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tabl
         _check(lib.ibp_sparse_attention(kp, vp, dt, seqs, codes.data_ptr(), scales.data_ptr(), q.data_ptr(), *rows,
                                         None if n_query is None else n_query.data_ptr(), budget, keep_first,
                                         keep_last, usual if scale is None else scale, out.data_ptr(), lse.data_ptr(),
-                                        pages.data_ptr(), ws.data_ptr(), size, _status(status, device), handle),
-               "ibp_sparse_attention")
+                                        pages.data_ptr(), None if ws is None else ws.data_ptr(), size,
+                                        _status(status, device), handle), "ibp_sparse_attention")
     return out, lse, pages

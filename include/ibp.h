@@ -656,15 +656,15 @@ int ibp_kv_accept(const ibp_kv_pages* pages, const ibp_kv_seqs* seqs, const int3
  * mask     n_seqs x T x ceil(T / 32) words, or NULL.
  * out      n_seqs x T x q_heads x dim, contiguous; lse  n_seqs x T x q_heads
  *          floats, or NULL.
- * ws       ibp_tree_attention_workspace bytes.
+ * ws       ibp_tree_attention_workspace bytes (0: may be NULL).
  * Errors: IBP_EINVAL, IBP_ECUDA.
  */
 int ibp_tree_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t dtype, const ibp_kv_seqs* seqs,
                        const void* q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
                        uint32_t T, uint32_t q_heads, const int32_t* n_draft, const uint32_t* mask, float scale,
                        void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* status, void* stream);
-size_t ibp_tree_attention_workspace(uint32_t n_seqs, uint32_t T, uint32_t q_heads, uint32_t kv_heads,
-                                    uint32_t dim);
+size_t ibp_tree_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t page_tokens, uint32_t T,
+                                    uint32_t q_heads, uint32_t kv_heads, uint32_t dim);
 
 /*
  * Bounds of a page's keys in 8 bits, the cheap stand-in that
@@ -710,8 +710,8 @@ int ibp_sparse_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t 
                          const int32_t* n_query, uint32_t budget, uint32_t keep_first, uint32_t keep_last,
                          float scale, void* out, float* lse, int32_t* pages_out, void* ws, size_t ws_bytes,
                          uint32_t* status, void* stream);
-size_t ibp_sparse_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t T, uint32_t q_heads,
-                                      uint32_t kv_heads, uint32_t dim, uint32_t budget);
+size_t ibp_sparse_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t page_tokens, uint32_t T,
+                                      uint32_t q_heads, uint32_t kv_heads, uint32_t dim, uint32_t budget);
 
 #ifdef __cplusplus
 }

@@ -556,7 +556,9 @@ def test_refusals():
     for bad in (dict(q=q.float()), dict(q=q[0]), dict(table=table.long()), dict(lens=dev(np.array([1, 2]))),
                 dict(q=q[..., :32]), dict(mask=dev(np.zeros((1, 1, 2)))), dict(n_draft=dev(np.array([1, 1]))),
                 dict(out=torch.empty_like(q)[..., :32]), dict(v=k.half()), dict(k=k.cpu()), dict(k=k[0]),
-                dict(workspace=torch.empty(1, dtype=torch.uint8, device="cuda"))):
+                # enough work to need scratch
+                dict(table=dev(np.zeros((64, 60))), lens=dev(np.full(64, 20)), q=q.expand(64, 1, 4, 64),
+                     workspace=torch.empty(1, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(ValueError):
             tree(**bad)
     for bad in (dict(budget=0), dict(budget=5000), dict(keep_last=0), dict(keep_first=2), dict(codes=codes[:3]),
@@ -610,6 +612,9 @@ def test_no_sequences():
     k = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
     q = torch.zeros((0, 2, 4, 64), dtype=torch.bfloat16, device="cuda")
     assert kv.ibp_tree_attention(q, k, k, none, lens)[0].shape == q.shape
+    codes, scales = torch.zeros((4, 2, 2, 64), dtype=torch.int8, device="cuda"), torch.zeros((4, 2), device="cuda")
+    assert kv.ibp_sparse_attention(q, k, k, none, lens, codes, scales, 4)[2].shape == (0, 2, 2, 4)
+    kv.ibp_kv_summarize(k, none, lens, codes, scales)
     refs = dev(np.array([1, 0, 2, 0]))
     assert host(kv.ibp_kv_fork(none, lens, refs, lens, 16)[2]).tolist() == [1, 0, 2, 0]
     assert host(kv.ibp_kv_compact(none, refs, 16)[1]).tolist() == [1, 2, 0, 0]
