@@ -204,8 +204,11 @@ struct TcShape {
   static constexpr uint32_t kHalves = DP / 64;                       // 128-byte wide panels of a tile
   static constexpr uint32_t kPanel = kTcTile * 128;                  // bytes of a panel
   static constexpr uint32_t kTileBytes = kHalves * kPanel;           // K or V of a stage, Q of a tile
-  static constexpr uint32_t kStages = DP == 128 ? (MT == 2 ? 2 : 3) : (MT == 2 ? 4 : 6);
-  static constexpr uint32_t kBytes = MT * kTileBytes + kStages * 2 * kTileBytes;
+  // One row tile has room for a second Q: the next segment's scores then begin
+  // while this one's output is still written.
+  static constexpr uint32_t kQ = MT == 1 ? 2 : MT;
+  static constexpr uint32_t kStages = DP == 128 ? 2 : (MT == 2 ? 4 : 5);
+  static constexpr uint32_t kBytes = kQ * kTileBytes + kStages * 2 * kTileBytes;
   static constexpr uint32_t kSmem = kBytes + 1024 + 512;             // alignment, barriers
   static constexpr uint32_t kThreads = MT * 128 + 64;
   static constexpr uint32_t kOCol = 256;                             // first column of O
@@ -216,7 +219,7 @@ struct TcShared {
   uint64_t s_full[2], p_full[2][2], pv_done[2], q_full[2];  // p_full: per slot and half
   uint32_t tmem;
   uint32_t stop;
-  uint32_t odd;       // 1 + the last segment whose draft holds infinities or NaN among its values
+  uint32_t odd[2];    // even and odd segments: 1 + the last whose draft holds infinities or NaN among its values
   uint32_t pair0, b0; // row block and sequence in which this CTA's range begins
   uint64_t in0;       // tiles of that sequence before the range
   uint32_t sums[12];
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
   TcShared& sh = *reinterpret_cast<TcShared*>(sm + S::kBytes);
   static_assert(sizeof(TcShared) <= 512, "barriers");
   const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
-  const uint32_t q_sm = base, kv_sm = base + MT * S::kTileBytes;
+  const uint32_t q_sm = base, kv_sm = base + S::kQ * S::kTileBytes;
   auto k_at = [&](uint32_t st) { return kv_sm + st * 2 * S::kTileBytes; };
   auto v_at = [&](uint32_t st) { return kv_sm + st * 2 * S::kTileBytes + S::kTileBytes; };
 
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       tc::bar_init(tc::s32(&sh.q_full[i]), 128);
     }
     sh.stop = 0;
-    sh.odd = 0;
+    sh.odd[0] = sh.odd[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
     constexpr uint32_t kTileStep = S::kTileBytes >> 4;
     auto qk = [&](uint32_t tile, uint32_t slot, uint32_t st) {
       if (tc::elect()) {
-        const uint64_t qa = qd + tile * kTileStep, ka = kd + st * (2 * kTileStep);
+        const uint64_t qa = qd + (MT == 1 ? segs & 1u : tile) * kTileStep, ka = kd + st * (2 * kTileStep);
         const uint32_t d = tmem + slot * 128;
 #pragma unroll
         for (uint32_t kk = 0; kk < DP / 16; ++kk) {
@@ -500,7 +503,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
         tc::mma_ts(d, p, va, id_pv, add);
 #pragma unroll
         for (uint32_t kk = 1; kk < kTcTile / 32; ++kk) tc::mma_ts(d, p + kk * 8, va + kk * (2048 >> 4), id_pv, 1);
-        if (hf) tc::commit(tc::s32(&sh.pv_done[tile]));
+        if (hf) tc::commit(tc::s32(&sh.pv_done[slot]));
       }
       __syncwarp();
     };
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
           if (hit) *w = x;
           odd |= hit;
         }
-      if (__any_sync(0xFFFFFFFFu, odd != 0) && lane == 0) *reinterpret_cast<volatile uint32_t*>(&sh.odd) = segs + 1;
+      if (__any_sync(0xFFFFFFFFu, odd != 0) && lane == 0) *reinterpret_cast<volatile uint32_t*>(&sh.odd[segs & 1u]) = segs + 1;
       tc::fence_async();
       __syncwarp();
     };
@@ -620,33 +623,48 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
     const uint32_t m = warp / 4, r = tid & 127u;
     const uint32_t lanes = (warp & 3u) << 21;  // this warp's quarter of the TMEM lanes
     TcWalk walk(t, sh, at, end);
-    TcSeg s;
+    TcSeg s, following;
     uint32_t g = 0, segs = 0;
     bool ok = true;
-    while (ok && walk.next(&s)) {
+    // This thread's row of Q of a segment.
+    auto load_q = [&](const TcSeg& sg, uint32_t nth) {
+      const uint32_t gr = (sg.pair * MT + m) * kTcTile + r;
+      const uint32_t tok = gr / a.group, head = gr - tok * a.group;
+      const bool live = static_cast<int32_t>(tok) < sg.n_live;
+      const char* q = a.q + static_cast<int64_t>(sg.b) * a.q_seq + static_cast<int64_t>(live ? tok : 0) * a.q_token +
+                      static_cast<int64_t>(sg.h * a.group + (live ? head : 0)) * a.q_head;
+      unsigned char* dst = sm + (MT == 1 ? nth & 1u : m) * S::kTileBytes + r * 128;
+#pragma unroll
+      for (uint32_t c = 0; c < DP / 8; ++c) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (live && c * 8 < a.dim) {
+          if (t.q16)
+            x = *reinterpret_cast<const uint4*>(q + c * 16);
+          else {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(q + c * 16);
+            x = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        *reinterpret_cast<uint4*>(dst + (c / 8) * S::kPanel + (((c & 7u) ^ (r & 7u)) << 4)) = x;
+      }
+      tc::fence_async();
+      tc::bar_arrive(tc::s32(&sh.q_full[m]));
+    };
+    // Waits for P V of a tile, and so for all before it.  A wait by parity must be
+    // neither a phase behind its barrier nor two ahead.  With alternating slots the
+    // last two products may both be under way, or both done, so each slot has a
+    // barrier: its product before was done when this tile's scores were, and its
+    // next one needs this thread's P.
+    auto product_done = [&](uint32_t x) {
+      const bool r = tc::bar_wait(tc::s32(&sh.pv_done[MT == 2 ? m : x & 1u]), (MT == 2 ? x : x >> 1) & 1u, stop);
+      return __all_sync(0xFFFFFFFFu, r) != 0;
+    };
+    bool more = walk.next(&s);
+    if (more) load_q(s, 0);
+    while (ok && more) {
       const uint32_t gr = (s.pair * MT + m) * kTcTile + r;
       const uint32_t tok = gr / a.group, head = gr - tok * a.group;
       const bool exists = tok < a.T, live = static_cast<int32_t>(tok) < s.n_live;
-      {  // this row of Q; every product of the previous segment that read Q has been waited for
-        const char* q = a.q + static_cast<int64_t>(s.b) * a.q_seq + static_cast<int64_t>(live ? tok : 0) * a.q_token +
-                        static_cast<int64_t>(s.h * a.group + (live ? head : 0)) * a.q_head;
-        unsigned char* dst = sm + m * S::kTileBytes + r * 128;
-#pragma unroll
-        for (uint32_t c = 0; c < DP / 8; ++c) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (live && c * 8 < a.dim) {
-            if (t.q16)
-              x = *reinterpret_cast<const uint4*>(q + c * 16);
-            else {
-              const uint32_t* w = reinterpret_cast<const uint32_t*>(q + c * 16);
-              x = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          *reinterpret_cast<uint4*>(dst + (c / 8) * S::kPanel + (((c & 7u) ^ (r & 7u)) << 4)) = x;
-        }
-        tc::fence_async();
-        tc::bar_arrive(tc::s32(&sh.q_full[m]));
-      }
       const uint32_t* words =
           a.mask ? a.mask + (static_cast<uint64_t>(s.b) * a.T + (live ? tok : 0)) * a.mask_words : nullptr;
       float top = -INFINITY, sum = 0.f;  // running maximum (of score * log2 e) and sum
@@ -698,8 +716,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
           sum *= f;
           if (j > 0) {
             // O holds the sums up to the tile before
-            ok = tc::bar_wait(tc::s32(&sh.pv_done[MT == 2 ? m : 0]), (g + j - 1) & 1u, stop);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+            ok = product_done(g + j - 1);
             if (!ok) break;
             tc::fence_after();
 #pragma unroll
@@ -742,19 +759,19 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
         sum += s0 + s1;
       }
       if (!ok) break;
-      // ---- this segment's sums.  A wait by parity must not be two phases behind:
-      // with alternating slots the last two products may both be under way.
-      if (MT == 1 && s.tiles > 1) ok = tc::bar_wait(tc::s32(&sh.pv_done[0]), (g + s.tiles - 2) & 1u, stop);
-      ok = ok && tc::bar_wait(tc::s32(&sh.pv_done[MT == 2 ? m : 0]), (g + s.tiles - 1) & 1u, stop);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
+      // Every product of the segment before that read the other buffer has been
+      // waited for.
+      const bool again = walk.next(&following);
+      if (MT == 1 && again) load_q(following, segs + 1);
+      // ---- this segment's sums
+      if (!(ok = product_done(g + s.tiles - 1))) break;
       tc::fence_after();
       const bool whole = s.tiles == s.all;
       const uint64_t slot = 2ull * blockIdx.x + (s.tile0 == 0 ? 1 : 0);  // as k_kv_tree_join reads them
       const uint64_t prow = slot * (MT * kTcTile) + m * kTcTile + r;
       const uint64_t orow = (static_cast<uint64_t>(s.b) * a.T + tok) * a.kv_heads * a.group + s.h * a.group + head;
       const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-      const bool odd = *reinterpret_cast<volatile uint32_t*>(&sh.odd) == segs + 1;
+      const bool odd = *reinterpret_cast<volatile uint32_t*>(&sh.odd[segs & 1u]) == segs + 1;
 #pragma unroll
       for (uint32_t c = 0; c < DP / 32; ++c) {
         float o[32];
@@ -813,6 +830,9 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       ++segs;
       // O is read: the next segment's first product may overwrite it
       tc::fence_before();
+      if (MT == 2 && again) load_q(following, segs);
+      s = following;
+      more = again;
     }
     if (at >= end && tid == 0) t.first[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (blockIdx.x == 0 && tid == 0)
