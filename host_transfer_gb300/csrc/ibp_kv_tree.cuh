@@ -204,18 +204,22 @@ struct TcShape {
   static constexpr uint32_t kHalves = DP / 64;                       // 128-byte wide panels of a tile
   static constexpr uint32_t kPanel = kTcTile * 128;                  // bytes of a panel
   static constexpr uint32_t kTileBytes = kHalves * kPanel;           // K or V of a stage, Q of a tile
-  // One row tile has room for a second Q: the next segment's scores then begin
-  // while this one's output is still written.
-  static constexpr uint32_t kQ = MT == 1 ? 2 : MT;
-  static constexpr uint32_t kStages = DP == 128 ? 2 : (MT == 2 ? 4 : 5);
-  static constexpr uint32_t kBytes = kQ * kTileBytes + kStages * 2 * kTileBytes;
+  // Two tiles of Q: one for each row tile, or for one row tile the next segment's
+  // beside this one's, so that its scores begin while the output is still written.
+  static constexpr uint32_t kQ = 2;
+  // Ring of tiles, K and V in turn.  One row tile is bound by the loads and takes
+  // all that fit, two and a half cache tiles (a batch of 16 ragged caches of up to
+  // 32768: 231 us, with two 242); two row tiles are bound by the products and do
+  // no better with more than two (571 us, with two and a half 583).
+  static constexpr uint32_t kSlots = DP == 128 ? (MT == 1 ? 5 : 4) : (MT == 1 ? 11 : 8);
+  static constexpr uint32_t kBytes = (kQ + kSlots) * kTileBytes;
   static constexpr uint32_t kSmem = kBytes + 1024 + 512;             // alignment, barriers
   static constexpr uint32_t kThreads = MT * 128 + 64;
   static constexpr uint32_t kOCol = 256;                             // first column of O
 };
 
 struct TcShared {
-  uint64_t k_full[6], v_full[6], k_empty[6], v_empty[6];
+  uint64_t full[11], empty[11];
   uint64_t s_full[2], p_full[2][2], pv_done[2], q_full[2];  // p_full: per slot and half
   uint32_t tmem;
   uint32_t stop;
@@ -325,15 +329,15 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
   static_assert(sizeof(TcShared) <= 512, "barriers");
   const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
   const uint32_t q_sm = base, kv_sm = base + S::kQ * S::kTileBytes;
-  auto k_at = [&](uint32_t st) { return kv_sm + st * 2 * S::kTileBytes; };
-  auto v_at = [&](uint32_t st) { return kv_sm + st * 2 * S::kTileBytes + S::kTileBytes; };
+  // Fill f of the ring is K of tile f / 2 of this CTA's range, or its V.
+  auto ring = [](uint32_t f) { return f % S::kSlots; };
+  auto ring_phase = [](uint32_t f) { return (f / S::kSlots) & 1u; };
+  auto ring_at = [&](uint32_t f) { return kv_sm + ring(f) * S::kTileBytes; };
 
   if (tid == 0) {
-    for (uint32_t i = 0; i < S::kStages; ++i) {
-      tc::bar_init(tc::s32(&sh.k_full[i]), 1);
-      tc::bar_init(tc::s32(&sh.v_full[i]), 1);
-      tc::bar_init(tc::s32(&sh.k_empty[i]), 1);
-      tc::bar_init(tc::s32(&sh.v_empty[i]), 1);
+    for (uint32_t i = 0; i < S::kSlots; ++i) {
+      tc::bar_init(tc::s32(&sh.full[i]), 1);
+      tc::bar_init(tc::s32(&sh.empty[i]), 1);
     }
     for (uint32_t i = 0; i < 2; ++i) {
       tc::bar_init(tc::s32(&sh.s_full[i]), 1);
@@ -407,8 +411,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
     // ---- producer: one lane issues; all follow the same path
     TcWalk walk(t, sh, at, end);
     TcSeg s;
-    uint32_t g = 0;  // tiles of this CTA so far
-    uint32_t k_fills = 0, v_fills = 0;
+    uint32_t f = 0;  // fills so far
     bool ok = true;
     const uint32_t boxes = kTcTile / t.box;
     while (ok && walk.next(&s)) {
@@ -417,8 +420,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
         const int32_t raw = a.lens[s.b], n = a.n_live ? a.n_live[s.b] : static_cast<int32_t>(a.T);
         if (raw != s.len || n != s.n_live || n > s.len) kv_status(a.status, IBP_ERANGE);
       }
-      for (uint32_t j = 0; j < s.tiles && ok; ++j, ++g) {
-        const uint32_t st = g % S::kStages, ph = (g / S::kStages) & 1u;
+      for (uint32_t j = 0; j < s.tiles && ok; ++j) {
         const int32_t p0 = static_cast<int32_t>((s.tile0 + j) * kTcTile);
         // lane i finds the page of box i
         const int32_t p = p0 + static_cast<int32_t>(lane * t.box);
@@ -435,36 +437,26 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
         }
         const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, have));
         const uint32_t bytes = n * t.box * 128 * S::kHalves;
-        ok = tc::bar_wait(tc::s32(&sh.k_empty[st]), ph ^ 1u, stop);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        if (lane == 0) tc::bar_expect(tc::s32(&sh.k_full[st]), bytes);
-        __syncwarp();
-        if (have)
 #pragma unroll
-          for (uint32_t hf = 0; hf < S::kHalves; ++hf)
-            tc::tma_box(k_at(st) + hf * S::kPanel + lane * t.box * 128, &map_k, hf * 64, slot, s.h, page,
-                        tc::s32(&sh.k_full[st]));
-        ++k_fills;
-        ok = tc::bar_wait(tc::s32(&sh.v_empty[st]), ph ^ 1u, stop);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        if (lane == 0) tc::bar_expect(tc::s32(&sh.v_full[st]), bytes);
-        __syncwarp();
-        if (have)
+        for (uint32_t kv = 0; kv < 2; ++kv, ++f) {
+          ok = tc::bar_wait(tc::s32(&sh.empty[ring(f)]), ring_phase(f) ^ 1u, stop);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          const uint32_t bar = tc::s32(&sh.full[ring(f)]), dst = ring_at(f) + lane * t.box * 128;
+          if (lane == 0) tc::bar_expect(bar, bytes);
+          __syncwarp();
+          if (have)
 #pragma unroll
-          for (uint32_t hf = 0; hf < S::kHalves; ++hf)
-            tc::tma_box(v_at(st) + hf * S::kPanel + lane * t.box * 128, &map_v, hf * 64, slot, s.h, page,
-                        tc::s32(&sh.v_full[st]));
-        ++v_fills;
+            for (uint32_t hf = 0; hf < S::kHalves; ++hf)
+              tc::tma_box(dst + hf * S::kPanel, kv ? &map_v : &map_k, hf * 64, slot, s.h, page, bar);
+        }
       }
     }
     if (!ok || *stop)  // copies in flight land before the CTA leaves
-      for (uint32_t i = 0; i < S::kStages; ++i) {
-        const uint32_t fk = (k_fills + S::kStages - 1 - i) / S::kStages, fv = (v_fills + S::kStages - 1 - i) / S::kStages;
+      for (uint32_t i = 0; i < S::kSlots; ++i) {
+        const uint32_t n = (f + S::kSlots - 1 - i) / S::kSlots;  // fills of slot i
         const long long t0 = clock64();
-        while (clock64() - t0 < kTcWait && ((fk && !tc::bar_try(tc::s32(&sh.k_full[i]), (fk - 1) & 1u)) ||
-                                            (fv && !tc::bar_try(tc::s32(&sh.v_full[i]), (fv - 1) & 1u)))) {
+        while (n && clock64() - t0 < kTcWait && !tc::bar_try(tc::s32(&sh.full[i]), (n - 1) & 1u)) {
         }
       }
   } else if (warp == MT * 4 + 1) {
@@ -480,11 +472,11 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
     // first by constants, so that eight products are little more than eight
     // instructions: built one by one from addresses, beside two busy softmax warps
     // on the scheduler, each took 110 cycles instead of the 64 it runs for.
-    const uint64_t qd = tc::operand(q_sm, 16), kd = tc::operand(k_at(0), 16), vd = tc::operand(v_at(0), S::kPanel);
+    const uint64_t qd = tc::operand(q_sm, 16), kd = tc::operand(kv_sm, 16), vd = tc::operand(kv_sm, S::kPanel);
     constexpr uint32_t kTileStep = S::kTileBytes >> 4;
-    auto qk = [&](uint32_t tile, uint32_t slot, uint32_t st) {
+    auto qk = [&](uint32_t tile, uint32_t slot, uint32_t f) {
       if (tc::elect()) {
-        const uint64_t qa = qd + (MT == 1 ? segs & 1u : tile) * kTileStep, ka = kd + st * (2 * kTileStep);
+        const uint64_t qa = qd + (MT == 1 ? segs & 1u : tile) * kTileStep, ka = kd + ring(f) * kTileStep;
         const uint32_t d = tmem + slot * 128;
 #pragma unroll
         for (uint32_t kk = 0; kk < DP / 16; ++kk) {
@@ -496,9 +488,9 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       __syncwarp();
     };
     // Half hf of P V: 64 tokens.
-    auto pv = [&](uint32_t tile, uint32_t slot, uint32_t st, uint32_t hf, bool add) {
+    auto pv = [&](uint32_t tile, uint32_t slot, uint32_t f, uint32_t hf, bool add) {
       if (tc::elect()) {
-        const uint64_t va = vd + st * (2 * kTileStep) + hf * (8192 >> 4);
+        const uint64_t va = vd + ring(f) * kTileStep + hf * (8192 >> 4);
         const uint32_t d = tmem + S::kOCol + tile * DP, p = tmem + slot * 128 + hf * 32;
         tc::mma_ts(d, p, va, id_pv, add);
 #pragma unroll
@@ -518,11 +510,11 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
     // V of the item's last tiles: tokens past the length become zeros (what the
     // pages hold there must not meet a zero probability), and infinities and NaN
     // of drafted tokens are taken out for the epilogue to add.
-    auto clean = [&](const TcSeg& sg, uint32_t j, uint32_t st) {
+    auto clean = [&](const TcSeg& sg, uint32_t j, uint32_t f) {
       const int32_t p0 = static_cast<int32_t>((sg.tile0 + j) * kTcTile);
       const int32_t end_tok = sg.len - p0;                        // tokens of this tile
       if (end_tok >= static_cast<int32_t>(kTcTile) && p0 + static_cast<int32_t>(kTcTile) <= sg.ctx) return;
-      unsigned char* v = sm + (v_at(st) - base);
+      unsigned char* v = sm + (ring_at(f) - base);
       const uint32_t valid = end_tok <= 0 ? 0u : (end_tok < static_cast<int32_t>(kTcTile) ? end_tok : kTcTile);
       for (uint32_t i = valid * 8 + lane; i < kTcTile * 8; i += 32)
 #pragma unroll
@@ -559,59 +551,60 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       if (!ok) break;
       tc::fence_after();
       const uint32_t n = s.tiles;
-      auto stage = [&](uint32_t j) { return (g + j) % S::kStages; };
-      auto phase = [&](uint32_t j) { return ((g + j) / S::kStages) & 1u; };
+      auto kf = [&](uint32_t j) { return 2 * (g + j); };
+      auto vf = [&](uint32_t j) { return 2 * (g + j) + 1; };
+      auto loaded = [&](uint32_t f) { return wait(&sh.full[ring(f)], ring_phase(f)); };
       if (MT == 2) {
-        if (!(ok = wait(&sh.k_full[stage(0)], phase(0)))) break;
-        qk(0, 0, stage(0));
-        qk(1, 1, stage(0));
-        release(&sh.k_empty[stage(0)]);
+        if (!(ok = loaded(kf(0)))) break;
+        qk(0, 0, kf(0));
+        qk(1, 1, kf(0));
+        release(&sh.empty[ring(kf(0))]);
         for (uint32_t j = 0; j < n; ++j) {
-          if (!(ok = wait(&sh.v_full[stage(j)], phase(j)))) break;
-          clean(s, j, stage(j));
+          if (!(ok = loaded(vf(j)))) break;
+          clean(s, j, vf(j));
           if (!(ok = wait(&sh.p_full[0][0], (g + j) & 1u))) break;
           tc::fence_after();
-          pv(0, 0, stage(j), 0, j > 0);
+          pv(0, 0, vf(j), 0, j > 0);
           if (!(ok = wait(&sh.p_full[0][1], (g + j) & 1u))) break;
           tc::fence_after();
-          pv(0, 0, stage(j), 1, true);
+          pv(0, 0, vf(j), 1, true);
           if (j + 1 < n) {
-            if (!(ok = wait(&sh.k_full[stage(j + 1)], phase(j + 1)))) break;
-            qk(0, 0, stage(j + 1));
+            if (!(ok = loaded(kf(j + 1)))) break;
+            qk(0, 0, kf(j + 1));
           }
           if (!(ok = wait(&sh.p_full[1][0], (g + j) & 1u))) break;
           tc::fence_after();
-          pv(1, 1, stage(j), 0, j > 0);
+          pv(1, 1, vf(j), 0, j > 0);
           if (!(ok = wait(&sh.p_full[1][1], (g + j) & 1u))) break;
           tc::fence_after();
-          pv(1, 1, stage(j), 1, true);
-          release(&sh.v_empty[stage(j)]);
+          pv(1, 1, vf(j), 1, true);
+          release(&sh.empty[ring(vf(j))]);
           if (j + 1 < n) {
-            qk(1, 1, stage(j + 1));
-            release(&sh.k_empty[stage(j + 1)]);
+            qk(1, 1, kf(j + 1));
+            release(&sh.empty[ring(kf(j + 1))]);
           }
         }
       } else {
         for (uint32_t j = 0; j < 2 && j < n; ++j) {
-          if (!(ok = wait(&sh.k_full[stage(j)], phase(j)))) break;
-          qk(0, (g + j) & 1u, stage(j));
-          release(&sh.k_empty[stage(j)]);
+          if (!(ok = loaded(kf(j)))) break;
+          qk(0, (g + j) & 1u, kf(j));
+          release(&sh.empty[ring(kf(j))]);
         }
         for (uint32_t j = 0; j < n && ok; ++j) {
-          if (!(ok = wait(&sh.v_full[stage(j)], phase(j)))) break;
-          clean(s, j, stage(j));
+          if (!(ok = loaded(vf(j)))) break;
+          clean(s, j, vf(j));
           const uint32_t slot = (g + j) & 1u, ph = ((g + j) >> 1) & 1u;
           if (!(ok = wait(&sh.p_full[slot][0], ph))) break;
           tc::fence_after();
-          pv(0, slot, stage(j), 0, j > 0);
+          pv(0, slot, vf(j), 0, j > 0);
           if (!(ok = wait(&sh.p_full[slot][1], ph))) break;
           tc::fence_after();
-          pv(0, slot, stage(j), 1, true);
-          release(&sh.v_empty[stage(j)]);
+          pv(0, slot, vf(j), 1, true);
+          release(&sh.empty[ring(vf(j))]);
           if (j + 2 < n) {
-            if (!(ok = wait(&sh.k_full[stage(j + 2)], phase(j + 2)))) break;
-            qk(0, (g + j) & 1u, stage(j + 2));
-            release(&sh.k_empty[stage(j + 2)]);
+            if (!(ok = loaded(kf(j + 2)))) break;
+            qk(0, (g + j) & 1u, kf(j + 2));
+            release(&sh.empty[ring(kf(j + 2))]);
           }
         }
       }
