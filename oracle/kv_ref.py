@@ -115,7 +115,7 @@ def attend(q, keys, vals, scale):
     p = np.exp(s - m)
     total = p.sum()
     return ((p @ vals) / total, m + np.log(total), (p @ np.abs(vals)) / total,
-            float((np.abs(keys) @ np.abs(q)).max() * scale))
+            float((np.abs(keys) @ np.abs(q)).max() * abs(scale)))
 
 
 def rows_of(pages, table_row, positions, head):

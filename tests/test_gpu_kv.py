@@ -410,6 +410,176 @@ def test_tree_pool_past_32_bits(T, G):
 
 
 # ---------------------------------------------------------------------------
+# Tree attention, enough work for the tensor-core kernel
+
+
+def scratch_of(lens, T, hk, G, page, D):
+    """Scratch of the call: the tensor-core kernel wants some, the few-row kernel here none."""
+    width = max(1, -(-max(lens) // page)) + 1
+    return kv._load().ibp_tree_attention_workspace(len(lens), width, page, T, hk * G, hk, D)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("lens,T,hk,G,page,D,layout", [
+    ([300, 17, 129], 4, 40, 4, 16, 128, "hnd"),      # one row tile, sequences in and between tiles
+    ([250, 640], 7, 33, 3, 24, 80, "nhd"),           # pages that end inside a tile, odd group
+    ([131, 1, 128], 1, 64, 16, 64, 64, "padded"),    # single tokens
+    ([70, 200], 40, 12, 5, 8, 128, "padded"),        # two row tiles, the second partly filled
+    ([400], 70, 9, 8, 128, 128, "hnd"),              # several row blocks
+    ([333, 40], 35, 20, 8, 256, 64, "nhd"),
+    ([900], 129, 2, 16, 32, 40, "hnd"),              # a draft longer than a tile, many row blocks
+    ([1300, 128, 5], 5, 13, 8, 40, 120, "hnd"),
+])
+def test_tree_wide(lens, T, hk, G, page, D, layout, dt):
+    assert scratch_of(lens, T, hk, G, page, D) > 0
+    run_tree(dt, layout, lens, T, hk, G, page, D)
+
+
+@pytest.mark.parametrize("T,hk,G", [(6, 40, 8), (48, 16, 8)])
+def test_tree_wide_mask_kinds(T, hk, G):
+    rng = np.random.default_rng(1)
+    lens = [160, T, 300]
+    assert scratch_of(lens, T, hk, G, 16, 64) > 0
+    run_tree("f16", "hnd", lens, T, hk, G, 16, 64, mask=None)
+    nothing = np.zeros((3, T, (T + 31) // 32), np.int32)
+    got = run_tree("bf16", "hnd", lens, T, hk, G, 16, 64, mask=nothing)
+    assert (host(got[1])[1] == -np.inf).all()
+    dense = rng.integers(-2**31, 2**31, nothing.shape).astype(np.int32)
+    run_tree("bf16", "nhd", lens, T, hk, G, 16, 64, mask=dense)
+    run_tree("bf16", "hnd", [160, T, 300, 0, 9], T, hk, G, 16, 128, n_draft=[T, 3, 0, 0, 1])
+    run_tree("bf16", "hnd", lens, T, hk, G, 16, 128, scale=30.0)
+    run_tree("f16", "hnd", lens, T, hk, G, 16, 128, scale=1e-4)
+    # a scale that is not positive goes another way
+    run_tree("bf16", "hnd", lens, T, hk, G, 16, 128, scale=-0.2)
+    run_tree("bf16", "hnd", lens, T, hk, G, 16, 128, scale=0.0)
+
+
+@pytest.mark.parametrize("T,hk,G,D", [(6, 40, 8, 128), (48, 16, 8, 64)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_tree_wide_masked_infinities_and_nan(T, hk, G, D, dt):
+    rng = np.random.default_rng(2)
+    lens, page = np.array([290, 150], np.int32), 16
+    assert scratch_of(lens, T, hk, G, page, D) > 0
+    table, _ = tables(lens, page, 40, 20, rng)
+    g = gen(3)
+    k, v = (pool((40, hk, page, D), DTYPES[dt], "hnd", g) for _ in range(2))
+    q = torch.randn((2, T, hk * G, D), device="cuda", generator=g).to(DTYPES[dt])
+    sees = random_tree(rng, 2, T)
+    sees[0, :, 1] = False
+    sees[0, 1, 1] = sees[0, 3, 1] = True
+    sees[0, :, 2] = False
+    sees[0, 2, 2] = True
+    clean = kv.ibp_tree_attention(q, k, v, dev(table), dev(lens), mask=dev(mask_words(sees)))
+    at = lambda p: (int(table[0, p // page]), slice(None), p % page)  # noqa: E731
+    ctx = 290 - T
+    x = v[at(ctx + 1)]
+    x[:, : D // 2] = float("inf")
+    x[:, D // 2] = float("nan")
+    k[at(ctx + 2)] = float("nan")
+    out, _ = kv.ibp_tree_attention(q, k, v, dev(table), dev(lens), mask=dev(mask_words(sees)))
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[[1, 3, 2]] = False
+    assert torch.equal(out[0, keep], clean[0][0, keep]) and torch.equal(out[1], clean[0][1])
+    for t in (1, 3):
+        assert (out[0, t, :, : D // 2] == float("inf")).all() and out[0, t, :, D // 2].isnan().all()
+        assert torch.equal(out[0, t, :, D // 2 + 1 :], clean[0][0, t, :, D // 2 + 1 :])
+    assert out[0, 2].isnan().all()
+
+
+def test_tree_wide_bad_pages_and_lengths():
+    rng = np.random.default_rng(8)
+    lens, T, hk, G = np.array([200, 150], np.int32), 12, 20, 8
+    assert scratch_of(lens, T, hk, G, 16, 64) > 0
+    table, _ = tables(lens, 16, 30, 14, rng)
+    table[0, 3], table[0, 5], table[1, 9] = 30, -7, 1 << 30
+    g = gen(4)
+    k, v = (pool((30, hk, 16, 64), torch.bfloat16, "hnd", g) for _ in range(2))
+    q = torch.randn((2, T, hk * G, 64), device="cuda", generator=g).bfloat16()
+    got = kv.ibp_tree_attention(q, k, v, dev(table), dev(lens))
+    check_attention(*got, *kv_ref.tree_attention(host(q), host(k), host(v), table, lens), "bf16")
+    err(ibp.IBP_ERANGE)
+    lens = np.array([T - 1, 0], np.int32)  # drafts longer than their sequences
+    got = kv.ibp_tree_attention(q, k, v, dev(table), dev(lens))
+    check_attention(*got, *kv_ref.tree_attention(host(q), host(k), host(v), table, lens), "bf16")
+    err(ibp.IBP_ERANGE)
+
+
+def test_tree_wide_strides_streams_graphs_and_the_same_bits():
+    g = gen(6)
+    lens, T, hk, G = np.array([900, 350, 60], np.int32), 9, 16, 8
+    assert scratch_of(lens, T, hk, G, 16, 64) > 0
+    table, _ = tables(lens, 16, 100, 60, np.random.default_rng(0))
+    k, v = (pool((100, hk, 16, 64), torch.float16, "hnd", g) for _ in range(2))
+    wide = torch.randn((3, T, 3, hk * G, 66), device="cuda", generator=g).half()
+    q = wide[:, :, 1, :, :64]  # 4-byte aligned rows of a fused projection
+    t, n = dev(table), dev(lens)
+    want = kv.ibp_tree_attention(q.contiguous(), k, v, t, n)
+    check_attention(*want, *kv_ref.tree_attention(host(q), host(k), host(v), table, lens), "f16")
+    for _ in range(3):
+        got = kv.ibp_tree_attention(q, k, v, t, n)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = kv.ibp_tree_attention(q, k, v, t, n, stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = kv.ibp_tree_attention(q, k, v, t, n)
+        again = kv.ibp_tree_attention(q, k, v, t, n)
+    for _ in range(20):
+        graph.replay()
+    assert torch.equal(got[0], want[0]) and torch.equal(again[0], want[0])
+
+
+def test_tree_wide_pool_past_32_bits():
+    n, page, D, T, G = 70000, 256, 128, 128, 8
+    assert scratch_of([600], T, 1, G, page, D) > 0
+    k = torch.zeros((n, 1, page, D), dtype=torch.bfloat16, device="cuda")
+    table = np.array([[n - 1, 3, n - 2]], np.int32)
+    g = gen(1)
+    for p in (n - 1, 3, n - 2):
+        k[p].normal_(generator=g)
+    q = torch.randn((1, T, G, D), device="cuda", generator=g).bfloat16()
+    got = kv.ibp_tree_attention(q, k, k, dev(table), dev(np.array([600])))
+    small, at = k[[n - 1, 3, n - 2]], np.array([[0, 1, 2]], np.int32)
+    check_attention(*got, *kv_ref.tree_attention(host(q), host(small), host(small), at, np.array([600])), "bf16")
+
+
+@pytest.mark.parametrize("T,G", [(2, 4), (16, 8), (40, 8)])
+def test_tree_wide_long_ragged(T, G):
+    """Ranges of many tiles that begin and end inside items, against the few-row kernel
+    (every sequence by itself, a kv head at a time)."""
+    lens = [9000, T, 4097, 300, 7001, 128, 2600]
+    hk, page, D = 8, 64, 128
+    assert scratch_of(lens, T, hk, G, page, D) > 0
+    rng = np.random.default_rng(4)
+    table, _ = tables(lens, page, 400, 142, rng)
+    g = gen(9)
+    k, v = (pool((400, hk, page, D), torch.bfloat16, "hnd", g) for _ in range(2))
+    q = torch.randn((len(lens), T, hk * G, D), device="cuda", generator=g).bfloat16()
+    words = dev(mask_words(random_tree(rng, len(lens), T)))
+    t, n = dev(table), dev(np.array(lens))
+    out, lse = kv.ibp_tree_attention(q, k, v, t, n, mask=words)
+    for _ in range(30):
+        again = kv.ibp_tree_attention(q, k, v, t, n, mask=words)
+    assert torch.equal(again[0], out)
+    for b in range(len(lens)):
+        for h in (0, hk - 1):
+            at = slice(h * G, h * G + G)
+            keys = k[t[b].long().clamp(min=0), h].reshape(-1, D)[: lens[b]].double()
+            vals = v[t[b].long().clamp(min=0), h].reshape(-1, D)[: lens[b]].double()
+            bits = (words[b].long()[:, torch.arange(T, device="cuda") // 32] >> (torch.arange(T, device="cuda") % 32)) & 1
+            sees = torch.cat([torch.ones(T, lens[b] - T, device="cuda"), bits], 1).bool()
+            s = torch.einsum("tgd,nd->tgn", q[b, :, at].double(), keys) / math.sqrt(D)
+            top = torch.einsum("tgd,nd->tgn", q[b, :, at].double().abs(), keys.abs()).amax(-1) / math.sqrt(D)
+            s = s.masked_fill(~sees[:, None], -math.inf)
+            p = torch.softmax(s, -1)
+            want = [x.cpu().numpy() for x in (p @ vals, torch.logsumexp(s, -1), p @ vals.abs(), top)]
+            check_attention(out[b, :, at], lse[b, :, at], *want, "bf16")
+
+
+# ---------------------------------------------------------------------------
 # Bounds and sparse attention
 
 
