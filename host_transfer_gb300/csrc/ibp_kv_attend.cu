@@ -16,6 +16,11 @@
 // Tensor-core work is far from the bound here: for 8 rows of 128 dimensions a
 // 16-token step is 16 instructions for 8 KB of cache.
 //
+// Measured on one GB300: 32 queries over 64 pages of 64 tokens each, 8 kv heads of
+// 4 query heads and 128 dimensions (533 MB): 84 us, 6.3 TB/s; 1022 queries of 8
+// heads over 24 pages of 32 tokens of 64 dimensions (803 MB out of L2): 74 us,
+// bound by issue (33 M instructions) and the few warps its stages leave room for.
+//
 // Softmax statistics and sums are 32-bit; the probabilities are rounded to the
 // cache's type for the second product (the tensor core wants both operands
 // alike), which adds an error of the size of the output's own rounding.

@@ -52,7 +52,7 @@ __device__ __forceinline__ bool finite_f(float x) { return fabsf(x) <= 3.4028234
 // A warp takes one head of one page: each lane holds the minima and maxima of
 // eight dimensions over every (32 / (dim / 8))-th token and the lanes of a
 // dimension meet at the end.  Bound by DRAM: the keys are read once, 16 bytes a
-// lane with eight loads in flight.
+// lane with eight loads in flight (737 MB: 117 us, 6.3 TB/s).
 template <bool F16>
 __global__ void __launch_bounds__(kSumThreads)
     k_kv_summarize(const KvView k, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
@@ -203,8 +203,9 @@ __device__ __forceinline__ int32_t query_place(const SelectArgs& a, uint32_t b, 
 // the upper), four or eight pages a lane group in flight, and the queries' 16 sums for the
 // same dimensions stay in registers.  One query is summed over its lanes by a
 // butterfly; eight are by a halving exchange that leaves each lane one query's
-// total, 7 to 9 shuffles for the eight.  Single tokens are bound by the codes'
-// bytes and the latency of two dependent loads, chunks by dp2a issue.
+// total, 7 to 9 shuffles for the eight.  Bound by the latency of two dependent
+// loads and the start of each CTA: 32 tokens over up to 1024 pages and 8 heads
+// (45 MB of codes) 18 us, 1022 tokens over up to 512 pages and 4 heads 23 us.
 // pages a lane group has in flight
 template <int NQ>
 constexpr uint32_t kScFly = NQ == 1 ? 8 : 4;
@@ -376,7 +377,8 @@ __device__ __forceinline__ uint32_t order_key(float s) {
 // 8-bit histogram over the scores that are neither forced nor hidden, and ends
 // early when a digit's keys are all wanted (two passes, as a rule); then each
 // warp counts what it takes in its own stretch of pages and writes it, ascending,
-// behind the warps before it.  Bound by the latency of its passes.
+// behind the warps before it.  Bound by the latency of its passes (256 rows of up
+// to 1024 pages 9 us, 4088 rows of up to 512 19 us).
 template <int NT>
 __global__ void __launch_bounds__(NT) k_kv_select(const SelectArgs a, uint32_t key_cap) {
   extern __shared__ uint32_t keys[];
