@@ -28,7 +28,8 @@
 // k_kv_tree_join in a fixed order.  Ragged lengths thus cost nothing and the
 // scratch is two slots per CTA.  The row blocks of a kv head are furthest apart
 // in that order and the number of CTAs is a multiple of theirs, so the CTAs that
-// read the same cache tiles do so at the same time and DRAM is read once.
+// read the same cache tiles do so at about the same time: two row blocks read
+// DRAM 1.5 times, not twice.
 //
 // Measured on one GB300: 16 ragged caches of up to 32768 tokens, 8 kv heads of 128
 // (1.48 GB): 64 rows a head 231 us (6.4 TB/s, 0.94 of the copy rate), 512 rows
