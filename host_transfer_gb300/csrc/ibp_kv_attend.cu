@@ -148,7 +148,8 @@ __device__ __forceinline__ Ahead look_ahead(const AttendArgs& a, const Item& it,
   if (ln.shift < -1 || sub * A::kSub >= it.n_tok) return x;
   const uint32_t at = ln.shift >= 0 ? sub >> ln.shift : sub * A::kSub / a.page_tokens;
   x.nth = PICK ? static_cast<uint32_t>(it.picks[at]) : at;
-  x.page = static_cast<uint32_t>(ln.row[x.nth]);
+  // the list may lie in the caller's buffer: an entry outside the table row is a bad page
+  if (!PICK || x.nth < a.max_pages) x.page = static_cast<uint32_t>(ln.row[x.nth]);
   return x;
 }
 
@@ -196,7 +197,7 @@ __device__ __forceinline__ void load_stage(const AttendArgs& a, const Item& it, 
     const uint32_t nth = PICK ? static_cast<uint32_t>(it.picks[at]) : at;
     pos = static_cast<int32_t>(nth * a.page_tokens + slot);
     if (pos < it.seen) {
-      page = static_cast<uint32_t>(ln.row[nth]);
+      if (!PICK || nth < a.max_pages) page = static_cast<uint32_t>(ln.row[nth]);
       if (page >= a.n_pages) {
         kv_status(a.status, IBP_ERANGE);
         page = 0xFFFFFFFFu;

@@ -189,9 +189,11 @@ __device__ __forceinline__ int dp2a(uint32_t a16, uint32_t b8, int c, bool high)
   return d;
 }
 
-// Position of query t of sequence b, or -1 where there is no such query.
+// Position of query t of sequence b, or -1 where there is no such query.  A count
+// above T is cut to it, as the attention does: both have to place a query alike,
+// for the attention reads as many entries of its list as its place calls for.
 __device__ __forceinline__ int32_t query_place(const SelectArgs& a, uint32_t b, uint32_t t, int32_t len) {
-  const int32_t n = a.n_live ? a.n_live[b] : static_cast<int32_t>(a.T);
+  const int32_t T = static_cast<int32_t>(a.T), raw = a.n_live ? a.n_live[b] : T, n = raw < T ? raw : T;
   if (static_cast<int32_t>(t) >= n) return -1;
   const int32_t p = len - n + static_cast<int32_t>(t);
   return p < 0 ? -1 : p;
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(NT) k_kv_select(const SelectArgs a, uint32_t k
   const int32_t place = query_place(a, b, t, len);
   if (tid == 0) {
     const int32_t nl = a.n_live ? a.n_live[b] : static_cast<int32_t>(a.T);
-    if (raw != len || nl > len || nl < 0) kv_status(a.status, IBP_ERANGE);
+    if (raw != len || nl > len || nl < 0 || nl > static_cast<int32_t>(a.T)) kv_status(a.status, IBP_ERANGE);
   }
   int32_t* out = a.picks + row * a.budget;
   const uint32_t n = place < 0 ? 0 : static_cast<uint32_t>(place) / a.page_tokens + 1;

@@ -1,0 +1,73 @@
+"""GPU tests of the paged key/value cache operators where a call's data, values or
+surroundings are out of the ordinary."""
+
+import numpy as np
+import pytest
+import torch
+
+from host_transfer_gb300 import ibp, kv
+from tests.kv_util import DTYPES, dev, pool, tables
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    yield
+    assert kv.ibp_kv_get_status(raise_on_error=False) == ibp.IBP_OK
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def err(code):
+    """The status the test has provoked, read and cleared."""
+    assert kv.ibp_kv_get_status(raise_on_error=False) == code
+
+
+class Cache:
+    """A small cache with the bounds of its keys, and queries."""
+
+    def __init__(self, lens, T, hk, G, page, D, dt="bf16", seed=0, spare=3):
+        rng = np.random.default_rng(seed)
+        self.np_lens = np.array(lens, np.int32)
+        n_pages = int((-(-self.np_lens // page)).sum()) + spare
+        self.np_table, self.np_refs = tables(lens, page, n_pages, max(1, -(-int(max(lens)) // page)) + 1, rng)
+        g = gen(seed)
+        self.k, self.v = (pool((n_pages, hk, page, D), DTYPES[dt], "hnd", g) for _ in range(2))
+        self.q = torch.randn((len(lens), T, hk * G, D), device="cuda", generator=g).to(DTYPES[dt])
+        self.table, self.lens, self.refs = dev(self.np_table), dev(self.np_lens), dev(self.np_refs)
+        self.codes = torch.zeros((n_pages, hk, 2, D), dtype=torch.int8, device="cuda")
+        self.scales = torch.zeros((n_pages, hk), device="cuda")
+        kv.ibp_kv_summarize(self.k, self.table, self.lens, self.codes, self.scales)
+
+    def sparse(self, budget, **kw):
+        return kv.ibp_sparse_attention(self.q, self.k, self.v, self.table, self.lens, self.codes, self.scales, budget, **kw)
+
+    def tree(self, **kw):
+        return kv.ibp_tree_attention(self.q, self.k, self.v, self.table, self.lens, **kw)
+
+
+# ---------------------------------------------------------------------------
+# Counts of queries and drafted tokens above T
+
+
+@pytest.mark.parametrize("page", [16, 7])  # whole steps a page, and steps that cross pages
+@pytest.mark.parametrize("T,more", [(1, 1), (1, 1989), (3, 2), (9, 60), (2, 2**31 - 3)])
+def test_more_queries_than_rows(T, more, page):
+    """n_query above T is an error; the call gives what n_query = T gives."""
+    c = Cache([2000, 40, 300], T, 2, 2, page, 64)
+    want = c.sparse(8, keep_first=1, keep_last=2)
+    got = c.sparse(8, keep_first=1, keep_last=2, n_query=dev(np.full(3, T + more)))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    err(ibp.IBP_ERANGE)
+
+
+@pytest.mark.parametrize("T,hk,G", [(3, 2, 2), (24, 16, 8)])
+def test_more_drafted_tokens_than_rows(T, hk, G):
+    c = Cache([700, 60, 300], T, hk, G, 16, 64)
+    want = c.tree()
+    got = c.tree(n_draft=dev(np.full(3, T + 5)))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    err(ibp.IBP_ERANGE)
