@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(kAtWarps * 32)
           cm[n][0] = fmaxf(cm[n][0], __shfl_xor_sync(0xFFFFFFFFu, cm[n][0], w));
           cm[n][1] = fmaxf(cm[n][1], __shfl_xor_sync(0xFFFFFFFFu, cm[n][1], w));
         }
+        if (F16) cm[n][0] = __fadd_ru(cm[n][0], -kLift<F16>), cm[n][1] = __fadd_ru(cm[n][1], -kLift<F16>);
       }
       bool grow = false;
 #pragma unroll
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kAtWarps * 32)
         for (uint32_t e = 0; e < 2; ++e) grow = grow || cm[n][e] > m[n][e];
       if (__any_sync(0xFFFFFFFFu, grow)) {
         // Rescale what was summed under the lower maximum.  At once: the largest
-        // probability is then exactly 1 and its rounding costs nothing, where a
+        // probability is then a power of two and its rounding costs nothing, where a
         // row has one key that outweighs the rest (putting it off until the
         // maximum had grown by 2^8 took the output's error from 1.1 to 1.5 of the
         // rounding of the result itself).
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(kAtWarps * 32)
     }
     if (lane == 0) {
       if (whole) {
-        if (a.lse) a.lse[orow] = (top + log2f(sum)) * 0.6931471805599453f;
+        if (a.lse) a.lse[orow] = row_lse<F16>(top, sum);
       } else {
         part[0] = top;
         part[1] = sum;
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kAtWarps * 32)
         *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) =
             pack2<F16>(acc[i].x * inv, acc[i].y * inv);
     }
-    if (lane == 0 && a.lse) a.lse[orow] = (top + log2f(sum)) * 0.6931471805599453f;
+    if (lane == 0 && a.lse) a.lse[orow] = row_lse<F16>(top, sum);
   }
   // no CTA leaves while another reads its shared memory
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(128) k_kv_join(const AttendArgs a, uint32_t ro
       *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) =
           pack2<F16>(acc[i].x * inv, acc[i].y * inv);
   }
-  if (lane == 0 && a.lse) a.lse[orow] = (top + log2f(sum)) * 0.6931471805599453f;
+  if (lane == 0 && a.lse) a.lse[orow] = row_lse<F16>(top, sum);
 }
 
 // ---------------------------------------------------------------------------

@@ -59,6 +59,22 @@ __device__ __forceinline__ int32_t clamp_len(int32_t len, uint32_t page_tokens, 
   return len < 0 ? 0 : (len > cap ? static_cast<int32_t>(cap) : len);
 }
 
+// Half precision ends at 2^-25, so with the largest probability at 1 a row's keys
+// below that would leave the product and stay in the sum: with one key that
+// outweighs the rest, 65536 others of 2^-25 are 0.2 % of the output.  Their powers
+// are taken against a reference kLift below the maximum, the same in product and sum,
+// so the largest is 2^15 and the smallest that counts 2^-40 of it.  The reference
+// is rounded up: no power is above 2^15.  bfloat16 has the exponents of a float.
+template <bool F16>
+constexpr float kLift = F16 ? 15.f : 0.f;
+
+// Natural logarithm of a row's sum of exponentials from its reference and sum;
+// the lift leaves the sum first, exactly, so that it costs the logarithm nothing.
+template <bool F16>
+__device__ __forceinline__ float row_lse(float top, float sum) {
+  return (F16 ? top + kLift<F16> + log2f(sum * (1.f / 32768.f)) : top + log2f(sum)) * 0.6931471805599453f;
+}
+
 struct KvMeta {  // arguments of the page bookkeeping kernels
   const int32_t* table;
   const int32_t* lens;

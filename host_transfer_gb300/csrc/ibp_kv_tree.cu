@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_tree_join(const __grid_cons
       *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) =
           tc::pack2<F16>(acc[e].x * inv, acc[e].y * inv);
   }
-  if (lane == 0 && a.lse) a.lse[orow] = (top + log2f(sum)) * 0.6931471805599453f;
+  if (lane == 0 && a.lse) a.lse[orow] = row_lse<F16>(top, sum);
 }
 
 static size_t align256(size_t x) { return (x + 255) / 256 * 256; }

@@ -18,7 +18,7 @@
 // two are taken wherever there are more than 128 rows.
 //
 // O is rescaled as soon as a row's maximum grows, so that the largest probability
-// is exactly 1 and its rounding to the cache's type costs nothing.  Putting the
+// is a power of two and its rounding to the cache's type costs nothing.  Putting the
 // rescaling off until the maximum has grown by 2^8 saves 2 % on two row tiles
 // (573 us to 587 us on the widest tree below) and takes the output's error
 // from 1.15 to 1.3 - 1.5 of the result's own rounding.
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       const bool exists = tok < a.T, live = static_cast<int32_t>(tok) < s.n_live;
       const uint32_t* words =
           a.mask ? a.mask + (static_cast<uint64_t>(s.b) * a.T + (live ? tok : 0)) * a.mask_words : nullptr;
-      float top = -INFINITY, sum = 0.f;  // running maximum (of score * log2 e) and sum
+      float top = -INFINITY, sum = 0.f;  // running maximum (of score * log2 e, less the lift) and sum
       const uint32_t o_col = tmem + lanes + S::kOCol + m * DP;
       for (uint32_t j = 0; j < s.tiles; ++j) {
         const uint32_t slot = MT == 2 ? m : (g + j) & 1u;
@@ -716,7 +716,8 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
 #pragma unroll
             for (uint32_t e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(x[i + e], x[i + e + 4]));
         }
-        const float tile_top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        const float high = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float tile_top = F16 ? __fmaf_ru(high, a.scale_log2, -kLift<F16>) : high * a.scale_log2;
         const bool grow = tile_top > top;
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float f = grow ? tc::ex2(top - tile_top) : 1.f;
@@ -828,7 +829,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       }
       if (!live) top = -INFINITY, sum = 0.f;
       if (whole) {
-        if (exists && a.lse) a.lse[orow] = (top + log2f(sum)) * 0.6931471805599453f;
+        if (exists && a.lse) a.lse[orow] = row_lse<F16>(top, sum);
       } else {
         t.ml_part[prow] = make_float2(top, sum);
       }

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 from host_transfer_gb300 import ibp, kv
-from tests.kv_util import DTYPES, dev, pool, tables
+from oracle import kv_ref
+from tests.kv_util import DTYPES, check_attention, dev, host, pool, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +72,33 @@ def test_more_drafted_tokens_than_rows(T, hk, G):
     got = c.tree(n_draft=dev(np.full(3, T + 5)))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     err(ibp.IBP_ERANGE)
+
+
+# ---------------------------------------------------------------------------
+# Values
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("form,page,D,G", [
+    ("tree", 20, 64, 1), ("tree", 20, 136, 3),      # few rows
+    ("tree", 64, 64, 4), ("tree", 64, 128, 136),    # tensor cores: one row tile, two
+    ("sparse", 64, 64, 2), ("sparse", 20, 128, 2),
+])
+def test_a_long_tail_under_one_key(form, page, D, G, dt):
+    """One key outweighs 65536 others of e^-17.55 (2^-25.3) each, which are 0.16 % of
+    the output together and all of it where the one key's value is zero."""
+    n = 65537
+    c = Cache([n], 1, 1, G, page, D, dt)
+    c.k.zero_(), c.q.zero_(), c.v.uniform_(0.5, 1.5, generator=gen(3))
+    c.k[..., 0] = -17.546875 if dt == "f16" else -17.5
+    c.q[..., 0] = 1
+    sink = int(c.np_table[0, 5000 // page]), 0, 5000 % page
+    c.k[sink] = 0
+    c.v[sink] = 0
+    if form == "tree":
+        out, lse = c.tree(scale=1.0)
+    else:
+        out, lse, _ = c.sparse(4096, scale=1.0)
+    want = kv_ref.tree_attention(host(c.q), host(c.k), host(c.v), c.np_table, c.np_lens, scale=1.0)
+    assert (want[0] > 1e-3).all()
+    check_attention(out, lse, *want, dt)
