@@ -51,6 +51,7 @@ namespace ibp {
 
 constexpr uint32_t kTcTile = 128;      // tokens of a cache tile, rows of a query tile
 constexpr uint32_t kTcMinTiles = 2;    // smallest share of a CTA
+constexpr float kTcLarge = 262144.f;   // scores (in powers of two) from which the rounding of the maximum shows
 constexpr long long kTcWait = 1ll << 32;  // clock cycles (about 2 s) after which a wait gives up
 
 struct TcArgs {
@@ -716,8 +717,30 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
 #pragma unroll
             for (uint32_t e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(x[i + e], x[i + e + 4]));
         }
-        const float high = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float tile_top = F16 ? __fmaf_ru(high, a.scale_log2, -kLift<F16>) : high * a.scale_log2;
+        float high = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // The exponent scale x - top keeps what the rounding of top lost, up to an ulp of
+        // it: nothing beside the row's own roundings for ordinary scores, but powers of two
+        // by the dozen for scores past 2^26.  A row with such a maximum has its scores
+        // scaled first, in place, so that its largest exponent is exact again.
+        const bool large = fabsf(high) * a.scale_log2 >= kTcLarge && fabsf(high) < INFINITY;
+        if (__any_sync(0xFFFFFFFFu, large)) {
+          const float f = large ? a.scale_log2 : 1.f;
+          tc::ld_wait32(y[0]);
+#pragma unroll 1
+          for (uint32_t c = 0; c < 4; ++c) {
+            float x[32];
+            tc::ld32(x, s_col + 32 * c);
+            tc::ld_wait32(x);
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) x[i] *= f;
+            tc::st32(s_col + 32 * c, x);
+          }
+          tc::st_wait();
+          tc::ld32(y[0], s_col);
+          high *= f;
+        }
+        const float scale = large ? 1.f : a.scale_log2;
+        const float tile_top = F16 ? __fmaf_ru(high, scale, -kLift<F16>) : high * scale;
         const bool grow = tile_top > top;
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float f = grow ? tc::ex2(top - tile_top) : 1.f;
@@ -741,7 +764,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
         }
         const float off = top == -INFINITY ? 0.f : -top;
         uint64_t part[2] = {0, 0};  // two sums of two lanes
-        const uint64_t scale2 = tc::two(a.scale_log2, a.scale_log2), off2 = tc::two(off, off);
+        const uint64_t scale2 = tc::two(scale, scale), off2 = tc::two(off, off);
         float w[32];
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {

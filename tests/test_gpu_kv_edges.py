@@ -102,3 +102,47 @@ def test_a_long_tail_under_one_key(form, page, D, G, dt):
     want = kv_ref.tree_attention(host(c.q), host(c.k), host(c.v), c.np_table, c.np_lens, scale=1.0)
     assert (want[0] > 1e-3).all()
     check_attention(out, lse, *want, dt)
+
+
+@pytest.mark.parametrize("G,page", [(2, 20), (4, 64), (136, 64)])
+def test_scores_of_all_magnitudes_in_half_precision(G, page):
+    """The powers stay within half precision where single precision is coarse: scores
+    from 2^-10 to 2^34 in steps, of either sign, equal ones side by side."""
+    D, n = 64, 300
+    c = Cache([n] * 140, 1, 2, G, page, D, "f16")
+    c.k.zero_(), c.q.zero_()
+    c.k[..., 0] = 1
+    c.q[..., 0] = 1
+    c.v.fill_(1.5)
+    for sign in (1, -1):
+        for e in range(-10, 35):
+            c.k[..., 0] = sign * 2.0 ** min(e, 15) * (1 + 2.0**-10)
+            out, lse = c.tree(scale=2.0 ** max(0, e - 15))
+            # every probability is rounded alike (2^-11), then the output is (2^-11); sums in 32 bits
+            assert ((out.double() - 1.5).abs() <= 1.5 * (2 * 2.0**-11 + 2.0**-15)).all()
+            score = sign * 2.0**e * (1 + 2.0**-10)
+            assert torch.allclose(lse.double(), torch.full_like(lse, 1).double() * (score + np.log(n)), rtol=2.0**-21, atol=2.0**-19)
+
+
+@pytest.mark.parametrize("dt,low", [("bf16", -3.3895313892515355e38), ("f16", -65504.0)])
+@pytest.mark.parametrize("G,page", [(2, 20), (4, 64), (136, 64)])
+def test_keys_of_the_lowest_value(G, page, dt, low):
+    """A row whose keys all give the type's lowest value is a mean like any other, and
+    beside ordinary keys they weigh nothing."""
+    n, D = 300, 64
+    c = Cache([n] * 140, 1, 2, G, page, D, dt)
+    c.k.zero_(), c.q.zero_()
+    c.k[..., 0] = low
+    c.q[..., 0] = 1
+    out, lse = c.tree()
+    few = slice(0, 3)
+    want = kv_ref.tree_attention(host(c.q)[few], host(c.k), host(c.v), c.np_table[few], c.np_lens[few])
+    u = 2.0**-8 if dt == "bf16" else 2.0**-11  # equal probabilities: rounded once, then the output
+    assert (np.abs(host(out)[few] - want[0]) <= (2 * u + 2.0**-15) * want[2] + 2.0**-25).all()
+    assert torch.equal(out.isfinite(), torch.ones_like(out, dtype=torch.bool)) and lse.isfinite().all()
+    c.k[:, :, 5::16, 0] = 0.25  # at least one in a tile of each row
+    out, lse = c.tree()
+    want = kv_ref.tree_attention(host(c.q)[few], host(c.k), host(c.v), c.np_table[few], c.np_lens[few])
+    # the kept keys' scores are equal: the same bound
+    assert (np.abs(host(out)[few] - want[0]) <= (2 * u + 2.0**-15) * want[2] + 2.0**-25).all()
+    assert np.abs(host(lse)[few] - want[1]).max() <= 2.0**-19
