@@ -86,22 +86,24 @@ def test_more_drafted_tokens_than_rows(T, hk, G):
 ])
 def test_a_long_tail_under_one_key(form, page, D, G, dt):
     """One key outweighs 65536 others of e^-17.55 (2^-25.3) each, which are 0.16 % of
-    the output together and all of it where the one key's value is zero."""
-    n = 65537
+    the output together and all of it where the one key's value is zero.  Sequences
+    enough that no row is shared out over CTAs with maxima of their own."""
+    n, B = 65537, 320
     c = Cache([n], 1, 1, G, page, D, dt)
     c.k.zero_(), c.q.zero_(), c.v.uniform_(0.5, 1.5, generator=gen(3))
     c.k[..., 0] = -17.546875 if dt == "f16" else -17.5
     c.q[..., 0] = 1
-    sink = int(c.np_table[0, 5000 // page]), 0, 5000 % page
-    c.k[sink] = 0
-    c.v[sink] = 0
+    first = int(c.np_table[0, 0]), 0, 0
+    c.k[first] = 0
+    c.v[first] = 0
+    want = kv_ref.tree_attention(host(c.q), host(c.k), host(c.v), c.np_table, c.np_lens, scale=1.0)
+    assert (want[0] > 1e-3).all()
+    c.table, c.lens, c.q = c.table.repeat(B, 1), c.lens.repeat(B), c.q.repeat(B, 1, 1, 1)
     if form == "tree":
         out, lse = c.tree(scale=1.0)
     else:
         out, lse, _ = c.sparse(4096, scale=1.0)
-    want = kv_ref.tree_attention(host(c.q), host(c.k), host(c.v), c.np_table, c.np_lens, scale=1.0)
-    assert (want[0] > 1e-3).all()
-    check_attention(out, lse, *want, dt)
+    check_attention(out, lse, *(x.repeat(B, 0) for x in want), dt)
 
 
 @pytest.mark.parametrize("G,page", [(2, 20), (4, 64), (136, 64)])
