@@ -7,11 +7,14 @@
 namespace ibp {
 
 // Every kernel of these operators is launched as a programmatic dependent: it
-// lets the next launch be placed at once and reads or writes no memory before
-// the previous kernel of the stream has completed.
+// reads or writes no memory before the previous kernel of the stream has
+// completed, and lets the next one be placed only then.  In the other order the
+// kernel after next could begin while this kernel's predecessor still writes: the
+// kernels here would wait for it all the same, but a decoder with
+// IBP_HINT_EARLY_FETCH reads its inputs before it waits.
 __device__ __forceinline__ void pdl_begin() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 template <typename... P, typename... A>

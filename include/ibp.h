@@ -516,7 +516,10 @@ int ibp_gather_raw(const uint32_t* rows, uint64_t n_rows, uint32_t W, const int6
  * Conventions beyond those at the top of this file:
  * - Every pointer is memory of the current device (tables and status words may
  *   also be mapped pinned host memory); calls are asynchronous on `stream`,
- *   launched as programmatic dependents and ordered on it.
+ *   launched as programmatic dependents and ordered on it.  Their kernels let
+ *   the kernel after them start when everything before them has completed, so
+ *   a decompress call with IBP_HINT_EARLY_FETCH behind one of them may read
+ *   anything but what the last kernel of that call writes.
  * - `status` is a device-accessible uint32 word of the caller, or NULL: data
  *   errors a kernel meets (a page or sequence id out of range: IBP_ERANGE; no
  *   free page: IBP_ENOMEM; a reference count below zero: IBP_ECORRUPT; a wait

@@ -148,3 +148,34 @@ def test_keys_of_the_lowest_value(G, page, dt, low):
     # the kept keys' scores are equal: the same bound
     assert (np.abs(host(out)[few] - want[0]) <= (2 * u + 2.0**-15) * want[2] + 2.0**-25).all()
     assert np.abs(host(lse)[few] - want[1]).max() <= 2.0**-19
+
+
+# ---------------------------------------------------------------------------
+# Order on the stream
+
+
+def test_early_fetch_behind_two_calls_reads_what_the_first_wrote():
+    """Compressed rows move as pages, another call follows, then a decode with the
+    early-fetch hint: the kernel just before it wrote none of its inputs, the one
+    before that all of them."""
+    n, W = 200000, 128
+    g = gen(1)
+    tables_ = [torch.randint(0, 1 << 20, (n, W), generator=g, device="cuda", dtype=torch.int32) | (5 << 24) for _ in range(2)]
+    plan = ibp.ibp_plan_create(*ibp.ibp_preprocess(tables_[0][:4096].contiguous(), 0.99))
+    old, new = [ibp.ibp_compress(plan, t.clone()) for t in tables_]
+    assert torch.equal(old[1], new[1])  # every row of both is compressed
+    pages = torch.empty((2 * n, 1, 1, W), dtype=torch.int32, device="cuda")
+    pages[n:, 0, 0] = new[0]
+    rows = torch.arange(n, dtype=torch.int32, device="cuda")
+    moves = torch.stack([rows + n, rows, torch.ones_like(rows)], 1).contiguous()
+    count, ids = dev(np.array([n])), torch.randperm(n, generator=g, device="cuda")
+    small = dev(np.array([[0, -1]])), dev(np.array([5])), dev(np.array([1, 0])), dev(np.array([0]))
+    plan.set_hints(ibp.IBP_HINT_EARLY_FETCH)
+    for _ in range(10):
+        pages[:n, 0, 0] = old[0]
+        torch.cuda.synchronize()
+        kv.ibp_kv_copy(pages, moves, count)
+        kv.ibp_kv_free(*small, 16)
+        out = ibp.ibp_gather_decompress(plan, pages[:n, 0, 0], new[1], ids)
+        assert torch.equal(out, tables_[1][ids])
+    assert ibp.ibp_get_status(plan) == ibp.IBP_OK
