@@ -28,7 +28,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_tree_join(const __grid_cons
   if (tok >= a.T) return;
   auto row_of = [&](uint32_t c) { return (2ull * c + (c < j ? 1 : 0)) * kRows + r; };
   // Weights of up to 32 parts at a time, a part a lane; their rows follow with
-  // four loads in flight.  The running maximum makes room for any number.
+  // four loads in flight.  The running maximum makes room for any number.  A part of
+  // weight 0 is added like the others: what is not finite in it the row has seen, and
+  // the result must not depend on where the ranges of the CTAs end.
   float top = -INFINITY, sum = 0.f;
   float2 acc[DP / 64];
 #pragma unroll
@@ -63,7 +65,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_tree_join(const __grid_cons
         const float wc = __shfl_sync(0xFFFFFFFFu, w, c + u);
 #pragma unroll
         for (uint32_t e = 0; e < DP / 64; ++e)
-          if (wc != 0.f) acc[e].x += wc * o[u][e].x, acc[e].y += wc * o[u][e].y;
+          acc[e].x += wc * o[u][e].x, acc[e].y += wc * o[u][e].y;
       }
     }
   }

@@ -150,6 +150,42 @@ def test_keys_of_the_lowest_value(G, page, dt, low):
     assert np.abs(host(lse)[few] - want[1]).max() <= 2.0**-19
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("n,T,G,page", [
+    (6000, 16, 8, 16), (6000, 40, 8, 64),   # tensor cores, ranges of a few tiles
+    (900, 3, 2, 16), (20000, 3, 2, 20),     # few rows: joined in a cluster, by a second kernel
+])
+def test_infinite_values_of_no_weight_are_seen_in_every_part(n, T, G, page, dt):
+    """One key of the context outweighs all others by 2^-288, so the parts of a split
+    row that hold the draft have weight 0; a drafted value that is not finite
+    decides the rows that see it all the same."""
+    D = 64
+    c = Cache([n], T, 1, G, page, D, dt)
+    c.k.zero_(), c.q.zero_()
+    c.q[..., 0] = 1
+    top = int(c.np_table[0, 0]), 0, 1
+    c.k[top][0] = 200
+    sees = np.tril(np.ones((T, T), bool))
+    sees[0, 0] = False  # row 0 sees no drafted token; token 1 is the infinite one
+    sees[T - 1, 1] = False
+    words = np.zeros((1, T, (T + 31) // 32), np.uint32)
+    for i in range(T):
+        words[0, :, i // 32] |= sees[:, i].astype(np.uint32) << np.uint32(i % 32)
+    mask = dev(words.view(np.int32))
+    clean, lse = c.tree(mask=mask, scale=1.0)
+    assert torch.equal(clean, c.v[top].expand_as(clean))
+    at = n - T + 1
+    c.v[int(c.np_table[0, at // page]), 0, at % page, 3] = float("inf")
+    c.v[int(c.np_table[0, at // page]), 0, at % page, 7] = float("nan")
+    out, lse2 = c.tree(mask=mask, scale=1.0)
+    assert torch.equal(lse, lse2)
+    hit = torch.from_numpy(sees[:, 1]).cuda()
+    assert torch.equal(out[0, ~hit], clean[0, ~hit])
+    assert not out[0, hit][..., [3, 7]].isfinite().any()
+    keep = [d for d in range(D) if d not in (3, 7)]
+    assert torch.equal(out[..., keep], clean[..., keep])
+
+
 # ---------------------------------------------------------------------------
 # Order on the stream
 
