@@ -4,6 +4,7 @@
 #include <stdio.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "ibp_kv_internal.cuh"
 
@@ -27,10 +28,13 @@ int current_device(int* device) {
   return IBP_OK;
 }
 
-// Replaces p by the address kernels use; NULL stays NULL when `optional`.
+// Replaces p by the address kernels use; NULL stays NULL when `optional`.  An
+// address that is not a multiple of its type's size would be a fault on the GPU.
 template <typename T>
 bool resolve(T*& p, int device, bool optional = false) {
   if (!p) return optional;
+  if constexpr (!std::is_void_v<T>)
+    if (reinterpret_cast<uintptr_t>(p) % alignof(T)) return false;
   const void* d;
   if (resolve_ptr(p, device, &d)) return false;
   p = static_cast<T*>(const_cast<void*>(d));
@@ -62,7 +66,7 @@ int meta_of(KvMeta* m, const ibp_kv_seqs* s, uint32_t page_tokens, const int32_t
   const bool rows = s->n_seqs > 0, entries = rows && s->max_pages > 0;
   if (!resolve(m->table, device, !entries) || !resolve(m->lens, device, !rows) || !resolve(m->refs, device) ||
       !resolve(m->refs_out, device) || !resolve(m->status, device, true))
-    return refuse("a table, length, reference or status pointer is not device-accessible");
+    return refuse("a table, length, reference or status pointer is misaligned or not device-accessible");
   return IBP_OK;
 }
 
@@ -151,7 +155,7 @@ int attend_of(AttendArgs* a, const ibp_kv_pages* k, const ibp_kv_pages* v, uint3
   if (!resolve(a->q, device) || !resolve(a->out, device) || !resolve(a->lse, device, true) ||
       !resolve(a->part, device, true) || !resolve(a->table, device, seqs->max_pages == 0) ||
       !resolve(a->lens, device) || !resolve(a->n_live, device, true) || !resolve(a->status, device, true))
-    return refuse("a pointer is NULL or not device-accessible");
+    return refuse("a pointer is NULL, misaligned or not device-accessible");
   if ((reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->out)) % 4 ||
       (static_cast<uint64_t>(qs) | static_cast<uint64_t>(qt) | static_cast<uint64_t>(qh)) % 2)
     return refuse("q is not 4-byte aligned in base and strides, or out in base");
@@ -193,7 +197,7 @@ int ibp_kv_fork(const ibp_kv_seqs* seqs, uint32_t page_tokens, const int32_t* re
   if (!resolve(parents, device, !rows) || !resolve(m.table_out, device, !rows || !m.max_pages) ||
       !resolve(m.lens_out, device, !rows) || !resolve(m.moves, device, !rows) || !resolve(m.count, device) ||
       !resolve(m.ws, device))
-    return refuse("a pointer is NULL or not device-accessible");
+    return refuse("a pointer is NULL, misaligned or not device-accessible");
   if (ws_bytes < ibp_kv_pages_workspace(n_pages, n_out)) return refuse("ws is smaller than ibp_kv_pages_workspace");
   const size_t row = 4ull * m.max_pages;
   if (overlap(m.table, row * m.n_seqs, m.table_out, row * n_out) ||
@@ -214,7 +218,7 @@ int ibp_kv_free(const ibp_kv_seqs* seqs, uint32_t page_tokens, const int32_t* re
   if (rc) return rc;
   if (!resolve(rows, device, n_rows == 0) || !resolve(m.table_out, device, !m.n_seqs || !m.max_pages) ||
       !resolve(m.lens_out, device, !m.n_seqs))
-    return refuse("a pointer is NULL or not device-accessible");
+    return refuse("a pointer is NULL, misaligned or not device-accessible");
   return launch_kv_free(m, rows, n_rows, static_cast<cudaStream_t>(stream));
 }
 
@@ -231,7 +235,7 @@ int ibp_kv_compact(const ibp_kv_seqs* seqs, uint32_t page_tokens, const int32_t*
   m.moves = moves, m.count = count, m.ws = static_cast<int32_t*>(ws);
   if (!resolve(m.table_out, device, !m.n_seqs || !m.max_pages) || !resolve(m.moves, device) ||
       !resolve(m.count, device) || !resolve(m.ws, device))
-    return refuse("a pointer is NULL or not device-accessible");
+    return refuse("a pointer is NULL, misaligned or not device-accessible");
   if (ws_bytes < ibp_kv_pages_workspace(n_pages, 0)) return refuse("ws is smaller than ibp_kv_pages_workspace");
   return launch_kv_compact(m, static_cast<cudaStream_t>(stream));
 }
@@ -247,7 +251,7 @@ int ibp_kv_copy(const ibp_kv_pages* pages, const int32_t* moves, const int32_t* 
   if (rc) return rc;
   if (max_moves == 0) return IBP_OK;
   if (!resolve(moves, device) || !resolve(count, device) || !resolve(status, device, true))
-    return refuse("a pointer is NULL or not device-accessible");
+    return refuse("a pointer is NULL, misaligned or not device-accessible");
   return launch_kv_copy(r, moves, count, max_moves, status, device, static_cast<cudaStream_t>(stream));
 }
 
@@ -270,7 +274,7 @@ int ibp_kv_accept(const ibp_kv_pages* pages, const ibp_kv_seqs* seqs, const int3
   }
   if (!resolve(n_draft, device) || !resolve(path, device, max_accept == 0) || !resolve(n_accept, device) ||
       !resolve(m.table_out, device, !m.max_pages) || !resolve(m.lens_out, device))
-    return refuse("a pointer is NULL or not device-accessible");
+    return refuse("a pointer is NULL, misaligned or not device-accessible");
   return launch_kv_accept(r, m, n_draft, path, n_accept, max_accept, device, static_cast<cudaStream_t>(stream));
 }
 
@@ -299,7 +303,7 @@ int ibp_tree_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t dt
                  out, lse, ws, status, device);
   if (rc) return rc;
   a.mask = mask;
-  if (!resolve(a.mask, device, true)) return refuse("mask is not device-accessible");
+  if (!resolve(a.mask, device, true)) return refuse("mask is misaligned or not device-accessible");
   const size_t need = ibp_tree_attention_workspace(seqs->n_seqs, seqs->max_pages, k->page_tokens, T, q_heads, k->heads, k->dim);
   if (need && (ws_bytes < need || !ws))
     return refuse("ws is smaller than ibp_tree_attention_workspace");
@@ -324,7 +328,7 @@ int ibp_kv_summarize(const ibp_kv_pages* k, uint32_t dtype, const ibp_kv_seqs* s
   const int32_t *table = seqs->table, *lens = seqs->lens;
   if (!resolve(table, device) || !resolve(lens, device) || !resolve(first, device, true) || !resolve(codes, device) ||
       !resolve(scales, device) || !resolve(status, device, true))
-    return refuse("a pointer is NULL or not device-accessible");
+    return refuse("a pointer is NULL, misaligned or not device-accessible");
   if (reinterpret_cast<uintptr_t>(codes) % 4) return refuse("codes is not 4-byte aligned");
   return launch_kv_summarize(kv, table, lens, first, seqs->n_seqs, seqs->max_pages, static_cast<uint32_t>(k->n_pages),
                              k->page_tokens, k->heads, k->dim, dtype == IBP_KV_F16, codes, scales, status, device,
@@ -363,7 +367,7 @@ int ibp_sparse_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t 
   if (static_cast<uint64_t>(a.group) * a.dim > 65536 || a.group > 256)
     return refuse("a group of more than 256 heads or 65536 elements");
   if (!resolve(codes, device) || !resolve(scales, device) || !resolve(pages_out, device, true))
-    return refuse("a pointer is NULL or not device-accessible");
+    return refuse("a pointer is NULL, misaligned or not device-accessible");
   if (reinterpret_cast<uintptr_t>(codes) % 4) return refuse("codes is not 4-byte aligned");
   if (!ws || ws_bytes < ibp_sparse_attention_workspace(seqs->n_seqs, seqs->max_pages, k->page_tokens, T, q_heads,
                                                         k->heads, k->dim, budget))

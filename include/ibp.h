@@ -515,7 +515,7 @@ int ibp_gather_raw(const uint32_t* rows, uint64_t n_rows, uint32_t W, const int6
  *
  * Conventions beyond those at the top of this file:
  * - Every pointer is memory of the current device (tables and status words may
- *   also be mapped pinned host memory); calls are asynchronous on `stream`,
+ *   also be mapped pinned host memory) and aligned to its type; calls are asynchronous on `stream`,
  *   launched as programmatic dependents and ordered on it.  Their kernels let
  *   the kernel after them start when everything before them has completed, so
  *   a decompress call with IBP_HINT_EARLY_FETCH behind one of them may read

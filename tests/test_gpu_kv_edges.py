@@ -1,6 +1,8 @@
 """GPU tests of the paged key/value cache operators where a call's data, values or
 surroundings are out of the ordinary."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -215,3 +217,64 @@ def test_early_fetch_behind_two_calls_reads_what_the_first_wrote():
         out = ibp.ibp_gather_decompress(plan, pages[:n, 0, 0], new[1], ids)
         assert torch.equal(out, tables_[1][ids])
     assert ibp.ibp_get_status(plan) == ibp.IBP_OK
+
+
+# ---------------------------------------------------------------------------
+# Refusals
+
+
+def test_misaligned_pointers_are_refused():
+    """Every 32-bit array of the C entry points, two bytes off its alignment, is refused
+    before a launch."""
+    lib = kv._load()
+    c = Cache([40, 20], 1, 2, 2, 16, 64)
+    none = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    room = [torch.zeros(4096, dtype=torch.int32, device="cuda") for _ in range(13)]
+    table, lens, refs, parents, t_out, l_out, r_out, moves, count, ws, word, path, lse = [r.data_ptr() for r in room]
+    n = len(c.np_refs)
+    kp, vp = kv._as_pages("k", c.k), kv._as_pages("v", c.v)
+    kp.data, vp.data = c.k.data_ptr(), c.v.data_ptr()
+    q, out = c.q.data_ptr(), torch.empty_like(c.q)
+    codes, scales = c.codes, c.scales
+    rows = (*c.q.stride()[:3], 1, 4)
+    size = 4096 * 4
+
+    def seqs(a):
+        return kv._Seqs(a["table"], a["lens"], 2, c.table.shape[1])
+
+    calls = {
+        "fork": (lambda a: lib.ibp_kv_fork(seqs(a), 16, a["refs"], n, a["parents"], 2, a["t_out"], a["l_out"], a["r_out"],
+                                           a["moves"], a["count"], a["ws"], size, a["word"], none),
+                 dict(table=table, lens=lens, refs=refs, parents=parents, t_out=t_out, l_out=l_out, r_out=r_out, moves=moves,
+                      count=count, ws=ws, word=word)),
+        "free": (lambda a: lib.ibp_kv_free(seqs(a), 16, a["refs"], n, a["rows"], 1, a["t_out"], a["l_out"], a["r_out"],
+                                           a["word"], none),
+                 dict(table=table, lens=lens, refs=refs, rows=parents, t_out=t_out, l_out=l_out, r_out=r_out, word=word)),
+        "compact": (lambda a: lib.ibp_kv_compact(seqs(a), 16, a["refs"], n, a["t_out"], a["r_out"], a["moves"], a["count"],
+                                                 a["ws"], size, a["word"], none),
+                    dict(table=table, lens=lens, refs=refs, t_out=t_out, r_out=r_out, moves=moves, count=count, ws=ws,
+                         word=word)),
+        "copy": (lambda a: lib.ibp_kv_copy(kp, a["moves"], a["count"], 1, a["word"], none),
+                 dict(moves=moves, count=count, word=word)),
+        "accept": (lambda a: lib.ibp_kv_accept(kp, seqs(a), a["refs"], a["n_draft"], a["path"], a["n_accept"], 1, a["t_out"],
+                                               a["l_out"], a["r_out"], a["word"], none),
+                   dict(table=table, lens=lens, refs=refs, n_draft=parents, path=path, n_accept=count, t_out=t_out,
+                        l_out=l_out, r_out=r_out, word=word)),
+        "tree": (lambda a: lib.ibp_tree_attention(kp, vp, 0, seqs(a), q, *rows, a["n_draft"], a["mask"], 1.0, out.data_ptr(),
+                                                  a["lse"], None, 0, a["word"], none),
+                 dict(table=table, lens=lens, n_draft=parents, mask=path, lse=lse, word=word)),
+        "summarize": (lambda a: lib.ibp_kv_summarize(kp, 0, seqs(a), a["first"], a["codes"], a["scales"], a["word"], none),
+                      dict(table=table, lens=lens, first=parents, codes=codes.data_ptr(), scales=scales.data_ptr(),
+                           word=word)),
+        "sparse": (lambda a: lib.ibp_sparse_attention(kp, vp, 0, seqs(a), a["codes"], a["scales"], q, *rows, a["n_query"], 2,
+                                                      1, 1, 1.0, out.data_ptr(), a["lse"], a["pages"], ws, size, a["word"],
+                                                      none),
+                   dict(table=table, lens=lens, n_query=parents, codes=codes.data_ptr(), scales=scales.data_ptr(), lse=lse,
+                        pages=moves, word=word)),
+    }
+    for name, (call, args) in calls.items():
+        assert call(args) == ibp.IBP_OK, name  # lengths, counts and lists of zeros: little to do
+        for which in args:
+            assert call({**args, which: args[which] + 2}) == ibp.IBP_EINVAL, (name, which)
+            assert lib.ibp_last_error_detail(), (name, which)
+    torch.cuda.synchronize()
