@@ -313,6 +313,10 @@ int ibp_tree_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t dt
   return launch_kv_attend(a, device, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
+uint64_t ibp_kv_set_wait_limit(uint64_t cycles) {
+  return kv_tree_wait_limit(cycles < IBP_KV_WAIT_CYCLES ? cycles : IBP_KV_WAIT_CYCLES);
+}
+
 int ibp_kv_summarize(const ibp_kv_pages* k, uint32_t dtype, const ibp_kv_seqs* seqs, const int32_t* first,
                      int8_t* codes, float* scales, uint32_t* status, void* stream) {
   clear_error_detail();

@@ -151,6 +151,8 @@ int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_
 size_t kv_tree_workspace(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint32_t page_tokens,
                          uint64_t tokens, int device);
 
+uint64_t kv_tree_wait_limit(uint64_t cycles);  // sets it, returns the one before
+
 struct SelectArgs {
   const char* q;
   int64_t q_seq, q_token, q_head;  // bytes

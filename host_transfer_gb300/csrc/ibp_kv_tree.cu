@@ -160,6 +160,10 @@ static int launch(TcArgs& t, const CUtensorMap& mk, const CUtensorMap& mv, int d
                    dim3(t.n_ctas - 1, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows)), kJoinThreads, 0, 1, stream, t);
 }
 
+static std::atomic<uint64_t> wait_limit{IBP_KV_WAIT_CYCLES};
+
+uint64_t kv_tree_wait_limit(uint64_t cycles) { return wait_limit.exchange(cycles, std::memory_order_relaxed); }
+
 int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_t stream, bool* done) {
   *done = false;
   const uint64_t rows = static_cast<uint64_t>(a.T) * a.group;
@@ -177,6 +181,7 @@ int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_
   TcArgs t = {};
   t.a = a;
   t.box = box;
+  t.limit = static_cast<long long>(wait_limit.load(std::memory_order_relaxed));
   t.row_pairs = static_cast<uint32_t>((rows + mt * kTcTile - 1) / (mt * kTcTile));
   t.q16 = ((reinterpret_cast<uintptr_t>(a.q) | static_cast<uint64_t>(a.q_seq) | static_cast<uint64_t>(a.q_token) |
             static_cast<uint64_t>(a.q_head)) & 15u) == 0;

@@ -37,8 +37,10 @@
 // sustained one; without any softmax work the products alone take 502 us, the clock
 // being held down by power).
 //
-// Every wait has a limit (kTcWait): a CTA that runs into it raises a flag all its
-// waits heed, records IBP_ETIMEOUT, waits for its copies and returns.
+// Every wait has a limit: a CTA that runs into it raises a flag all its waits heed,
+// records IBP_ETIMEOUT and returns.  Whether it does or not, the producer leaves
+// when its last copies have landed and the MMA warp when its last products and
+// their arrivals are done, so nothing writes to a CTA that has left.
 #pragma once
 
 #include <cuda.h>
@@ -52,7 +54,7 @@ namespace ibp {
 constexpr uint32_t kTcTile = 128;      // tokens of a cache tile, rows of a query tile
 constexpr uint32_t kTcMinTiles = 2;    // smallest share of a CTA
 constexpr float kTcLarge = 262144.f;   // scores (in powers of two) from which the rounding of the maximum shows
-constexpr long long kTcWait = 1ll << 32;  // clock cycles (about 2 s) after which a wait gives up
+constexpr long long kTcWait = IBP_KV_WAIT_CYCLES;  // clock cycles (about 2 s) after which a wait gives up
 
 struct TcArgs {
   AttendArgs a;
@@ -64,6 +66,7 @@ struct TcArgs {
   int4* first;        // [per CTA]: sequence, kv head, row block of its first segment, its tiles before the range;
                       // then one entry: the tiles of a CTA's range, as 64 bits
   uint32_t n_ctas;
+  long long limit;    // clock cycles after which a wait gives up
 };
 
 namespace tc {
@@ -88,17 +91,24 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// False when the limit was met or another wait of the CTA has met it.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* stop) {
-  if (bar_try(bar, parity)) return true;
+// False when the limit was met or another wait of the CTA has met it.  A limit of 0
+// is met at once, done or not.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* stop, long long limit) {
+  if (limit && bar_try(bar, parity)) return true;
   const long long t0 = clock64();
-  while (clock64() - t0 < kTcWait) {
+  while (clock64() - t0 < limit) {
     for (uint32_t i = 0; i < 16; ++i)
       if (bar_try(bar, parity)) return true;
     if (*stop) return false;
   }
   *stop = 1;
   return false;
+}
+// Waits for what the CTA has in flight itself, whatever the flag says.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!bar_try(bar, parity) && clock64() - t0 < kTcWait) {
+  }
 }
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int tok, int head, int page,
@@ -230,7 +240,7 @@ struct TcShape {
 
 struct TcShared {
   uint64_t full[11], empty[11];
-  uint64_t s_full[2], p_full[2][2], pv_done[2], q_full[2];  // p_full: per slot and half
+  uint64_t s_full[2], p_full[2][2], pv_done[2], q_full[2], done;  // p_full: per slot and half
   uint32_t tmem;
   uint32_t stop;
   uint32_t odd[2];    // even and odd segments: 1 + the last whose draft holds infinities or NaN among its values
@@ -356,6 +366,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       tc::bar_init(tc::s32(&sh.pv_done[i]), 1);
       tc::bar_init(tc::s32(&sh.q_full[i]), 128);
     }
+    tc::bar_init(tc::s32(&sh.done), 1);
     sh.stop = 0;
     sh.odd[0] = sh.odd[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -449,7 +460,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
         const uint32_t bytes = n * t.box * 128 * S::kHalves;
 #pragma unroll
         for (uint32_t kv = 0; kv < 2; ++kv, ++f) {
-          ok = tc::bar_wait(tc::s32(&sh.empty[ring(f)]), ring_phase(f) ^ 1u, stop);
+          ok = tc::bar_wait(tc::s32(&sh.empty[ring(f)]), ring_phase(f) ^ 1u, stop, t.limit);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           const uint32_t bar = tc::s32(&sh.full[ring(f)]), dst = ring_at(f) + lane * t.box * 128;
@@ -462,13 +473,10 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
         }
       }
     }
-    if (!ok || *stop)  // copies in flight land before the CTA leaves
-      for (uint32_t i = 0; i < S::kSlots; ++i) {
-        const uint32_t n = (f + S::kSlots - 1 - i) / S::kSlots;  // fills of slot i
-        const long long t0 = clock64();
-        while (n && clock64() - t0 < kTcWait && !tc::bar_try(tc::s32(&sh.full[i]), (n - 1) & 1u)) {
-        }
-      }
+    for (uint32_t i = 0; i < S::kSlots; ++i) {  // copies in flight land before the CTA leaves
+      const uint32_t n = (f + S::kSlots - 1 - i) / S::kSlots;  // fills of slot i
+      if (n) tc::bar_drain(tc::s32(&sh.full[i]), (n - 1) & 1u);
+    }
   } else if (warp == MT * 4 + 1) {
     // ---- MMA
     const uint32_t fmt = F16 ? 0u : 1u;
@@ -510,7 +518,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       __syncwarp();
     };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool r = tc::bar_wait(tc::s32(bar), parity, stop);
+      const bool r = tc::bar_wait(tc::s32(bar), parity, stop, t.limit);
       return __all_sync(0xFFFFFFFFu, r) != 0;
     };
     auto release = [&](uint64_t* bar) {
@@ -621,6 +629,10 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       g += n;
       ++segs;
     }
+    // the last products and the arrivals they cause end before the CTA leaves
+    release(&sh.done);
+    tc::bar_drain(tc::s32(&sh.done), 0);
+    __syncwarp();
   } else if (warp < MT * 4) {
     // ---- softmax: warpgroup m, a thread per row
     const uint32_t m = warp / 4, r = tid & 127u;
@@ -659,7 +671,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
     // barrier: its product before was done when this tile's scores were, and its
     // next one needs this thread's P.
     auto product_done = [&](uint32_t x) {
-      const bool r = tc::bar_wait(tc::s32(&sh.pv_done[MT == 2 ? m : x & 1u]), (MT == 2 ? x : x >> 1) & 1u, stop);
+      const bool r = tc::bar_wait(tc::s32(&sh.pv_done[MT == 2 ? m : x & 1u]), (MT == 2 ? x : x >> 1) & 1u, stop, t.limit);
       return __all_sync(0xFFFFFFFFu, r) != 0;
     };
     bool more = walk.next(&s);
@@ -681,7 +693,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
       for (uint32_t j = 0; j < s.tiles; ++j) {
         const uint32_t slot = MT == 2 ? m : (g + j) & 1u;
         const uint32_t ph = MT == 2 ? (g + j) & 1u : ((g + j) >> 1) & 1u;
-        ok = tc::bar_wait(tc::s32(&sh.s_full[slot]), ph, stop);
+        ok = tc::bar_wait(tc::s32(&sh.s_full[slot]), ph, stop, t.limit);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc::fence_after();
@@ -749,7 +761,10 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
           if (j > 0) {
             // O holds the sums up to the tile before
             ok = product_done(g + j - 1);
-            if (!ok) break;
+            if (!ok) {
+              tc::ld_wait32(y[0]);  // no load is under way into registers that are used again
+              break;
+            }
             tc::fence_after();
 #pragma unroll
             for (uint32_t c = 0; c < DP / 32; ++c) {

@@ -42,6 +42,7 @@ IBP_KV_BF16 = 0
 IBP_KV_F16 = 1
 IBP_KV_MAX_DIM = 256
 IBP_SPARSE_MAX_BUDGET = 4096
+IBP_KV_WAIT_CYCLES = 1 << 32
 
 _DTYPES = {torch.bfloat16: IBP_KV_BF16, torch.float16: IBP_KV_F16}
 
@@ -79,6 +80,7 @@ def _load():
         "ibp_tree_attention": ([pages, pages, u32, seqs, vp, i64, i64, i64, u32, u32, vp, vp, f32, vp, vp, vp, size,
                                 vp, vp], i32),
         "ibp_tree_attention_workspace": ([u32] * 7, size),
+        "ibp_kv_set_wait_limit": ([u64], u64),
         "ibp_kv_summarize": ([pages, u32, seqs, vp, vp, vp, vp, vp], i32),
         "ibp_sparse_attention": ([pages, pages, u32, seqs, vp, vp, vp, i64, i64, i64, u32, u32, vp, u32, u32, u32,
                                   f32, vp, vp, vp, vp, size, vp, vp], i32),
@@ -441,6 +443,12 @@ def ibp_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table:
                                       out.data_ptr(), lse.data_ptr(), None if ws is None else ws.data_ptr(), size,
                                       _status(status, device), handle), "ibp_tree_attention")
     return out, lse
+
+
+def ibp_kv_set_wait_limit(cycles: int = IBP_KV_WAIT_CYCLES) -> int:
+    """Clock cycles after which a wait inside ibp_tree_attention gives up with
+    IBP_ETIMEOUT (0: at once, to test what follows); returns the limit before."""
+    return _load().ibp_kv_set_wait_limit(cycles)
 
 
 def _bounds(k: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):

@@ -68,8 +68,9 @@ extern "C" {
 
 /* 3: ibp_plan_info.short_rows, ibp_get_status_async, IBP_HINT_EARLY_FETCH
  * 4: the paged key/value cache entry points (ibp_kv_*, ibp_tree_attention,
- *    ibp_sparse_attention) */
-#define IBP_VERSION 4
+ *    ibp_sparse_attention)
+ * 5: ibp_kv_set_wait_limit */
+#define IBP_VERSION 5
 #define IBP_MAX_W 8192u
 #define IBP_NOALLOC_MAX_W 4096u
 
@@ -668,6 +669,17 @@ int ibp_tree_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t dt
                        void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* status, void* stream);
 size_t ibp_tree_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t page_tokens, uint32_t T,
                                     uint32_t q_heads, uint32_t kv_heads, uint32_t dim);
+
+/*
+ * Clock cycles after which a wait inside a kernel of ibp_tree_attention gives up:
+ * the kernel records IBP_ETIMEOUT and ends, and the call's results are undefined.
+ * No call meets the default (about two seconds) unless something else is wrong;
+ * with 0 every wait gives up, which lets a program test what it does then.  Values
+ * above the default mean the default.  Holds for later calls of the process, on every
+ * device; returns the limit before.
+ */
+#define IBP_KV_WAIT_CYCLES 0x100000000ull
+uint64_t ibp_kv_set_wait_limit(uint64_t cycles);
 
 /*
  * Bounds of a page's keys in 8 bits, the cheap stand-in that

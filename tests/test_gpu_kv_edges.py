@@ -278,3 +278,35 @@ def test_misaligned_pointers_are_refused():
             assert call({**args, which: args[which] + 2}) == ibp.IBP_EINVAL, (name, which)
             assert lib.ibp_last_error_detail(), (name, which)
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# Waits that run out
+
+
+@pytest.mark.parametrize("lens,T,hk,G,page,D", [
+    ([700, 60, 1300], 4, 40, 4, 16, 128),   # one row tile
+    ([700, 2000], 40, 12, 5, 64, 64),       # two
+])
+def test_waits_that_run_out_end_the_call(lens, T, hk, G, page, D):
+    """Every wait of the kernel has a limit.  Met, the kernel reports IBP_ETIMEOUT and ends, and
+    the calls behind it are right; the limits here are met in ordinary work."""
+    c = Cache(lens, T, hk, G, page, D)
+    want = c.tree()
+    err(ibp.IBP_OK)
+    try:
+        for limit in (0, 1, 300, 1000, 3000, 10000):
+            kv.ibp_kv_set_wait_limit(limit)
+            got = c.tree()
+            code = kv.ibp_kv_get_status(raise_on_error=False)
+            assert code == ibp.IBP_ETIMEOUT if limit == 0 else code in (ibp.IBP_OK, ibp.IBP_ETIMEOUT)
+            if code == ibp.IBP_OK:
+                assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            assert kv.ibp_kv_set_wait_limit() == limit
+            got = c.tree()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            err(ibp.IBP_OK)
+    finally:
+        assert kv.ibp_kv_set_wait_limit() == kv.IBP_KV_WAIT_CYCLES
+    assert kv.ibp_kv_set_wait_limit(1 << 40) == kv.IBP_KV_WAIT_CYCLES  # no more than the default
+    assert kv.ibp_kv_set_wait_limit() == kv.IBP_KV_WAIT_CYCLES
