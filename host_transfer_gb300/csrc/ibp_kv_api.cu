@@ -43,19 +43,20 @@ bool resolve(T*& p, int device, bool optional = false) {
 
 constexpr uint64_t kMaxPages = 0x7FFFFFFFull;
 
-int check_seqs(const ibp_kv_seqs* s, uint32_t page_tokens) {
+int check_seqs(const ibp_kv_seqs* s, uint32_t page_tokens, bool lens_read = true) {
   if (!s) return refuse("seqs is NULL");
   if (page_tokens == 0 || page_tokens > 65536) return refuse("page_tokens outside [1, 65536]");
   if (s->n_seqs > 65535) return refuse("more than 65535 sequences");
   if (static_cast<uint64_t>(s->max_pages) * page_tokens > 0x7FFFFF00ull)
     return refuse("max_pages * page_tokens is 2^31 or more");
-  if (s->n_seqs && (!s->lens || (s->max_pages && !s->table))) return refuse("table or lens is NULL");
+  if (s->n_seqs && ((lens_read && !s->lens) || (s->max_pages && !s->table))) return refuse("table or lens is NULL");
   return IBP_OK;
 }
 
 int meta_of(KvMeta* m, const ibp_kv_seqs* s, uint32_t page_tokens, const int32_t* refs, uint64_t n_pages,
-            int32_t* table_out, int32_t* lens_out, int32_t* refs_out, uint32_t* status, int device) {
-  const int rc = check_seqs(s, page_tokens);
+            int32_t* table_out, int32_t* lens_out, int32_t* refs_out, uint32_t* status, int device,
+            bool lens_read = true) {
+  const int rc = check_seqs(s, page_tokens, lens_read);
   if (rc) return rc;
   if (n_pages == 0 || n_pages > kMaxPages) return refuse("n_pages outside [1, 2^31)");
   *m = {};
@@ -64,7 +65,7 @@ int meta_of(KvMeta* m, const ibp_kv_seqs* s, uint32_t page_tokens, const int32_t
   m->n_pages = static_cast<uint32_t>(n_pages);
   m->table_out = table_out, m->lens_out = lens_out, m->refs_out = refs_out, m->status = status;
   const bool rows = s->n_seqs > 0, entries = rows && s->max_pages > 0;
-  if (!resolve(m->table, device, !entries) || !resolve(m->lens, device, !rows) || !resolve(m->refs, device) ||
+  if (!resolve(m->table, device, !entries) || !resolve(m->lens, device, !rows || !lens_read) || !resolve(m->refs, device) ||
       !resolve(m->refs_out, device) || !resolve(m->status, device, true))
     return refuse("a table, length, reference or status pointer is misaligned or not device-accessible");
   return IBP_OK;
@@ -230,7 +231,8 @@ int ibp_kv_compact(const ibp_kv_seqs* seqs, uint32_t page_tokens, const int32_t*
   int rc = current_device(&device);
   if (rc) return rc;
   KvMeta m;
-  rc = meta_of(&m, seqs, page_tokens, refs, n_pages, table_out, nullptr, refs_out, status, device);
+  // the references say which pages live
+  rc = meta_of(&m, seqs, page_tokens, refs, n_pages, table_out, nullptr, refs_out, status, device, false);
   if (rc) return rc;
   m.moves = moves, m.count = count, m.ws = static_cast<int32_t*>(ws);
   if (!resolve(m.table_out, device, !m.n_seqs || !m.max_pages) || !resolve(m.moves, device) ||

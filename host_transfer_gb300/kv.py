@@ -323,8 +323,7 @@ def ibp_kv_compact(table: torch.Tensor, refs: torch.Tensor, page_tokens: int, in
         moves = torch.empty((n_pages, 3), dtype=torch.int32, device=device)
         count = torch.empty(1, dtype=torch.int32, device=device)
         ws = torch.empty(size, dtype=torch.uint8, device=device)
-        # the lengths are not used: the references say which pages live
-        seqs.table = seqs.lens = table.data_ptr()
+        seqs.table = table.data_ptr()  # the lengths are not read: the references say which pages live
         _check(lib.ibp_kv_compact(seqs, page_tokens, refs.data_ptr(), n_pages, out[0].data_ptr(), out[1].data_ptr(),
                                   moves.data_ptr(), count.data_ptr(), ws.data_ptr(), size, _status(status, device),
                                   handle), "ibp_kv_compact")

@@ -601,7 +601,8 @@ int ibp_kv_free(const ibp_kv_seqs* seqs, uint32_t page_tokens, const int32_t* re
  * pages numbered n_live or more move, in order, to the free pages below n_live,
  * in order.  Tables and references follow; `moves` (n_pages x 3, unused
  * entries -1) and `count` list the copies for ibp_kv_copy, whole pages each.
- * The outputs may be the inputs.  ws: ibp_kv_pages_workspace(n_pages, 0).
+ * The outputs may be the inputs.  ws: ibp_kv_pages_workspace(n_pages, 0).  The
+ * lengths are not read and may be NULL.
  * Negative table entries give -1, entries of n_pages or more -1 and IBP_ERANGE.
  */
 int ibp_kv_compact(const ibp_kv_seqs* seqs, uint32_t page_tokens, const int32_t* refs, uint64_t n_pages,

@@ -280,6 +280,28 @@ def test_misaligned_pointers_are_refused():
     torch.cuda.synchronize()
 
 
+def test_tables_of_no_pages():
+    """Sequences whose table rows have no entries yet: every call takes them."""
+    none, lens = torch.empty((3, 0), dtype=torch.int32, device="cuda"), dev(np.zeros(3))
+    refs = dev(np.array([0, 2, 0, 1]))
+    table, new, moves, count = kv.ibp_kv_compact(none, refs, 16)
+    assert table.shape == (3, 0) and host(new).tolist() == [1, 2, 0, 0] and count.item() == 1
+    assert host(moves)[0].tolist() == [3, 0, 16]
+    assert host(kv.ibp_kv_fork(none, lens, refs, dev(np.array([0, 2])), 16)[2]).tolist() == [0, 2, 0, 1]
+    assert host(kv.ibp_kv_free(none, lens, refs, dev(np.array([1])), 16)[2]).tolist() == [0, 2, 0, 1]
+    c = Cache([40], 2, 2, 2, 16, 64, spare=1)
+    q = c.q.repeat(3, 1, 1, 1)
+    out, lse = kv.ibp_tree_attention(q, c.k, c.v, none, lens, n_draft=lens)
+    assert not out.any() and (lse == -float("inf")).all()
+    out, lse, pages = kv.ibp_sparse_attention(q, c.k, c.v, none, lens, c.codes, c.scales, 2, n_query=lens)
+    assert not out.any() and (lse == -float("inf")).all() and (pages == -1).all()
+    assert torch.equal(kv.ibp_kv_summarize(c.k, none, lens, c.codes, c.scales)[0], c.codes)
+    pool_ = torch.zeros((4, 1, 16, 8), dtype=torch.float16, device="cuda")
+    path = torch.zeros((3, 1), dtype=torch.int32, device="cuda")
+    got = kv.ibp_kv_accept(pool_, none, lens, refs, lens, path, lens)
+    assert host(got[1]).tolist() == [0, 0, 0] and host(got[2]).tolist() == [0, 2, 0, 1]
+
+
 # ---------------------------------------------------------------------------
 # Waits that run out
 
