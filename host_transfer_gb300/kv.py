@@ -23,7 +23,8 @@ page_tokens, dim]``, every layer's K and V at once.  ``table`` is int32
 ``stream`` is a torch stream or a raw handle (default: the current stream);
 results and scratch are allocated for that stream.  Data errors go to a status
 word: the caller's own (``status``, an int32 device tensor) or the device's,
-read by ``ibp_kv_get_status``.
+read by ``ibp_kv_get_status``.  Nothing here has a backward pass: one that
+reaches an attention call raises an error.
 """
 
 from __future__ import annotations
@@ -389,6 +390,25 @@ def ibp_kv_accept(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, 
 # Attention
 
 
+class _NoBackward(torch.autograd.Function):
+    """Passes results on; a gradient that comes back for them is an error, not silence."""
+
+    @staticmethod
+    def forward(ctx, name, out, lse, *inputs):
+        ctx.name = name
+        return out.view_as(out), lse.view_as(lse)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name} has no backward pass: detach q, k and v, or call it under torch.no_grad()")
+
+
+def _results(name: str, out: torch.Tensor, lse: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
+    if (q.requires_grad or k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
+        return _NoBackward.apply(name, out, lse, q, k, v)
+    return out, lse
+
+
 def _heads(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
     """(k pages, v pages, dtype, sequences) of an attention call."""
     kp, vp = _as_pages("k", k), _as_pages("v", v)
@@ -441,7 +461,7 @@ def ibp_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table:
                                       None if mask is None else mask.data_ptr(), usual if scale is None else scale,
                                       out.data_ptr(), lse.data_ptr(), None if ws is None else ws.data_ptr(), size,
                                       _status(status, device), handle), "ibp_tree_attention")
-    return out, lse
+    return _results("ibp_tree_attention", out, lse, q, k, v)
 
 
 def ibp_kv_set_wait_limit(cycles: int = IBP_KV_WAIT_CYCLES) -> int:
@@ -534,4 +554,4 @@ def ibp_sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tabl
                                         keep_last, usual if scale is None else scale, out.data_ptr(), lse.data_ptr(),
                                         pages.data_ptr(), None if ws is None else ws.data_ptr(), size,
                                         _status(status, device), handle), "ibp_sparse_attention")
-    return out, lse, pages
+    return *_results("ibp_sparse_attention", out, lse, q, k, v), pages

@@ -302,6 +302,23 @@ def test_tables_of_no_pages():
     assert host(got[1]).tolist() == [0, 0, 0] and host(got[2]).tolist() == [0, 2, 0, 1]
 
 
+def test_a_backward_through_attention_is_an_error():
+    c = Cache([300, 40], 2, 2, 2, 16, 64)
+    want, sparse = c.tree(), c.sparse(3)
+    assert not want[0].requires_grad
+    c.q.requires_grad_()
+    got = c.tree()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(RuntimeError, match="ibp_tree_attention has no backward"):
+        got[0].float().sum().backward()
+    got = c.sparse(3)
+    assert torch.equal(got[0], sparse[0]) and torch.equal(got[2], sparse[2])
+    with pytest.raises(RuntimeError, match="ibp_sparse_attention has no backward"):
+        got[1].sum().backward()
+    with torch.no_grad():
+        assert not c.tree()[0].requires_grad
+
+
 # ---------------------------------------------------------------------------
 # Waits that run out
 
