@@ -98,11 +98,12 @@ def _load():
 # ---------------------------------------------------------------------------
 # Arguments
 #
-# A call's checks depend on its tensors' shapes, strides and types alone.  They
-# run once for each combination of these; what they yield (the C structures
-# without their addresses, sizes of results and scratch) is kept per thread under
-# that combination, and a call fills in its addresses.  Nothing of a call's
-# data or addresses is kept.
+# A call's checks depend on its tensors' shapes, strides, types and devices alone.
+# They run once for each combination of these, with the tensors' device current (the
+# scratch goes by its number of SMs); what they yield (the C structures without
+# their addresses, sizes of results and scratch) is kept per thread under that
+# combination, and a call fills in its addresses.  Nothing of a call's data or
+# addresses is kept.
 
 
 class _Checked(threading.local):
@@ -116,7 +117,7 @@ _MOST_CHECKED = 1024
 
 def _form(t: torch.Tensor | None):
     """What the checks look at."""
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.is_cuda)
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
 
 
 def _once(key, check):
@@ -191,8 +192,10 @@ _as_is = contextlib.nullcontext()
 
 def _for(stream, device: torch.device):
     """(stream handle, context in which results of that stream are allocated)."""
+    index = device.index
+    if index is None:
+        raise ValueError("pages and tables must be on a CUDA device")
     if stream is None:
-        index = device.index
         handle = ibp._raw_stream(index) if ibp._raw_stream is not None else ibp._stream(None, device)
         return handle, _as_is if index == torch.cuda.current_device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
@@ -259,10 +262,10 @@ def ibp_kv_fork(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, par
         return _sequences(table, lens), n_pages, n_out, lib.ibp_kv_pages_workspace(n_pages, n_out)
 
     key = ("fork", _form(table), _form(lens), _form(refs), _form(parents))
-    seqs, n_pages, n_out, size = _once(key, check)
     device = table.device
     handle, where = _for(stream, device)
     with where:
+        seqs, n_pages, n_out, size = _once(key, check)
         table_out = torch.empty((n_out, table.shape[1]), dtype=torch.int32, device=device)
         lens_out = torch.empty(n_out, dtype=torch.int32, device=device)
         refs_out = torch.empty(n_pages, dtype=torch.int32, device=device)
@@ -289,10 +292,10 @@ def ibp_kv_free(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seq
         _ints("seqs", seqs, None)
         return _sequences(table, lens), refs.shape[0], seqs.shape[0]
 
-    s, n_pages, n_rows = _once(("free", _form(table), _form(lens), _form(refs), _form(seqs)), check)
     device = table.device
     handle, where = _for(stream, device)
     with where:
+        s, n_pages, n_rows = _once(("free", _form(table), _form(lens), _form(refs), _form(seqs)), check)
         out = (table, lens, refs)
         if not inplace:
             out = torch.empty_like(table), torch.empty_like(lens), torch.empty_like(refs)
@@ -316,10 +319,10 @@ def ibp_kv_compact(table: torch.Tensor, refs: torch.Tensor, page_tokens: int, in
         n_pages = refs.shape[0]
         return _Seqs(0, 0, *table.shape), n_pages, lib.ibp_kv_pages_workspace(n_pages, 0)
 
-    seqs, n_pages, size = _once(("compact", _form(table), _form(refs)), check)
     device = table.device
     handle, where = _for(stream, device)
     with where:
+        seqs, n_pages, size = _once(("compact", _form(table), _form(refs)), check)
         out = (table, refs) if inplace else (torch.empty_like(table), torch.empty_like(refs))
         moves = torch.empty((n_pages, 3), dtype=torch.int32, device=device)
         count = torch.empty(1, dtype=torch.int32, device=device)
@@ -341,10 +344,10 @@ def ibp_kv_copy(pages: torch.Tensor, moves: torch.Tensor, count: torch.Tensor, s
         _ints("count", count, 1)
         return _as_pages("pages", pages, pools=True), moves.shape[0]
 
-    p, most = _once(("copy", _form(pages), _form(moves), _form(count)), check)
     device = pages.device
     handle, where = _for(stream, device)
     with where:
+        p, most = _once(("copy", _form(pages), _form(moves), _form(count)), check)
         p.data = pages.data_ptr()
         _check(lib.ibp_kv_copy(p, moves.data_ptr(), count.data_ptr(), most, _status(status, device), handle),
                "ibp_kv_copy")
@@ -369,10 +372,10 @@ def ibp_kv_accept(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, 
 
     key = ("accept", _form(pages), _form(table), _form(lens), _form(refs), _form(n_draft), _form(path),
            _form(n_accept))
-    p, seqs, most = _once(key, check)
     device = pages.device
     handle, where = _for(stream, device)
     with where:
+        p, seqs, most = _once(key, check)
         out = (table, lens, refs)
         if seqs.n_seqs == 0:
             return out if inplace else (table.clone(), lens.clone(), refs.clone())
@@ -444,10 +447,10 @@ def ibp_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table:
         return kp, vp, dt, seqs, (*q.stride()[:3], T, heads), size, 1.0 / math.sqrt(kp.dim)
 
     key = ("tree", _form(q), _form(k), _form(v), _form(table), _form(lens), _form(mask), _form(n_draft))
-    kp, vp, dt, seqs, rows, size, usual = _once(key, check)
     device = k.device
     handle, where = _for(stream, device)
     with where:
+        kp, vp, dt, seqs, rows, size, usual = _once(key, check)
         out = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else _given("out", out, q.shape, q.dtype)
         if lse is None:
             lse = torch.empty(q.shape[:3], dtype=torch.float32, device=device)
@@ -492,10 +495,10 @@ def ibp_kv_summarize(k: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, c
         return kp, seqs, _dtype(k)
 
     key = ("summarize", _form(k), _form(table), _form(lens), _form(codes), _form(scales), _form(first))
-    kp, seqs, dt = _once(key, check)
     device = k.device
     handle, where = _for(stream, device)
     with where:
+        kp, seqs, dt = _once(key, check)
         kp.data = k.data_ptr()
         seqs.table, seqs.lens = table.data_ptr(), lens.data_ptr()
         _check(lib.ibp_kv_summarize(kp, dt, seqs, None if first is None else first.data_ptr(), codes.data_ptr(),
@@ -532,10 +535,10 @@ def ibp_sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tabl
 
     key = ("sparse", _form(q), _form(k), _form(v), _form(table), _form(lens), _form(codes), _form(scales),
            _form(n_query), budget, keep_first, keep_last)
-    kp, vp, dt, seqs, rows, size, usual = _once(key, check)
     device = k.device
     handle, where = _for(stream, device)
     with where:
+        kp, vp, dt, seqs, rows, size, usual = _once(key, check)
         out = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else _given("out", out, q.shape, q.dtype)
         if lse is None:
             lse = torch.empty(q.shape[:3], dtype=torch.float32, device=device)
