@@ -23,7 +23,8 @@ page_tokens, dim]``, every layer's K and V at once.  ``table`` is int32
 ``stream`` is a torch stream or a raw handle (default: the current stream);
 results and scratch are allocated for that stream.  Data errors go to a status
 word: the caller's own (``status``, an int32 device tensor) or the device's,
-read by ``ibp_kv_get_status``.  Nothing here has a backward pass: one that
+read by ``ibp_kv_get_status`` (call it once before the first call is captured
+in a graph: it makes the word).  Nothing here has a backward pass: one that
 reaches an attention call raises an error.
 """
 
@@ -209,14 +210,23 @@ def _for(stream, device: torch.device):
 _status_words: dict[int, torch.Tensor] = {}
 
 
+def _status_word(index: int) -> torch.Tensor:
+    word = _status_words.get(index)
+    if word is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the device's status word is not made yet, which a capture cannot hold: call "
+                               "ibp_kv_get_status() before it, or pass a status word")
+        with torch.cuda.device(index):
+            word = torch.zeros(1, dtype=torch.int32, device="cuda")
+            torch.cuda.synchronize()  # made once: every stream may use it
+        word = _status_words.setdefault(index, word)
+    return word
+
+
 def _status(status: torch.Tensor | None, device: torch.device) -> int:
     if status is None:
         word = _status_words.get(device.index)
-        if word is None:
-            word = torch.zeros(1, dtype=torch.int32, device=device)
-            torch.cuda.synchronize(device)  # made once: every stream may use it
-            word = _status_words.setdefault(device.index, word)
-        return word.data_ptr()
+        return (_status_word(device.index) if word is None else word).data_ptr()
     if status.element_size() != 4 or status.numel() < 1:
         raise ValueError("status must be a 32-bit word")
     return status.data_ptr()
@@ -224,11 +234,11 @@ def _status(status: torch.Tensor | None, device: torch.device) -> int:
 
 def ibp_kv_get_status(device: int | None = None, raise_on_error: bool = True) -> int:
     """Waits for the device, returns the first data error of the calls that
-    named no status word of their own since the last call, and clears it."""
+    named no status word of their own since the last call, and clears it.  The
+    first use of a device makes its word, which a graph capture cannot hold: a
+    program that captures its first call calls this before."""
     device = torch.cuda.current_device() if device is None else int(device)
-    word = _status_words.get(device)
-    if word is None:
-        return IBP_OK
+    word = _status_word(device)
     torch.cuda.synchronize(device)
     code = int(word.item())
     if code != IBP_OK:

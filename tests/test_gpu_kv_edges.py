@@ -219,6 +219,34 @@ def test_early_fetch_behind_two_calls_reads_what_the_first_wrote():
     assert ibp.ibp_get_status(plan) == ibp.IBP_OK
 
 
+def test_a_first_call_inside_a_capture(monkeypatch):
+    """The device's status word is made outside of captures: a first call inside one is
+    refused and leaves the capture whole; ibp_kv_get_status makes the word."""
+    c = Cache([300, 40], 2, 2, 2, 16, 64)
+    want = c.tree()
+    err(ibp.IBP_OK)
+    monkeypatch.setattr(kv, "_status_words", {})
+    a, more, graph = torch.ones(8, device="cuda"), dev(np.full(2, 7)), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b = a + 1
+        with pytest.raises(RuntimeError, match="ibp_kv_get_status"):
+            c.tree()
+    graph.replay()
+    assert (b == 2).all()
+    own, graph = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = c.tree(status=own)
+    graph.replay()
+    assert torch.equal(got[0], want[0]) and own.item() == 0 and not kv._status_words
+    assert kv.ibp_kv_get_status() == ibp.IBP_OK and len(kv._status_words) == 1
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = c.tree(n_draft=more)
+    graph.replay()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    err(ibp.IBP_ERANGE)
+
+
 # ---------------------------------------------------------------------------
 # Refusals
 
