@@ -2,6 +2,7 @@
 surroundings are out of the ordinary."""
 
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -217,6 +218,130 @@ def test_early_fetch_behind_two_calls_reads_what_the_first_wrote():
         out = ibp.ibp_gather_decompress(plan, pages[:n, 0, 0], new[1], ids)
         assert torch.equal(out, tables_[1][ids])
     assert ibp.ibp_get_status(plan) == ibp.IBP_OK
+
+
+class Step:
+    """A pass through every call but tree attention, on buffers of its own: a fork with its
+    copies, bounds, sparse attention, an acceptance, a free, a compaction.  The lengths leave
+    room for the draft in a row's last page, its own after the fork."""
+
+    def __init__(self, seed, lens=(300, 77, 139), T=2, page=16, D=64, dt="bf16"):
+        self.page, rng = page, np.random.default_rng(seed)
+        table, refs = tables(list(lens), page, 70, -(-max(lens) // page) + 2, rng)
+        g = gen(seed)
+        self.first = dict(pool=torch.randn((2, 70, 2, page, D), device="cuda", generator=g).to(DTYPES[dt]), table=dev(table),
+                          lens=dev(np.array(lens)), refs=dev(refs), parents=dev(rng.integers(0, 3, 4)),
+                          n_draft=dev(np.full(4, 8)), path=dev(np.sort(np.argsort(rng.random((4, 8)), 1)[:, :5], 1)),
+                          n_accept=dev(rng.integers(0, 6, 4)), gone=dev(rng.integers(0, 4, 2)),
+                          q=torch.randn((4, T, 6, D), device="cuda", generator=g).to(DTYPES[dt]))
+        self.buffers = {name: torch.empty_like(x) for name, x in self.first.items()}
+        self.codes = torch.zeros((70, 2, 2, D), dtype=torch.int8, device="cuda")
+        self.scales = torch.zeros((70, 2), device="cuda")
+
+    def load(self, zero=False):
+        for name, x in self.buffers.items():
+            x.zero_() if zero else x.copy_(self.first[name])
+        self.codes.zero_(), self.scales.zero_()
+
+    def run(self, stream=None):
+        b, page = self.buffers, self.page
+        table, lens, refs, moves, count = kv.ibp_kv_fork(b["table"], b["lens"], b["refs"], b["parents"], page, stream=stream)
+        kv.ibp_kv_copy(b["pool"], moves, count, stream=stream)
+        kv.ibp_kv_summarize(b["pool"][0], table, lens, self.codes, self.scales, stream=stream)
+        sparse = kv.ibp_sparse_attention(b["q"], b["pool"][0], b["pool"][1], table, lens, self.codes, self.scales, 4,
+                                         stream=stream)
+        state = kv.ibp_kv_accept(b["pool"], table, lens, refs, b["n_draft"], b["path"], b["n_accept"], stream=stream)
+        state = kv.ibp_kv_free(*state, b["gone"], page, stream=stream)
+        packed = kv.ibp_kv_compact(state[0], state[2], page, stream=stream)
+        kv.ibp_kv_copy(b["pool"], packed[2], packed[3], stream=stream)
+        return [table, lens, refs, moves, count, *sparse, *state, *packed, b["pool"], self.codes, self.scales]
+
+
+NAMES = ["table", "lens", "refs", "moves", "count", "out", "lse", "pages", "accepted and freed table", "lens", "refs",
+         "packed table", "refs", "moves", "count", "pool", "codes", "scales"]
+
+
+def unlike(got, want):
+    """What differs, by name."""
+    return [f"{name} at {(a != b).nonzero()[0].tolist()}: {a[a != b][:4].tolist()} for {b[a != b][:4].tolist()}"
+            for name, a, b in zip(NAMES, got, want) if not torch.equal(a, b)]
+
+
+def test_every_call_goes_to_its_stream():
+    """The stream holds the inputs back: a call that went elsewhere would read zeros."""
+    step, side = Step(1), torch.cuda.Stream()
+    step.load()
+    want = [x.clone() for x in step.run()]
+    step.load(zero=True)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        step.load()
+    got = step.run(stream=side)
+    side.synchronize()
+    assert not unlike(got, want)
+    step.load(zero=True)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        step.load()
+        got = step.run()  # the current stream
+    side.synchronize()
+    assert not unlike(got, want)
+
+
+def test_every_call_in_a_graph():
+    steps = [Step(2), Step(3)]
+    wants = []
+    for s in steps:
+        s.load()
+        wants.append([x.clone() for x in s.run()])
+    held, inputs, graph = steps[0], [s.first for s in steps], torch.cuda.CUDAGraph()
+    held.load()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = held.run()
+    for first, want in [*zip(inputs, wants)] * 2:  # other inputs on every replay
+        held.first = first
+        held.load()
+        graph.replay()
+        assert not unlike(got, want)
+
+
+def test_calls_from_two_host_threads():
+    """Each thread on its own stream, with forms of its own and a form they share."""
+    forms = [dict(), dict(lens=(200, 90, 43), T=3, D=128, dt="f16")]
+    wants = {}
+    for i, f in enumerate(forms):
+        step = Step(5, **f)
+        step.load()
+        wants[i] = [x.clone() for x in step.run()]
+    c = Cache([700, 60, 1300], 4, 40, 4, 16, 128)
+    tree = c.tree()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(mine):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                steps = {i: Step(5, **forms[i]) for i in (mine, 0)}
+                for _ in range(60):
+                    for i, step in steps.items():
+                        step.load()
+                        wrong.extend(unlike(step.run(), wants[i]))
+                    if not all(torch.equal(a, b) for a, b in zip(c.tree(), tree)):
+                        wrong.append("tree")
+        except Exception as e:  # shown by the assertion below
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong
 
 
 def test_a_first_call_inside_a_capture(monkeypatch):
