@@ -3,8 +3,8 @@
 The prompt's keys and values lie compressed in pinned host memory, as
 ``bench.py --config llm`` holds them.  The step
 
-1. decodes them straight into pages of an HBM pool (ibp_gather_decompress with
-   the rows in page order),
+1. decodes them with the rows in page order (ibp_gather_decompress) and copies
+   the result into the pages of an HBM pool,
 2. summarises the pages' keys and lets each sequence's last token attend to the
    few pages that score highest (ibp_kv_summarize, ibp_sparse_attention),
 3. forks each sequence into beams (ibp_kv_fork, ibp_kv_copy), appends a tree of
@@ -45,8 +45,8 @@ def compressed_cache(seq: int, heads: int, layer: int):
 
 
 def decode_into(pool: torch.Tensor, table, pages: torch.Tensor, seq: int):
-    """Decodes a compressed cache into the given pages of a pool [n_pages, heads,
-    page_tokens, dim]: row (head, position) of the table becomes its page's row."""
+    """Decodes a compressed cache and copies it into the given pages of a pool [n_pages,
+    heads, page_tokens, dim]: row (head, position) of the table becomes its page's row."""
     plan, slots, bitmask = table
     _, heads, page, _ = pool.shape
     at = torch.arange(len(pages) * page, device="cuda").clamp(max=seq - 1).reshape(len(pages), 1, page)
@@ -58,7 +58,8 @@ def decode_into(pool: torch.Tensor, table, pages: torch.Tensor, seq: int):
 
 def append(pool: torch.Tensor, table, lens, refs, rows):
     """Appends rows [2, n_seqs, T, heads, dim] to every sequence: takes the lowest
-    free pages for those that grow past their last one."""
+    free pages for those that grow past their last one.  Plain torch, which reads
+    their number back to the host."""
     n_seqs, T, page = rows.shape[1], rows.shape[2], pool.shape[3]
     before, after = (lens + page - 1) // page, (lens + T + page - 1) // page
     place = torch.arange(table.shape[1], device="cuda")

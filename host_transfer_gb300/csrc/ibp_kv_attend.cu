@@ -18,8 +18,8 @@
 //
 // Measured on one GB300: 32 queries over 64 pages of 64 tokens each, 8 kv heads of
 // 4 query heads and 128 dimensions (533 MB): 84 us, 6.3 TB/s; 1022 queries of 8
-// heads over 24 pages of 32 tokens of 64 dimensions (803 MB out of L2): 74 us,
-// bound by issue (33 M instructions) and the few warps its stages leave room for.
+// heads over 24 pages of 32 tokens of 64 dimensions (803 MB out of L2): 75 us,
+// bound by issue (34 M instructions) and the few warps its stages leave room for.
 //
 // Softmax statistics and sums are 32-bit; the probabilities are rounded to the
 // cache's type for the second product (the tensor core wants both operands

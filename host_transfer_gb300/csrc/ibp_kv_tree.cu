@@ -83,7 +83,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_tree_join(const __grid_cons
 
 static size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Heads that fit TMEM beside the scores.
+// Two row tiles of 128 fill TMEM beside the scores.  One row tile of 256 would fit
+// too (256 columns of scores, 256 of output); it is not built, and wider heads take
+// the few-row kernel.
 static bool tc_shape(uint32_t dim) { return dim <= 128; }
 static uint32_t tc_dim(uint32_t dim) { return dim <= 64 ? 64 : 128; }
 static uint32_t tc_tiles(uint64_t rows) { return rows > kTcTile ? 2 : 1; }

@@ -20,8 +20,7 @@
 // O is rescaled as soon as a row's maximum grows, so that the largest probability
 // is a power of two and its rounding to the cache's type costs nothing.  Putting the
 // rescaling off until the maximum has grown by 2^8 saves 2 % on two row tiles
-// (573 us to 587 us on the widest tree below) and takes the output's error
-// from 1.15 to 1.3 - 1.5 of the result's own rounding.
+// and takes the output's error from 1.15 to 1.3 - 1.5 of the result's own rounding.
 //
 // Work is split evenly over the CTAs, one per SM, by tiles of all items in a
 // row: a CTA's range may end inside an item, whose parts are then joined by
@@ -32,10 +31,11 @@
 // DRAM 1.5 times, not twice.
 //
 // Measured on one GB300: 16 ragged caches of up to 32768 tokens, 8 kv heads of 128
-// (1.48 GB): 64 rows a head 231 us (6.4 TB/s, 0.94 of the copy rate), 512 rows
-// 587 us (1.28 PFLOP/s, 0.68 of the library's burst product rate and 0.76 of its
-// sustained one; without any softmax work the products alone take 502 us, the clock
-// being held down by power).
+// (1.48 GB): 64 rows a head 233 us (6.4 TB/s, 0.94 of the copy rate), 512 rows
+// 600 to 640 us in replayed graphs (1.18 to 1.26 PFLOP/s, 0.62 to 0.66 of the library's
+// burst product rate and 0.70 to 0.74 of its sustained one; the clock is held down by
+// power, and the products alone, without any softmax work, took 502 us) and 680 us
+// a pass among single calls on inputs that change.
 //
 // Every wait has a limit: a CTA that runs into it raises a flag all its waits heed,
 // records IBP_ETIMEOUT and returns.  Whether it does or not, the producer leaves
@@ -228,9 +228,9 @@ struct TcShape {
   // beside this one's, so that its scores begin while the output is still written.
   static constexpr uint32_t kQ = 2;
   // Ring of tiles, K and V in turn.  One row tile is bound by the loads and takes
-  // all that fit, two and a half cache tiles (a batch of 16 ragged caches of up to
-  // 32768: 231 us, with two 242); two row tiles are bound by the products and do
-  // no better with more than two (571 us, with two and a half 583).
+  // all that fit, two and a half cache tiles (with two, the 16 caches above take 5 %
+  // more); two row tiles are bound by the products and do no better with more than
+  // two (with two and a half 2 % more).
   static constexpr uint32_t kSlots = DP == 128 ? (MT == 1 ? 5 : 4) : (MT == 1 ? 11 : 8);
   static constexpr uint32_t kBytes = (kQ + kSlots) * kTileBytes;
   static constexpr uint32_t kSmem = kBytes + 1024 + 512;             // alignment, barriers

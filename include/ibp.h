@@ -652,7 +652,7 @@ int ibp_kv_accept(const ibp_kv_pages* pages, const ibp_kv_seqs* seqs, const int3
  * decoding.  What a query does not see has no influence on it, whatever its
  * bits (infinities and NaN included).  A position whose page id is out of
  * range reads as a zero key and value and records IBP_ERANGE, as does a length
- * below n (positions before the first do not exist).
+ * below n (positions before the first do not exist) and an n above T (read as T).
  *
  * dtype    IBP_KV_BF16 or IBP_KV_F16: queries, pages and output.
  * q        n_seqs x T x q_heads x dim by strides; dim contiguous.
@@ -700,8 +700,9 @@ int ibp_kv_summarize(const ibp_kv_pages* k, uint32_t dtype, const ibp_kv_seqs* s
 
 /*
  * Attention over the pages that a cheap score selects for each query.  The T
- * queries of sequence b are its last n = n_query[b] tokens (NULL: T; queries
- * t >= n give zeros, -infinity and no pages); query t sits at position
+ * queries of sequence b are its last n = n_query[b] tokens (NULL: T; an n
+ * above T is read as T and records IBP_ERANGE; queries t >= n give zeros,
+ * -infinity and no pages); query t sits at position
  * p = lens[b] - n + t and sees positions up to p.  Per query and kv head, with
  * c = rint(q * ((1 / a) * 127)), a = max |q| over the head's group (zeros when a
  * is below 2^-100 or not finite): total = sum over the group's heads and dims
