@@ -1,0 +1,172 @@
+// ibp_kv_evict.cu - the tokens of a cache that stay when a budget is exceeded.
+//
+// A cluster takes a sequence, each CTA a stretch of its positions.  The weight at
+// which the budget is full is found digit by digit from the top (three digits of 11,
+// 11 and 10 bits of an order-preserving code): a histogram in shared memory, added up
+// over the cluster.  Positions with that very weight stay from the lowest on.  A second
+// walk writes the kept positions and their weights at places known from the counts of
+// the warps before.  Nothing depends on the order in which threads run.  Bound by the
+// latency of the walks and the cluster's barriers.
+#include "ibp_kv_serve.cuh"
+
+namespace ibp {
+
+constexpr int kEvThreads = 512;
+constexpr uint32_t kEvWarps = kEvThreads / 32;
+constexpr uint32_t kEvBins = 2048;
+
+// Larger weights have larger codes; both zeros are alike, and NaN is below all.
+__device__ __forceinline__ uint32_t weight_code(float w) {
+  if (w != w) return 0u;
+  uint32_t b = __float_as_uint(w);
+  if (b == 0x80000000u) b = 0u;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+struct EvictShared {
+  uint32_t hist[kEvBins];
+  uint32_t all[kEvBins];
+  uint32_t digit, above;      // the bin found, and how many lie above it
+  uint32_t n_more[kEvWarps], n_equal[kEvWarps];
+  uint32_t cta_more, cta_equal;
+};
+
+__device__ __forceinline__ uint32_t remote_u32(const uint32_t* p, uint32_t rank) {
+  uint32_t addr = smem_u32(p), v;
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <uint32_t C>
+__device__ __forceinline__ void ev_sync() {
+  if (C == 1)
+    __syncthreads();
+  else
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <uint32_t C>
+__global__ void __launch_bounds__(kEvThreads) k_kv_evict(const EvictArgs a) {
+  __shared__ EvictShared sh;
+  pdl_begin();
+  const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+  const uint32_t rank = C == 1 ? 0 : blockIdx.x % C, b = blockIdx.x / C;
+  const int32_t raw = a.lens[b];
+  const uint32_t len = raw < 0 ? 0u : (static_cast<uint32_t>(raw) < a.width ? static_cast<uint32_t>(raw) : a.width);
+  if (static_cast<int64_t>(raw) != static_cast<int64_t>(len) && rank == 0 && tid == 0) kv_status(a.status, IBP_ERANGE);
+  const float* w = a.w + static_cast<uint64_t>(b) * a.width;
+  float* out = a.w_out + static_cast<uint64_t>(b) * a.width;
+  int32_t* path = a.path + static_cast<uint64_t>(b) * a.budget;
+  const bool over = len > a.budget;
+  if (rank == 0 && tid == 0) {
+    a.n_draft[b] = over ? static_cast<int32_t>(len) : 0;
+    a.n_keep[b] = over ? static_cast<int32_t>(a.budget) : 0;
+  }
+  const uint32_t me = rank * kEvThreads + tid;
+  if (!over) {  // the same for the whole cluster
+    for (uint32_t i = me; i < a.width; i += C * kEvThreads) out[i] = i < len ? w[i] : 0.f;
+    for (uint32_t i = me; i < a.budget; i += C * kEvThreads) path[i] = -1;
+    return;
+  }
+  for (uint32_t i = a.budget + me; i < a.width; i += C * kEvThreads) out[i] = 0.f;
+  // Positions that do not stay in any case: [lo, hi); keep_first + keep_last <= budget < len.
+  const uint32_t lo = a.keep_first, hi = len - a.keep_last, want = a.budget - a.keep_first - a.keep_last;
+  const uint32_t part = (len + C * kEvWarps * 32 - 1) / (C * kEvWarps * 32) * 32;  // of a warp
+  auto clip = [&](uint32_t x) { return x < len ? x : len; };
+  const uint32_t from = clip((rank * kEvWarps + warp) * part), to = clip(from + part);
+
+  // The code at which `want` are reached, and how many above it.
+  uint32_t prefix = 0, left = want;
+  if (want) {
+#pragma unroll 1
+    for (uint32_t d = 0; d < 3; ++d) {
+      const uint32_t shift = d == 0 ? 21 : (d == 1 ? 10 : 0), bins = d == 2 ? 1024 : 2048;
+      const uint32_t known = d == 0 ? 0u : 0xFFFFFFFFu << (d == 1 ? 21 : 10);
+      for (uint32_t i = tid; i < bins; i += kEvThreads) sh.hist[i] = 0;
+      __syncthreads();
+      for (uint32_t i = from + lane; i < to; i += 32) {
+        if (i < lo || i >= hi) continue;
+        const uint32_t c = weight_code(__ldg(w + i));
+        if ((c & known) == prefix) atomicAdd(&sh.hist[(c >> shift) & (bins - 1)], 1u);
+      }
+      ev_sync<C>();
+      for (uint32_t i = tid; i < bins; i += kEvThreads) {
+        uint32_t s = 0;
+#pragma unroll
+        for (uint32_t r = 0; r < C; ++r) s += C == 1 ? sh.hist[i] : remote_u32(&sh.hist[i], r);
+        sh.all[i] = s;
+      }
+      ev_sync<C>();  // the histogram may be cleared again
+      if (warp == 0) {
+        // from the highest bin down; a lane takes bins / 32 of them
+        const uint32_t per = bins / 32, top = bins - lane * per;
+        uint32_t s = 0;
+        for (uint32_t i = 1; i <= per; ++i) s += sh.all[top - i];
+        uint32_t run = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, run, o);
+          if (static_cast<int>(lane) >= o) run += y;
+        }
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, run >= left);
+        if (lane == static_cast<uint32_t>(__ffs(hit) - 1)) {
+          uint32_t above = run - s, i = 1;
+          while (above + sh.all[top - i] < left) above += sh.all[top - i++];
+          sh.digit = top - i;
+          sh.above = above;
+        }
+      }
+      __syncthreads();
+      prefix |= sh.digit << shift;
+      left -= sh.above;
+      __syncthreads();
+    }
+  }
+  // left: how many of the positions with the code `prefix` stay
+  auto kind = [&](uint32_t i) -> uint32_t {  // 2 stays, 1 has the last weight, 0 goes
+    if (i < lo || i >= hi) return 2u;
+    if (!want) return 0u;
+    const uint32_t c = weight_code(__ldg(w + i));
+    return c > prefix ? 2u : (c == prefix ? 1u : 0u);
+  };
+  uint32_t more = 0, equal = 0;
+  for (uint32_t i0 = from; i0 < to; i0 += 32) {
+    const uint32_t k = i0 + lane < to ? kind(i0 + lane) : 0u;
+    more += __popc(__ballot_sync(0xFFFFFFFFu, k == 2u));
+    equal += __popc(__ballot_sync(0xFFFFFFFFu, k == 1u));
+  }
+  if (lane == 0) sh.n_more[warp] = more, sh.n_equal[warp] = equal;
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t m = 0, e = 0;
+    for (uint32_t x = 0; x < kEvWarps; ++x) m += sh.n_more[x], e += sh.n_equal[x];
+    sh.cta_more = m, sh.cta_equal = e;
+  }
+  ev_sync<C>();
+  uint32_t before_more = 0, before_equal = 0;
+  if constexpr (C > 1)
+    for (uint32_t r = 0; r < rank; ++r) before_more += remote_u32(&sh.cta_more, r), before_equal += remote_u32(&sh.cta_equal, r);
+  for (uint32_t x = 0; x < warp; ++x) before_more += sh.n_more[x], before_equal += sh.n_equal[x];
+  for (uint32_t i0 = from; i0 < to; i0 += 32) {
+    const uint32_t i = i0 + lane, k = i < to ? kind(i) : 0u;
+    const uint32_t eq = __ballot_sync(0xFFFFFFFFu, k == 1u), mo = __ballot_sync(0xFFFFFFFFu, k == 2u);
+    const uint32_t lt = lanemask_lt();
+    const uint32_t e = before_equal + __popc(eq & lt), m = before_more + __popc(mo & lt);
+    if (k == 2u || (k == 1u && e < left)) {
+      const uint32_t at = m + (e < left ? e : left);
+      path[at] = static_cast<int32_t>(i);
+      out[at] = __ldg(w + i);
+    }
+    before_equal += __popc(eq);
+    before_more += __popc(mo);
+  }
+  if (C > 1) ev_sync<C>();  // no CTA leaves while another reads its counts
+}
+
+int launch_kv_evict(const EvictArgs& a, cudaStream_t stream) {
+  if (a.width <= 2048) return kv_launch("k_kv_evict", k_kv_evict<1>, dim3(a.n_seqs), kEvThreads, 0, 1, stream, a);
+  return kv_launch("k_kv_evict", k_kv_evict<8>, dim3(a.n_seqs * 8), kEvThreads, 0, 8, stream, a);
+}
+
+}  // namespace ibp

@@ -1,0 +1,239 @@
+// ibp_kv_verify.cu - drafted tokens against the target's probabilities.
+//
+// A cluster takes a sequence.  Whether a token is accepted when it is the first one
+// tried behind its parent depends on two probabilities alone, so all these tests are
+// made at once; the walk then follows the answers.  Only a rejection needs a whole
+// row of probabilities (what is left of the target's after the draft's is taken out,
+// and its sum), and the last row is needed for the drawn token.  Rows are split over
+// the cluster's warps in the order of the vocabulary.
+//
+// Sums are of whole numbers, 2^44 times the probability, in 64 bits: they do not
+// depend on the order, so neither do the choices.  What is left after several
+// rejections is computed anew from the rows (m subtractions and products an element)
+// and not stored.  Bound by latency for few sequences, by DRAM for many.
+#include "ibp_kv_serve.cuh"
+
+namespace ibp {
+
+constexpr int kVfThreads = 512;
+constexpr uint32_t kVfWarps = kVfThreads / 32;
+constexpr float kVfUnit = 17592186044416.f;  // 2^44
+
+__device__ __forceinline__ float probability(float x) { return fminf(fmaxf(x, 0.f), 1.f); }  // NaN: 0
+
+struct VerifyShared {
+  long long warp[2][kVfWarps];  // sums of the warps' parts of a row, this pass and the one before
+  long long cta[2];             // and of the CTA's
+  long long part[kVfWarps];
+};
+
+// What is left of row p behind `depth` rejections, the last one not scaled to a sum of
+// one again: the weight by which a token is drawn.
+struct Left {
+  const float *p, *q;
+  const float* scale;
+  const int32_t* x;
+  uint32_t depth;
+  __device__ __forceinline__ float drawn(uint32_t i, float qi, uint32_t k) const {
+    return q ? qi : (static_cast<int32_t>(i) == x[k] ? 1.f : 0.f);
+  }
+  __device__ __forceinline__ float operator()(uint32_t i) const {
+    float v = probability(__ldg(p + i));
+    if (depth == 0) return v;
+    const float qi = q ? probability(__ldg(q + i)) : 0.f;
+    v = fmaxf(__fsub_rn(v, drawn(i, qi, 0)), 0.f);
+    for (uint32_t k = 1; k < depth; ++k) v = fmaxf(__fsub_rn(__fmul_rn(v, scale[k - 1]), drawn(i, qi, k)), 0.f);
+    return v;
+  }
+};
+
+__device__ __forceinline__ long long whole(float w) { return __float2ll_rn(__fmul_rn(w, kVfUnit)); }
+
+__device__ __forceinline__ long long warp_total(long long s) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  return s;
+}
+
+__device__ __forceinline__ long long remote_ll(const long long* p, uint32_t rank) {
+  uint32_t addr = smem_u32(p);
+  long long v;
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(rank));
+  asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <uint32_t C>
+__device__ __forceinline__ void vf_sync() {
+  if (C == 1)
+    __syncthreads();
+  else
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Sums of the weights, in slot `buf`: every warp's, the CTA's, and the row's (returned).
+template <uint32_t C>
+__device__ __forceinline__ long long vf_sum(VerifyShared& sh, uint32_t buf, const Left& f, uint32_t from, uint32_t to) {
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  long long s = 0;
+#pragma unroll 4
+  for (uint32_t i = from + lane; i < to; i += 32) s += whole(f(i));
+  s = warp_total(s);
+  if (lane == 0) sh.warp[buf][warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    const long long all = warp_total(lane < kVfWarps ? sh.warp[buf][lane] : 0);
+    if (lane == 0) sh.cta[buf] = all;
+  }
+  vf_sync<C>();
+  long long total = 0;
+#pragma unroll
+  for (uint32_t r = 0; r < C; ++r) total += C == 1 ? sh.cta[buf] : remote_ll(&sh.cta[buf], r);
+  vf_sync<C>();  // the slot may be written again
+  return total;
+}
+
+template <uint32_t C>
+__global__ void __launch_bounds__(kVfThreads) k_kv_verify(const VerifyArgs a) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  __shared__ VerifyShared sh;
+  pdl_begin();
+  const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, T = a.T, V = a.vocab;
+  const uint32_t rank = C == 1 ? 0 : blockIdx.x % C, b = blockIdx.x / C;
+  int32_t* tok = reinterpret_cast<int32_t*>(dyn);  // [T]; -1: out of range
+  int32_t* par = tok + T;                          // [T]; -2: out of range
+  float* ut = reinterpret_cast<float*>(par + T);   // [T]
+  float* scale = ut + T;                           // [T]: of the rejections behind the present node
+  int32_t* gone = reinterpret_cast<int32_t*>(scale + T);  // [T]: their tokens
+  uint8_t* first = reinterpret_cast<uint8_t*>(gone + T);  // [T]: accepted if the first one tried
+  const float* p = a.p + static_cast<int64_t>(b) * a.p_seq;
+  const float* q = a.q ? a.q + static_cast<int64_t>(b) * a.q_seq : nullptr;
+  const float* u = a.u + static_cast<uint64_t>(b) * (T + 1);
+  const int32_t want = a.n_draft ? a.n_draft[b] : static_cast<int32_t>(T);
+  const int32_t n = want < 0 ? 0 : (want > static_cast<int32_t>(T) ? static_cast<int32_t>(T) : want);
+  bool bad = want != n;
+  for (uint32_t t = tid; t < static_cast<uint32_t>(n); t += kVfThreads) {
+    const uint64_t at = static_cast<uint64_t>(b) * T + t;
+    int32_t x = a.tokens[at], r = a.parents ? a.parents[at] : static_cast<int32_t>(t) - 1;
+    const float ux = u[t];
+    if (x < 0 || static_cast<uint32_t>(x) >= V) x = -1, bad = true;
+    if (r < -1 || r >= static_cast<int32_t>(t)) r = -2, bad = true;
+    bool ok = false;
+    if (x >= 0 && r >= -1) {
+      const float px = probability(p[static_cast<int64_t>(r + 1) * a.p_row + x]);
+      const float qx = q ? probability(q[static_cast<int64_t>(r + 1) * a.q_row + x]) : 1.f;
+      ok = static_cast<double>(ux) * qx < px;  // the product of two floats is exact
+    }
+    tok[t] = x, par[t] = r, ut[t] = ux, first[t] = ok;
+  }
+  if (bad && rank == 0) kv_status(a.status, IBP_ERANGE);
+  __syncthreads();
+
+  // This warp's part of a row.
+  const uint32_t part = (V + C * kVfWarps * 32 - 1) / (C * kVfWarps * 32) * 32;
+  auto clip = [&](uint32_t x) { return x < V ? x : V; };
+  const uint32_t from = clip((rank * kVfWarps + warp) * part), to = clip(from + part);
+
+  int32_t node = -1;
+  uint32_t count = 0, keep = 0;
+  long long total = -1;  // of the weights that a token would be drawn by, in slot `keep`; -1: not known
+  Left f = {p, q, scale, gone, 0u};
+  for (int32_t t = 0; t < n; ++t) {
+    if (par[t] != node || tok[t] < 0) continue;
+    const int32_t x = tok[t];
+    bool ok = first[t];
+    if (f.depth) {
+      const float left = __fmul_rn(f(x), scale[f.depth - 1]);
+      const float qx = q ? probability(__ldg(f.q + x)) : 1.f;
+      ok = static_cast<double>(ut[t]) * qx < left;
+    }
+    if (ok) {
+      if (rank == 0 && tid == 0) a.path[static_cast<uint64_t>(b) * T + count] = t;
+      ++count;
+      node = t;
+      f.p = p + static_cast<int64_t>(node + 1) * a.p_row;
+      if (q && node + 1 < static_cast<int32_t>(T)) f.q = q + static_cast<int64_t>(node + 1) * a.q_row;
+      f.depth = 0;
+      total = -1;
+    } else {
+      // every thread is past the loads of the entry that is written (it is not read before depth grows)
+      if (tid == 0) gone[f.depth] = x;
+      __syncthreads();
+      ++f.depth;
+      const long long z = vf_sum<C>(sh, keep ^ 1u, f, from, to);
+      if (z > 0) {
+        keep ^= 1u;
+        total = z;
+        if (tid == 0) scale[f.depth - 1] = static_cast<float>(__ddiv_rn(17592186044416.0, static_cast<double>(z)));
+        __syncthreads();
+      } else {
+        --f.depth;  // nothing would be left: the token is out, the rest stays
+      }
+    }
+  }
+  if (total < 0) total = vf_sum<C>(sh, keep, f, from, to);
+  if (rank == 0) {
+    for (uint32_t t = count + tid; t < T; t += kVfThreads) a.path[static_cast<uint64_t>(b) * T + t] = -1;
+    if (tid == 0) a.n_accept[b] = static_cast<int32_t>(count);
+  }
+  if (total == 0) {
+    if (rank == 0 && tid == 0) {
+      a.token[b] = -1;
+      kv_status(a.status, IBP_ERANGE);
+    }
+  } else {
+    // The first token whose running sum is above floor(u total): CTA, warp's part, the
+    // part shared out over the warps again, token.
+    const double want_sum = static_cast<double>(u[T]) * static_cast<double>(total);
+    long long aim = want_sum >= static_cast<double>(total) ? total - 1 : (want_sum > 0 ? static_cast<long long>(want_sum) : 0);
+    if (aim > total - 1) aim = total - 1;
+    if constexpr (C > 1)
+      for (uint32_t r = 0; r < rank; ++r) aim -= remote_ll(&sh.cta[keep], r);
+    const bool mine = aim >= 0 && aim < sh.cta[keep];
+    if (mine) {
+      uint32_t w = 0;
+      while (w < kVfWarps - 1 && aim >= sh.warp[keep][w]) aim -= sh.warp[keep][w++];
+      const uint32_t lo = clip((rank * kVfWarps + w) * part), hi = clip(lo + part);
+      const uint32_t sub = (part + kVfWarps * 32 - 1) / (kVfWarps * 32) * 32;
+      const uint32_t s0 = lo + warp * sub < hi ? lo + warp * sub : hi, s1 = s0 + sub < hi ? s0 + sub : hi;
+      long long s = 0;
+      for (uint32_t i = s0 + lane; i < s1; i += 32) s += whole(f(i));
+      s = warp_total(s);
+      if (lane == 0) sh.part[warp] = s;
+      __syncthreads();
+      w = 0;
+      while (w < kVfWarps - 1 && aim >= sh.part[w]) aim -= sh.part[w++];
+      if (warp == w) {
+        for (uint32_t i0 = s0; i0 < s1; i0 += 32) {
+          const uint32_t i = i0 + lane;
+          const long long me = i < s1 ? whole(f(i)) : 0;
+          long long run = me;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, run, o);
+            if (static_cast<int>(lane) >= o) run += y;
+          }
+          const uint32_t hit = __ballot_sync(0xFFFFFFFFu, run > aim);
+          if (hit) {
+            if (lane == 0) a.token[b] = static_cast<int32_t>(i0 + __ffs(hit) - 1);
+            break;
+          }
+          aim -= __shfl_sync(0xFFFFFFFFu, run, 31);
+        }
+      }
+    }
+  }
+  if (C > 1) vf_sync<C>();  // no CTA leaves while another reads its sums
+}
+
+int launch_kv_verify(const VerifyArgs& a, cudaStream_t stream) {
+  const size_t smem = static_cast<size_t>(a.T) * 21;
+  auto go = [&](auto kern, uint32_t c) {
+    return kv_launch("k_kv_verify", kern, dim3(a.n_seqs * c), kVfThreads, smem, c, stream, a);
+  };
+  if (a.vocab <= 4096) return go(k_kv_verify<1>, 1);
+  if (a.vocab <= 16384) return go(k_kv_verify<4>, 4);
+  return go(k_kv_verify<8>, 8);
+}
+
+}  // namespace ibp

@@ -11,13 +11,21 @@ in the library's CUDA kernels.  Names and formulas follow include/ibp.h:
     out, lse = ibp_tree_attention(q, k, v, table, lens, mask=mask)
     ibp_kv_summarize(k, table, lens, codes, scales)         # in place
     out, lse, picked = ibp_sparse_attention(q, k, v, table, lens, codes, scales, budget)
+    ibp_kv4_store(k, v, k4, v4, table, lens)                # into a cache in 4 bits, in place
+    k, v = ibp_kv4_load(k4, v4, table, lens, n)             # the last n tokens, as it holds them
+    out, lse = ibp_kv4_attention(q, k4, v4, table, lens, mask=mask)
+    path, n_accept, token = ibp_kv_verify(p, tokens, u, q=draft, parents=parents)
+    weights = ibp_kv_weigh(q, k, table, lens, lse, weights) # k: pages of 16 bits, or a cache in 4 bits
+    path, n_draft, n_keep, weights = ibp_kv_evict(weights, lens, budget)
     ibp_kv_get_status()                                     # raises on a data error
 
 Keys and values of a layer are tensors ``[n_pages, heads, page_tokens, dim]``
 (bfloat16 or float16) of any strides whose last is 1: tokens-first pages are a
 transposed view.  The page copies also take ``[n_pools, n_pages, heads,
-page_tokens, dim]``, every layer's K and V at once.  ``table`` is int32
-``[n_seqs, max_pages]``, ``lens`` int32 ``[n_seqs]``, ``refs`` int32
+page_tokens, dim]``, every layer's K and V at once.  A cache in 4 bits is a pair
+``(codes, scales)``: uint8 ``[n_pages, heads, page_tokens, dim / 2]`` and the queries'
+type ``[n_pages, heads, page_tokens, dim / 32]``; to the page copies either is a pool.
+``table`` is int32 ``[n_seqs, max_pages]``, ``lens`` int32 ``[n_seqs]``, ``refs`` int32
 ``[n_pages]``, all on the device.
 
 ``stream`` is a torch stream or a raw handle (default: the current stream);
@@ -45,6 +53,9 @@ IBP_KV_F16 = 1
 IBP_KV_MAX_DIM = 256
 IBP_SPARSE_MAX_BUDGET = 4096
 IBP_KV_WAIT_CYCLES = 1 << 32
+IBP_KV4_GROUP = 32
+IBP_VERIFY_MAX_VOCAB = 262144
+IBP_VERIFY_MAX_DRAFT = 1024
 
 _DTYPES = {torch.bfloat16: IBP_KV_BF16, torch.float16: IBP_KV_F16}
 
@@ -54,6 +65,14 @@ class _Pages(ctypes.Structure):
                 ("n_pages", ctypes.c_uint64), ("page_stride", ctypes.c_int64), ("heads", ctypes.c_uint32),
                 ("head_stride", ctypes.c_int64), ("page_tokens", ctypes.c_uint32),
                 ("token_stride", ctypes.c_int64), ("dim", ctypes.c_uint32), ("elem_bytes", ctypes.c_uint32)]
+
+
+class _Pages4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("scales", ctypes.c_void_p), ("scale_page_stride", ctypes.c_int64),
+                ("scale_head_stride", ctypes.c_int64), ("scale_token_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_uint64), ("heads", ctypes.c_uint32), ("page_tokens", ctypes.c_uint32),
+                ("dim", ctypes.c_uint32)]
 
 
 class _Seqs(ctypes.Structure):
@@ -71,7 +90,8 @@ def _load():
         return lib
     vp, u64, i64, u32, i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int64, ctypes.c_uint32, ctypes.c_int
     size, f32 = ctypes.c_size_t, ctypes.c_float
-    pages, seqs = ctypes.POINTER(_Pages), ctypes.POINTER(_Seqs)
+    pages, seqs, pages4 = ctypes.POINTER(_Pages), ctypes.POINTER(_Seqs), ctypes.POINTER(_Pages4)
+    weigh = [u32, seqs, vp, i64, i64, i64, u32, u32, vp, vp, f32, vp, vp, vp, u32, f32, vp, vp]
     sigs = {
         "ibp_kv_fork": ([seqs, u32, vp, u64, vp, u32, vp, vp, vp, vp, vp, vp, size, vp, vp], i32),
         "ibp_kv_free": ([seqs, u32, vp, u64, vp, u32, vp, vp, vp, vp, vp], i32),
@@ -87,6 +107,15 @@ def _load():
         "ibp_sparse_attention": ([pages, pages, u32, seqs, vp, vp, vp, i64, i64, i64, u32, u32, vp, u32, u32, u32,
                                   f32, vp, vp, vp, vp, size, vp, vp], i32),
         "ibp_sparse_attention_workspace": ([u32] * 8, size),
+        "ibp_kv4_store": ([pages4, pages4, u32, seqs, vp, i64, i64, i64, vp, i64, i64, i64, u32, vp, vp, vp], i32),
+        "ibp_kv4_load": ([pages4, pages4, u32, seqs, u32, vp, vp, vp, vp, vp], i32),
+        "ibp_kv4_attention": ([pages4, pages4, u32, seqs, vp, i64, i64, i64, u32, u32, vp, vp, f32, vp, vp, vp, size,
+                               vp, vp], i32),
+        "ibp_kv4_attention_workspace": ([u32] * 7, size),
+        "ibp_kv_verify": ([vp, i64, i64, vp, i64, i64, u32, vp, vp, vp, u32, u32, vp, vp, vp, vp, vp, vp], i32),
+        "ibp_kv_weigh": ([pages, *weigh], i32),
+        "ibp_kv4_weigh": ([pages4, *weigh], i32),
+        "ibp_kv_evict": ([vp, u32, vp, u32, u32, u32, u32, vp, vp, vp, vp, vp, vp], i32),
     }
     for name, (args, res) in sigs.items():
         f = getattr(lib, name)
@@ -568,3 +597,279 @@ def ibp_sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tabl
                                         pages.data_ptr(), None if ws is None else ws.data_ptr(), size,
                                         _status(status, device), handle), "ibp_sparse_attention")
     return *_results("ibp_sparse_attention", out, lse, q, k, v), pages
+
+
+# ---------------------------------------------------------------------------
+# Caches in 4 bits
+
+
+def _form4(pages):
+    return _form(pages[0]), _form(pages[1])
+
+
+def _as_pages4(name: str, pages) -> _Pages4:
+    codes, scales = pages
+    for what, t in (("codes", codes), ("scales", scales)):
+        _on_device(f"the {what} of {name}", t)
+        if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+            raise ValueError(f"the {what} of {name} must have the dimensions pages, heads, tokens, dim, the last contiguous")
+    if codes.dtype != torch.uint8 or scales.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be codes in uint8 and scales in bfloat16 or float16")
+    dim = 2 * codes.shape[3]
+    if dim % IBP_KV4_GROUP or scales.shape != (*codes.shape[:3], dim // IBP_KV4_GROUP) or codes.device != scales.device:
+        raise ValueError(f"the scales of {name} must be one for each {IBP_KV4_GROUP} elements of the codes, on their device")
+    return _Pages4(0, *codes.stride()[:3], 0, *scales.stride()[:3], *codes.shape[:3], dim)
+
+
+def _place4(p: _Pages4, pages):
+    p.codes, p.scales = pages[0].data_ptr(), pages[1].data_ptr()
+
+
+def _caches4(k4, v4, table: torch.Tensor, lens: torch.Tensor):
+    kp, vp = _as_pages4("k4", k4), _as_pages4("v4", v4)
+    return kp, vp, _dtype(k4[1], v4[1]), _sequences(table, lens)
+
+
+def ibp_kv4_store(k: torch.Tensor, v: torch.Tensor, k4, v4, table: torch.Tensor, lens: torch.Tensor,
+                  n_new: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """Puts k and v [n_seqs, T, heads, dim], the last T (or n_new[b]) tokens of each
+    sequence, into caches in 4 bits, (codes, scales) each, in place.  Returns (k4, v4)."""
+    lib = _load()
+
+    def check():
+        kp, vp, dt, seqs = _caches4(k4, v4, table, lens)
+        for name, t in (("k", k), ("v", v)):
+            _on_device(name, t)
+            if t.dim() != 4 or t.shape != (seqs.n_seqs, k.shape[1], kp.heads, kp.dim) or t.dtype != k4[1].dtype:
+                raise ValueError(f"{name} must be [n_seqs, T, heads, dim] of the cache's type")
+            if t.stride(3) != 1:
+                raise ValueError(f"the last dimension of {name} must be contiguous")
+        if n_new is not None:
+            _ints("n_new", n_new, seqs.n_seqs)
+        return kp, vp, dt, seqs, k.stride()[:3], v.stride()[:3]
+
+    key = ("store4", _form(k), _form(v), _form4(k4), _form4(v4), _form(table), _form(lens), _form(n_new))
+    device = k4[0].device
+    handle, where = _for(stream, device)
+    with where:
+        kp, vp, dt, seqs, ks, vs = _once(key, check)
+        _place4(kp, k4), _place4(vp, v4)
+        seqs.table, seqs.lens = table.data_ptr(), lens.data_ptr()
+        _check(lib.ibp_kv4_store(kp, vp, dt, seqs, k.data_ptr(), *ks, v.data_ptr(), *vs, k.shape[1],
+                                 None if n_new is None else n_new.data_ptr(), _status(status, device), handle),
+               "ibp_kv4_store")
+    return k4, v4
+
+
+def ibp_kv4_load(k4, v4, table: torch.Tensor, lens: torch.Tensor, T: int, n_load: torch.Tensor | None = None,
+                 k: torch.Tensor | None = None, v: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                 stream=None):
+    """The last T (or n_load[b]) tokens of each sequence as caches in 4 bits hold them:
+    (k, v) [n_seqs, T, heads, dim], zeros behind n_load[b]."""
+    lib = _load()
+
+    def check():
+        kp, vp, dt, seqs = _caches4(k4, v4, table, lens)
+        if n_load is not None:
+            _ints("n_load", n_load, seqs.n_seqs)
+        return kp, vp, dt, seqs
+
+    device = k4[0].device
+    handle, where = _for(stream, device)
+    with where:
+        kp, vp, dt, seqs = _once(("load4", _form4(k4), _form4(v4), _form(table), _form(lens), _form(n_load)), check)
+        shape = seqs.n_seqs, T, kp.heads, kp.dim
+        k = torch.empty(shape, dtype=k4[1].dtype, device=device) if k is None else _given("k", k, shape, k4[1].dtype)
+        v = torch.empty(shape, dtype=k4[1].dtype, device=device) if v is None else _given("v", v, shape, k4[1].dtype)
+        _place4(kp, k4), _place4(vp, v4)
+        seqs.table, seqs.lens = table.data_ptr(), lens.data_ptr()
+        _check(lib.ibp_kv4_load(kp, vp, dt, seqs, T, None if n_load is None else n_load.data_ptr(), k.data_ptr(),
+                                v.data_ptr(), _status(status, device), handle), "ibp_kv4_load")
+    return k, v
+
+
+def _queries(q: torch.Tensor, seqs: _Seqs, dim: int, dtype, mask, n_draft):
+    _on_device("q", q)
+    if q.dim() != 4 or q.shape[0] != seqs.n_seqs or q.shape[3] != dim or q.dtype != dtype:
+        raise ValueError("q must be [n_seqs, T, q_heads, dim] with the table's sequences and the cache's dim and type")
+    if q.shape[3] > 1 and q.stride(3) != 1:
+        raise ValueError("the last dimension of q must be contiguous")
+    T = q.shape[1]
+    if mask is not None:
+        _ints("mask", mask, seqs.n_seqs, T, (T + 31) // 32)
+    if n_draft is not None:
+        _ints("n_draft", n_draft, seqs.n_seqs)
+    return *q.stride()[:3], T, q.shape[2]
+
+
+def ibp_kv4_attention(q: torch.Tensor, k4, v4, table: torch.Tensor, lens: torch.Tensor,
+                      mask: torch.Tensor | None = None, n_draft: torch.Tensor | None = None,
+                      scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """ibp_tree_attention over caches in 4 bits, (codes, scales) each.
+    Returns (out [n_seqs, T, q_heads, dim], lse [n_seqs, T, q_heads])."""
+    lib = _load()
+
+    def check():
+        kp, vp, dt, seqs = _caches4(k4, v4, table, lens)
+        rows = _queries(q, seqs, kp.dim, k4[1].dtype, mask, n_draft)
+        size = lib.ibp_kv4_attention_workspace(seqs.n_seqs, seqs.max_pages, kp.page_tokens, *rows[3:], kp.heads, kp.dim)
+        return kp, vp, dt, seqs, rows, size, 1.0 / math.sqrt(kp.dim)
+
+    key = ("attention4", _form(q), _form4(k4), _form4(v4), _form(table), _form(lens), _form(mask), _form(n_draft))
+    device = k4[0].device
+    handle, where = _for(stream, device)
+    with where:
+        kp, vp, dt, seqs, rows, size, usual = _once(key, check)
+        out = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else _given("out", out, q.shape, q.dtype)
+        if lse is None:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=device)
+        else:
+            _given("lse", lse, q.shape[:3], torch.float32)
+        ws = _scratch(workspace, size, device)
+        _place4(kp, k4), _place4(vp, v4)
+        seqs.table, seqs.lens = table.data_ptr(), lens.data_ptr()
+        _check(lib.ibp_kv4_attention(kp, vp, dt, seqs, q.data_ptr(), *rows,
+                                     None if n_draft is None else n_draft.data_ptr(),
+                                     None if mask is None else mask.data_ptr(), usual if scale is None else scale,
+                                     out.data_ptr(), lse.data_ptr(), None if ws is None else ws.data_ptr(), size,
+                                     _status(status, device), handle), "ibp_kv4_attention")
+    return _results("ibp_kv4_attention", out, lse, q, k4[1], v4[1])
+
+
+# ---------------------------------------------------------------------------
+# Drafted tokens, eviction
+
+
+def _floats(name: str, t: torch.Tensor, *shape):
+    _on_device(name, t)
+    if t.dtype != torch.float32 or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {list(shape)}")
+
+
+def _probabilities(name: str, t: torch.Tensor, *shape):
+    _on_device(name, t)
+    if t.dtype != torch.float32 or t.shape != shape or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be a float32 tensor of shape {list(shape)}, the last dimension contiguous")
+
+
+def ibp_kv_verify(p: torch.Tensor, tokens: torch.Tensor, u: torch.Tensor, q: torch.Tensor | None = None,
+                  parents: torch.Tensor | None = None, n_draft: torch.Tensor | None = None,
+                  status: torch.Tensor | None = None, stream=None):
+    """Drafted tokens against the target's probabilities, and the next token.
+
+    p        float32 [n_seqs, T + 1, vocab]: row 0 behind the context, row 1 + t
+             behind drafted token t.
+    tokens   int32 [n_seqs, T].
+    u        float32 [n_seqs, T + 1], uniform in [0, 1): u[:, t] decides on token t,
+             the last column draws.
+    q        float32 [n_seqs, T, vocab], what the draft drew from (row 1 + parents of a
+             token); None: every drafted token was certain.
+    parents  int32 [n_seqs, T], an earlier token or -1; None: a chain.
+    Returns (path [n_seqs, T], n_accept [n_seqs], token [n_seqs]), the first two as
+    ibp_kv_accept takes them."""
+    lib = _load()
+
+    def check():
+        _on_device("tokens", tokens)
+        _ints("tokens", tokens, None, None)
+        n, T = tokens.shape
+        if p.dim() != 3:
+            raise ValueError("p must have the dimensions sequences, tokens + 1, vocabulary")
+        V = p.shape[2]
+        _probabilities("p", p, n, T + 1, V)
+        _floats("u", u, n, T + 1)
+        if q is not None:
+            _probabilities("q", q, n, T, V)
+        if parents is not None:
+            _ints("parents", parents, n, T)
+        if n_draft is not None:
+            _ints("n_draft", n_draft, n)
+        if not 1 <= V <= IBP_VERIFY_MAX_VOCAB or T > IBP_VERIFY_MAX_DRAFT:
+            raise ValueError(f"a vocabulary of 1 to {IBP_VERIFY_MAX_VOCAB} and at most {IBP_VERIFY_MAX_DRAFT} drafted tokens")
+        return n, T, V, p.stride()[:2], (0, 0) if q is None else q.stride()[:2]
+
+    key = ("verify", _form(p), _form(tokens), _form(u), _form(q), _form(parents), _form(n_draft))
+    device = p.device
+    handle, where = _for(stream, device)
+    with where:
+        n, T, V, ps, qs = _once(key, check)
+        path = torch.empty((n, T), dtype=torch.int32, device=device)
+        n_accept = torch.empty(n, dtype=torch.int32, device=device)
+        token = torch.empty(n, dtype=torch.int32, device=device)
+        _check(lib.ibp_kv_verify(p.data_ptr(), *ps, None if q is None else q.data_ptr(), *qs, V, tokens.data_ptr(),
+                                 None if parents is None else parents.data_ptr(),
+                                 None if n_draft is None else n_draft.data_ptr(), n, T, u.data_ptr(), path.data_ptr(),
+                                 n_accept.data_ptr(), token.data_ptr(), _status(status, device), handle), "ibp_kv_verify")
+    return path, n_accept, token
+
+
+def ibp_kv_weigh(q: torch.Tensor, k, table: torch.Tensor, lens: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor,
+                 mask: torch.Tensor | None = None, n_draft: torch.Tensor | None = None, scale: float | None = None,
+                 decay: float = 1.0, inplace: bool = False, status: torch.Tensor | None = None, stream=None):
+    """Adds the attention weight that the last T (or n_draft[b]) tokens' queries give to
+    each cached position, with the lse that their attention has returned.
+
+    k        pages of 16 bits, or a cache in 4 bits (codes, scales).
+    weights  float32 [n_seqs, width], width at least the longest length.
+    Returns the new weights (`weights` itself with `inplace`)."""
+    lib = _load()
+    four = isinstance(k, (tuple, list))
+
+    def check():
+        kp = _as_pages4("k", k) if four else _as_pages("k", k)
+        seqs = _sequences(table, lens)
+        kind = k[1] if four else k
+        rows = _queries(q, seqs, kp.dim, kind.dtype, mask, n_draft)
+        _floats("lse", lse, *q.shape[:3])
+        _floats("weights", weights, seqs.n_seqs, *weights.shape[1:2])
+        return kp, _dtype(kind), seqs, rows, weights.shape[1], 1.0 / math.sqrt(kp.dim)
+
+    key = ("weigh", _form(q), _form4(k) if four else _form(k), _form(table), _form(lens), _form(lse), _form(weights),
+           _form(mask), _form(n_draft))
+    device = lse.device
+    handle, where = _for(stream, device)
+    with where:
+        kp, dt, seqs, rows, width, usual = _once(key, check)
+        out = weights if inplace else torch.empty_like(weights)
+        if four:
+            _place4(kp, k)
+        else:
+            kp.data = k.data_ptr()
+        seqs.table, seqs.lens = table.data_ptr(), lens.data_ptr()
+        call = lib.ibp_kv4_weigh if four else lib.ibp_kv_weigh
+        _check(call(kp, dt, seqs, q.data_ptr(), *rows, None if n_draft is None else n_draft.data_ptr(),
+                    None if mask is None else mask.data_ptr(), usual if scale is None else scale, lse.data_ptr(),
+                    weights.data_ptr(), out.data_ptr(), width, decay, _status(status, device), handle), "ibp_kv_weigh")
+    return out
+
+
+def ibp_kv_evict(weights: torch.Tensor, lens: torch.Tensor, budget: int, keep_first: int = 0, keep_last: int = 0,
+                 status: torch.Tensor | None = None, stream=None):
+    """Which tokens of a sequence longer than `budget` stay: the first keep_first, the last
+    keep_last, and those of the largest weights [n_seqs, width] among the others.
+
+    Returns (path [n_seqs, budget], n_draft [n_seqs], n_keep [n_seqs], weights): the
+    first three make ibp_kv_accept(pool, table, lens, refs, n_draft, path, n_keep) move
+    what stays to the front; the weights have moved already."""
+    lib = _load()
+
+    def check():
+        _on_device("lens", lens)
+        _ints("lens", lens, None)
+        _floats("weights", weights, lens.shape[0], *weights.shape[1:2])
+        return weights.shape
+
+    if not 1 <= budget < 1 << 31 or keep_first < 0 or keep_last < 0 or keep_first + keep_last > budget:
+        raise ValueError("budget must be 1 or more and hold keep_first >= 0 and keep_last >= 0 tokens")
+    device = weights.device
+    handle, where = _for(stream, device)
+    with where:
+        n, width = _once(("evict", _form(weights), _form(lens)), check)
+        path = torch.empty((n, budget), dtype=torch.int32, device=device)
+        n_draft, n_keep = (torch.empty(n, dtype=torch.int32, device=device) for _ in range(2))
+        out = torch.empty_like(weights)
+        _check(lib.ibp_kv_evict(weights.data_ptr(), width, lens.data_ptr(), n, budget, keep_first, keep_last,
+                                path.data_ptr(), n_draft.data_ptr(), n_keep.data_ptr(), out.data_ptr(),
+                                _status(status, device), handle), "ibp_kv_evict")
+    return path, n_draft, n_keep, out

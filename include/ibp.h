@@ -69,8 +69,9 @@ extern "C" {
 /* 3: ibp_plan_info.short_rows, ibp_get_status_async, IBP_HINT_EARLY_FETCH
  * 4: the paged key/value cache entry points (ibp_kv_*, ibp_tree_attention,
  *    ibp_sparse_attention)
- * 5: ibp_kv_set_wait_limit */
-#define IBP_VERSION 5
+ * 5: ibp_kv_set_wait_limit
+ * 6: caches in 4 bits (ibp_kv4_*), ibp_kv_verify, ibp_kv_weigh, ibp_kv_evict */
+#define IBP_VERSION 6
 #define IBP_MAX_W 8192u
 #define IBP_NOALLOC_MAX_W 4096u
 
@@ -729,6 +730,160 @@ int ibp_sparse_attention(const ibp_kv_pages* k, const ibp_kv_pages* v, uint32_t 
                          uint32_t* status, void* stream);
 size_t ibp_sparse_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t page_tokens, uint32_t T,
                                       uint32_t q_heads, uint32_t kv_heads, uint32_t dim, uint32_t budget);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Paged caches in 4 bits
+ * ---------------------------------------------------------------------------
+ * The dim elements of one token of one head are dim / 2 bytes of codes (element
+ * 2 i in the low half of byte i) and dim / 32 scales of the queries' type, one
+ * for each group of 32 elements.  An element stands for (c - 8) s, c its code and
+ * s its group's scale.  ibp_kv4_store sets s to a / 7, a the group's largest
+ * magnitude, rounded to 5 significant bits (ties to even; in half precision then
+ * to that type; 0 below 2^-100, 2^121 at most), and c to 8 + x / s rounded to
+ * whole (ties to even) and kept within 1 to 15.  So bfloat16 and half precision
+ * hold every element exactly.  A group with an element that is not finite gets a
+ * scale that is not a number and stands for that.  Of scales written by others,
+ * bfloat16 ones are read without their 3 lowest bits and as NaN from 2^122 on;
+ * half-precision ones give (c - 8) s rounded to half precision.
+ *
+ * Codes and scales are pages of elem_bytes 1 and 2 to ibp_kv_copy and
+ * ibp_kv_accept (one call each; the second with the table, lengths and references
+ * that the first was given), so forks, compaction, acceptance and eviction serve
+ * these caches too.
+ */
+#define IBP_KV4_GROUP 32u
+
+typedef struct ibp_kv4_pages {
+  void* codes;                  /* token 0 of head 0 of page 0; strides in bytes, base and strides multiples of 16 */
+  int64_t page_stride, head_stride, token_stride;
+  void* scales;                 /* strides in elements of 2 bytes */
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+  uint64_t n_pages;             /* < 2^31 */
+  uint32_t heads;
+  uint32_t page_tokens;
+  uint32_t dim;                 /* a multiple of 32, at most IBP_KV_MAX_DIM */
+} ibp_kv4_pages;
+
+/*
+ * Puts keys and values into the cache: row t < n of sequence b, n = n_new[b]
+ * (NULL: T), becomes position lens[b] - n + t, so the lengths count the new tokens
+ * already.  The pages that are written must not be shared.  Rows whose position is
+ * below 0 or whose page id is out of range are not stored and record IBP_ERANGE, as
+ * does an n outside [0, T] (read as the nearer end).
+ *
+ * k, v     n_seqs x T x heads x dim by strides (elements); dim contiguous.
+ */
+int ibp_kv4_store(const ibp_kv4_pages* k_pages, const ibp_kv4_pages* v_pages, uint32_t dtype, const ibp_kv_seqs* seqs,
+                  const void* k, int64_t k_seq_stride, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                  int64_t v_seq_stride, int64_t v_token_stride, int64_t v_head_stride, uint32_t T, const int32_t* n_new,
+                  uint32_t* status, void* stream);
+
+/*
+ * Reads the last n = n_load[b] (NULL: T) tokens of each sequence back: k and v,
+ * n_seqs x T x heads x dim, contiguous and 16-byte aligned, get what the cache stands
+ * for in rows t < n and zeros behind; rows without a position or page as for
+ * ibp_kv4_store, as zeros.
+ */
+int ibp_kv4_load(const ibp_kv4_pages* k_pages, const ibp_kv4_pages* v_pages, uint32_t dtype, const ibp_kv_seqs* seqs,
+                 uint32_t T, const int32_t* n_load, void* k, void* v, uint32_t* status, void* stream);
+
+/*
+ * ibp_tree_attention over a cache in 4 bits: the same formulas, arguments and
+ * rules, with what the codes stand for as keys and values.  A position whose page id
+ * is out of range reads as a zero key and value and records IBP_ERANGE.
+ *
+ * ws       ibp_kv4_attention_workspace bytes (0: may be NULL).  Calls of more than
+ *          128 rows a kv head (T * q_heads / kv_heads) and dim <= 128 decode the
+ *          cache once, so theirs holds the sequences in 16 bits.
+ */
+int ibp_kv4_attention(const ibp_kv4_pages* k, const ibp_kv4_pages* v, uint32_t dtype, const ibp_kv_seqs* seqs,
+                      const void* q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride, uint32_t T,
+                      uint32_t q_heads, const int32_t* n_draft, const uint32_t* mask, float scale, void* out, float* lse,
+                      void* ws, size_t ws_bytes, uint32_t* status, void* stream);
+size_t ibp_kv4_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t page_tokens, uint32_t T,
+                                   uint32_t q_heads, uint32_t kv_heads, uint32_t dim);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Drafted tokens against the target's probabilities
+ * ---------------------------------------------------------------------------
+ * Row 0 of p[b] is the target's distribution behind the context of sequence b, row
+ * 1 + t the one behind drafted token t; q[b] has the draft's, so token t was drawn
+ * from row 1 + parents[b][t] of q (parents NULL: t - 1, a chain; -1: the context).
+ * Probabilities are cut to [0, 1], NaN counts as 0.  Starting behind the context
+ * (node -1) with left = row 0 of p, for t = 0, 1, ... with parents[b][t] == node and
+ * x = tokens[b][t]:
+ *   accepted when u[b][t] * q_x < left_x (the product exact): node = t, left = row
+ *   1 + t of p;
+ *   otherwise rest = max(left - q, 0), Z = sum of rint(rest * 2^44), left = rest *
+ *   float(2^44 / Z), every operation rounded to single precision; with Z == 0 left
+ *   stays as it was.
+ * With q NULL every drafted token was certain (q_x = 1, all others 0).  The next
+ * token is drawn from the rest of the last rejection that left something behind the
+ * last node, or from its row of p: the first token whose running sum of
+ * rint(w * 2^44) is above floor(u[b][T] * total).  These sums are of whole numbers, so the results are the same on every run.
+ * Tokens out of range and parents that are not an earlier token or -1 are passed
+ * over and record IBP_ERANGE; where nothing has a probability the token is -1 and
+ * IBP_ERANGE is recorded.  A u of 1 or more draws the last token with a weight; one
+ * that is not a number, or below 0, the first, and a test with a NaN rejects.
+ *
+ * p        n_seqs x (T + 1) x vocab floats by strides (elements); vocab contiguous.
+ * q        n_seqs x T x vocab likewise, or NULL.
+ * tokens, parents  n_seqs x T; n_draft  per sequence, or NULL: T.
+ * u        n_seqs x (T + 1), in [0, 1).
+ * path     n_seqs x T: the accepted tokens ascending, then -1; n_accept  their
+ *          number: the arguments of ibp_kv_accept.  token  the drawn tokens.
+ */
+#define IBP_VERIFY_MAX_VOCAB 262144u
+#define IBP_VERIFY_MAX_DRAFT 1024u
+int ibp_kv_verify(const float* p, int64_t p_seq_stride, int64_t p_row_stride, const float* q, int64_t q_seq_stride,
+                  int64_t q_row_stride, uint32_t vocab, const int32_t* tokens, const int32_t* parents,
+                  const int32_t* n_draft, uint32_t n_seqs, uint32_t T, const float* u, int32_t* path, int32_t* n_accept,
+                  int32_t* token, uint32_t* status, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Eviction by accumulated attention weight
+ * ---------------------------------------------------------------------------
+ * ibp_kv_weigh adds what a step's queries gave to each position j < lens[b] of
+ * the cache: w_out[b][j] = decay * w[b][j] + sum of exp(scale * q . k_j - lse) over the
+ * queries and heads that see j, as ibp_tree_attention lets them and with the lse that
+ * it or ibp_kv4_attention has returned; the positions of the draft itself (the last n
+ * tokens) start from 0 instead of decay * w.  Positions from lens[b] on keep their w.
+ * A row with lse -infinity adds nothing.  Positions whose page id is out of range
+ * count as zero keys and record IBP_ERANGE, as lengths above width do (positions from
+ * width on are not weighed).
+ *
+ * w, w_out  n_seqs x width floats; w_out may be w.
+ * The rest as for ibp_tree_attention; ibp_kv4_weigh reads keys in 4 bits.
+ */
+int ibp_kv_weigh(const ibp_kv_pages* k, uint32_t dtype, const ibp_kv_seqs* seqs, const void* q, int64_t q_seq_stride,
+                 int64_t q_token_stride, int64_t q_head_stride, uint32_t T, uint32_t q_heads, const int32_t* n_draft,
+                 const uint32_t* mask, float scale, const float* lse, const float* w, float* w_out, uint32_t width,
+                 float decay, uint32_t* status, void* stream);
+int ibp_kv4_weigh(const ibp_kv4_pages* k, uint32_t dtype, const ibp_kv_seqs* seqs, const void* q, int64_t q_seq_stride,
+                  int64_t q_token_stride, int64_t q_head_stride, uint32_t T, uint32_t q_heads, const int32_t* n_draft,
+                  const uint32_t* mask, float scale, const float* lse, const float* w, float* w_out, uint32_t width,
+                  float decay, uint32_t* status, void* stream);
+
+/*
+ * Which tokens stay when a sequence is longer than `budget`: the first keep_first,
+ * the last keep_last, and of the others those of the largest weights, the lower position
+ * first when equal (NaN is below everything), up to `budget` in all.
+ * path[b] lists them ascending, n_keep[b] = budget, n_draft[b] = lens[b]: the
+ * arguments with which ibp_kv_accept moves them to the front of the sequence in every
+ * pool and frees the pages behind.  Sequences within the budget get n_draft =
+ * n_keep = 0, which ibp_kv_accept leaves alone.  w_out[b] has the weights of the
+ * tokens that stay at their new positions and 0 behind.  Lengths outside [0,
+ * width] are cut to it and record IBP_ERANGE.
+ *
+ * w, w_out  n_seqs x width floats, not overlapping.
+ * path      n_seqs x budget, unused entries -1; n_draft, n_keep  per sequence.
+ */
+int ibp_kv_evict(const float* w, uint32_t width, const int32_t* lens, uint32_t n_seqs, uint32_t budget,
+                 uint32_t keep_first, uint32_t keep_last, int32_t* path, int32_t* n_draft, int32_t* n_keep, float* w_out,
+                 uint32_t* status, void* stream);
 
 #ifdef __cplusplus
 }
