@@ -49,7 +49,7 @@ int rows4_of(Kv4Rows* r, const ibp_kv4_pages* k, const ibp_kv4_pages* v, uint32_
   if (!alike(k, v)) return refuse("k and v pages differ in shape");
   if (T == 0 || T > 0x7FFFFF00u) return refuse("T outside [1, 2^31 - 256]");
   r->table = seqs->table, r->lens = seqs->lens, r->n_rows = n_rows, r->status = status;
-  if (!resolve(r->table, device, seqs->max_pages == 0) || !resolve(r->lens, device, seqs->n_seqs == 0) ||
+  if (!resolve(r->table, device, seqs->max_pages == 0) || !resolve(r->lens, device) ||
       !resolve(r->n_rows, device, true) || !resolve(r->status, device, true))
     return refuse("a pointer is NULL, misaligned or not device-accessible");
   r->n_seqs = seqs->n_seqs, r->max_pages = seqs->max_pages, r->n_pages = static_cast<uint32_t>(k->n_pages);
@@ -106,10 +106,10 @@ int ibp_kv4_store(const ibp_kv4_pages* k_pages, const ibp_kv4_pages* v_pages, ui
   int device;
   int rc = current_device(&device);
   if (rc) return rc;
+  if (seqs && seqs->n_seqs == 0) return IBP_OK;
   Kv4Rows r;
   rc = rows4_of(&r, k_pages, v_pages, dtype, seqs, T, n_new, status, device);
   if (rc) return rc;
-  if (r.n_seqs == 0) return IBP_OK;
   const uint16_t *kk = static_cast<const uint16_t*>(k), *vv = static_cast<const uint16_t*>(v);
   if (!resolve(kk, device) || !resolve(vv, device)) return refuse("k or v is NULL, misaligned or not device-accessible");
   r.x[0] = reinterpret_cast<const char*>(kk), r.x[1] = reinterpret_cast<const char*>(vv);
@@ -129,10 +129,10 @@ int ibp_kv4_load(const ibp_kv4_pages* k_pages, const ibp_kv4_pages* v_pages, uin
   int device;
   int rc = current_device(&device);
   if (rc) return rc;
+  if (seqs && seqs->n_seqs == 0) return IBP_OK;
   Kv4Rows r;
   rc = rows4_of(&r, k_pages, v_pages, dtype, seqs, T, n_load, status, device);
   if (rc) return rc;
-  if (r.n_seqs == 0) return IBP_OK;
   char *kk = static_cast<char*>(k), *vv = static_cast<char*>(v);
   if (!resolve(kk, device) || !resolve(vv, device)) return refuse("k or v is NULL or not device-accessible");
   if ((reinterpret_cast<uintptr_t>(kk) | reinterpret_cast<uintptr_t>(vv)) % 16) return refuse("k or v is not 16-byte aligned");
