@@ -139,8 +139,9 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_store(const Kv4Rows r, uint
 template <bool F16>
 __device__ __forceinline__ uint4 decode8(uint32_t word, uint32_t scale) {
   const quad::Pair<F16> p(scale * 0x10001u);
-  const uint32_t a = quad::decode<F16, 0>(word, p), b = quad::decode<F16, 1>(word, p);  // elements (0, 4), (1, 5)
-  const uint32_t c = quad::decode<F16, 2>(word, p), d = quad::decode<F16, 3>(word, p);
+  const quad::Magic<F16> m;
+  const uint32_t a = quad::decode<F16, 0>(word, p, m), b = quad::decode<F16, 1>(word, p, m);  // elements (0, 4), (1, 5)
+  const uint32_t c = quad::decode<F16, 2>(word, p, m), d = quad::decode<F16, 3>(word, p, m);
   return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(c, d, 0x7632));
 }
 
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_load(const Kv4Rows r, uint6
     uint4 u = make_uint4(0u, 0u, 0u, 0u);
     if (s.page != 0xFFFFFFFFu) {
       const uint32_t word = *reinterpret_cast<const uint32_t*>(codes_at(r.p[e.which], s, e.h, e.c));
-      u = decode8<F16>(word, quad::scale_bits<F16>(*reinterpret_cast<const uint16_t*>(scale_at(r.p[e.which], s, e.h, e.c))));
+      u = decode8<F16>(word, *reinterpret_cast<const uint16_t*>(scale_at(r.p[e.which], s, e.h, e.c)));
     }
     *reinterpret_cast<uint4*>(dst) = u;
   }
@@ -208,8 +209,8 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_expand(const Attend4Args x,
       if (s.page < a.n_pages) {
         const uint32_t kw = *reinterpret_cast<const uint32_t*>(codes_at(x.k, s, h, c)), vw = *reinterpret_cast<const uint32_t*>(codes_at(x.v, s, h, c));
         const uint32_t ks = *reinterpret_cast<const uint16_t*>(scale_at(x.k, s, h, c)), vs = *reinterpret_cast<const uint16_t*>(scale_at(x.v, s, h, c));
-        uk = decode8<F16>(kw, quad::scale_bits<F16>(ks));
-        uv = decode8<F16>(vw, quad::scale_bits<F16>(vs));
+        uk = decode8<F16>(kw, ks);
+        uv = decode8<F16>(vw, vs);
       } else {
         kv_status(a.status, IBP_ERANGE);
       }

@@ -39,10 +39,16 @@ int launch_kv4_load(const Kv4Rows& r, int device, cudaStream_t stream);
 struct Attend4Args {
   AttendArgs a;    // k and v are not used
   Kv4View k, v;
+  int32_t shift;   // pages of 2^shift tokens, or -1
 };
 
 size_t kv4_attend_workspace(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint64_t tokens, int device);
-int launch_kv4_attend(Attend4Args& x, int device, size_t ws_bytes, cudaStream_t stream);
+int launch_kv4_attend(const Attend4Args& x, int device, size_t ws_bytes, cudaStream_t stream);
+
+// The tensor-core kernel on codes (ibp_kv4_tree.cu): positive scales only.
+bool kv4_tree_takes(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint64_t tokens, int device);
+size_t kv4_tree_workspace(uint32_t dim, int device);
+int launch_kv4_tree(const Attend4Args& x, int device, size_t ws_bytes, cudaStream_t stream);
 
 // Decodes every sequence into pages of kExpand tokens (page b * ceil(tokens / kExpand) + j
 // of sequence b), with a table and lengths that say so.
@@ -58,8 +64,8 @@ int launch_kv4_expand(const Attend4Args& x, const Kv4Expanded& e, int device, cu
 
 namespace quad {
 
-// A scale as the decoders take it, in the low half.  bfloat16: 5 significant bits (the
-// rest are ignored), and not a number from 2^122 on, where 24 s may overflow.
+// A scale as `odd` and `value` take it, in the low half.  bfloat16: 5 significant bits
+// (the rest are ignored), and not a number from 2^122 on, where 24 s may overflow.
 template <bool F16>
 __device__ __forceinline__ uint32_t scale_bits(uint32_t s) {
   if (F16) return s;
@@ -90,15 +96,33 @@ __device__ __forceinline__ float value(uint32_t word, uint32_t i, uint32_t scale
   return F16 ? to_float<true>(pack2<true>(v, 0.f) & 0xFFFFu) : v;
 }
 
-// A pair of scales and what the decoding adds.
+// A pair of scales as read, and what the decoding adds.  bfloat16: 64 s is infinite from
+// 2^122 on, and then everything decoded is NaN; the products with 1 / 64 and
+// -24 / 64 are exact for 5 bits.  `keep` 0 makes the group zeros.
 template <bool F16>
 struct Pair {
   uint32_t s, m;
-  __device__ __forceinline__ explicit Pair(uint32_t both) : s(both) {
-    if (F16)
+  __device__ __forceinline__ explicit Pair(uint32_t both, bool keep = true) {
+    if (F16) {
+      s = keep ? both : 0u;
       m = 0xCE00CE00u;  // -24
-    else
-      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(s), "r"(0xC1C0C1C0u));  // -24 s, exact for 5 bits
+    } else {
+      uint32_t w;
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w) : "r"(both & (keep ? 0xFFF8FFF8u : 0u)), "r"(0x42804280u));  // 64
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(s) : "r"(w), "r"(0x3C803C80u));
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(w), "r"(0xBEC0BEC0u));
+    }
+  }
+};
+
+// The constants of a decoding, kept in registers: with two immediates a mask with the
+// exponent put in would be two instructions.
+template <bool F16>
+struct Magic {
+  uint32_t mask, one;
+  __device__ __forceinline__ Magic() {
+    asm volatile("mov.u32 %0, %1;" : "=r"(mask) : "n"(F16 ? 0x03C003C0 : 0x00780078));
+    asm volatile("mov.u32 %0, %1;" : "=r"(one) : "n"(F16 ? 0x4C004C00 : 0x41804180));
   }
 };
 
@@ -107,16 +131,16 @@ struct Pair {
 // bfloat16: (16 + c) s - 24 s in one fused operation, exact since the result is
 // representable.  Half precision, where 24 s may overflow: ((16 + c) - 24) s.
 template <bool F16, int I>
-__device__ __forceinline__ uint32_t decode(uint32_t w, const Pair<F16>& p) {
+__device__ __forceinline__ uint32_t decode(uint32_t w, const Pair<F16>& p, const Magic<F16>& c) {
   uint32_t r;
   if (F16) {
     r = I == 0 ? w << 6 : (I == 1 ? w << 2 : (I == 2 ? w >> 2 : w >> 6));
-    r = (r & 0x03C003C0u) | 0x4C004C00u;
+    asm("lop3.b32 %0, %0, %1, %2, 0xEA;" : "+r"(r) : "r"(c.mask), "r"(c.one));
     asm("add.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(p.m));
     asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(p.s));
   } else {
     r = I == 0 ? w << 3 : (I == 1 ? w >> 1 : (I == 2 ? w >> 5 : w >> 9));
-    r = (r & 0x00780078u) | 0x41804180u;
+    asm("lop3.b32 %0, %0, %1, %2, 0xEA;" : "+r"(r) : "r"(c.mask), "r"(c.one));
     asm("fma.rn.bf16x2 %0, %0, %1, %2;" : "+r"(r) : "r"(p.s), "r"(p.m));
   }
   return r;

@@ -1,60 +1,52 @@
 // ibp_kv4_attend.cu - attention of few queries over a paged cache held in 4 bits.
 //
 // A CTA holds 8 or 16 query rows of one sequence and kv head (drafted tokens times
-// the group's heads) and walks a share of the tokens, 16 to a warp's step, each warp
-// with its own running maximum and sum.  The products are taken transposed, S^T = K Q^T
-// and O^T = V^T P^T, so that tokens and dimensions fill the 16-row side of
-// mma.m16n8k16 and queries the 8-wide side.
+// the group's heads) and walks a share of the tokens; its four warps take a step of 16
+// or 32 tokens in turn, each with a ring of stages that asynchronous copies fill and a
+// running maximum and sum of its own.  The products are taken transposed, S^T = K Q^T and
+// O^T = V^T P^T, so that tokens and dimensions fill the 16-row side of mma.m16n8k16
+// and queries the 8-wide side.
 //
 // A dot product may add its dimensions in any order, so a lane takes for its part of
 // a K row the codes that lie next to one another, up to 32 of one group: one 16-byte
-// load, one scale, and the queries are laid out to match.  The same holds for the rows
-// of O^T: a lane takes neighbouring dimensions of V for the four tokens that are its
-// part of the product, and pairs of tokens are made by byte permutations.  So codes go
-// from global memory to registers, are decoded there and are the operands: nothing
-// passes through shared memory until the warps are joined.
+// read, one scale, and the queries are laid out to match.  The same holds for the rows of
+// O^T: a lane takes neighbouring dimensions of V for the four tokens that are its part
+// of the product, and pairs of tokens are made by byte permutations.  Codes are
+// decoded in registers and are the operands.
+//
+// Work is split evenly over the CTAs that the GPU holds at once, by tiles of all items
+// in a row, as in the tensor-core kernel (ibp_kv_tree.cuh), whose walk and join serve
+// here too: ragged lengths cost nothing.
 //
 // Decoding is what counts beside the cache's bytes: 12 instructions for 8 elements
 // (a shift, a mask with the exponent put in, one fused multiply-add a pair).
 #include <type_traits>
 
-#include "ibp_kv4.cuh"
+#include "ibp_kv_tree.cuh"
 
 namespace ibp {
 
 constexpr uint32_t kQdWarps = 4;
+// CTAs of a SM for 8 rows: at 168 registers a thread the decoding has the independent
+// instructions that four CTAs at 128 lack (32 ragged caches of up to 32768 tokens, 8 kv
+// heads of 8 query heads: 199 us against 216 us).
+constexpr uint32_t kQdCtas = 3;
 
-// What a lane holds of a step's 16 tokens.
-template <uint32_t DP>
-struct QuadStep {
-  uint32_t kw[2][DP / 32];               // K codes of tokens g and g + 8
-  uint32_t ks[2][DP == 256 ? 2 : 1];     // their scales
-  uint32_t vw[4][DP / 64];               // V codes of tokens 2t, 2t + 1, 2t + 8, 2t + 9
-  uint32_t vs[4];
-};
-
-template <uint32_t N>
-__device__ __forceinline__ void ld_words(uint32_t (&w)[N], const char* p, bool on) {
-  static_assert(N == 1 || N == 2 || N == 4, "");
-#pragma unroll
-  for (uint32_t i = 0; i < N; ++i) w[i] = 0u;
-  if (!on) return;
-  if constexpr (N == 4)
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-  else if constexpr (N == 2)
-    asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-  else
-    asm("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
-}
-__device__ __forceinline__ uint32_t ld_scale(const char* p, bool on) {
-  return on ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p))) : 0u;
-}
-
-template <uint32_t DP, uint32_t NT, bool F16>
+template <uint32_t DP, uint32_t NT>
 struct Quad {
+  // Tokens of a step: what a step costs besides decoding and products (maxima over the
+  // lanes, bookkeeping) is shared by two blocks of 16 where the registers allow it.
+    static constexpr uint32_t kMma = DP == 256 ? 1 : 2;
+  static constexpr uint32_t kSub = 16 * kMma;
+  static constexpr uint32_t kTile = kSub * kQdWarps;       // a step of every warp
   static constexpr uint32_t kRows = 8 * NT;
-  // the join: [warp][row][DP] and [warp][row][2], then a cluster's part [row][2 + DP]
-  static constexpr uint32_t kBytes = (kQdWarps * kRows * (DP + 2) + kRows * (DP + 2)) * 4;
+  static constexpr uint32_t kCodes = kSub * DP / 2;        // bytes of K's or V's codes in a stage
+  static constexpr uint32_t kScale = DP / 16;              // bytes of a token's scales
+  static constexpr uint32_t kStage = 2 * kCodes + 2 * kSub * kScale;
+  static constexpr uint32_t kStages = 3;
+  static constexpr uint32_t kRing = kQdWarps * kStages * kStage;
+  static constexpr uint32_t kJoin = kQdWarps * kRows * (DP + 2) * 4;
+  static constexpr uint32_t kBytes = kRing > kJoin ? kRing : kJoin;
 
   static __device__ __forceinline__ bool sees(const AttendArgs& a, uint32_t b, int32_t ctx, int32_t len, uint32_t r, int32_t pos) {
     if (pos >= len) return false;
@@ -63,491 +55,569 @@ struct Quad {
     if (!a.mask) return i <= t;
     return (a.mask[(static_cast<uint64_t>(b) * a.T + t) * a.mask_words + (i >> 5)] >> (i & 31u)) & 1u;
   }
+
+  // Place of 16 bytes of a token's codes: a line of 128 bytes holds 4, 2 or 1 tokens,
+  // its pieces in an order that differs from line to line, so that neither the reads of K
+  // (eight lanes on neighbouring rows) nor those of V (lanes on rows two apart) meet in a
+  // bank.  Eight tokens on, the order is the same.
+  static __device__ __forceinline__ uint32_t at(uint32_t tok, uint32_t c) {
+    const uint32_t piece = tok * (DP / 32) + c, line = piece >> 3;
+    const uint32_t turn = DP == 64 ? (line & 1u) * 2 : (DP == 128 ? (line & 3u) * 2 : line & 7u);
+    return (piece ^ turn) * 16;
+  }
 };
 
-// Where a lane's parts of a step lie.
-struct QuadLane {
-  const char *kc, *ks, *vc, *vs;  // this lane's part of token 0 of slot 0 of page 0
-  const int32_t* row;
-  int32_t shift;                  // pages hold 2^shift steps; -1: another whole number; -2: steps cross pages
-  bool k_on[2], v_on;             // the dim reaches this lane's groups
-};
-
-__device__ __forceinline__ uint32_t quad_page(const AttendArgs& a, const QuadLane& ln, uint32_t step, uint32_t steps) {
-  if (ln.shift < -1 || step >= steps) return 0xFFFFFFFFu;
-  return static_cast<uint32_t>(__ldg(ln.row + (ln.shift >= 0 ? step >> ln.shift : step * 16 / a.page_tokens)));
+// A copy of N bytes into shared memory, or zeros.
+template <uint32_t N>
+__device__ __forceinline__ void quad_copy(uint32_t dst, const void* src, bool on) {
+  if constexpr (N == 16)
+    cp16(dst, src, on);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(on ? N : 0u) : "memory");
 }
 
-template <uint32_t DP>
-__device__ __forceinline__ void quad_load(const Attend4Args& x, const QuadLane& ln, uint32_t step, uint32_t n_tok, uint32_t page,
-                                          QuadStep<DP>& s) {
-  const AttendArgs& a = x.a;
-  const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
-  constexpr uint32_t kK = DP / 32;  // words of K a lane and token
-  auto load_k = [&](uint32_t i, const char* codes, const char* scales, bool on) {
-    if constexpr (kK == 8) {
-      uint32_t lo[4], hi[4];
-      ld_words<4>(lo, codes, on && ln.k_on[0]);
-      ld_words<4>(hi, codes + 16, on && ln.k_on[1]);
+// How the cache is laid out: pages of whole blocks of 16 tokens, a token's scales all of
+// DP's and aligned (kEven); anything else (kAny).
+enum QuadForm { kEven, kAny };
+
+// Pages of a step's blocks of 16 (kEven), or the page and slot of the lane's token
+// (kAny), still on their way.
+struct QuadSpot {
+  uint32_t page[2];
+  bool there;
+};
+
+template <QuadForm FORM, uint32_t KM>
+__device__ __forceinline__ QuadSpot quad_spot(const AttendArgs& a, int32_t shift, const int32_t* row, uint32_t tok, uint32_t n_tok) {
+  QuadSpot s;
+  s.page[0] = s.page[1] = 0xFFFFFFFFu;
+  auto page_of = [&](uint32_t x) { return static_cast<uint32_t>(__ldg(row + (shift >= 0 ? x >> shift : x / a.page_tokens))); };
+  if (FORM == kEven) {
+    s.there = tok < n_tok;
+    if (s.there) s.page[0] = page_of(tok);
+    if (KM == 2 && tok + 16 < n_tok) s.page[1] = page_of(tok + 16);
+  } else {
+    const uint32_t mine = tok + (threadIdx.x & 31u);
+    s.there = (threadIdx.x & 31u) < 16 * KM && mine < n_tok;
+    if (s.there) s.page[0] = page_of(mine);
+  }
+  return s;
+}
+
+// Asks for the codes and scales of the step at token tok.  Tokens past the last, pages
+// that are not there and dimensions that do not exist become zeros.  base: K's codes and
+// scales, V's codes and scales of this head; with kEven of this lane's chunk and first
+// token (codes) and of this lane's token modulo 16 (scales).
+template <uint32_t DP, uint32_t NT, QuadForm FORM>
+__device__ __forceinline__ void quad_fill(const TcArgs& t, const QuadSpot& sp, int32_t shift, uint32_t tok, uint32_t n_tok,
+                                          const char* const (&base)[4], uint32_t stage, unsigned char* stage_p) {
+  using Q = Quad<DP, NT>;
+  const AttendArgs& a = t.a;
+  const uint32_t lane = threadIdx.x & 31u;
+  constexpr uint32_t kChunks = DP / 32, kPer = 32 / kChunks;  // 16-byte chunks of a token, tokens an instruction
+  constexpr uint32_t kTurns = kPer < 8 ? 8 / kPer : 1;        // instructions after which the order repeats
+  const uint32_t c = lane % kChunks, r0 = lane / kChunks;
+  uint32_t dst[kTurns];
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) s.kw[i][j] = lo[j], s.kw[i][4 + j] = hi[j];
-      s.ks[i][0] = ld_scale(scales, on && ln.k_on[0]);
-      s.ks[i][DP == 256 ? 1 : 0] = ld_scale(scales + 2, on && ln.k_on[1]);
-    } else {
-      ld_words<kK>(s.kw[i], codes, on && ln.k_on[0]);
-      s.ks[i][0] = ld_scale(scales, on && ln.k_on[0]);
+  for (uint32_t i = 0; i < kTurns; ++i) dst[i] = stage + Q::at(r0 + i * kPer, c) - i * kPer * (DP / 2);
+  if (FORM == kEven) {
+    // strides of 32 bits, and a page's tokens within 32 bits
+    auto small = [](int64_t x) { return static_cast<uint32_t>(x); };
+    auto at_page = [&](uint32_t page, int64_t stride) { return static_cast<uint64_t>(page) * small(stride); };
+    const uint32_t left = n_tok - tok;
+    const char *k[Q::kMma], *v[Q::kMma];
+    bool good[Q::kMma];
+    uint32_t slot[Q::kMma];
+#pragma unroll
+    for (uint32_t x = 0; x < Q::kMma; ++x) {
+      const uint32_t first = tok + 16 * x;
+      slot[x] = shift >= 0 ? first & ((1u << shift) - 1u) : first % a.page_tokens;
+      good[x] = sp.page[x] < a.n_pages;
+      if (!good[x] && first < n_tok) kv_status(a.status, IBP_ERANGE);
+      const uint32_t page = good[x] ? sp.page[x] : 0;
+      k[x] = base[0] + at_page(page, t.four[0].page_stride) + slot[x] * small(t.four[0].token_stride);
+      v[x] = base[2] + at_page(page, t.four[1].page_stride) + slot[x] * small(t.four[1].token_stride);
     }
-  };
-  if (ln.shift >= -1) {
-    const uint32_t at = ln.shift >= 0 ? step >> ln.shift : step * 16 / a.page_tokens;
-    const uint32_t s0 = step * 16 - at * a.page_tokens, left = n_tok - step * 16;
-    const bool good = page < a.n_pages;
-    if (!good) kv_status(a.status, IBP_ERANGE);
-    const int64_t pg = good ? page : 0;
-    const char* kc = ln.kc + pg * x.k.page_stride + static_cast<int64_t>(s0 + g) * x.k.token_stride;
-    const char* ks = ln.ks + pg * x.k.s_page + static_cast<int64_t>(s0 + g) * x.k.s_token;
-    load_k(0, kc, ks, good && g < left);
-    load_k(1, kc + 8 * x.k.token_stride, ks + 8 * x.k.s_token, good && g + 8 < left);
-    const char* vc = ln.vc + pg * x.v.page_stride + static_cast<int64_t>(s0 + 2 * t) * x.v.token_stride;
-    const char* vs = ln.vs + pg * x.v.s_page + static_cast<int64_t>(s0 + 2 * t) * x.v.s_token;
+    const bool all = left >= Q::kSub && good[0] && good[Q::kMma - 1];
+    const uint32_t mine = lane / 16 % Q::kMma;  // the block of this lane's token
+    const uint32_t page = (mine ? good[Q::kMma - 1] : good[0]) ? (mine ? sp.page[Q::kMma - 1] : sp.page[0]) : 0;
+    const uint32_t sl = mine ? slot[Q::kMma - 1] : slot[0];
+    const uint32_t to = stage + 2 * Q::kCodes + lane * Q::kScale;
+    const char* ks = base[1] + at_page(page, t.four[0].s_page) + sl * small(t.four[0].s_token);
+    const char* vs = base[3] + at_page(page, t.four[1].s_page) + sl * small(t.four[1].s_token);
+    constexpr uint32_t kEach = 16 / kPer;  // instructions a block
+    if (all) {
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-      const uint32_t off = (i & 1u) + (i >> 1) * 8;
-      const bool on = good && 2 * t + off < left && ln.v_on;
-      ld_words<DP / 64>(s.vw[i], vc + off * x.v.token_stride, on);
-      s.vs[i] = ld_scale(vs + off * x.v.s_token, on);
+      for (uint32_t i = 0; i < Q::kSub / kPer; ++i) {
+        quad_copy<16>(dst[i % kTurns] + i * kPer * (DP / 2), k[i / kEach] + i % kEach * kPer * small(t.four[0].token_stride), true);
+        quad_copy<16>(dst[i % kTurns] + i * kPer * (DP / 2) + Q::kCodes, v[i / kEach] + i % kEach * kPer * small(t.four[1].token_stride), true);
+      }
+      if (Q::kSub == 32 || lane < Q::kSub) {
+        quad_copy<Q::kScale>(to, ks, true);
+        quad_copy<Q::kScale>(to + Q::kSub * Q::kScale, vs, true);
+      }
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < Q::kSub / kPer; ++i) {
+        const bool on = good[i / kEach] && r0 + i * kPer < left;
+        quad_copy<16>(dst[i % kTurns] + i * kPer * (DP / 2), on ? k[i / kEach] + i % kEach * kPer * small(t.four[0].token_stride) : base[0], on);
+        quad_copy<16>(dst[i % kTurns] + i * kPer * (DP / 2) + Q::kCodes, on ? v[i / kEach] + i % kEach * kPer * small(t.four[1].token_stride) : base[2], on);
+      }
+      if (lane < Q::kSub) {
+        const bool on = (mine ? good[Q::kMma - 1] : good[0]) && lane < left;
+        quad_copy<Q::kScale>(to, on ? ks : base[1], on);
+        quad_copy<Q::kScale>(to + Q::kSub * Q::kScale, on ? vs : base[3], on);
+      }
     }
     return;
   }
-  // Steps cross pages: lane i finds token i and tells the others.
-  const uint32_t tok = step * 16 + (lane & 15u);
-  uint32_t pg = 0xFFFFFFFFu, slot = 0;
-  if (tok < n_tok) {
-    const uint32_t nth = tok / a.page_tokens;
-    slot = tok - nth * a.page_tokens;
-    pg = static_cast<uint32_t>(ln.row[nth]);
-    if (pg >= a.n_pages) {
-      kv_status(a.status, IBP_ERANGE);
-      pg = 0xFFFFFFFFu;
+  const bool good = sp.there && sp.page[0] < a.n_pages;
+  if (sp.there && !good) kv_status(a.status, IBP_ERANGE);
+  const bool col = c * 32 < a.dim;
+  const uint32_t page = good ? sp.page[0] : 0xFFFFFFFFu, own = tok + lane;
+  const uint32_t slot_of_mine = shift >= 0 ? own & ((1u << shift) - 1u) : own % a.page_tokens;
+#pragma unroll
+  for (uint32_t i = 0; i < Q::kSub / kPer; ++i) {
+    const uint32_t r = r0 + i * kPer;
+    const uint32_t pg = __shfl_sync(0xFFFFFFFFu, page, r), slot = __shfl_sync(0xFFFFFFFFu, slot_of_mine, r);
+    const bool on = pg != 0xFFFFFFFFu && col;
+    const int64_t p = on ? pg : 0, sl = on ? slot : 0;
+    quad_copy<16>(dst[i % kTurns] + i * kPer * (DP / 2), base[0] + p * t.four[0].page_stride + sl * t.four[0].token_stride + (on ? c * 16 : 0), on);
+    quad_copy<16>(dst[i % kTurns] + i * kPer * (DP / 2) + Q::kCodes, base[2] + p * t.four[1].page_stride + sl * t.four[1].token_stride + (on ? c * 16 : 0), on);
+  }
+  if (lane < Q::kSub) {
+    const int64_t p = good ? page : 0, sl = good ? slot_of_mine : 0;
+#pragma unroll
+    for (uint32_t kv = 0; kv < 2; ++kv) {
+      const char* src = base[2 * kv + 1] + p * t.four[kv].s_page + sl * t.four[kv].s_token;
+#pragma unroll
+      for (uint32_t g = 0; g < DP / 32; ++g)
+        *reinterpret_cast<uint16_t*>(stage_p + 2 * Q::kCodes + (kv * Q::kSub + lane) * Q::kScale + 2 * g) =
+            good && g * 32 < a.dim ? __ldg(reinterpret_cast<const uint16_t*>(src) + g) : uint16_t(0);
     }
-  }
-#pragma unroll
-  for (uint32_t i = 0; i < 2; ++i) {
-    const uint32_t p = __shfl_sync(0xFFFFFFFFu, pg, g + 8 * i), sl = __shfl_sync(0xFFFFFFFFu, slot, g + 8 * i);
-    const bool on = p != 0xFFFFFFFFu;
-    const int64_t q = on ? p : 0;
-    load_k(i, ln.kc + q * x.k.page_stride + static_cast<int64_t>(sl) * x.k.token_stride,
-           ln.ks + q * x.k.s_page + static_cast<int64_t>(sl) * x.k.s_token, on);
-  }
-#pragma unroll
-  for (uint32_t i = 0; i < 4; ++i) {
-    const uint32_t from = 2 * t + (i & 1u) + (i >> 1) * 8;
-    const uint32_t p = __shfl_sync(0xFFFFFFFFu, pg, from), sl = __shfl_sync(0xFFFFFFFFu, slot, from);
-    const bool on = p != 0xFFFFFFFFu && ln.v_on;
-    const int64_t q = on ? p : 0;
-    ld_words<DP / 64>(s.vw[i], ln.vc + q * x.v.page_stride + static_cast<int64_t>(sl) * x.v.token_stride, on);
-    s.vs[i] = ld_scale(ln.vs + q * x.v.s_page + static_cast<int64_t>(sl) * x.v.s_token, on);
   }
 }
 
-// A warp's running softmax of its rows.
-template <uint32_t DP, uint32_t NT>
-struct QuadAcc {
-  float o[DP / 16][NT][4];  // rows: dimensions 2j and 2j + 1 of the lane's; columns: queries 2t, 2t + 1
-  float m[NT][2], l[NT][2];
-};
+template <uint32_t DP, uint32_t NT, bool F16, QuadForm FORM>
+__global__ void __launch_bounds__(kQdWarps * 32, DP == 256 || NT == 2 ? 2 : kQdCtas) k_kv4_attend(const __grid_constant__ TcArgs t, int32_t shift) {
+  using Q = Quad<DP, NT>;
+  constexpr uint32_t kM = Q::kMma, kSub = Q::kSub;
+  const AttendArgs& a = t.a;
+  extern __shared__ __align__(128) unsigned char sm[];
+  __shared__ struct {
+    uint32_t pair0, b0, sums[kQdWarps];
+    uint64_t in0;
+  } sh;
+  pdl_begin();
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, tq = lane & 3u;
 
-template <uint32_t DP, uint32_t NT, bool F16>
-__device__ __forceinline__ void quad_step(const AttendArgs& a, QuadStep<DP>& s, const uint32_t (&qf)[NT][DP / 16][2],
-                                          QuadAcc<DP, NT>& acc, uint32_t b, int32_t ctx, int32_t len, uint32_t row0,
-                                          uint32_t live_rows, int32_t first) {
-  using Q = Quad<DP, NT, F16>;
-  const uint32_t lane = threadIdx.x & 31u;
-  float c[NT][4];
+  // Where this CTA's range begins, as in k_kv_tree.
+  {
+    uint32_t n = 0;
+    for (uint32_t b = threadIdx.x; b < a.n_seqs; b += kQdWarps * 32) n += tiles_of<Q::kTile>(a, b);
 #pragma unroll
-  for (uint32_t n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+    if (lane == 0) sh.sums[warp] = n;
+    __syncthreads();
+  }
+  uint64_t total = 0;
 #pragma unroll
-  for (uint32_t w = 0; w < DP / 32; ++w) {
-    const uint32_t gi = DP == 256 ? w / 4 : 0;
-    const quad::Pair<F16> p0(quad::scale_bits<F16>(s.ks[0][gi]) * 0x10001u), p1(quad::scale_bits<F16>(s.ks[1][gi]) * 0x10001u);
-    const uint32_t x = s.kw[0][w], y = s.kw[1][w];
-    const uint32_t lo[4] = {quad::decode<F16, 0>(x, p0), quad::decode<F16, 0>(y, p1), quad::decode<F16, 1>(x, p0), quad::decode<F16, 1>(y, p1)};
-    const uint32_t hi[4] = {quad::decode<F16, 2>(x, p0), quad::decode<F16, 2>(y, p1), quad::decode<F16, 3>(x, p0), quad::decode<F16, 3>(y, p1)};
+  for (uint32_t i = 0; i < kQdWarps; ++i) total += sh.sums[i];
+  const uint64_t block = total * a.kv_heads;  // tiles of a row block
+  total = block * t.row_pairs;
+  const uint64_t share = (total + t.n_ctas - 1) / t.n_ctas;
+  const uint64_t at = blockIdx.x * share < total ? blockIdx.x * share : total;
+  const uint64_t end = total - at < share ? total : at + share;
+  if (warp == 0 && at < end) {
+    const uint32_t pair = static_cast<uint32_t>(at / block);
+    const uint64_t in = at - pair * block;
+    uint64_t seen = 0;
+    for (uint32_t c = 0; c < a.n_seqs; c += 32) {
+      const uint32_t b = c + lane;
+      uint64_t n = b < a.n_seqs ? static_cast<uint64_t>(tiles_of<Q::kTile>(a, b)) * a.kv_heads : 0, incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= static_cast<uint32_t>(o)) incl += v;
+      }
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, seen + incl > in);
+      if (hit) {
+        if (lane == static_cast<uint32_t>(__ffs(hit) - 1)) {
+          sh.pair0 = pair;
+          sh.b0 = b;
+          sh.in0 = in - (seen + incl - n);
+        }
+        break;
+      }
+      seen += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+  }
+  __syncthreads();
+  TcWalkOf<Q::kTile> walk(t, sh.pair0, sh.b0, sh.in0, at, end);
+  TcSeg s;
+  bool first_seg = true;
+  const quad::Magic<F16> magic;
+  unsigned char* const ring_p = sm + warp * Q::kStages * Q::kStage;
+  const uint32_t ring = smem_u32(ring_p);
+  if (threadIdx.x == 0 && blockIdx.x == 0)
+    t.first[t.n_ctas] = make_int4(static_cast<int>(share & 0xFFFFFFFFu), static_cast<int>(share >> 32), 0, 0);
+  if (threadIdx.x == 0 && at >= end) t.first[blockIdx.x] = make_int4(-1, 0, 0, 0);
+
+  while (walk.next(&s)) {
+    const uint32_t row0 = s.pair * Q::kRows, b = s.b, h = s.h;
+    const int32_t len = s.len, ctx = s.ctx;
+    if (threadIdx.x == 0) {
+      const int32_t raw = a.lens[b], n = a.n_live ? a.n_live[b] : static_cast<int32_t>(a.T);
+      if (raw != len || n != s.n_live || n > len) kv_status(a.status, IBP_ERANGE);
+      if (first_seg) t.first[blockIdx.x] = make_int4(b, h, s.pair, s.tile0);
+    }
+    first_seg = false;
+    const uint32_t all_rows = a.T * a.group;
+    const uint32_t rows = all_rows - row0 < Q::kRows ? all_rows - row0 : Q::kRows;
+    const uint32_t lr = static_cast<uint32_t>(s.n_live) * a.group;
+    const uint32_t live_rows = lr > row0 ? (lr - row0 < rows ? lr - row0 : rows) : 0;
+    const uint32_t n_tok = live_rows && len > 0 ? static_cast<uint32_t>(len) : 0;
+
+    const int32_t* row = a.table + static_cast<uint64_t>(b) * a.max_pages;
+    constexpr uint32_t kChunks = DP / 32;
+    const uint32_t ahead_c = FORM == kEven ? lane % kChunks * 16 : 0, ahead_r = FORM == kEven ? lane / kChunks : 0;
+    const uint32_t ahead_t = FORM == kEven ? lane % 16 : 0;
+    const char* const base[4] = {
+        t.four[0].codes + static_cast<int64_t>(h) * t.four[0].head_stride + ahead_c + static_cast<int64_t>(ahead_r) * t.four[0].token_stride,
+        t.four[0].scales + static_cast<int64_t>(h) * t.four[0].s_head + static_cast<int64_t>(ahead_t) * t.four[0].s_token,
+        t.four[1].codes + static_cast<int64_t>(h) * t.four[1].head_stride + ahead_c + static_cast<int64_t>(ahead_r) * t.four[1].token_stride,
+        t.four[1].scales + static_cast<int64_t>(h) * t.four[1].s_head + static_cast<int64_t>(ahead_t) * t.four[1].s_token};
+    // Step j of this warp: tokens of tile tile0 + j; without live rows there is none.
+    const uint32_t steps = n_tok ? s.tiles : 0;
+    auto token = [&](uint32_t j) { return (s.tile0 + j) * Q::kTile + warp * kSub; };
+    auto spot = [&](uint32_t j) { return quad_spot<FORM, kM>(a, shift, row, token(j), j < steps ? n_tok : 0); };
+    auto fill = [&](uint32_t j, const QuadSpot& sp, uint32_t stage) {
+      if (token(j) < n_tok) {
+        quad_fill<DP, NT, FORM>(t, sp, shift, token(j), n_tok, base, ring + stage * Q::kStage, ring_p + stage * Q::kStage);
+      } else {  // the item's last tile, past its last token
+        for (uint32_t i = lane * 16; i < Q::kStage; i += 512)
+          *reinterpret_cast<uint4*>(ring_p + stage * Q::kStage + i) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    constexpr uint32_t kAhead = Q::kStages - 1;
+    QuadSpot sp[kAhead];
+#pragma unroll
+    for (uint32_t i = 0; i < kAhead; ++i) sp[i] = spot(i);
+    QuadSpot next = spot(kAhead);
+
+    // Q^T as B operands, dimensions in the order in which a lane decodes K.
+    uint32_t qf[NT][DP / 16][2];
 #pragma unroll
     for (uint32_t n = 0; n < NT; ++n) {
-      mma16816<F16>(c[n], lo, qf[n][2 * w][0], qf[n][2 * w][1]);
-      mma16816<F16>(c[n], hi, qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
-    }
-  }
-  // Scores in powers of two; what a row does not see is -infinity.
-  const bool open = first + 16 <= (ctx < len ? ctx : len);
+      const bool on = n * 8 + g < live_rows;
+      const uint32_t r = on ? row0 + n * 8 + g : 0;
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q + static_cast<int64_t>(b) * a.q_seq + static_cast<int64_t>(r / a.group) * a.q_token +
+                                                            static_cast<int64_t>(h * a.group + r % a.group) * a.q_head);
 #pragma unroll
-  for (uint32_t n = 0; n < NT; ++n)
-#pragma unroll
-    for (uint32_t e = 0; e < 4; ++e) c[n][e] *= a.scale_log2;
-  if (!open) {
-#pragma unroll
-    for (uint32_t n = 0; n < NT; ++n)
-#pragma unroll
-      for (uint32_t e = 0; e < 4; ++e) {
-        const uint32_t r = n * 8 + (lane & 3u) * 2 + (e & 1u);
-        const int32_t pos = first + static_cast<int32_t>(lane / 4 + (e < 2 ? 0 : 8));
-        if (r >= live_rows || !Q::sees(a, b, ctx, len, row0 + r, pos)) c[n][e] = -INFINITY;
+      for (uint32_t w = 0; w < DP / 32; ++w) {  // eight dimensions
+        const uint32_t d = tq * (DP / 4) + 8 * w;
+        const bool in = on && d < a.dim;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (in) {
+          if (t.q16)
+            x = *reinterpret_cast<const uint4*>(q + d);
+          else
+            x = make_uint4(q[d] | static_cast<uint32_t>(q[d + 1]) << 16, q[d + 2] | static_cast<uint32_t>(q[d + 3]) << 16,
+                           q[d + 4] | static_cast<uint32_t>(q[d + 5]) << 16, q[d + 6] | static_cast<uint32_t>(q[d + 7]) << 16);
+        }
+        qf[n][2 * w][0] = __byte_perm(x.x, x.z, 0x5410), qf[n][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);
+        qf[n][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410), qf[n][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
       }
-  }
-  float cm[NT][2];
-  bool grow = false;
-#pragma unroll
-  for (uint32_t n = 0; n < NT; ++n) {
-    cm[n][0] = fmaxf(c[n][0], c[n][2]);
-    cm[n][1] = fmaxf(c[n][1], c[n][3]);
-#pragma unroll
-    for (uint32_t w = 4; w < 32; w <<= 1) {
-      cm[n][0] = fmaxf(cm[n][0], __shfl_xor_sync(0xFFFFFFFFu, cm[n][0], w));
-      cm[n][1] = fmaxf(cm[n][1], __shfl_xor_sync(0xFFFFFFFFu, cm[n][1], w));
     }
-    if (F16) cm[n][0] = __fadd_ru(cm[n][0], -kLift<F16>), cm[n][1] = __fadd_ru(cm[n][1], -kLift<F16>);
-    grow = grow || cm[n][0] > acc.m[n][0] || cm[n][1] > acc.m[n][1];
-  }
-  if (__any_sync(0xFFFFFFFFu, grow)) {
-    // Rescaled at once, so that a row's largest probability is a power of two and its
-    // rounding to the cache's type costs nothing.
+#pragma unroll
+    for (uint32_t i = 0; i < kAhead; ++i) {
+      if (i < steps) fill(i, sp[i], i);
+      cp_commit();
+    }
+
+    float o[DP / 16][NT][4];  // rows: dimensions 2j and 2j + 1 of the lane's; columns: queries 2t, 2t + 1
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (uint32_t n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (uint32_t d = 0; d < DP / 16; ++d) o[d][n][0] = o[d][n][1] = o[d][n][2] = o[d][n][3] = 0.f;
+    }
+
+    // This lane's places in a stage, for the first of the tokens eight apart.
+    const uint32_t k_at = DP == 64 ? Q::at(g, tq / 2) + (tq & 1u) * 8 : Q::at(g, tq * (DP == 256 ? 2 : 1));
+    const uint32_t k_two = DP == 256 ? Q::at(g, tq * 2 + 1) : 0;
+    const uint32_t v_at[2] = {Q::at(2 * tq, g * (DP / 16) / 16) + g * (DP / 16) % 16, Q::at(2 * tq + 1, g * (DP / 16) / 16) + g * (DP / 16) % 16};
+    uint32_t slot = 0;  // of step j
+#pragma unroll 1
+    for (uint32_t j = 0; j < steps; ++j) {
+      __syncwarp();  // every lane is done with the stage that is filled next
+      if (j + kAhead < steps) {
+        fill(j + kAhead, next, slot == 0 ? kAhead : slot - 1);
+      }
+      next = spot(j + kAhead + 1);
+      cp_commit();
+      cp_wait<kAhead>();
+      __syncwarp();
+      const unsigned char* st = ring_p + slot * Q::kStage;
+      const unsigned char *ksc = st + 2 * Q::kCodes, *vsc = ksc + kSub * Q::kScale;
+      slot = slot == kAhead ? 0 : slot + 1;
+      const int32_t first = static_cast<int32_t>(token(j));
+      float c[kM][NT][4];
+#pragma unroll
+      for (uint32_t x = 0; x < kM; ++x) {
+#pragma unroll
+        for (uint32_t n = 0; n < NT; ++n) c[x][n][0] = c[x][n][1] = c[x][n][2] = c[x][n][3] = 0.f;
+        // this lane's dimensions: DP / 4 from tq * DP / 4 on
+        constexpr uint32_t kW = DP / 32, kG = DP == 256 ? 2 : 1;
+        uint32_t w[2][kW];
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i) {
+          if constexpr (kW == 2) {
+            const uint2 u = *reinterpret_cast<const uint2*>(st + k_at + (16 * x + 8 * i) * (DP / 2));
+            w[i][0] = u.x, w[i][1] = u.y;
+          } else {
+#pragma unroll
+            for (uint32_t e = 0; e < kG; ++e) {
+              const uint4 u = *reinterpret_cast<const uint4*>(st + (e ? k_two : k_at) + (16 * x + 8 * i) * (DP / 2));
+              w[i][4 * e] = u.x, w[i][4 * e + 1] = u.y, w[i][4 * e + 2] = u.z, w[i][4 * e + 3] = u.w;
+            }
+          }
+        }
+#pragma unroll
+        for (uint32_t e = 0; e < kG; ++e) {
+          const uint32_t gi = DP == 64 ? tq / 2 : tq * kG + e;
+          const quad::Pair<F16> p0(*reinterpret_cast<const uint16_t*>(ksc + (16 * x + g) * Q::kScale + 2 * gi) * 0x10001u);
+          const quad::Pair<F16> p1(*reinterpret_cast<const uint16_t*>(ksc + (16 * x + g + 8) * Q::kScale + 2 * gi) * 0x10001u);
+#pragma unroll
+          for (uint32_t y = e * (kW / kG); y < (e + 1) * (kW / kG); ++y) {
+            const uint32_t lo[4] = {quad::decode<F16, 0>(w[0][y], p0, magic), quad::decode<F16, 0>(w[1][y], p1, magic),
+                                    quad::decode<F16, 1>(w[0][y], p0, magic), quad::decode<F16, 1>(w[1][y], p1, magic)};
+            const uint32_t hi[4] = {quad::decode<F16, 2>(w[0][y], p0, magic), quad::decode<F16, 2>(w[1][y], p1, magic),
+                                    quad::decode<F16, 3>(w[0][y], p0, magic), quad::decode<F16, 3>(w[1][y], p1, magic)};
+#pragma unroll
+            for (uint32_t n = 0; n < NT; ++n) {
+              mma16816<F16>(c[x][n], lo, qf[n][2 * y][0], qf[n][2 * y][1]);
+              mma16816<F16>(c[x][n], hi, qf[n][2 * y + 1][0], qf[n][2 * y + 1][1]);
+            }
+          }
+        }
+      }
+      // Scores in powers of two; what a row does not see is -infinity.
+      const bool open = first + static_cast<int32_t>(kSub) <= (ctx < len ? ctx : len);
+#pragma unroll
+      for (uint32_t x = 0; x < kM; ++x)
+#pragma unroll
+        for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) c[x][n][e] *= a.scale_log2;
+      if (!open) {
+#pragma unroll
+        for (uint32_t x = 0; x < kM; ++x)
+#pragma unroll
+          for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) {
+              const uint32_t r = n * 8 + tq * 2 + (e & 1u);
+              const int32_t pos = first + static_cast<int32_t>(16 * x + g + (e < 2 ? 0 : 8));
+              if (r >= live_rows || !Q::sees(a, b, ctx, len, row0 + r, pos)) c[x][n][e] = -INFINITY;
+            }
+      }
+      float cm[NT][2];
+      bool grow = false;
+#pragma unroll
+      for (uint32_t n = 0; n < NT; ++n) {
+#pragma unroll
+        for (uint32_t e = 0; e < 2; ++e) {
+          cm[n][e] = fmaxf(c[0][n][e], c[0][n][2 + e]);
+          if (kM == 2) cm[n][e] = fmaxf(cm[n][e], fmaxf(c[kM - 1][n][e], c[kM - 1][n][2 + e]));
+#pragma unroll
+          for (uint32_t w = 4; w < 32; w <<= 1) cm[n][e] = fmaxf(cm[n][e], __shfl_xor_sync(0xFFFFFFFFu, cm[n][e], w));
+          if (F16) cm[n][e] = __fadd_ru(cm[n][e], -kLift<F16>);
+          grow = grow || cm[n][e] > m[n][e];
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        // Rescaled at once, so that a row's largest probability is a power of two and its
+        // rounding to the cache's type costs nothing.
+#pragma unroll
+        for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+          for (uint32_t e = 0; e < 2; ++e) {
+            const float top = fmaxf(m[n][e], cm[n][e]);
+            const float f = top > m[n][e] ? ex2(m[n][e] - top) : 1.f;
+            m[n][e] = top;
+            l[n][e] *= f;
+#pragma unroll
+            for (uint32_t d = 0; d < DP / 16; ++d) o[d][n][e] *= f, o[d][n][2 + e] *= f;
+          }
+      }
+      uint32_t pf[kM][NT][2];
+#pragma unroll
+      for (uint32_t n = 0; n < NT; ++n) {
+        const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+        for (uint32_t x = 0; x < kM; ++x) {
+          float(&p)[4] = c[x][n];
+          p[0] = ex2(p[0] - m0), p[1] = ex2(p[1] - m1), p[2] = ex2(p[2] - m0), p[3] = ex2(p[3] - m1);
+          l[n][0] += p[0] + p[2];
+          l[n][1] += p[1] + p[3];
+          pf[x][n][0] = transpose8(pack2<F16>(p[0], p[1]));
+          pf[x][n][1] = transpose8(pack2<F16>(p[2], p[3]));
+        }
+      }
+#pragma unroll
+      for (uint32_t x = 0; x < kM; ++x) {
+        constexpr uint32_t kW = DP / 64;
+        // tokens 2t, 2t + 1, 2t + 8, 2t + 9; DP / 8 dimensions from g * DP / 8 on
+        uint32_t w[4][kW], sc[4];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t tok = 16 * x + 2 * tq + (i & 1u) + (i >> 1) * 8;
+          const unsigned char* src = st + Q::kCodes + v_at[i & 1u] + (16 * x + (i >> 1) * 8) * (DP / 2);
+          if constexpr (kW == 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(src);
+            w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
+          } else if constexpr (kW == 2) {
+            const uint2 u = *reinterpret_cast<const uint2*>(src);
+            w[i][0] = u.x, w[i][1] = u.y;
+          } else {
+            w[i][0] = *reinterpret_cast<const uint32_t*>(src);
+          }
+          sc[i] = *reinterpret_cast<const uint16_t*>(vsc + tok * Q::kScale + g * (DP / 8) / kQuadGroup * 2);
+        }
+        if (!open) {
+          // Groups of V that may hold infinities or NaN: a row that does not see them must
+          // not meet them, even with probability zero.  They leave the product and are
+          // added to the rows that see them.
+          bool bad = false;
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) bad = bad || quad::odd<F16>(quad::scale_bits<F16>(sc[i]));
+          if (__any_sync(0xFFFFFFFFu, bad)) {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+#pragma unroll 1
+              for (uint32_t tt = 0; tt < 4; ++tt) {
+                const uint32_t tok = 2 * tt + (i & 1u) + (i >> 1) * 8;  // its row in S^T
+                const uint32_t from = (lane & 28u) | tt, sb = quad::scale_bits<F16>(__shfl_sync(0xFFFFFFFFu, sc[i], from));
+                uint32_t words[kW];
+#pragma unroll
+                for (uint32_t y = 0; y < kW; ++y) words[y] = __shfl_sync(0xFFFFFFFFu, w[i][y], from);
+#pragma unroll
+                for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+                  for (uint32_t e = 0; e < 2; ++e) {
+                    const float p = __shfl_sync(0xFFFFFFFFu, c[x][n][(i >> 1) * 2 + e], ((tok & 7u) << 2) | tq);
+                    const uint32_t r = n * 8 + tq * 2 + e;
+                    if (quad::odd<F16>(sb) && r < live_rows &&
+                        Q::sees(a, b, ctx, len, row0 + r, first + static_cast<int32_t>(16 * x + tok))) {
+#pragma unroll
+                      for (uint32_t d = 0; d < DP / 16; ++d) {
+                        o[d][n][e] += p * quad::value<F16>(words[d / 4], (2 * d) & 7u, sb);
+                        o[d][n][2 + e] += p * quad::value<F16>(words[d / 4], (2 * d + 1) & 7u, sb);
+                      }
+                    }
+                  }
+              }
+              if (quad::odd<F16>(quad::scale_bits<F16>(sc[i]))) sc[i] = 0u;
+            }
+          }
+        }
+        const quad::Pair<F16> pa(__byte_perm(sc[0], sc[1], 0x5410)), pb(__byte_perm(sc[2], sc[3], 0x5410));
+#pragma unroll
+        for (uint32_t y = 0; y < kW; ++y) {
+          // elements 0 - 3 and 4 - 7 of a word for a pair of tokens
+          const uint32_t a0 = __byte_perm(w[0][y], w[1][y], 0x5410), a1 = __byte_perm(w[0][y], w[1][y], 0x7632);
+          const uint32_t b0 = __byte_perm(w[2][y], w[3][y], 0x5410), b1 = __byte_perm(w[2][y], w[3][y], 0x7632);
+          auto product = [&](uint32_t d, const uint32_t(&f)[4]) {
+#pragma unroll
+            for (uint32_t n = 0; n < NT; ++n) mma16816<F16>(o[4 * y + d][n], f, pf[x][n][0], pf[x][n][1]);
+          };
+          product(0, {quad::decode<F16, 0>(a0, pa, magic), quad::decode<F16, 1>(a0, pa, magic),
+                      quad::decode<F16, 0>(b0, pb, magic), quad::decode<F16, 1>(b0, pb, magic)});
+          product(1, {quad::decode<F16, 2>(a0, pa, magic), quad::decode<F16, 3>(a0, pa, magic),
+                      quad::decode<F16, 2>(b0, pb, magic), quad::decode<F16, 3>(b0, pb, magic)});
+          product(2, {quad::decode<F16, 0>(a1, pa, magic), quad::decode<F16, 1>(a1, pa, magic),
+                      quad::decode<F16, 0>(b1, pb, magic), quad::decode<F16, 1>(b1, pb, magic)});
+          product(3, {quad::decode<F16, 2>(a1, pa, magic), quad::decode<F16, 3>(a1, pa, magic),
+                      quad::decode<F16, 2>(b1, pb, magic), quad::decode<F16, 3>(b1, pb, magic)});
+        }
+      }
+    }
+    cp_wait<0>();
+
+    // Join the warps: sums of a lane's tokens first.
 #pragma unroll
     for (uint32_t n = 0; n < NT; ++n)
 #pragma unroll
       for (uint32_t e = 0; e < 2; ++e)
-        if (cm[n][e] > acc.m[n][e]) {
-          const float f = ex2(acc.m[n][e] - cm[n][e]);
-          acc.m[n][e] = cm[n][e];
-          acc.l[n][e] *= f;
 #pragma unroll
-          for (uint32_t d = 0; d < DP / 16; ++d) acc.o[d][n][e] *= f, acc.o[d][n][2 + e] *= f;
+        for (uint32_t w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], w);
+    float* so = reinterpret_cast<float*>(sm);    // [warp][row][DP]
+    float* sml = so + kQdWarps * Q::kRows * DP;  // [warp][row][2]
+    __syncthreads();                             // the rings are done with
+#pragma unroll
+    for (uint32_t n = 0; n < NT; ++n)
+#pragma unroll
+      for (uint32_t e = 0; e < 2; ++e) {
+        const uint32_t r = n * 8 + tq * 2 + e;
+        float* dst = so + (warp * Q::kRows + r) * DP + g * (DP / 8);
+#pragma unroll
+        for (uint32_t d = 0; d < DP / 16; ++d) *reinterpret_cast<float2*>(dst + 2 * d) = make_float2(o[d][n][e], o[d][n][2 + e]);
+        if (g == 0) {
+          sml[(warp * Q::kRows + r) * 2] = m[n][e];
+          sml[(warp * Q::kRows + r) * 2 + 1] = l[n][e];
         }
-  }
-  uint32_t pf[NT][2];
-#pragma unroll
-  for (uint32_t n = 0; n < NT; ++n) {
-    const float m0 = acc.m[n][0] == -INFINITY ? 0.f : acc.m[n][0], m1 = acc.m[n][1] == -INFINITY ? 0.f : acc.m[n][1];
-    c[n][0] = ex2(c[n][0] - m0), c[n][1] = ex2(c[n][1] - m1);
-    c[n][2] = ex2(c[n][2] - m0), c[n][3] = ex2(c[n][3] - m1);
-    acc.l[n][0] += c[n][0] + c[n][2];
-    acc.l[n][1] += c[n][1] + c[n][3];
-    pf[n][0] = transpose8(pack2<F16>(c[n][0], c[n][1]));
-    pf[n][1] = transpose8(pack2<F16>(c[n][2], c[n][3]));
-  }
-#pragma unroll
-  for (uint32_t i = 0; i < 4; ++i) s.vs[i] = quad::scale_bits<F16>(s.vs[i]);
-  if (!open) {
-    // Groups of V that may hold infinities or NaN: a row that does not see them must
-    // not meet them, even with probability zero.  They leave the product and are
-    // added to the rows that see them.
-    bool bad = false;
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) bad = bad || quad::odd<F16>(s.vs[i]);
-    if (__any_sync(0xFFFFFFFFu, bad)) {
-#pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
-#pragma unroll 1
-        for (uint32_t tt = 0; tt < 4; ++tt) {
-          const uint32_t tok = 2 * tt + (i & 1u) + (i >> 1) * 8;  // its row in S^T
-          const uint32_t sc = __shfl_sync(0xFFFFFFFFu, s.vs[i], (lane & 28u) | tt);
-          uint32_t words[DP / 64];
-#pragma unroll
-          for (uint32_t w = 0; w < DP / 64; ++w) words[w] = __shfl_sync(0xFFFFFFFFu, s.vw[i][w], (lane & 28u) | tt);
-#pragma unroll
-          for (uint32_t n = 0; n < NT; ++n)
-#pragma unroll
-            for (uint32_t e = 0; e < 2; ++e) {
-              const float p = __shfl_sync(0xFFFFFFFFu, c[n][(i >> 1) * 2 + e], ((tok & 7u) << 2) | (lane & 3u));
-              const uint32_t r = n * 8 + (lane & 3u) * 2 + e;
-              if (quad::odd<F16>(sc) && r < live_rows &&
-                  Q::sees(a, b, ctx, len, row0 + r, first + static_cast<int32_t>(tok))) {
-#pragma unroll
-                for (uint32_t d = 0; d < DP / 16; ++d) {
-                  acc.o[d][n][e] += p * quad::value<F16>(words[d / 4], (2 * d) & 7u, sc);
-                  acc.o[d][n][2 + e] += p * quad::value<F16>(words[d / 4], (2 * d + 1) & 7u, sc);
-                }
-              }
-            }
-        }
-        if (quad::odd<F16>(s.vs[i])) s.vs[i] = 0u;
       }
-    }
-  }
-  const quad::Pair<F16> pa(s.vs[0] | s.vs[1] << 16), pb(s.vs[2] | s.vs[3] << 16);
-#pragma unroll
-  for (uint32_t w = 0; w < DP / 64; ++w) {
-    // elements 0 - 3 and 4 - 7 of a word for a pair of tokens
-    const uint32_t a0 = __byte_perm(s.vw[0][w], s.vw[1][w], 0x5410), a1 = __byte_perm(s.vw[0][w], s.vw[1][w], 0x7632);
-    const uint32_t b0 = __byte_perm(s.vw[2][w], s.vw[3][w], 0x5410), b1 = __byte_perm(s.vw[2][w], s.vw[3][w], 0x7632);
-    const uint32_t f[4][4] = {
-        {quad::decode<F16, 0>(a0, pa), quad::decode<F16, 1>(a0, pa), quad::decode<F16, 0>(b0, pb), quad::decode<F16, 1>(b0, pb)},
-        {quad::decode<F16, 2>(a0, pa), quad::decode<F16, 3>(a0, pa), quad::decode<F16, 2>(b0, pb), quad::decode<F16, 3>(b0, pb)},
-        {quad::decode<F16, 0>(a1, pa), quad::decode<F16, 1>(a1, pa), quad::decode<F16, 0>(b1, pb), quad::decode<F16, 1>(b1, pb)},
-        {quad::decode<F16, 2>(a1, pa), quad::decode<F16, 3>(a1, pa), quad::decode<F16, 2>(b1, pb), quad::decode<F16, 3>(b1, pb)}};
-#pragma unroll
-    for (uint32_t j = 0; j < 4; ++j)
-#pragma unroll
-      for (uint32_t n = 0; n < NT; ++n) mma16816<F16>(acc.o[4 * w + j][n], f[j], pf[n][0], pf[n][1]);
-  }
-}
-
-template <uint32_t DP, uint32_t NT, bool F16>
-__global__ void __launch_bounds__(kQdWarps * 32, DP == 256 || NT == 2 ? 2 : 4)
-    k_kv4_attend(const Attend4Args x, uint32_t row_tiles, int32_t shift, uint32_t chunk) {
-  using Q = Quad<DP, NT, F16>;
-  const AttendArgs& a = x.a;
-  extern __shared__ __align__(16) unsigned char sm[];
-  pdl_begin();
-  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
-  const uint32_t split = blockIdx.x % a.splits, item = blockIdx.x / a.splits;
-  const uint32_t tile = item % row_tiles, h = item / row_tiles % a.kv_heads, b = item / row_tiles / a.kv_heads;
-  const uint32_t row0 = tile * Q::kRows;
-  const int32_t raw = a.lens[b], len = clamp_len(raw, a.page_tokens, a.max_pages);
-  const int32_t live = a.n_live ? a.n_live[b] : static_cast<int32_t>(a.T);
-  if ((raw != len || live > len || live < 0 || live > static_cast<int32_t>(a.T)) && threadIdx.x == 0)
-    kv_status(a.status, IBP_ERANGE);
-  const int32_t n_live = live < 0 ? 0 : (live > static_cast<int32_t>(a.T) ? static_cast<int32_t>(a.T) : live);
-  const int32_t ctx = len - n_live;  // below 0: the draft's first tokens do not exist
-  const uint32_t all_rows = a.T * a.group;
-  const uint32_t rows = all_rows - row0 < Q::kRows ? all_rows - row0 : Q::kRows;
-  const uint32_t lr = static_cast<uint32_t>(n_live) * a.group;
-  const uint32_t live_rows = lr > row0 ? (lr - row0 < rows ? lr - row0 : rows) : 0;
-  const uint32_t n_tok = live_rows ? static_cast<uint32_t>(len) : 0;
-  const uint32_t steps = ceil_div(n_tok, 16);
-  // This CTA's share: an even one in a cluster, a chunk otherwise.
-  const uint32_t per = a.cluster ? ceil_div(steps, a.splits) : chunk;
-  const uint32_t s0 = split * per < steps ? split * per : steps, s1 = steps - s0 < per ? steps : s0 + per;
-  if (!a.cluster && split && s0 == s1) return;  // the join does not look at it
-
-  // Q^T as B operands, dimensions in the order in which a lane decodes K.
-  uint32_t qf[NT][DP / 16][2];
-#pragma unroll
-  for (uint32_t n = 0; n < NT; ++n) {
-    const bool on = n * 8 + g < live_rows;
-    const uint32_t r = on ? row0 + n * 8 + g : 0;
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q + static_cast<int64_t>(b) * a.q_seq + static_cast<int64_t>(r / a.group) * a.q_token +
-                                                          static_cast<int64_t>(h * a.group + r % a.group) * a.q_head);
-#pragma unroll
-    for (uint32_t kk = 0; kk < DP / 16; ++kk)
-#pragma unroll
-      for (uint32_t i = 0; i < 2; ++i) {
-        const uint32_t d = t * (DP / 4) + kk / 2 * 8 + (kk & 1u) * 2 + i;  // and d + 4
-        qf[n][kk][i] = on && d < a.dim ? q[d] | static_cast<uint32_t>(q[d + 4]) << 16 : 0u;
-      }
-  }
-
-  QuadAcc<DP, NT> acc;
-#pragma unroll
-  for (uint32_t n = 0; n < NT; ++n) {
-    acc.m[n][0] = acc.m[n][1] = -INFINITY;
-    acc.l[n][0] = acc.l[n][1] = 0.f;
-#pragma unroll
-    for (uint32_t d = 0; d < DP / 16; ++d) acc.o[d][n][0] = acc.o[d][n][1] = acc.o[d][n][2] = acc.o[d][n][3] = 0.f;
-  }
-
-  QuadLane ln;
-  ln.kc = x.k.codes + static_cast<int64_t>(h) * x.k.head_stride + t * (DP / 8);
-  ln.ks = x.k.scales + static_cast<int64_t>(h) * x.k.s_head + t * (DP / 4) / kQuadGroup * 2;
-  ln.vc = x.v.codes + static_cast<int64_t>(h) * x.v.head_stride + g * (DP / 16);
-  ln.vs = x.v.scales + static_cast<int64_t>(h) * x.v.s_head + g * (DP / 8) / kQuadGroup * 2;
-  ln.row = a.table + static_cast<uint64_t>(b) * a.max_pages;
-  ln.shift = shift;
-  ln.k_on[0] = t * (DP / 4) < a.dim;
-  ln.k_on[1] = DP == 256 && t * (DP / 4) + 32 < a.dim;
-  ln.v_on = g * (DP / 8) < a.dim;
-
-  // One step ahead of the one that is computed.
-  QuadStep<DP> st[2];
-  uint32_t s = s0 + warp;
-  uint32_t page = quad_page(a, ln, s, s1);
-  if (s < s1) quad_load<DP>(x, ln, s, n_tok, page, st[0]);
-  page = quad_page(a, ln, s + kQdWarps, s1);
-  while (s < s1) {
-#pragma unroll
-    for (uint32_t u = 0; u < 2; ++u) {
-      if (s >= s1) break;
-      if (s + kQdWarps < s1) quad_load<DP>(x, ln, s + kQdWarps, n_tok, page, st[u ^ 1]);
-      page = quad_page(a, ln, s + 2 * kQdWarps, s1);
-      quad_step<DP, NT, F16>(a, st[u], qf, acc, b, ctx, len, row0, live_rows, static_cast<int32_t>(s * 16));
-      s += kQdWarps;
-    }
-  }
-
-  // Join the warps: sums of a lane's tokens first.
-#pragma unroll
-  for (uint32_t n = 0; n < NT; ++n)
-#pragma unroll
-    for (uint32_t e = 0; e < 2; ++e)
-#pragma unroll
-      for (uint32_t w = 4; w < 32; w <<= 1) acc.l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, acc.l[n][e], w);
-  float* so = reinterpret_cast<float*>(sm);           // [warp][row][DP]
-  float* sml = so + kQdWarps * Q::kRows * DP;         // [warp][row][2]
-  float* sp = sml + kQdWarps * Q::kRows * 2;          // [row][2 + DP]
-#pragma unroll
-  for (uint32_t n = 0; n < NT; ++n)
-#pragma unroll
-    for (uint32_t e = 0; e < 2; ++e) {
-      const uint32_t r = n * 8 + t * 2 + e;
-      float* dst = so + (warp * Q::kRows + r) * DP + g * (DP / 8);
-#pragma unroll
-      for (uint32_t d = 0; d < DP / 16; ++d) *reinterpret_cast<float2*>(dst + 2 * d) = make_float2(acc.o[d][n][e], acc.o[d][n][2 + e]);
-      if (g == 0) {
-        sml[(warp * Q::kRows + r) * 2] = acc.m[n][e];
-        sml[(warp * Q::kRows + r) * 2 + 1] = acc.l[n][e];
-      }
-    }
-  __syncthreads();
-  for (uint32_t r = warp; r < rows; r += kQdWarps) {
-    float mw[kQdWarps], top = -INFINITY, sum = 0.f;
-    const bool live_row = r < live_rows;
-#pragma unroll
-    for (uint32_t w = 0; w < kQdWarps; ++w) {
-      mw[w] = live_row ? sml[(w * Q::kRows + r) * 2] : -INFINITY;
-      top = fmaxf(top, mw[w]);
-    }
-#pragma unroll
-    for (uint32_t w = 0; w < kQdWarps; ++w) {
-      const float ls = live_row ? sml[(w * Q::kRows + r) * 2 + 1] : 0.f;
-      // a NaN sum stays one: only an empty warp is left out
-      mw[w] = mw[w] == -INFINITY ? (ls == 0.f ? 0.f : 1.f) : exp2f(mw[w] - top);
-      sum += mw[w] * ls;
-    }
-    const uint32_t gr = row0 + r;
-    const uint64_t orow = (static_cast<uint64_t>(b) * a.T + gr / a.group) * a.kv_heads * a.group + h * a.group + gr % a.group;
-    const bool whole = a.splits == 1;
-    const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-    float* part = a.cluster ? sp + r * (DP + 2)
-                            : a.part + (static_cast<uint64_t>(item) * a.splits + split) * Q::kRows * (DP + 2) + r * (DP + 2);
-    for (uint32_t d = lane * 2; d < a.dim; d += 64) {
-      float v0 = 0.f, v1 = 0.f;
+    __syncthreads();
+    const bool whole = s.tiles == s.all;
+    const uint64_t part = (2ull * blockIdx.x + (s.tile0 == 0 ? 1 : 0)) * Q::kRows;  // as k_kv_tree_join reads them
+    for (uint32_t r = warp; r < rows; r += kQdWarps) {
+      float mw[kQdWarps], top = -INFINITY, sum = 0.f;
+      const bool live_row = r < live_rows;
 #pragma unroll
       for (uint32_t w = 0; w < kQdWarps; ++w) {
-        const float2 y = *reinterpret_cast<const float2*>(so + (w * Q::kRows + r) * DP + d);
-        if (live_row) v0 += mw[w] * y.x, v1 += mw[w] * y.y;
+        mw[w] = live_row ? sml[(w * Q::kRows + r) * 2] : -INFINITY;
+        top = fmaxf(top, mw[w]);
       }
-      if (whole)
-        *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) = pack2<F16>(v0 * inv, v1 * inv);
-      else
-        *reinterpret_cast<float2*>(part + 2 + d) = make_float2(v0, v1);
-    }
-    if (lane == 0) {
-      if (whole) {
-        if (a.lse) a.lse[orow] = row_lse<F16>(top, sum);
-      } else {
-        part[0] = top;
-        part[1] = sum;
+#pragma unroll
+      for (uint32_t w = 0; w < kQdWarps; ++w) {
+        const float ls = live_row ? sml[(w * Q::kRows + r) * 2 + 1] : 0.f;
+        // a NaN sum stays one: only an empty warp is left out
+        mw[w] = mw[w] == -INFINITY ? (ls == 0.f ? 0.f : 1.f) : exp2f(mw[w] - top);
+        sum += mw[w] * ls;
       }
-    }
-  }
-  if (!a.cluster) return;
-  // The splits of an item are a cluster: each CTA joins every a.splits-th row out
-  // of the others' shared memory.
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  for (uint32_t r = split + a.splits * warp; r < rows; r += a.splits * kQdWarps) {
-    auto remote = [&](uint32_t rank, uint32_t at) {
-      uint32_t addr = smem_u32(sp + r * (DP + 2) + at);
-      asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(rank));
-      return addr;
-    };
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < a.splits)
-      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml.x), "=f"(ml.y) : "r"(remote(lane, 0)) : "memory");
-    float top = ml.x;
+      const uint32_t gr = row0 + r;
+      const uint64_t orow = (static_cast<uint64_t>(b) * a.T + gr / a.group) * a.kv_heads * a.group + h * a.group + gr % a.group;
+      const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+      for (uint32_t d = lane * 2; d < DP; d += 64) {
+        float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-    for (int w = 4; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
-    top = __shfl_sync(0xFFFFFFFFu, top, 0);
-    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - top);
-    float sum = 0.f;
-    float2 o[DP / 64];
-#pragma unroll
-    for (uint32_t i = 0; i < DP / 64; ++i) o[i] = make_float2(0.f, 0.f);
-    for (uint32_t c = 0; c < a.splits; ++c) {
-      const float fc = __shfl_sync(0xFFFFFFFFu, f, c);
-      sum += fc * __shfl_sync(0xFFFFFFFFu, ml.y, c);
-#pragma unroll
-      for (uint32_t i = 0; i < DP / 64; ++i) {
-        if (lane * 2 + i * 64 >= a.dim) continue;
-        float2 y;
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(y.x), "=f"(y.y) : "r"(remote(c, 2 + lane * 2 + i * 64)) : "memory");
-        o[i].x += fc * y.x, o[i].y += fc * y.y;
+        for (uint32_t w = 0; w < kQdWarps; ++w) {
+          const float2 y = *reinterpret_cast<const float2*>(so + (w * Q::kRows + r) * DP + d);
+          if (live_row) v0 += mw[w] * y.x, v1 += mw[w] * y.y;
+        }
+        if (!whole)
+          *reinterpret_cast<float2*>(t.o_part + (part + r) * DP + d) = make_float2(v0, v1);
+        else if (d < a.dim)
+          *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) = pack2<F16>(v0 * inv, v1 * inv);
+      }
+      if (lane == 0) {
+        if (!whole)
+          t.ml_part[part + r] = make_float2(top, sum);
+        else if (a.lse)
+          a.lse[orow] = row_lse<F16>(top, sum);
       }
     }
-    const uint32_t gr = row0 + r;
-    const uint64_t orow = (static_cast<uint64_t>(b) * a.T + gr / a.group) * a.kv_heads * a.group + h * a.group + gr % a.group;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (uint32_t i = 0; i < DP / 64; ++i) {
-      const uint32_t d = lane * 2 + i * 64;
-      if (d < a.dim)
-        *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) = pack2<F16>(o[i].x * inv, o[i].y * inv);
-    }
-    if (lane == 0 && a.lse) a.lse[orow] = row_lse<F16>(top, sum);
+    __syncthreads();  // the next segment's copies may overwrite the sums
   }
-  // no CTA leaves while another reads its shared memory
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Joins the chunks of items: a warp per row, in the chunks' order.
-template <uint32_t DP, bool F16>
-__global__ void __launch_bounds__(128) k_kv4_join(const AttendArgs a, uint32_t row_tiles, uint32_t tile_rows, uint32_t n_rows,
-                                                  uint32_t chunk) {
-  pdl_begin();
-  const uint32_t lane = threadIdx.x & 31u;
-  const uint64_t w = static_cast<uint64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const uint64_t item = w / tile_rows;
-  const uint32_t r = static_cast<uint32_t>(w % tile_rows), tile = static_cast<uint32_t>(item % row_tiles);
-  const uint32_t h = static_cast<uint32_t>(item / row_tiles % a.kv_heads);
-  const uint64_t b = item / row_tiles / a.kv_heads;
-  const uint32_t gr = tile * tile_rows + r;
-  if (b >= a.n_seqs || gr >= n_rows) return;
-  // the chunks that the item's CTAs have walked
-  const int32_t len = clamp_len(a.lens[b], a.page_tokens, a.max_pages);
-  const int32_t live = a.n_live ? a.n_live[b] : static_cast<int32_t>(a.T);
-  const int32_t n_live = live < 0 ? 0 : (live > static_cast<int32_t>(a.T) ? static_cast<int32_t>(a.T) : live);
-  const bool any = static_cast<uint32_t>(n_live) * a.group > tile * tile_rows;
-  uint32_t parts = any ? ceil_div(ceil_div(static_cast<uint32_t>(len), 16), chunk) : 1u;
-  if (parts == 0) parts = 1;
-  const float* part = a.part + (item * a.splits * tile_rows + r) * (DP + 2);
-  const uint64_t stride = static_cast<uint64_t>(tile_rows) * (DP + 2);
-  float top = -INFINITY;
-  for (uint32_t s = lane; s < parts; s += 32) top = fmaxf(top, part[s * stride]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  float sum = 0.f;
-  float2 acc[DP / 64];
-#pragma unroll
-  for (uint32_t i = 0; i < DP / 64; ++i) acc[i] = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (uint32_t s = 0; s < parts; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(part + s * stride);
-    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - top);
-    sum += f * ml.y;
-#pragma unroll
-    for (uint32_t i = 0; i < DP / 64; ++i) {
-      const uint32_t d = lane * 2 + i * 64;
-      if (d < a.dim) {
-        const float2 y = *reinterpret_cast<const float2*>(part + s * stride + 2 + d);
-        acc[i].x += f * y.x, acc[i].y += f * y.y;
-      }
-    }
-  }
-  const uint64_t orow = (b * a.T + gr / a.group) * a.kv_heads * a.group + h * a.group + gr % a.group;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (uint32_t i = 0; i < DP / 64; ++i) {
-    const uint32_t d = lane * 2 + i * 64;
-    if (d < a.dim)
-      *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) = pack2<F16>(acc[i].x * inv, acc[i].y * inv);
-  }
-  if (lane == 0 && a.lse) a.lse[orow] = row_lse<F16>(top, sum);
 }
 
 // ---------------------------------------------------------------------------
 
 struct QuadPlan {
-  uint32_t dp, rows_per, tiles, splits, cluster, chunk;  // chunk: steps of a CTA where splits are not a cluster
-  uint64_t items;
+  uint32_t dp, rows_per, tiles, tile, n_ctas;  // tiles: of rows
 };
 
 static QuadPlan quad_plan(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint64_t tokens, int device) {
@@ -555,65 +625,79 @@ static QuadPlan quad_plan(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uin
   p.dp = dim <= 64 ? 64 : (dim <= 128 ? 128 : 256);
   p.rows_per = rows > 8 && p.dp < 256 ? 16 : 8;
   p.tiles = static_cast<uint32_t>((rows + p.rows_per - 1) / p.rows_per);
-  p.items = static_cast<uint64_t>(n_seqs) * kv_heads * p.tiles;
-  const uint64_t resident = static_cast<uint64_t>(sm_count(device)) * (p.dp == 256 || p.rows_per == 16 ? 2 : 4);
-  const uint64_t steps = (tokens + 15) / 16;
-  uint64_t s = 1;
-  while (s < 8 && 2 * s * p.items <= resident && steps >= 2 * s * 2 * kQdWarps) s *= 2;
-  p.splits = static_cast<uint32_t>(s);
-  p.cluster = s > 1;
-  // Chunks of 64 steps, where they are more than a cluster's worth: units enough that
-  // ragged lengths even out over the SMs.
-  const uint64_t chunk = 64, parts = (steps + chunk - 1) / chunk;
-  if (parts > p.splits && parts * p.items > resident) {
-    p.splits = static_cast<uint32_t>(parts);
-    p.cluster = 0;
-    p.chunk = static_cast<uint32_t>(chunk);
-  } else {
-    p.chunk = static_cast<uint32_t>(steps);
-  }
+  p.tile = (p.dp == 256 ? 16 : 32) * kQdWarps;
+  const uint64_t resident = static_cast<uint64_t>(sm_count(device)) * (p.dp == 256 || p.rows_per == 16 ? 2 : kQdCtas);
+  const uint64_t longest = tokens ? (tokens + p.tile - 1) / p.tile : 1;
+  const uint64_t work = longest * n_seqs * kv_heads * p.tiles;
+  p.n_ctas = static_cast<uint32_t>(work < resident ? work : resident);
   return p;
 }
 
+static size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
 size_t kv4_attend_workspace(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint64_t tokens, int device) {
   const QuadPlan p = quad_plan(n_seqs, kv_heads, rows, dim, tokens, device);
-  return p.cluster || p.splits == 1 ? 0 : p.items * p.splits * p.rows_per * (p.dp + 2) * 4;
+  return align256((p.n_ctas + 1) * sizeof(int4)) + align256(2ull * p.n_ctas * p.rows_per * sizeof(float2)) +
+         2ull * p.n_ctas * p.rows_per * p.dp * 4;
 }
 
 template <uint32_t DP, uint32_t NT, bool F16>
-static int launch_quad(Attend4Args& x, const QuadPlan& p, cudaStream_t stream) {
-  using Q = Quad<DP, NT, F16>;
-  static_assert(Q::kBytes <= 48 * 1024, "no attribute is set for the shared memory");
-  int32_t shift = -2;
-  if (x.a.page_tokens % 16 == 0) {
-    const uint32_t steps = x.a.page_tokens / 16;
-    shift = steps & (steps - 1) ? -1 : 0;
-    while (shift >= 0 && (1u << shift) < steps) ++shift;
+static int launch_quad(const TcArgs& t, int device, cudaStream_t stream) {
+  using Q = Quad<DP, NT>;
+  int32_t shift = -1;
+  if ((t.a.page_tokens & (t.a.page_tokens - 1)) == 0)
+    for (shift = 0; (1u << shift) < t.a.page_tokens;) ++shift;
+  uint64_t all = 0;
+  for (int i = 0; i < 2; ++i)
+    all |= reinterpret_cast<uintptr_t>(t.four[i].scales) | static_cast<uint64_t>(t.four[i].s_page) |
+           static_cast<uint64_t>(t.four[i].s_head) | static_cast<uint64_t>(t.four[i].s_token);
+  bool even = t.a.dim == DP && all % Q::kScale == 0 && t.a.page_tokens % 16 == 0;
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t most = 0xFFFFFFFFull / t.a.page_tokens;
+    even = even && static_cast<uint64_t>(t.four[i].page_stride) <= 0xFFFFFFFFull && static_cast<uint64_t>(t.four[i].s_page) <= 0xFFFFFFFFull &&
+           static_cast<uint64_t>(t.four[i].token_stride) <= most && static_cast<uint64_t>(t.four[i].s_token) <= most;
   }
-  const int rc = kv_launch("k_kv4_attend", k_kv4_attend<DP, NT, F16>, dim3(static_cast<unsigned>(p.items * p.splits)), kQdWarps * 32,
-                           Q::kBytes, p.cluster ? p.splits : 1, stream, x, p.tiles, shift, p.chunk);
-  if (rc != IBP_OK || p.cluster || p.splits == 1) return rc;
-  const uint64_t warps = p.items * Q::kRows;
-  return kv_launch("k_kv4_join", k_kv4_join<DP, F16>, dim3(static_cast<unsigned>((warps + 3) / 4)), 128, 0, 1, stream, x.a, p.tiles,
-                   Q::kRows, x.a.T * x.a.group, p.chunk);
+  auto kern = even ? k_kv4_attend<DP, NT, F16, kEven> : k_kv4_attend<DP, NT, F16, kAny>;
+  static std::atomic<int> ready[2][64];
+  if (device < 0 || device >= 64 || !ready[even][device].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::kBytes);
+    if (e != cudaSuccess) {
+      set_cuda_error(e, "set-up of k_kv4_attend");
+      cudaGetLastError();
+      return IBP_ECUDA;
+    }
+    if (device >= 0 && device < 64) ready[even][device].store(1, std::memory_order_release);
+  }
+  const int rc = kv_launch("k_kv4_attend", kern, dim3(t.n_ctas), kQdWarps * 32, Q::kBytes, 1, stream, t, shift);
+  if (rc != IBP_OK || t.n_ctas == 1) return rc;
+  return kv_launch("k_kv_tree_join", k_kv_tree_join<DP, Q::kRows, F16, Q::kTile>,
+                   dim3(t.n_ctas - 1, (Q::kRows + kJoinRows - 1) / kJoinRows), kJoinThreads, 0, 1, stream, t);
 }
 
-int launch_kv4_attend(Attend4Args& x, int device, size_t ws_bytes, cudaStream_t stream) {
-  AttendArgs& a = x.a;
+int launch_kv4_attend(const Attend4Args& x, int device, size_t ws_bytes, cudaStream_t stream) {
+  const AttendArgs& a = x.a;
   const uint64_t tokens = static_cast<uint64_t>(a.max_pages) * a.page_tokens;
   const QuadPlan p = quad_plan(a.n_seqs, a.kv_heads, static_cast<uint64_t>(a.T) * a.group, a.dim, tokens, device);
-  if (p.items * p.splits > 0x7FFFFFFFull) {
-    set_detail("more than 2^31 blocks");
+  if (!a.part || ws_bytes < kv4_attend_workspace(a.n_seqs, a.kv_heads, static_cast<uint64_t>(a.T) * a.group, a.dim, tokens, device))
     return IBP_EINVAL;
-  }
-  if (!p.cluster && p.splits > 1 && (!a.part || ws_bytes < p.items * p.splits * p.rows_per * (p.dp + 2) * 4)) return IBP_EINVAL;
-  a.splits = p.splits;
-  a.cluster = p.cluster;
+  TcArgs t = {};
+  t.a = a;
+  t.four[0] = x.k, t.four[1] = x.v;
+  t.row_pairs = p.tiles;
+  t.n_ctas = p.n_ctas;
+  t.q16 = ((reinterpret_cast<uintptr_t>(a.q) | static_cast<uint64_t>(a.q_seq) | static_cast<uint64_t>(a.q_token) |
+            static_cast<uint64_t>(a.q_head)) & 15u) == 0;
+  char* w = reinterpret_cast<char*>(a.part);
+  t.first = reinterpret_cast<int4*>(w);
+  w += align256((p.n_ctas + 1) * sizeof(int4));
+  t.ml_part = reinterpret_cast<float2*>(w);
+  w += align256(2ull * p.n_ctas * p.rows_per * sizeof(float2));
+  t.o_part = reinterpret_cast<float*>(w);
   auto go = [&](auto f16) {
     constexpr bool F = decltype(f16)::value;
-    if (p.dp == 64) return p.rows_per == 16 ? launch_quad<64, 2, F>(x, p, stream) : launch_quad<64, 1, F>(x, p, stream);
-    if (p.dp == 128) return p.rows_per == 16 ? launch_quad<128, 2, F>(x, p, stream) : launch_quad<128, 1, F>(x, p, stream);
-    return launch_quad<256, 1, F>(x, p, stream);
+    if (p.dp == 64) return p.rows_per == 16 ? launch_quad<64, 2, F>(t, device, stream) : launch_quad<64, 1, F>(t, device, stream);
+    if (p.dp == 128) return p.rows_per == 16 ? launch_quad<128, 2, F>(t, device, stream) : launch_quad<128, 1, F>(t, device, stream);
+    return launch_quad<256, 1, F>(t, device, stream);
   };
   return a.f16 ? go(std::true_type{}) : go(std::false_type{});
 }

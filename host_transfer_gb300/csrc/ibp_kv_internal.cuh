@@ -152,6 +152,7 @@ size_t kv_tree_workspace(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint
                          uint64_t tokens, int device);
 
 uint64_t kv_tree_wait_limit(uint64_t cycles);  // sets it, returns the one before
+long long kv_tree_limit();
 
 struct SelectArgs {
   const char* q;

@@ -89,9 +89,18 @@ int queries_of(AttendArgs* a, uint32_t heads, uint32_t page_tokens, uint64_t n_p
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Calls with work enough for the tensor-core kernel decode the cache once, to 16 bits.
-bool expands(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint64_t tokens, int device) {
-  return rows > 128 && kv_tree_workspace(n_seqs, kv_heads, rows, dim, kExpand, (tokens + kExpand - 1) / kExpand * kExpand, device) > 0;
+// Which kernel takes a call.  Rows: drafted tokens times query heads of a kv head.
+// Measured (us; few rows / tensor cores on codes / decoded once, then tensor cores),
+// 8 ragged caches of up to 16384 tokens, 8 kv heads of 128: 16 rows 58 / 100 / -, 32 rows
+// 89 / 100 / -, 64 rows 160 / 98 / -, 256 rows 580 / 175 / 217, 512 rows 1120 / 330 /
+// 297, 1024 rows 2230 / 650 / 455; one cache of 65536 tokens: 4 rows 48 / 72, 64 rows 115 /
+// 70; one of 777: 64 rows 17 / 26.
+enum Path { kFew, kCodes, kDecoded };
+constexpr uint64_t kFewRows = 32, kCodesRows = 256;
+
+Path path_of(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint64_t tokens, int device) {
+  if (rows <= kFewRows || !kv4_tree_takes(n_seqs, kv_heads, rows, dim, tokens, device)) return kFew;
+  return rows <= kCodesRows ? kCodes : kDecoded;
 }
 
 }  // namespace
@@ -152,10 +161,15 @@ size_t ibp_kv4_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t
   const uint64_t rows = static_cast<uint64_t>(T) * (q_heads / kv_heads), tokens = static_cast<uint64_t>(max_pages) * page_tokens;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) cudaGetLastError();
-  const size_t few = kv4_attend_workspace(n_seqs, kv_heads, rows, dim, tokens, device);
-  if (!expands(n_seqs, kv_heads, rows, dim, tokens, device)) return few;
-  const uint64_t padded = (tokens + kExpand - 1) / kExpand * kExpand;
-  const size_t many = kv4_expand_workspace(n_seqs, tokens, kv_heads, dim) + kv_tree_workspace(n_seqs, kv_heads, rows, dim, kExpand, padded, device);
+  const size_t few = kv4_attend_workspace(n_seqs, kv_heads, rows, dim, tokens, device);  // for scales below 0, too
+  size_t many = 0;
+  switch (path_of(n_seqs, kv_heads, rows, dim, tokens, device)) {
+    case kFew: break;
+    case kCodes: many = kv4_tree_workspace(dim, device); break;
+    case kDecoded:
+      many = kv4_expand_workspace(n_seqs, tokens, kv_heads, dim) +
+             kv_tree_workspace(n_seqs, kv_heads, rows, dim, kExpand, (tokens + kExpand - 1) / kExpand * kExpand, device);
+  }
   return few > many ? few : many;
 }
 
@@ -186,8 +200,9 @@ int ibp_kv4_attention(const ibp_kv4_pages* k, const ibp_kv4_pages* v, uint32_t d
   if (need && (ws_bytes < need || !ws)) return refuse("ws is smaller than ibp_kv4_attention_workspace");
   const uint64_t rows = static_cast<uint64_t>(T) * a.group, tokens = static_cast<uint64_t>(a.max_pages) * a.page_tokens;
   // The tensor-core kernel takes positive scales only.
-  if (!(a.scale_log2 > 0.f) || !expands(a.n_seqs, a.kv_heads, rows, a.dim, tokens, device))
-    return launch_kv4_attend(x, device, ws_bytes, static_cast<cudaStream_t>(stream));
+  const Path path = a.scale_log2 > 0.f ? path_of(a.n_seqs, a.kv_heads, rows, a.dim, tokens, device) : kFew;
+  if (path == kFew) return launch_kv4_attend(x, device, ws_bytes, static_cast<cudaStream_t>(stream));
+  if (path == kCodes) return launch_kv4_tree(x, device, ws_bytes, static_cast<cudaStream_t>(stream));
   const uint64_t tiles = (tokens + kExpand - 1) / kExpand;
   const size_t pool = align256(a.n_seqs * tiles * kExpand * a.kv_heads * a.dim * 2);
   char* w = reinterpret_cast<char*>(a.part);

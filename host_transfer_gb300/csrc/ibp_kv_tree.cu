@@ -1,85 +1,7 @@
-// ibp_kv_tree.cu - launch of the tensor-core tree attention, and the join of
-// items that several CTAs share.
+// ibp_kv_tree.cu - launch of the tensor-core tree attention.
 #include "ibp_kv_tree.cuh"
 
 namespace ibp {
-
-constexpr int kJoinThreads = 256;
-constexpr uint32_t kJoinRows = kJoinThreads / 32;  // rows of a CTA, a warp each
-
-// CTA (j, rows): joins the item that crosses the start of range j, if j is the
-// first range boundary inside it.  The range before holds its first part (slot
-// 1), the ranges from j on the others (slot 0), added in that order.
-template <uint32_t DP, uint32_t MT, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) k_kv_tree_join(const __grid_constant__ TcArgs t) {
-  pdl_begin();
-  const AttendArgs& a = t.a;
-  const uint32_t j = blockIdx.x + 1, lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-  const int4 f = t.first[j], sh = t.first[t.n_ctas];
-  const uint64_t share = static_cast<uint32_t>(sh.x) | (static_cast<uint64_t>(static_cast<uint32_t>(sh.y)) << 32);
-  const uint64_t before = static_cast<uint32_t>(f.w);
-  if (f.x < 0 || before == 0 || before > share) return;
-  const uint32_t b = f.x, h = f.y;
-  const uint64_t start = j * share - before, end = start + tiles_of(a, b);
-  const uint32_t last = static_cast<uint32_t>((end - 1) / share);
-  constexpr uint32_t kRows = MT * kTcTile;
-  const uint32_t r = blockIdx.y * kJoinRows + warp, gr = f.z * kRows + r;
-  const uint32_t tok = gr / a.group, head = gr - tok * a.group;
-  if (tok >= a.T) return;
-  auto row_of = [&](uint32_t c) { return (2ull * c + (c < j ? 1 : 0)) * kRows + r; };
-  // Weights of up to 32 parts at a time, a part a lane; their rows follow with
-  // four loads in flight.  The running maximum makes room for any number.  A part of
-  // weight 0 is added like the others: what is not finite in it the row has seen, and
-  // the result must not depend on where the ranges of the CTAs end.
-  float top = -INFINITY, sum = 0.f;
-  float2 acc[DP / 64];
-#pragma unroll
-  for (uint32_t e = 0; e < DP / 64; ++e) acc[e] = make_float2(0.f, 0.f);
-  for (uint32_t c0 = j - 1; c0 <= last; c0 += 32) {
-    const uint32_t n = last - c0 + 1 < 32 ? last - c0 + 1 : 32;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < n) ml = t.ml_part[row_of(c0 + lane)];
-    float m = ml.x;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    m = fmaxf(m, top);
-    const float was = top == -INFINITY ? (sum == 0.f ? 0.f : 1.f) : tc::ex2(top - m);
-    top = m;
-    const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : tc::ex2(ml.x - top);
-    float s = w * ml.y;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    sum = was * sum + s;
-#pragma unroll
-    for (uint32_t e = 0; e < DP / 64; ++e) acc[e].x *= was, acc[e].y *= was;
-    for (uint32_t c = 0; c < n; c += 4) {
-      float2 o[4][DP / 64];
-#pragma unroll
-      for (uint32_t u = 0; u < 4; ++u)
-#pragma unroll
-        for (uint32_t e = 0; e < DP / 64; ++e)
-          o[u][e] = c + u < n ? *reinterpret_cast<const float2*>(t.o_part + row_of(c0 + c + u) * DP + e * 64 + lane * 2)
-                              : make_float2(0.f, 0.f);
-#pragma unroll
-      for (uint32_t u = 0; u < 4; ++u) {
-        const float wc = __shfl_sync(0xFFFFFFFFu, w, c + u);
-#pragma unroll
-        for (uint32_t e = 0; e < DP / 64; ++e)
-          acc[e].x += wc * o[u][e].x, acc[e].y += wc * o[u][e].y;
-      }
-    }
-  }
-  const uint64_t orow = (static_cast<uint64_t>(b) * a.T + tok) * a.kv_heads * a.group + h * a.group + head;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (uint32_t e = 0; e < DP / 64; ++e) {
-    const uint32_t d = e * 64 + lane * 2;
-    if (d < a.dim)
-      *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) =
-          tc::pack2<F16>(acc[e].x * inv, acc[e].y * inv);
-  }
-  if (lane == 0 && a.lse) a.lse[orow] = row_lse<F16>(top, sum);
-}
 
 static size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -158,13 +80,14 @@ static int launch(TcArgs& t, const CUtensorMap& mk, const CUtensorMap& mv, int d
   int rc = kv_launch("k_kv_tree", kern, dim3(t.n_ctas), S::kThreads, S::kSmem, 1, stream, t, mk, mv);
   if (rc != IBP_OK || t.n_ctas == 1) return rc;
   const uint64_t rows = static_cast<uint64_t>(t.a.T) * t.a.group, most = rows < MT * kTcTile ? rows : MT * kTcTile;
-  return kv_launch("k_kv_tree_join", k_kv_tree_join<DP, MT, F16>,
+  return kv_launch("k_kv_tree_join", k_kv_tree_join<DP, MT * kTcTile, F16>,
                    dim3(t.n_ctas - 1, static_cast<unsigned>((most + kJoinRows - 1) / kJoinRows)), kJoinThreads, 0, 1, stream, t);
 }
 
 static std::atomic<uint64_t> wait_limit{IBP_KV_WAIT_CYCLES};
 
 uint64_t kv_tree_wait_limit(uint64_t cycles) { return wait_limit.exchange(cycles, std::memory_order_relaxed); }
+long long kv_tree_limit() { return static_cast<long long>(wait_limit.load(std::memory_order_relaxed)); }
 
 int launch_kv_tree(const AttendArgs& a, int device, size_t ws_bytes, cudaStream_t stream, bool* done) {
   *done = false;

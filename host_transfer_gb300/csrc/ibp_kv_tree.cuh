@@ -30,6 +30,9 @@
 // read the same cache tiles do so at about the same time: two row blocks read
 // DRAM 1.5 times, not twice.
 //
+// The same kernel serves caches held in 4 bits (tc_load4): codes are decoded on their
+// way into the ring, which the tensor core reads as before.
+//
 // Measured on one GB300: 16 ragged caches of up to 32768 tokens, 8 kv heads of 128
 // (1.48 GB): 64 rows a head 233 us (6.4 TB/s, 0.94 of the copy rate), 512 rows
 // 600 to 640 us in replayed graphs (1.18 to 1.26 PFLOP/s, 0.62 to 0.66 of the library's
@@ -47,7 +50,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "ibp_kv_internal.cuh"
+#include "ibp_kv4.cuh"
 
 namespace ibp {
 
@@ -67,6 +70,7 @@ struct TcArgs {
                       // then one entry: the tiles of a CTA's range, as 64 bits
   uint32_t n_ctas;
   long long limit;    // clock cycles after which a wait gives up
+  Kv4View four[2];    // K and V of a cache in 4 bits
 };
 
 namespace tc {
@@ -219,7 +223,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 }  // namespace tc
 
-template <uint32_t DP, uint32_t MT>
+// FOUR: the cache is held in 4 bits.  Instead of the warp that issues TMA boxes, eight
+// warps read codes and write the tiles: a thread has one token of K or V.
+template <uint32_t DP, uint32_t MT, bool FOUR = false>
 struct TcShape {
   static constexpr uint32_t kHalves = DP / 64;                       // 128-byte wide panels of a tile
   static constexpr uint32_t kPanel = kTcTile * 128;                  // bytes of a panel
@@ -234,7 +240,10 @@ struct TcShape {
   static constexpr uint32_t kSlots = DP == 128 ? (MT == 1 ? 5 : 4) : (MT == 1 ? 11 : 8);
   static constexpr uint32_t kBytes = (kQ + kSlots) * kTileBytes;
   static constexpr uint32_t kSmem = kBytes + 1024 + 512;             // alignment, barriers
-  static constexpr uint32_t kThreads = MT * 128 + 64;
+  static constexpr uint32_t kLoaders = FOUR ? 8 : 1;                 // warps
+  static constexpr uint32_t kMmaWarp = MT * 4 + (FOUR ? 0 : 1);
+  static constexpr uint32_t kLoadWarp = MT * 4 + (FOUR ? 1 : 0);     // the first of them
+  static constexpr uint32_t kThreads = MT * 128 + 32 + kLoaders * 32;
   static constexpr uint32_t kOCol = 256;                             // first column of O
 };
 
@@ -246,7 +255,7 @@ struct TcShared {
   uint32_t odd[2];    // even and odd segments: 1 + the last whose draft holds infinities or NaN among its values
   uint32_t pair0, b0; // row block and sequence in which this CTA's range begins
   uint64_t in0;       // tiles of that sequence before the range
-  uint32_t sums[12];
+  uint32_t sums[14];
 };
 
 // A part of an item inside one CTA's range.
@@ -258,23 +267,25 @@ struct TcSeg {
 };
 
 // Cache tiles of a sequence, at least one, so that empty items write their zeros.
+template <uint32_t TILE = kTcTile>
 __device__ __forceinline__ uint32_t tiles_of(const AttendArgs& a, uint32_t b) {
   const int32_t len = clamp_len(a.lens[b], a.page_tokens, a.max_pages);
-  return len > 0 ? ceil_div(static_cast<uint32_t>(len), kTcTile) : 1u;
+  return len > 0 ? ceil_div(static_cast<uint32_t>(len), TILE) : 1u;
 }
 
 // Walks the segments of [at, end): every role of the CTA does so by itself.
-struct TcWalk {
+template <uint32_t TILE = kTcTile>
+struct TcWalkOf {
   const TcArgs& t;
   uint32_t pair, b;     // present row block and sequence
   uint32_t tiles;       // of each of its items
   uint64_t in;          // position inside the sequence's tiles
   uint64_t left;
-  __device__ TcWalk(const TcArgs& t_, const TcShared& sh, uint64_t at, uint64_t end) : t(t_) {
-    pair = sh.pair0;
-    b = sh.b0;
-    tiles = at < end ? tiles_of(t.a, b) : 1;
-    in = sh.in0;
+  __device__ TcWalkOf(const TcArgs& t_, uint32_t pair0, uint32_t b0, uint64_t in0, uint64_t at, uint64_t end) : t(t_) {
+    pair = pair0;
+    b = b0;
+    tiles = at < end ? tiles_of<TILE>(t.a, b) : 1;
+    in = in0;
     left = end - at;
   }
   __device__ bool next(TcSeg* s) {
@@ -285,7 +296,7 @@ struct TcWalk {
         ++pair;
       }
       in = 0;
-      tiles = tiles_of(t.a, b);
+      tiles = tiles_of<TILE>(t.a, b);
     }
     const uint32_t item = static_cast<uint32_t>(in / tiles);
     s->tile0 = static_cast<uint32_t>(in - static_cast<uint64_t>(item) * tiles);
@@ -304,6 +315,11 @@ struct TcWalk {
     left -= s->tiles;
     return true;
   }
+};
+
+struct TcWalk : TcWalkOf<> {
+  __device__ TcWalk(const TcArgs& t_, const TcShared& sh, uint64_t at, uint64_t end)
+      : TcWalkOf<>(t_, sh.pair0, sh.b0, sh.in0, at, end) {}
 };
 
 // Bit i: position p0 + i is seen by draft token t (false for rows that do not exist).
@@ -336,11 +352,112 @@ __device__ __forceinline__ uint32_t seen_bits(const AttendArgs& a, const TcSeg& 
   return bits;
 }
 
+// The tiles of a cache in 4 bits: thread r of the first half writes token r of every K
+// tile, one of the second half of every V tile, in the swizzled layout that TMA boxes
+// have, the elements of eight in the decoder's order.  Codes are two tiles ahead of
+// the one that is decoded, pages three.
 template <uint32_t DP, uint32_t MT, bool F16>
-__global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
+__device__ __forceinline__ void tc_load4(const TcArgs& t, TcShared& sh, uint64_t at, uint64_t end, unsigned char* ring_sm, uint32_t thread) {
+  using S = TcShape<DP, MT, true>;
+  const AttendArgs& a = t.a;
+  const uint32_t r = thread & 127u, kv = thread >> 7, lane = thread & 31u;
+  const Kv4View& v = t.four[kv];
+  volatile uint32_t* stop = &sh.stop;
+  struct Spot {  // nothing is done with the page here: it is still on its way
+    uint32_t page, slot, h;
+    bool there;
+  };
+  struct Raw {
+    uint4 w[DP / 32];
+    uint32_t s[DP / 32];
+  };
+  TcWalk walk(t, sh, at, end);
+  TcSeg s;
+  bool more = walk.next(&s);
+  uint32_t j = 0;
+  auto next_spot = [&](Spot& sp) {
+    sp.page = sp.slot = sp.h = 0;
+    sp.there = false;
+    if (!more) return;
+    if (j == 0 && thread == 0) {
+      const int32_t raw = a.lens[s.b], n = a.n_live ? a.n_live[s.b] : static_cast<int32_t>(a.T);
+      if (raw != s.len || n != s.n_live || n > s.len) kv_status(a.status, IBP_ERANGE);
+    }
+    const int32_t p = static_cast<int32_t>((s.tile0 + j) * kTcTile + r);
+    sp.h = s.h;
+    if (p < s.len) {
+      const uint32_t nth = static_cast<uint32_t>(p) / a.page_tokens;
+      sp.slot = static_cast<uint32_t>(p) - nth * a.page_tokens;
+      sp.there = true;
+      sp.page = static_cast<uint32_t>(__ldg(a.table + static_cast<uint64_t>(s.b) * a.max_pages + nth));
+    }
+    if (++j == s.tiles) {
+      more = walk.next(&s);
+      j = 0;
+    }
+  };
+  auto fetch = [&](const Spot& sp, Raw& raw) {
+    const bool on = sp.there && sp.page < a.n_pages;
+    if (!on && sp.there) kv_status(a.status, IBP_ERANGE);
+    const char* c = v.codes + static_cast<int64_t>(on ? sp.page : 0) * v.page_stride + static_cast<int64_t>(sp.h) * v.head_stride +
+                    static_cast<int64_t>(on ? sp.slot : 0) * v.token_stride;
+    const char* sc = v.scales + static_cast<int64_t>(on ? sp.page : 0) * v.s_page + static_cast<int64_t>(sp.h) * v.s_head +
+                     static_cast<int64_t>(on ? sp.slot : 0) * v.s_token;
+#pragma unroll
+    for (uint32_t g = 0; g < DP / 32; ++g) {
+      const bool in = on && g * 32 < a.dim;
+      raw.w[g] = in ? __ldg(reinterpret_cast<const uint4*>(c + g * 16)) : make_uint4(0u, 0u, 0u, 0u);
+      raw.s[g] = in ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(sc + g * 2))) : 0u;
+    }
+  };
+  const quad::Magic<F16> magic;
+  const uint64_t n = end - at;
+  Spot spot;
+  Raw raw[2];
+  next_spot(spot);
+  fetch(spot, raw[0]);
+  next_spot(spot);
+  fetch(spot, raw[1]);
+  next_spot(spot);
+  bool ok = true;
+  for (uint64_t i = 0; i < n && ok; i += 2) {
+#pragma unroll
+    for (uint32_t u = 0; u < 2; ++u) {
+      if (i + u >= n) break;
+      const uint32_t f = static_cast<uint32_t>(2 * (i + u)) + kv, slot = f % S::kSlots;
+      if (lane == 0) ok = tc::bar_wait(tc::s32(&sh.empty[slot]), (f / S::kSlots & 1u) ^ 1u, stop, t.limit);
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (!ok) break;
+      unsigned char* dst = ring_sm + slot * S::kTileBytes + r * 128;
+#pragma unroll
+      for (uint32_t g = 0; g < DP / 32; ++g) {
+        const quad::Pair<F16> p(__byte_perm(raw[u].s[g], 0, 0x1010));
+        const uint32_t w[4] = {raw[u].w[g].x, raw[u].w[g].y, raw[u].w[g].z, raw[u].w[g].w};
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) {
+          const uint32_t c = g * 4 + e;
+          *reinterpret_cast<uint4*>(dst + (c / 8) * S::kPanel + (((c & 7u) ^ (r & 7u)) << 4)) =
+              make_uint4(quad::decode<F16, 0>(w[e], p, magic), quad::decode<F16, 1>(w[e], p, magic),
+                         quad::decode<F16, 2>(w[e], p, magic), quad::decode<F16, 3>(w[e], p, magic));
+        }
+      }
+      tc::fence_async();
+      tc::bar_arrive(tc::s32(&sh.full[slot]));
+      fetch(spot, raw[u]);
+      next_spot(spot);
+    }
+  }
+}
+
+// Element of a group of eight that the decoder puts at place k, and the place of element e.
+__device__ constexpr uint32_t quad_element(uint32_t k) { return (k >> 1) + (k & 1u) * 4; }
+__device__ constexpr uint32_t quad_place(uint32_t e) { return (e & 3u) * 2 + (e >> 2); }
+
+template <uint32_t DP, uint32_t MT, bool F16, bool FOUR = false>
+__global__ void __launch_bounds__(TcShape<DP, MT, FOUR>::kThreads, 1)
     k_kv_tree(const __grid_constant__ TcArgs t, const __grid_constant__ CUtensorMap map_k,
               const __grid_constant__ CUtensorMap map_v) {
-  using S = TcShape<DP, MT>;
+  using S = TcShape<DP, MT, FOUR>;
   const AttendArgs& a = t.a;
   extern __shared__ unsigned char raw_sm[];
   unsigned char* sm = raw_sm + ((1024 - (tc::s32(raw_sm) & 1023u)) & 1023u);
@@ -356,7 +473,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
 
   if (tid == 0) {
     for (uint32_t i = 0; i < S::kSlots; ++i) {
-      tc::bar_init(tc::s32(&sh.full[i]), 1);
+      tc::bar_init(tc::s32(&sh.full[i]), FOUR ? 128 : 1);
       tc::bar_init(tc::s32(&sh.empty[i]), 1);
     }
     for (uint32_t i = 0; i < 2; ++i) {
@@ -370,10 +487,12 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
     sh.stop = 0;
     sh.odd[0] = sh.odd[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+    if constexpr (!FOUR) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+    }
   }
-  if (warp == MT * 4 + 1) {
+  if (warp == S::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::s32(&sh.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -428,56 +547,60 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
   const uint32_t tmem = sh.tmem;
   volatile uint32_t* stop = &sh.stop;
 
-  if (warp == MT * 4) {
-    // ---- producer: one lane issues; all follow the same path
-    TcWalk walk(t, sh, at, end);
-    TcSeg s;
-    uint32_t f = 0;  // fills so far
-    bool ok = true;
-    const uint32_t boxes = kTcTile / t.box;
-    while (ok && walk.next(&s)) {
-      const int32_t* row = a.table + static_cast<uint64_t>(s.b) * a.max_pages;
-      if (lane == 0) {
-        const int32_t raw = a.lens[s.b], n = a.n_live ? a.n_live[s.b] : static_cast<int32_t>(a.T);
-        if (raw != s.len || n != s.n_live || n > s.len) kv_status(a.status, IBP_ERANGE);
-      }
-      for (uint32_t j = 0; j < s.tiles && ok; ++j) {
-        const int32_t p0 = static_cast<int32_t>((s.tile0 + j) * kTcTile);
-        // lane i finds the page of box i
-        const int32_t p = p0 + static_cast<int32_t>(lane * t.box);
-        const bool have = lane < boxes && p < s.len;
-        int32_t page = 0, slot = 0;
-        if (have) {
-          const uint32_t nth = static_cast<uint32_t>(p) / a.page_tokens;
-          slot = p - static_cast<int32_t>(nth * a.page_tokens);
-          page = row[nth];
-          if (static_cast<uint32_t>(page) >= a.n_pages) {
-            kv_status(a.status, IBP_ERANGE);
-            page = static_cast<int32_t>(a.n_pages);  // past the last page: the box reads zeros
+  if (warp >= S::kLoadWarp && warp < S::kLoadWarp + S::kLoaders) {
+    if constexpr (FOUR) {
+      tc_load4<DP, MT, F16>(t, sh, at, end, sm + (kv_sm - base), tid - S::kLoadWarp * 32);
+    } else {
+      // ---- producer: one lane issues; all follow the same path
+      TcWalk walk(t, sh, at, end);
+      TcSeg s;
+      uint32_t f = 0;  // fills so far
+      bool ok = true;
+      const uint32_t boxes = kTcTile / t.box;
+      while (ok && walk.next(&s)) {
+        const int32_t* row = a.table + static_cast<uint64_t>(s.b) * a.max_pages;
+        if (lane == 0) {
+          const int32_t raw = a.lens[s.b], n = a.n_live ? a.n_live[s.b] : static_cast<int32_t>(a.T);
+          if (raw != s.len || n != s.n_live || n > s.len) kv_status(a.status, IBP_ERANGE);
+        }
+        for (uint32_t j = 0; j < s.tiles && ok; ++j) {
+          const int32_t p0 = static_cast<int32_t>((s.tile0 + j) * kTcTile);
+          // lane i finds the page of box i
+          const int32_t p = p0 + static_cast<int32_t>(lane * t.box);
+          const bool have = lane < boxes && p < s.len;
+          int32_t page = 0, slot = 0;
+          if (have) {
+            const uint32_t nth = static_cast<uint32_t>(p) / a.page_tokens;
+            slot = p - static_cast<int32_t>(nth * a.page_tokens);
+            page = row[nth];
+            if (static_cast<uint32_t>(page) >= a.n_pages) {
+              kv_status(a.status, IBP_ERANGE);
+              page = static_cast<int32_t>(a.n_pages);  // past the last page: the box reads zeros
+            }
+          }
+          const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, have));
+          const uint32_t bytes = n * t.box * 128 * S::kHalves;
+  #pragma unroll
+          for (uint32_t kv = 0; kv < 2; ++kv, ++f) {
+            ok = tc::bar_wait(tc::s32(&sh.empty[ring(f)]), ring_phase(f) ^ 1u, stop, t.limit);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            const uint32_t bar = tc::s32(&sh.full[ring(f)]), dst = ring_at(f) + lane * t.box * 128;
+            if (lane == 0) tc::bar_expect(bar, bytes);
+            __syncwarp();
+            if (have)
+  #pragma unroll
+              for (uint32_t hf = 0; hf < S::kHalves; ++hf)
+                tc::tma_box(dst + hf * S::kPanel, kv ? &map_v : &map_k, hf * 64, slot, s.h, page, bar);
           }
         }
-        const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, have));
-        const uint32_t bytes = n * t.box * 128 * S::kHalves;
-#pragma unroll
-        for (uint32_t kv = 0; kv < 2; ++kv, ++f) {
-          ok = tc::bar_wait(tc::s32(&sh.empty[ring(f)]), ring_phase(f) ^ 1u, stop, t.limit);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          const uint32_t bar = tc::s32(&sh.full[ring(f)]), dst = ring_at(f) + lane * t.box * 128;
-          if (lane == 0) tc::bar_expect(bar, bytes);
-          __syncwarp();
-          if (have)
-#pragma unroll
-            for (uint32_t hf = 0; hf < S::kHalves; ++hf)
-              tc::tma_box(dst + hf * S::kPanel, kv ? &map_v : &map_k, hf * 64, slot, s.h, page, bar);
-        }
+      }
+      for (uint32_t i = 0; i < S::kSlots; ++i) {  // copies in flight land before the CTA leaves
+        const uint32_t n = (f + S::kSlots - 1 - i) / S::kSlots;  // fills of slot i
+        if (n) tc::bar_drain(tc::s32(&sh.full[i]), (n - 1) & 1u);
       }
     }
-    for (uint32_t i = 0; i < S::kSlots; ++i) {  // copies in flight land before the CTA leaves
-      const uint32_t n = (f + S::kSlots - 1 - i) / S::kSlots;  // fills of slot i
-      if (n) tc::bar_drain(tc::s32(&sh.full[i]), (n - 1) & 1u);
-    }
-  } else if (warp == MT * 4 + 1) {
+  } else if (warp == S::kMmaWarp) {
     // ---- MMA
     const uint32_t fmt = F16 ? 0u : 1u;
     const uint32_t id_qk = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kTcTile >> 3) << 17) | ((kTcTile >> 4) << 24);
@@ -660,6 +783,9 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
             x = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
+        if constexpr (FOUR)  // dimensions as the decoder has them
+          x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                         __byte_perm(x.y, x.w, 0x7632));
         *reinterpret_cast<uint4*>(dst + (c / 8) * S::kPanel + (((c & 7u) ^ (r & 7u)) << 4)) = x;
       }
       tc::fence_async();
@@ -832,6 +958,22 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
             const uint32_t nth = static_cast<uint32_t>(p) / a.page_tokens;
             const uint32_t pg = static_cast<uint32_t>(a.table[static_cast<uint64_t>(s.b) * a.max_pages + nth]);
             if (pg >= a.n_pages) continue;
+            if constexpr (FOUR) {
+              const Kv4View& v4 = t.four[1];
+              const int64_t slot4 = p - static_cast<int64_t>(nth) * a.page_tokens;
+              if (32 * c >= a.dim) continue;
+              const uint32_t* codes = reinterpret_cast<const uint32_t*>(v4.codes + static_cast<int64_t>(pg) * v4.page_stride +
+                                                                        static_cast<int64_t>(s.h) * v4.head_stride + slot4 * v4.token_stride) + 4 * c;
+              const uint32_t sc = quad::scale_bits<F16>(*reinterpret_cast<const uint16_t*>(
+                  v4.scales + static_cast<int64_t>(pg) * v4.s_page + static_cast<int64_t>(s.h) * v4.s_head + slot4 * v4.s_token + 2 * c));
+              if (!quad::odd<F16>(sc)) continue;
+#pragma unroll
+              for (uint32_t i = 0; i < 32; ++i) {
+                const float x = quad::value<F16>(codes[i / 8], quad_element(i & 7u), sc);
+                if (!(fabsf(x) < INFINITY)) o[i] += x;
+              }
+              continue;
+            }
             const uint16_t* v = reinterpret_cast<const uint16_t*>(
                 a.v.data + static_cast<int64_t>(pg) * a.v.page_stride + static_cast<int64_t>(s.h) * a.v.head_stride +
                 static_cast<int64_t>(p - nth * a.page_tokens) * a.v.token_stride);
@@ -852,7 +994,9 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
               if (32 * c + i < a.dim) {
                 uint32_t w[4];
 #pragma unroll
-                for (uint32_t e = 0; e < 4; ++e) w[e] = tc::pack2<F16>(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv);
+                for (uint32_t e = 0; e < 4; ++e)
+                  w[e] = FOUR ? tc::pack2<F16>(o[i + quad_place(2 * e)] * inv, o[i + quad_place(2 * e + 1)] * inv)
+                              : tc::pack2<F16>(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv);
                 uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + 32 * c + i) * 2);
                 if ((reinterpret_cast<uintptr_t>(a.out) & 15u) == 0)
                   *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -861,8 +1005,12 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
               }
         } else {
 #pragma unroll
-          for (uint32_t i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(t.o_part + prow * DP + 32 * c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (uint32_t i = 0; i < 32; i += 4) {
+            const uint32_t i8 = i & ~7u, e = i & 7u;
+            *reinterpret_cast<float4*>(t.o_part + prow * DP + 32 * c + i) =
+                FOUR ? make_float4(o[i8 + quad_place(e)], o[i8 + quad_place(e + 1)], o[i8 + quad_place(e + 2)], o[i8 + quad_place(e + 3)])
+                     : make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
         }
       }
       if (!live) top = -INFINITY, sum = 0.f;
@@ -882,10 +1030,87 @@ __global__ void __launch_bounds__(TcShape<DP, MT>::kThreads, 1)
   }
   __syncthreads();
   if (tid == 0 && *stop) kv_status(a.status, IBP_ETIMEOUT);
-  if (warp == MT * 4 + 1) {
+  if (warp == S::kMmaWarp) {
     tc::fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
+}
+
+constexpr int kJoinThreads = 256;
+constexpr uint32_t kJoinRows = kJoinThreads / 32;  // rows of a CTA, a warp each
+
+// CTA (j, rows): joins the item that crosses the start of range j, if j is the
+// first range boundary inside it.  The range before holds its first part (slot
+// 1), the ranges from j on the others (slot 0), added in that order.
+template <uint32_t DP, uint32_t ROWS, bool F16, uint32_t TILE = kTcTile>
+__global__ void __launch_bounds__(kJoinThreads) k_kv_tree_join(const __grid_constant__ TcArgs t) {
+  pdl_begin();
+  const AttendArgs& a = t.a;
+  const uint32_t j = blockIdx.x + 1, lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  const int4 f = t.first[j], sh = t.first[t.n_ctas];
+  const uint64_t share = static_cast<uint32_t>(sh.x) | (static_cast<uint64_t>(static_cast<uint32_t>(sh.y)) << 32);
+  const uint64_t before = static_cast<uint32_t>(f.w);
+  if (f.x < 0 || before == 0 || before > share) return;
+  const uint32_t b = f.x, h = f.y;
+  const uint64_t start = j * share - before, end = start + tiles_of<TILE>(a, b);
+  const uint32_t last = static_cast<uint32_t>((end - 1) / share);
+  constexpr uint32_t kRows = ROWS;
+  const uint32_t r = blockIdx.y * kJoinRows + warp, gr = f.z * kRows + r;
+  const uint32_t tok = gr / a.group, head = gr - tok * a.group;
+  if (r >= kRows || tok >= a.T) return;
+  auto row_of = [&](uint32_t c) { return (2ull * c + (c < j ? 1 : 0)) * kRows + r; };
+  // Weights of up to 32 parts at a time, a part a lane; their rows follow with
+  // four loads in flight.  The running maximum makes room for any number.  A part of
+  // weight 0 is added like the others: what is not finite in it the row has seen, and
+  // the result must not depend on where the ranges of the CTAs end.
+  float top = -INFINITY, sum = 0.f;
+  float2 acc[DP / 64];
+#pragma unroll
+  for (uint32_t e = 0; e < DP / 64; ++e) acc[e] = make_float2(0.f, 0.f);
+  for (uint32_t c0 = j - 1; c0 <= last; c0 += 32) {
+    const uint32_t n = last - c0 + 1 < 32 ? last - c0 + 1 : 32;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) ml = t.ml_part[row_of(c0 + lane)];
+    float m = ml.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    m = fmaxf(m, top);
+    const float was = top == -INFINITY ? (sum == 0.f ? 0.f : 1.f) : tc::ex2(top - m);
+    top = m;
+    const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : tc::ex2(ml.x - top);
+    float s = w * ml.y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    sum = was * sum + s;
+#pragma unroll
+    for (uint32_t e = 0; e < DP / 64; ++e) acc[e].x *= was, acc[e].y *= was;
+    for (uint32_t c = 0; c < n; c += 4) {
+      float2 o[4][DP / 64];
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u)
+#pragma unroll
+        for (uint32_t e = 0; e < DP / 64; ++e)
+          o[u][e] = c + u < n ? *reinterpret_cast<const float2*>(t.o_part + row_of(c0 + c + u) * DP + e * 64 + lane * 2)
+                              : make_float2(0.f, 0.f);
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u) {
+        const float wc = __shfl_sync(0xFFFFFFFFu, w, c + u);
+#pragma unroll
+        for (uint32_t e = 0; e < DP / 64; ++e)
+          acc[e].x += wc * o[u][e].x, acc[e].y += wc * o[u][e].y;
+      }
+    }
+  }
+  const uint64_t orow = (static_cast<uint64_t>(b) * a.T + tok) * a.kv_heads * a.group + h * a.group + head;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (uint32_t e = 0; e < DP / 64; ++e) {
+    const uint32_t d = e * 64 + lane * 2;
+    if (d < a.dim)
+      *reinterpret_cast<uint32_t*>(static_cast<char*>(a.out) + (orow * a.dim + d) * 2) =
+          tc::pack2<F16>(acc[e].x * inv, acc[e].y * inv);
+  }
+  if (lane == 0 && a.lse) a.lse[orow] = row_lse<F16>(top, sum);
 }
 
 }  // namespace ibp

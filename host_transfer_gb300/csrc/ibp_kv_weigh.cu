@@ -55,14 +55,15 @@ struct WeighKeys {
           s[i][0] = in ? __ldg(reinterpret_cast<const uint16_t*>(sc)) : 0u;
         }
       }
+      const quad::Magic<F16> m;
 #pragma unroll
       for (uint32_t j = 0; j < DP / 32; ++j) {
         const uint32_t gi = DP == 256 ? j / 4 : 0;
-        const quad::Pair<F16> p0(quad::scale_bits<F16>(s[0][gi]) * 0x10001u), p1(quad::scale_bits<F16>(s[1][gi]) * 0x10001u);
-        f[2 * j][0] = quad::decode<F16, 0>(w[0][j], p0), f[2 * j][1] = quad::decode<F16, 0>(w[1][j], p1);
-        f[2 * j][2] = quad::decode<F16, 1>(w[0][j], p0), f[2 * j][3] = quad::decode<F16, 1>(w[1][j], p1);
-        f[2 * j + 1][0] = quad::decode<F16, 2>(w[0][j], p0), f[2 * j + 1][1] = quad::decode<F16, 2>(w[1][j], p1);
-        f[2 * j + 1][2] = quad::decode<F16, 3>(w[0][j], p0), f[2 * j + 1][3] = quad::decode<F16, 3>(w[1][j], p1);
+        const quad::Pair<F16> p0(s[0][gi] * 0x10001u), p1(s[1][gi] * 0x10001u);
+        f[2 * j][0] = quad::decode<F16, 0>(w[0][j], p0, m), f[2 * j][1] = quad::decode<F16, 0>(w[1][j], p1, m);
+        f[2 * j][2] = quad::decode<F16, 1>(w[0][j], p0, m), f[2 * j][3] = quad::decode<F16, 1>(w[1][j], p1, m);
+        f[2 * j + 1][0] = quad::decode<F16, 2>(w[0][j], p0, m), f[2 * j + 1][1] = quad::decode<F16, 2>(w[1][j], p1, m);
+        f[2 * j + 1][2] = quad::decode<F16, 3>(w[0][j], p0, m), f[2 * j + 1][3] = quad::decode<F16, 3>(w[1][j], p1, m);
       }
     } else {
 #pragma unroll

@@ -793,9 +793,9 @@ int ibp_kv4_load(const ibp_kv4_pages* k_pages, const ibp_kv4_pages* v_pages, uin
  * rules, with what the codes stand for as keys and values.  A position whose page id
  * is out of range reads as a zero key and value and records IBP_ERANGE.
  *
- * ws       ibp_kv4_attention_workspace bytes (0: may be NULL).  Calls of more than
- *          128 rows a kv head (T * q_heads / kv_heads) and dim <= 128 decode the
- *          cache once, so theirs holds the sequences in 16 bits.
+ * ws       ibp_kv4_attention_workspace bytes.  Large calls of more than 256 rows a
+ *          kv head (T * q_heads / kv_heads) and dim <= 128 decode the cache once,
+ *          so theirs holds the sequences in 16 bits.
  */
 int ibp_kv4_attention(const ibp_kv4_pages* k, const ibp_kv4_pages* v, uint32_t dtype, const ibp_kv_seqs* seqs,
                       const void* q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride, uint32_t T,

@@ -255,14 +255,15 @@ def test_attention_over_long_caches(lens, T, hk, G, page, D, dt):
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 @pytest.mark.parametrize("lens,T,hk,G,page,D,mask", [
     ([300, 290] * 3, 17, 2, 8, 64, 128, True), ([200, 141, 141, 150] * 2, 141, 3, 1, 7, 64, False),
-    ([170] * 12, 130, 2, 1, 16, 96, True),
+    ([170] * 12, 130, 2, 1, 16, 96, True), ([90, 700, 41] * 4, 40, 4, 1, 24, 32, True),
+    ([300, 290] * 2, 40, 2, 8, 64, 128, True), ([310, 305, 301], 300, 2, 1, 5, 64, True),
+    ([150, 160, 100], 37, 3, 8, 16, 96, False),
 ])
 def test_attention_of_many_rows(lens, T, hk, G, page, D, mask, dt):
-    """Calls that decode the cache once for the tensor-core kernel."""
+    """Calls for the tensor cores: on codes, and (above 256 rows) decoded once."""
     c = Cache(lens, T, hk, G, page, D, dt, seed=T, mask=mask)
     B = len(lens)
-    size = kv._load().ibp_kv4_attention_workspace(B, c.np_table.shape[1], page, T, hk * G, hk, D)
-    assert size > B * int(max(lens)) * hk * D * 4, "the call is meant to decode its cache"
+    assert -(-max(lens) // 128) * B * hk * -(-T * G // 16) >= 304, "work enough for the tensor cores"
     live = np.array([T - (i % 3) for i in range(B)], np.int32)
     c.check(n_draft=live)
 
@@ -855,3 +856,19 @@ def test_a_gradient_is_an_error():
     out, lse = c.attend()
     with pytest.raises(RuntimeError, match="no backward"):
         out.sum().backward()
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_waits_that_run_out(T):
+    """Every wait of the tensor-core kernels gives up: the status says so, and the next call is whole."""
+    c = Cache([300, 310, 333], T, 8 if T == 40 else 4, 2 if T == 40 else 1, 16, 64, seed=5)
+    want = c.attend()
+    torch.cuda.synchronize()
+    before = kv.ibp_kv_set_wait_limit(0)
+    try:
+        c.attend()
+        torch.cuda.synchronize()
+    finally:
+        kv.ibp_kv_set_wait_limit(before)
+    err(ibp.IBP_ETIMEOUT)
+    assert same(c.attend(), want)

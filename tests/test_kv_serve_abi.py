@@ -43,7 +43,7 @@ def test_scratch_sizes(lib):
     size = lib.ibp_kv4_attention_workspace
     # shapes that no call takes want nothing
     assert size(1, 4, 16, 1, 8, 0, 64) == size(1, 4, 16, 1, 7, 2, 64) == size(1, 4, 0, 1, 8, 2, 64) == size(1, 4, 16, 1, 8, 2, 288) == 0
-    assert size(1, 4, 16, 1, 8, 2, 64) == 0  # small calls need none
+    assert size(1, 4, 16, 1, 8, 2, 64) < 1 << 16  # a part of each of a few blocks
     assert size(64, 1024, 64, 1, 64, 8, 128) < 1 << 30  # chunks' sums are a few percent of the cache
 
 
