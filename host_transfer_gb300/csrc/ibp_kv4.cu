@@ -1,7 +1,7 @@
 // ibp_kv4.cu - tokens into and out of paged caches held in 4 bits.
 //
-// A thread takes 8 elements (16 bytes) and four threads a group of 32, so that
-// the largest magnitude is two exchanges and every access of a warp is a run of
+// A thread takes 8 elements (16 bytes) of four tokens and four threads a group of 32, so
+// that the largest magnitude is two exchanges and every access of a warp is a run of
 // whole sectors.  Bound by DRAM for prompts (2 bytes read and 9/16 written an
 // element, or the other way), by latency for single tokens.
 #include "ibp_kv4.cuh"
@@ -9,47 +9,49 @@
 namespace ibp {
 
 constexpr int kRowThreads = 256;
+constexpr uint32_t kRowFly = 4;  // tokens of a thread, all of them read before any is written
 
-struct Row8 {  // eight elements of a row: which tensor, sequence, token, head, chunk
-  uint32_t b, t, h, c, which;
-};
-
-__device__ __forceinline__ Row8 row8_of(const Kv4Rows& r, uint64_t x) {
-  Row8 e;
-  const uint32_t chunks = r.dim / 8;
-  e.c = static_cast<uint32_t>(x % chunks);
-  x /= chunks;
-  e.h = static_cast<uint32_t>(x % r.heads);
-  x /= r.heads;
-  e.t = static_cast<uint32_t>(x % r.T);
-  x /= r.T;
-  e.b = static_cast<uint32_t>(x % r.n_seqs);
-  e.which = static_cast<uint32_t>(x / r.n_seqs);
-  return e;
-}
-
-// The page and slot of row t of a sequence; page 2^32 - 1 where there is none.
+// The page and slot of a row; page 2^32 - 1 where there is none.
 struct Spot {
   uint32_t page, slot;
 };
-__device__ __forceinline__ Spot spot_of(const Kv4Rows& r, uint32_t b, uint32_t t) {
-  Spot s = {0xFFFFFFFFu, 0u};
-  const int32_t raw = r.lens[b], len = clamp_len(raw, r.page_tokens, r.max_pages);
-  const int32_t want = r.n_rows ? r.n_rows[b] : static_cast<int32_t>(r.T);
-  const int32_t n = want < 0 ? 0 : (want > static_cast<int32_t>(r.T) ? static_cast<int32_t>(r.T) : want);
-  if (raw != len || want != n || n > len) kv_status(r.status, IBP_ERANGE);
-  const int32_t pos = len - n + static_cast<int32_t>(t);
-  if (static_cast<int32_t>(t) >= n || pos < 0) return s;
-  const uint32_t nth = static_cast<uint32_t>(pos) / r.page_tokens;
-  const uint32_t page = static_cast<uint32_t>(r.table[static_cast<uint64_t>(b) * r.max_pages + nth]);
-  if (page >= r.n_pages) {
-    kv_status(r.status, IBP_ERANGE);
+
+// The rows of block (tokens, sequence, K or V): threads take neighbouring pieces of eight
+// elements of a token, as many tokens at a time as fit.
+struct Rows {
+  uint32_t pieces;      // of a token
+  uint32_t width;       // of them at a time
+  uint32_t at_once;     // tokens at a time
+  uint32_t first;       // this block's first token
+  uint32_t b, which;
+  int32_t n, base;      // rows of the sequence, position of row 0
+  __device__ __forceinline__ explicit Rows(const Kv4Rows& r) {
+    pieces = r.heads * (r.dim / 8);
+    width = pieces < kRowThreads ? pieces : kRowThreads;
+    at_once = kRowThreads / width;
+    first = blockIdx.x * at_once * kRowFly;
+    b = blockIdx.y, which = blockIdx.z;
+    const int32_t raw = r.lens[b], len = clamp_len(raw, r.page_tokens, r.max_pages);
+    const int32_t want = r.n_rows ? r.n_rows[b] : static_cast<int32_t>(r.T);
+    n = want < 0 ? 0 : (want > static_cast<int32_t>(r.T) ? static_cast<int32_t>(r.T) : want);
+    base = len - n;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && (raw != len || want != n || base < 0)) kv_status(r.status, IBP_ERANGE);
+  }
+  __device__ __forceinline__ Spot spot(const Kv4Rows& r, uint32_t t) const {
+    Spot s = {0xFFFFFFFFu, 0u};
+    const int32_t pos = base + static_cast<int32_t>(t);
+    if (static_cast<int32_t>(t) >= n || pos < 0) return s;
+    const uint32_t nth = static_cast<uint32_t>(pos) / r.page_tokens;
+    const uint32_t page = static_cast<uint32_t>(__ldg(r.table + static_cast<uint64_t>(b) * r.max_pages + nth));
+    if (page >= r.n_pages) {
+      kv_status(r.status, IBP_ERANGE);
+      return s;
+    }
+    s.page = page;
+    s.slot = static_cast<uint32_t>(pos) - nth * r.page_tokens;
     return s;
   }
-  s.page = page;
-  s.slot = static_cast<uint32_t>(pos) - nth * r.page_tokens;
-  return s;
-}
+};
 
 __device__ __forceinline__ char* codes_at(const Kv4View& v, const Spot& s, uint32_t h, uint32_t c) {
   return const_cast<char*>(v.codes) + static_cast<int64_t>(s.page) * v.page_stride + static_cast<int64_t>(h) * v.head_stride +
@@ -73,64 +75,66 @@ __device__ __forceinline__ uint32_t scale_of(float a) {
   return __float_as_uint(fminf(s, 0x1p121f)) >> 16;
 }
 
-// rint(x / s) for whole x / s + 1/2 too.  x times the rounded reciprocal is off by
-// 2^-23 of itself at most, while x / s (11 bits by 5) is a tie or 2^-16 away from one:
-// only at a tie may the product round to the wrong side, which the remainder shows.
-__device__ __forceinline__ float quotient(float x, float s, float inv) {
-  float r = rintf(__fmul_rn(x, inv));
-  const float e = __fmaf_rn(-r, s, x);                      // exact
-  const bool tie = __fmul_rn(2.f, fabsf(e)) == s;
-  const bool uneven = (static_cast<int>(fmaxf(fminf(r, 8.f), -8.f)) & 1) != 0;
-  if (tie && uneven) r += e > 0.f ? 1.f : -1.f;
-  return fmaxf(fminf(r, 7.f), -7.f);
+// 8 + rint(x / s), kept within 1 to 15, in the low bits of a float.  x times the rounded
+// reciprocal is off by 2^-21 at most, while x / s (11 bits by 5) is a tie k + 1/2 or 2^-12 away
+// from one: rounded to multiples of 2^-16 first, ties are exact again and go to
+// even like the quotient's own.
+__device__ __forceinline__ uint32_t code_of(float x, float inv) {
+  const float y = __fadd_rn(__fmaf_rn(x, inv, 192.f), -192.f);
+  return __float_as_uint(__fadd_rn(fmaxf(fminf(y, 7.f), -7.f), 12582920.f)) & 15u;  // 1.5 2^23 + 8
 }
 
 template <bool F16>
-__global__ void __launch_bounds__(kRowThreads) k_kv4_store(const Kv4Rows r, uint64_t total) {
+__global__ void __launch_bounds__(kRowThreads) k_kv4_store(const Kv4Rows r) {
   pdl_begin();
-  // whole groups of four threads run alike, since total is a multiple of four
-  for (uint64_t x = static_cast<uint64_t>(blockIdx.x) * kRowThreads + threadIdx.x; x < total;
-       x += static_cast<uint64_t>(gridDim.x) * kRowThreads) {
-    const uint32_t quad = 0xFu << (threadIdx.x & 28u);
-    const Row8 e = row8_of(r, x);
-    const Spot s = spot_of(r, e.b, e.t);
-    const bool live = s.page != 0xFFFFFFFFu;
-    const char* src = r.x[e.which] + static_cast<int64_t>(e.b) * r.x_seq[e.which] + static_cast<int64_t>(e.t) * r.x_token[e.which] +
-                      static_cast<int64_t>(e.h) * r.x_head[e.which] + e.c * 16;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (live) {
-      if (r.vec) {
-        const uint4 u = *reinterpret_cast<const uint4*>(src);
-        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-      } else {
+  const Rows o(r);
+  const Kv4View& p = r.p[o.which];
+  const uint32_t mine = threadIdx.x / o.width, chunks = r.dim / 8;
+  const uint32_t quad = 0xFu << (threadIdx.x & 28u);  // threads of a group; they run alike
+  if (mine >= o.at_once) return;
+  for (uint32_t piece = threadIdx.x - mine * o.width; piece < o.pieces; piece += o.width) {
+    const uint32_t h = piece / chunks, c = piece - h * chunks;
+    const char* src = r.x[o.which] + static_cast<int64_t>(o.b) * r.x_seq[o.which] + static_cast<int64_t>(h) * r.x_head[o.which] + c * 16;
+    Spot at[kRowFly];
+    uint32_t w[kRowFly][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = *reinterpret_cast<const uint16_t*>(src + 4 * i) | (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(src + 4 * i + 2)) << 16);
+    for (uint32_t i = 0; i < kRowFly; ++i) {
+      const uint32_t t = o.first + i * o.at_once + mine;
+      at[i] = o.spot(r, t);
+      w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
+      if (static_cast<int32_t>(t) < o.n) {
+        const char* x = src + static_cast<int64_t>(t) * r.x_token[o.which];
+        if (r.vec) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(x));
+          w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[i][j] = *reinterpret_cast<const uint16_t*>(x + 4 * j) | (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(x + 4 * j + 2)) << 16);
+        }
       }
     }
-    float v[8], a = 0.f;
-    bool fine = true;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = quad::to_float<F16>(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
-      fine = fine && isfinite(v[i]);
-      a = fmaxf(a, fabsf(v[i]));
-    }
-    a = fmaxf(a, __shfl_xor_sync(quad, a, 1));
-    a = fmaxf(a, __shfl_xor_sync(quad, a, 2));
-    fine = __ballot_sync(quad, fine) == quad;
-    uint32_t sb = fine ? scale_of<F16>(a) : 0u;
-    const float sc = quad::to_float<F16>(sb), inv = sc > 0.f ? __fdiv_rn(1.f, sc) : 0.f;
-    uint32_t word = 0;
+    for (uint32_t i = 0; i < kRowFly; ++i) {
+      float v[8], a = 0.f, all = 0.f;  // all: NaN where something is not finite
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = sc > 0.f ? quotient(v[i], sc, inv) : 0.f;
-      word |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * i);
-    }
-    if (!fine) sb = F16 ? 0x7E00u : 0x7FC0u;
-    if (live) {
-      *reinterpret_cast<uint32_t*>(codes_at(r.p[e.which], s, e.h, e.c)) = word;
-      if ((e.c & 3u) == 0) *reinterpret_cast<uint16_t*>(scale_at(r.p[e.which], s, e.h, e.c)) = static_cast<uint16_t>(sb);
+      for (int j = 0; j < 8; ++j) {
+        v[j] = quad::to_float<F16>(j & 1 ? w[i][j / 2] >> 16 : w[i][j / 2] & 0xFFFFu);
+        a = fmaxf(a, fabsf(v[j]));
+        all = __fmaf_rn(v[j], 0.f, all);
+      }
+      a = fmaxf(a, __shfl_xor_sync(quad, a, 1));
+      a = fmaxf(a, __shfl_xor_sync(quad, a, 2));
+      const bool fine = (__ballot_sync(quad, all == 0.f) & quad) == quad;
+      uint32_t sb = fine ? scale_of<F16>(a) : 0u;
+      const float sc = quad::to_float<F16>(sb), inv = sc > 0.f ? __fdiv_rn(1.f, sc) : 0.f;
+      uint32_t word = 0;
+#pragma unroll
+      for (int j = 7; j >= 0; --j) word = word << 4 | code_of(fine ? v[j] : 0.f, inv);
+      if (!fine) sb = F16 ? 0x7E00u : 0x7FC0u;
+      if (at[i].page == 0xFFFFFFFFu) continue;
+      *reinterpret_cast<uint32_t*>(codes_at(p, at[i], h, c)) = word;
+      if ((c & 3u) == 0) *reinterpret_cast<uint16_t*>(scale_at(p, at[i], h, c)) = static_cast<uint16_t>(sb);
     }
   }
 }
@@ -146,38 +150,47 @@ __device__ __forceinline__ uint4 decode8(uint32_t word, uint32_t scale) {
 }
 
 template <bool F16>
-__global__ void __launch_bounds__(kRowThreads) k_kv4_load(const Kv4Rows r, uint64_t total) {
+__global__ void __launch_bounds__(kRowThreads) k_kv4_load(const Kv4Rows r) {
   pdl_begin();
-  for (uint64_t x = static_cast<uint64_t>(blockIdx.x) * kRowThreads + threadIdx.x; x < total;
-       x += static_cast<uint64_t>(gridDim.x) * kRowThreads) {
-    const Row8 e = row8_of(r, x);
-    const Spot s = spot_of(r, e.b, e.t);
-    char* dst = const_cast<char*>(r.x[e.which]) + static_cast<int64_t>(e.b) * r.x_seq[e.which] +
-                static_cast<int64_t>(e.t) * r.x_token[e.which] + static_cast<int64_t>(e.h) * r.x_head[e.which] + e.c * 16;
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (s.page != 0xFFFFFFFFu) {
-      const uint32_t word = *reinterpret_cast<const uint32_t*>(codes_at(r.p[e.which], s, e.h, e.c));
-      u = decode8<F16>(word, *reinterpret_cast<const uint16_t*>(scale_at(r.p[e.which], s, e.h, e.c)));
+  const Rows o(r);
+  const Kv4View& p = r.p[o.which];
+  const uint32_t mine = threadIdx.x / o.width, chunks = r.dim / 8;
+  if (mine >= o.at_once) return;
+  for (uint32_t piece = threadIdx.x - mine * o.width; piece < o.pieces; piece += o.width) {
+    const uint32_t h = piece / chunks, c = piece - h * chunks;
+    char* dst = const_cast<char*>(r.x[o.which]) + static_cast<int64_t>(o.b) * r.x_seq[o.which] + static_cast<int64_t>(h) * r.x_head[o.which] + c * 16;
+    uint32_t word[kRowFly], scale[kRowFly];
+#pragma unroll
+    for (uint32_t i = 0; i < kRowFly; ++i) {
+      const Spot s = o.spot(r, o.first + i * o.at_once + mine);
+      word[i] = scale[i] = 0u;  // code 0 times 0
+      if (s.page != 0xFFFFFFFFu) {
+        word[i] = __ldg(reinterpret_cast<const uint32_t*>(codes_at(p, s, h, c)));
+        scale[i] = __ldg(reinterpret_cast<const uint16_t*>(scale_at(p, s, h, c)));
+      }
     }
-    *reinterpret_cast<uint4*>(dst) = u;
+#pragma unroll
+    for (uint32_t i = 0; i < kRowFly; ++i) {
+      const uint32_t t = o.first + i * o.at_once + mine;
+      if (t >= r.T) continue;
+      uint4 u = decode8<F16>(word[i], scale[i]);
+      if (F16 && scale[i] == 0u) u = make_uint4(0u, 0u, 0u, 0u);  // not -0
+      *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(t) * r.x_token[o.which]) = u;
+    }
   }
 }
 
-static uint64_t row_grid(uint64_t total, int device) {
-  const uint64_t want = (total + kRowThreads - 1) / kRowThreads, most = 16ull * sm_count(device);
-  return want < most ? want : most;
+static dim3 row_grid(const Kv4Rows& r) {
+  const uint32_t pieces = r.heads * (r.dim / 8), at_once = pieces < kRowThreads ? kRowThreads / pieces : 1;
+  return dim3((r.T + at_once * kRowFly - 1) / (at_once * kRowFly), r.n_seqs, 2);
 }
 
 int launch_kv4_store(const Kv4Rows& r, int device, cudaStream_t stream) {
-  const uint64_t total = 2ull * r.n_seqs * r.T * r.heads * (r.dim / 8);
-  return kv_launch("k_kv4_store", r.f16 ? k_kv4_store<true> : k_kv4_store<false>, dim3(static_cast<unsigned>(row_grid(total, device))),
-                   kRowThreads, 0, 1, stream, r, total);
+  return kv_launch("k_kv4_store", r.f16 ? k_kv4_store<true> : k_kv4_store<false>, row_grid(r), kRowThreads, 0, 1, stream, r);
 }
 
 int launch_kv4_load(const Kv4Rows& r, int device, cudaStream_t stream) {
-  const uint64_t total = 2ull * r.n_seqs * r.T * r.heads * (r.dim / 8);
-  return kv_launch("k_kv4_load", r.f16 ? k_kv4_load<true> : k_kv4_load<false>, dim3(static_cast<unsigned>(row_grid(total, device))),
-                   kRowThreads, 0, 1, stream, r, total);
+  return kv_launch("k_kv4_load", r.f16 ? k_kv4_load<true> : k_kv4_load<false>, row_grid(r), kRowThreads, 0, 1, stream, r);
 }
 
 // ---------------------------------------------------------------------------

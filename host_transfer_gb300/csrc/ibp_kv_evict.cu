@@ -3,7 +3,7 @@
 // A cluster takes a sequence, each CTA a stretch of its positions.  The weight at
 // which the budget is full is found digit by digit from the top (three digits of 11,
 // 11 and 10 bits of an order-preserving code): a histogram in shared memory, added up
-// over the cluster.  Positions with that very weight stay from the lowest on.  A second
+// in the cluster's first CTA.  Positions with that very weight stay from the lowest on.  A second
 // walk writes the kept positions and their weights at places known from the counts of
 // the warps before.  Nothing depends on the order in which threads run.  Bound by the
 // latency of the walks and the cluster's barriers.
@@ -24,18 +24,32 @@ __device__ __forceinline__ uint32_t weight_code(float w) {
 }
 
 struct EvictShared {
-  uint32_t hist[kEvBins];
-  uint32_t all[kEvBins];
+  uint32_t hist[kEvBins];     // of this CTA
+  uint32_t all[kEvBins];      // of the cluster, in its first CTA
   uint32_t digit, above;      // the bin found, and how many lie above it
+  uint32_t run[kEvWarps];
   uint32_t n_more[kEvWarps], n_equal[kEvWarps];
   uint32_t cta_more, cta_equal;
 };
+
+constexpr uint32_t kEvHold = 16;  // codes of a lane: sequences of up to 8192 positions a CTA are read once
 
 __device__ __forceinline__ uint32_t remote_u32(const uint32_t* p, uint32_t rank) {
   uint32_t addr = smem_u32(p), v;
   asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(rank));
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+
+__device__ __forceinline__ void remote_store(uint32_t* p, uint32_t rank, uint32_t x) {
+  uint32_t addr = smem_u32(p);
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ void remote_add(uint32_t* p, uint32_t rank, uint32_t x) {
+  uint32_t addr = smem_u32(p);
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(rank));
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
 
 template <uint32_t C>
@@ -76,6 +90,20 @@ __global__ void __launch_bounds__(kEvThreads) k_kv_evict(const EvictArgs a) {
   auto clip = [&](uint32_t x) { return x < len ? x : len; };
   const uint32_t from = clip((rank * kEvWarps + warp) * part), to = clip(from + part);
 
+  // Codes of 16 positions a lane at a time: kind() of 0 goes for positions outside the walk.
+  uint32_t held[kEvHold];
+  const bool once = part <= 32 * kEvHold;
+  auto read = [&](uint32_t at) {
+#pragma unroll
+    for (uint32_t u = 0; u < kEvHold; ++u) {
+      const uint32_t i = at + 32 * u + lane;
+      held[u] = i < to ? weight_code(__ldg(w + i)) : 0u;
+    }
+  };
+  if (once) read(from);
+  for (uint32_t i = tid; i < kEvBins; i += kEvThreads) sh.hist[i] = sh.all[i] = 0;
+  ev_sync<C>();
+
   // The code at which `want` are reached, and how many above it.
   uint32_t prefix = 0, left = want;
   if (want) {
@@ -83,58 +111,87 @@ __global__ void __launch_bounds__(kEvThreads) k_kv_evict(const EvictArgs a) {
     for (uint32_t d = 0; d < 3; ++d) {
       const uint32_t shift = d == 0 ? 21 : (d == 1 ? 10 : 0), bins = d == 2 ? 1024 : 2048;
       const uint32_t known = d == 0 ? 0u : 0xFFFFFFFFu << (d == 1 ? 21 : 10);
-      for (uint32_t i = tid; i < bins; i += kEvThreads) sh.hist[i] = 0;
+      for (uint32_t at = from; at < to; at += 32 * kEvHold) {
+        if (!once) read(at);
+#pragma unroll
+        for (uint32_t u = 0; u < kEvHold; ++u) {
+          const uint32_t i = at + 32 * u + lane;
+          if (i >= lo && i < hi && i < to && (held[u] & known) == prefix) atomicAdd(&sh.hist[(held[u] >> shift) & (bins - 1)], 1u);
+        }
+      }
       __syncthreads();
-      for (uint32_t i = from + lane; i < to; i += 32) {
-        if (i < lo || i >= hi) continue;
-        const uint32_t c = weight_code(__ldg(w + i));
-        if ((c & known) == prefix) atomicAdd(&sh.hist[(c >> shift) & (bins - 1)], 1u);
+      // counts come together in the first CTA; most bins are empty
+      for (uint32_t i = tid; i < bins; i += kEvThreads) {
+        const uint32_t n = sh.hist[i];
+        if (n) {
+          if (C == 1)
+            sh.all[i] = n;
+          else
+            remote_add(&sh.all[i], 0, n);
+          sh.hist[i] = 0;
+        }
       }
       ev_sync<C>();
-      for (uint32_t i = tid; i < bins; i += kEvThreads) {
-        uint32_t s = 0;
+      if (rank == 0) {
+        // from the highest bin down: a thread has bins / kEvThreads of them
+        const uint32_t per = bins / kEvThreads, top = bins - tid * per;
+        uint32_t n[4], sum = 0;
 #pragma unroll
-        for (uint32_t r = 0; r < C; ++r) s += C == 1 ? sh.hist[i] : remote_u32(&sh.hist[i], r);
-        sh.all[i] = s;
-      }
-      ev_sync<C>();  // the histogram may be cleared again
-      if (warp == 0) {
-        // from the highest bin down; a lane takes bins / 32 of them
-        const uint32_t per = bins / 32, top = bins - lane * per;
-        uint32_t s = 0;
-        for (uint32_t i = 1; i <= per; ++i) s += sh.all[top - i];
-        uint32_t run = s;
+        for (uint32_t i = 0; i < 4; ++i) {
+          n[i] = i < per ? sh.all[top - 1 - i] : 0u;
+          sum += n[i];
+        }
+        uint32_t run = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, run, o);
           if (static_cast<int>(lane) >= o) run += y;
         }
-        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, run >= left);
-        if (lane == static_cast<uint32_t>(__ffs(hit) - 1)) {
-          uint32_t above = run - s, i = 1;
-          while (above + sh.all[top - i] < left) above += sh.all[top - i++];
-          sh.digit = top - i;
-          sh.above = above;
+        if (lane == 31) sh.run[warp] = run;
+        __syncthreads();
+        for (uint32_t x = 0; x < warp; ++x) run += sh.run[x];
+        uint32_t above = run - sum;
+        if (above < left && left <= run) {  // one thread
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) {
+            if (above < left && left <= above + n[i]) {
+              for (uint32_t r = 0; r < C; ++r) {
+                if (C == 1) {
+                  sh.digit = top - 1 - i, sh.above = above;
+                } else {
+                  remote_store(&sh.digit, r, top - 1 - i);
+                  remote_store(&sh.above, r, above);
+                }
+              }
+            }
+            above += n[i];
+          }
         }
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+          if (i < per) sh.all[top - 1 - i] = 0;
       }
-      __syncthreads();
+      ev_sync<C>();
       prefix |= sh.digit << shift;
       left -= sh.above;
-      __syncthreads();
     }
   }
   // left: how many of the positions with the code `prefix` stay
-  auto kind = [&](uint32_t i) -> uint32_t {  // 2 stays, 1 has the last weight, 0 goes
+  auto kind = [&](uint32_t i, uint32_t c) -> uint32_t {  // 2 stays, 1 has the last weight, 0 goes
+    if (i >= to) return 0u;
     if (i < lo || i >= hi) return 2u;
     if (!want) return 0u;
-    const uint32_t c = weight_code(__ldg(w + i));
     return c > prefix ? 2u : (c == prefix ? 1u : 0u);
   };
   uint32_t more = 0, equal = 0;
-  for (uint32_t i0 = from; i0 < to; i0 += 32) {
-    const uint32_t k = i0 + lane < to ? kind(i0 + lane) : 0u;
-    more += __popc(__ballot_sync(0xFFFFFFFFu, k == 2u));
-    equal += __popc(__ballot_sync(0xFFFFFFFFu, k == 1u));
+  for (uint32_t at = from; at < to; at += 32 * kEvHold) {
+    if (!once) read(at);
+#pragma unroll
+    for (uint32_t u = 0; u < kEvHold; ++u) {
+      const uint32_t k = kind(at + 32 * u + lane, held[u]);
+      more += __popc(__ballot_sync(0xFFFFFFFFu, k == 2u));
+      equal += __popc(__ballot_sync(0xFFFFFFFFu, k == 1u));
+    }
   }
   if (lane == 0) sh.n_more[warp] = more, sh.n_equal[warp] = equal;
   __syncthreads();
@@ -148,24 +205,28 @@ __global__ void __launch_bounds__(kEvThreads) k_kv_evict(const EvictArgs a) {
   if constexpr (C > 1)
     for (uint32_t r = 0; r < rank; ++r) before_more += remote_u32(&sh.cta_more, r), before_equal += remote_u32(&sh.cta_equal, r);
   for (uint32_t x = 0; x < warp; ++x) before_more += sh.n_more[x], before_equal += sh.n_equal[x];
-  for (uint32_t i0 = from; i0 < to; i0 += 32) {
-    const uint32_t i = i0 + lane, k = i < to ? kind(i) : 0u;
-    const uint32_t eq = __ballot_sync(0xFFFFFFFFu, k == 1u), mo = __ballot_sync(0xFFFFFFFFu, k == 2u);
-    const uint32_t lt = lanemask_lt();
-    const uint32_t e = before_equal + __popc(eq & lt), m = before_more + __popc(mo & lt);
-    if (k == 2u || (k == 1u && e < left)) {
-      const uint32_t at = m + (e < left ? e : left);
-      path[at] = static_cast<int32_t>(i);
-      out[at] = __ldg(w + i);
+  const uint32_t lt = lanemask_lt();
+  for (uint32_t at = from; at < to; at += 32 * kEvHold) {
+    if (!once) read(at);
+#pragma unroll
+    for (uint32_t u = 0; u < kEvHold; ++u) {
+      const uint32_t i = at + 32 * u + lane, k = kind(i, held[u]);
+      const uint32_t eq = __ballot_sync(0xFFFFFFFFu, k == 1u), mo = __ballot_sync(0xFFFFFFFFu, k == 2u);
+      const uint32_t e = before_equal + __popc(eq & lt), m = before_more + __popc(mo & lt);
+      if (k == 2u || (k == 1u && e < left)) {
+        const uint32_t to_place = m + (e < left ? e : left);
+        path[to_place] = static_cast<int32_t>(i);
+        out[to_place] = __ldg(w + i);
+      }
+      before_equal += __popc(eq);
+      before_more += __popc(mo);
     }
-    before_equal += __popc(eq);
-    before_more += __popc(mo);
   }
   if (C > 1) ev_sync<C>();  // no CTA leaves while another reads its counts
 }
 
 int launch_kv_evict(const EvictArgs& a, cudaStream_t stream) {
-  if (a.width <= 2048) return kv_launch("k_kv_evict", k_kv_evict<1>, dim3(a.n_seqs), kEvThreads, 0, 1, stream, a);
+  if (a.width <= 8192) return kv_launch("k_kv_evict", k_kv_evict<1>, dim3(a.n_seqs), kEvThreads, 0, 1, stream, a);
   return kv_launch("k_kv_evict", k_kv_evict<8>, dim3(a.n_seqs * 8), kEvThreads, 0, 8, stream, a);
 }
 

@@ -15,7 +15,7 @@
 
 namespace ibp {
 
-constexpr int kVfThreads = 512;
+constexpr int kVfThreads = 256;
 constexpr uint32_t kVfWarps = kVfThreads / 32;
 constexpr float kVfUnit = 17592186044416.f;  // 2^44
 
@@ -37,13 +37,17 @@ struct Left {
   __device__ __forceinline__ float drawn(uint32_t i, float qi, uint32_t k) const {
     return q ? qi : (static_cast<int32_t>(i) == x[k] ? 1.f : 0.f);
   }
-  __device__ __forceinline__ float operator()(uint32_t i) const {
-    float v = probability(__ldg(p + i));
+  // of element i, whose probabilities are pi and qi
+  __device__ __forceinline__ float operator()(uint32_t i, float pi, float qi) const {
+    float v = probability(pi);
     if (depth == 0) return v;
-    const float qi = q ? probability(__ldg(q + i)) : 0.f;
+    qi = probability(qi);
     v = fmaxf(__fsub_rn(v, drawn(i, qi, 0)), 0.f);
     for (uint32_t k = 1; k < depth; ++k) v = fmaxf(__fsub_rn(__fmul_rn(v, scale[k - 1]), drawn(i, qi, k)), 0.f);
     return v;
+  }
+  __device__ __forceinline__ float operator()(uint32_t i) const {
+    return (*this)(i, __ldg(p + i), q && depth ? __ldg(q + i) : 0.f);
   }
 };
 
@@ -72,12 +76,35 @@ __device__ __forceinline__ void vf_sync() {
 }
 
 // Sums of the weights, in slot `buf`: every warp's, the CTA's, and the row's (returned).
-template <uint32_t C>
+// VEC: rows of whole aligned pieces of four.
+template <uint32_t C, bool VEC>
 __device__ __forceinline__ long long vf_sum(VerifyShared& sh, uint32_t buf, const Left& f, uint32_t from, uint32_t to) {
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   long long s = 0;
-#pragma unroll 4
-  for (uint32_t i = from + lane; i < to; i += 32) s += whole(f(i));
+  if (VEC) {
+    constexpr uint32_t kFly = 4;  // 16-byte reads of each row under way
+    const bool two = f.q && f.depth;
+    for (uint32_t i0 = from + 4 * lane; i0 < to; i0 += 128 * kFly) {
+      float4 x[kFly], y[kFly];
+#pragma unroll
+      for (uint32_t u = 0; u < kFly; ++u) {
+        const uint32_t i = i0 + 128 * u;
+        x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < to) {
+          x[u] = __ldg(reinterpret_cast<const float4*>(f.p + i));
+          if (two) y[u] = __ldg(reinterpret_cast<const float4*>(f.q + i));
+        }
+      }
+#pragma unroll
+      for (uint32_t u = 0; u < kFly; ++u) {
+        const uint32_t i = i0 + 128 * u;
+        if (i < to) s += (whole(f(i, x[u].x, y[u].x)) + whole(f(i + 1, x[u].y, y[u].y))) + (whole(f(i + 2, x[u].z, y[u].z)) + whole(f(i + 3, x[u].w, y[u].w)));
+      }
+    }
+  } else {
+#pragma unroll 8
+    for (uint32_t i = from + lane; i < to; i += 32) s += whole(f(i));
+  }
   s = warp_total(s);
   if (lane == 0) sh.warp[buf][warp] = s;
   __syncthreads();
@@ -93,8 +120,8 @@ __device__ __forceinline__ long long vf_sum(VerifyShared& sh, uint32_t buf, cons
   return total;
 }
 
-template <uint32_t C>
-__global__ void __launch_bounds__(kVfThreads) k_kv_verify(const VerifyArgs a) {
+template <uint32_t C, bool VEC>
+__global__ void __launch_bounds__(kVfThreads, 4) k_kv_verify(const VerifyArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ VerifyShared sh;
   pdl_begin();
@@ -130,7 +157,8 @@ __global__ void __launch_bounds__(kVfThreads) k_kv_verify(const VerifyArgs a) {
   __syncthreads();
 
   // This warp's part of a row.
-  const uint32_t part = (V + C * kVfWarps * 32 - 1) / (C * kVfWarps * 32) * 32;
+  constexpr uint32_t kPiece = VEC ? 128 : 32;
+  const uint32_t part = (V + C * kVfWarps * kPiece - 1) / (C * kVfWarps * kPiece) * kPiece;
   auto clip = [&](uint32_t x) { return x < V ? x : V; };
   const uint32_t from = clip((rank * kVfWarps + warp) * part), to = clip(from + part);
 
@@ -160,7 +188,7 @@ __global__ void __launch_bounds__(kVfThreads) k_kv_verify(const VerifyArgs a) {
       if (tid == 0) gone[f.depth] = x;
       __syncthreads();
       ++f.depth;
-      const long long z = vf_sum<C>(sh, keep ^ 1u, f, from, to);
+      const long long z = vf_sum<C, VEC>(sh, keep ^ 1u, f, from, to);
       if (z > 0) {
         keep ^= 1u;
         total = z;
@@ -171,7 +199,7 @@ __global__ void __launch_bounds__(kVfThreads) k_kv_verify(const VerifyArgs a) {
       }
     }
   }
-  if (total < 0) total = vf_sum<C>(sh, keep, f, from, to);
+  if (total < 0) total = vf_sum<C, VEC>(sh, keep, f, from, to);
   if (rank == 0) {
     for (uint32_t t = count + tid; t < T; t += kVfThreads) a.path[static_cast<uint64_t>(b) * T + t] = -1;
     if (tid == 0) a.n_accept[b] = static_cast<int32_t>(count);
@@ -231,9 +259,11 @@ int launch_kv_verify(const VerifyArgs& a, cudaStream_t stream) {
   auto go = [&](auto kern, uint32_t c) {
     return kv_launch("k_kv_verify", kern, dim3(a.n_seqs * c), kVfThreads, smem, c, stream, a);
   };
-  if (a.vocab <= 4096) return go(k_kv_verify<1>, 1);
-  if (a.vocab <= 16384) return go(k_kv_verify<4>, 4);
-  return go(k_kv_verify<8>, 8);
+  const uint64_t strides = static_cast<uint64_t>(a.p_seq) | static_cast<uint64_t>(a.p_row) | (a.q ? static_cast<uint64_t>(a.q_seq) | static_cast<uint64_t>(a.q_row) : 0);
+  const bool vec = a.vocab % 4 == 0 && strides % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.p) | reinterpret_cast<uintptr_t>(a.q)) & 15u) == 0;
+  if (a.vocab <= 4096) return vec ? go(k_kv_verify<1, true>, 1) : go(k_kv_verify<1, false>, 1);
+  if (a.vocab <= 16384) return vec ? go(k_kv_verify<4, true>, 4) : go(k_kv_verify<4, false>, 4);
+  return vec ? go(k_kv_verify<8, true>, 8) : go(k_kv_verify<8, false>, 8);
 }
 
 }  // namespace ibp
