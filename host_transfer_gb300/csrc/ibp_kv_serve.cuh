@@ -36,6 +36,8 @@ struct WeighArgs {
 };
 
 int launch_kv_weigh(const WeighArgs& x, int device, cudaStream_t stream);
+// Many rows, on the tensor cores (ibp_kv_weigh_tc.cu): dim <= 128.
+int launch_kv_weigh_tc(const WeighArgs& x, int device, cudaStream_t stream);
 
 struct EvictArgs {
   const float* w;

@@ -15,6 +15,7 @@
 namespace ibp {
 
 constexpr uint32_t kWgWarps = 8;
+constexpr uint64_t kWgMany = 64;  // rows a kv head from which the tensor cores take over
 
 // Keys of 16 tokens as operands A: [step][register].
 template <uint32_t DP, bool FOUR, bool F16>
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(kWgWarps * 32) k_kv_weigh(const WeighArgs x, u
 
 int launch_kv_weigh(const WeighArgs& x, int device, cudaStream_t stream) {
   const AttendArgs& a = x.a;
+  if (a.dim <= 128 && static_cast<uint64_t>(a.T) * a.group >= kWgMany) return launch_kv_weigh_tc(x, device, stream);
   uint32_t head_warps = 1;
   while (head_warps < kWgWarps && head_warps < a.kv_heads) head_warps *= 2;
   const uint32_t dp = a.dim <= 64 ? 64 : (a.dim <= 128 ? 128 : 256);

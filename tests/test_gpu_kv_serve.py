@@ -506,6 +506,9 @@ def check_weigh(got, want, top, lse, rows, was, decay):
     ([1], 1, 1, 1, 16, 32, False), ([70, 0, 33], 1, 2, 4, 16, 64, False), ([300, 17], 1, 8, 1, 7, 128, False),
     ([100, 64, 80], 5, 3, 2, 24, 96, True), ([90, 41], 41, 1, 3, 64, 160, True), ([60], 7, 12, 2, 16, 256, False),
     ([130, 200], 33, 9, 1, 1, 128, True), ([500], 2, 1, 9, 16, 192, False),
+    # the tensor cores: fewer heads than CTAs, more, a head's blocks shared out
+    ([300, 90], 70, 3, 1, 16, 64, False), ([700], 40, 1, 8, 24, 128, True), ([120, 300], 17, 10, 4, 7, 96, True),
+    ([0, 600], 64, 8, 1, 64, 128, False), ([260], 130, 2, 2, 16, 32, True),
 ])
 def test_weigh(lens, T, hk, G, page, D, mask, dt, four, inplace):
     c = Cache(lens, T, hk, G, page, D, dt, seed=D + T, mask=mask)
@@ -685,15 +688,19 @@ class Step:
         p, tokens, u, q, parents = draft(5, 6, 20000, True, seed)
         self.v = [dev(p, torch.float32), dev(tokens), dev(u, torch.float32), dev(q, torch.float32), dev(parents)]
         self.w = torch.rand((3, 9000), generator=g, device="cuda")
+        self.w2 = torch.rand((6, 500), generator=g, device="cuda")
 
     def __call__(self, stream=None, **kw):
+        """(a call of every kernel)"""
         c, o = self.c, []
         kv.ibp_kv4_store(*self.kv, c.k, c.v, c.table, c.lens, stream=stream, **kw)
         o += kv.ibp_kv4_load(c.k, c.v, c.table, c.lens, 900, n_load=c.lens, stream=stream, **kw)
         out, lse = kv.ibp_kv4_attention(c.q, c.k, c.v, c.table, c.lens, stream=stream, **kw)
         o += [out, lse]
         x = self.wide
-        o += kv.ibp_kv4_attention(x.q, x.k, x.v, x.table, x.lens, stream=stream, **kw)
+        wide, lse_wide = kv.ibp_kv4_attention(x.q, x.k, x.v, x.table, x.lens, stream=stream, **kw)
+        o += [wide, lse_wide]
+        o += [kv.ibp_kv_weigh(x.q, x.k, x.table, x.lens, lse_wide, self.w2, stream=stream, **kw)]
         o += kv.ibp_kv_verify(*self.v, stream=stream, **kw)
         w = kv.ibp_kv_weigh(c.q, c.k, c.table, c.lens, lse, self.w, decay=0.5, stream=stream, **kw)
         o += [w, *kv.ibp_kv_evict(w, c.lens, 64, keep_first=1, keep_last=4, stream=stream, **kw)]
@@ -872,3 +879,19 @@ def test_waits_that_run_out(T):
         kv.ibp_kv_set_wait_limit(before)
     err(ibp.IBP_ETIMEOUT)
     assert same(c.attend(), want)
+
+
+def test_weighing_waits_that_run_out():
+    c = Cache([300, 310, 333], 40, 3, 2, 16, 64, seed=5)
+    _, lse = c.attend()
+    w = torch.ones((3, 400), device="cuda")
+    want = kv.ibp_kv_weigh(c.q, c.k, c.table, c.lens, lse, w)
+    torch.cuda.synchronize()
+    before = kv.ibp_kv_set_wait_limit(0)
+    try:
+        kv.ibp_kv_weigh(c.q, c.k, c.table, c.lens, lse, w)
+        torch.cuda.synchronize()
+    finally:
+        kv.ibp_kv_set_wait_limit(before)
+    err(ibp.IBP_ETIMEOUT)
+    assert torch.equal(kv.ibp_kv_weigh(c.q, c.k, c.table, c.lens, lse, w), want)
