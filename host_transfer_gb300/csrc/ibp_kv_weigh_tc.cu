@@ -22,7 +22,7 @@ namespace ibp {
 
 constexpr uint32_t kWtTokens = 256;   // of a CTA
 constexpr uint32_t kWtCluster = 8;
-constexpr uint32_t kWtStages = 3;     // blocks of queries in flight
+constexpr uint32_t kWtStages = 4;     // blocks of queries in flight
 constexpr uint32_t kWtThreads = 256 + 32 + 128;
 
 struct WtArgs {
@@ -37,16 +37,49 @@ struct WtShape {
   static constexpr uint32_t kPanel = 128 * 128;
   static constexpr uint32_t kTile = kHalves * kPanel;  // 128 keys or queries
   static constexpr uint32_t kBytes = (2 + kWtStages) * kTile;
-  static constexpr uint32_t kSmem = kBytes + 1024 + 4096;
+  static constexpr uint32_t kSmem = kBytes + 1024 + 20480;
 };
 
 struct WtShared {
   uint64_t k_full, k_empty, q_full[kWtStages], q_empty[kWtStages], s_full[2][2], s_empty[2][2], done;
   alignas(16) float back[kWtStages][128];  // -lse log2 e of a block's rows; -infinity: nothing to add
   uint32_t plain[kWtStages][4]; // every one of 32 rows has something to add
+  alignas(16) uint32_t seen[kWtStages][2][4][128];  // where some row may not see a tile: bits of 32 tokens, by row
   float sums[kWtTokens];
   uint32_t tmem, stop;
 };
+
+constexpr int64_t kWtNone = INT64_MIN;
+
+// 32 rows of a warp, lane i's at base + off, on their way into rows first_row on of a
+// swizzled tile: half a warp copies a row of 128 dimensions at once.
+template <uint32_t DP>
+__device__ __forceinline__ void wt_rows(uint32_t tile, uint32_t first_row, const char* base, int64_t off, uint32_t dim, bool vec) {
+  constexpr uint32_t kChunks = DP / 8, kPer = 32 / kChunks;
+  const uint32_t lane = threadIdx.x & 31u, c = lane % kChunks;
+  const uint32_t dst = tile + (c / 8) * 128 * 128;
+  if (vec) {
+#pragma unroll
+    for (uint32_t j = 0; j < kChunks; ++j) {
+      const int64_t o = __shfl_sync(0xFFFFFFFFu, off, j * kPer + lane / kChunks);
+      const uint32_t r = first_row + j * kPer + lane / kChunks;
+      const bool on = o != kWtNone && c * 8 < dim;
+      cp16(dst + r * 128 + (((c & 7u) ^ (r & 7u)) << 4), on ? base + o + c * 16 : base, on);
+    }
+  } else {
+#pragma unroll 1
+    for (uint32_t j = 0; j < kChunks; ++j) {
+      const int64_t o = __shfl_sync(0xFFFFFFFFu, off, j * kPer + lane / kChunks);
+      const uint32_t r = first_row + j * kPer + lane / kChunks;
+      const bool on = o != kWtNone && c * 8 < dim;
+      const char* p = on ? base + o + c * 16 : base;
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + r * 128 + (((c & 7u) ^ (r & 7u)) << 4) + 4 * e), "l"(p + 4 * e), "r"(on ? 4u : 0u)
+                     : "memory");
+    }
+  }
+}
 
 template <uint32_t DP, bool FOUR, bool F16>
 __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_constant__ WtArgs w) {
@@ -57,7 +90,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
   unsigned char* sm = raw_sm + ((1024 - (tc::s32(raw_sm) & 1023u)) & 1023u);
   const uint32_t base = tc::s32(sm);
   WtShared& sh = *reinterpret_cast<WtShared*>(sm + S::kBytes);
-  static_assert(sizeof(WtShared) <= 4096, "shared");
+  static_assert(sizeof(WtShared) <= 20480, "shared");
   const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
   const uint32_t rank = blockIdx.x % kWtCluster, first = blockIdx.x / kWtCluster * kWtTokens, b = blockIdx.y;
   pdl_begin();
@@ -109,6 +142,9 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
     bool ok = true;
     uint32_t fill = 0, heads = 0;
     const quad::Magic<F16> magic;
+    const bool partly = static_cast<int32_t>(first + kWtTokens) > ctx;
+    TcSeg seg = {};
+    seg.len = all, seg.ctx = ctx;
     for (uint32_t h = head0; ok && mine && h < a.kv_heads; h += w.heads_at_once, ++heads) {
       ok = tc::bar_wait(tc::s32(&sh.k_empty), (heads & 1u) ^ 1u, stop, w.limit);
       ok = __all_sync(0xFFFFFFFFu, ok);
@@ -128,8 +164,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
             page = slot = 0;
           }
         }
-        unsigned char* dst = sm + m * S::kTile + r * 128;
         if constexpr (FOUR) {
+          unsigned char* dst = sm + m * S::kTile + r * 128;
           const char* c = x.k4.codes + static_cast<int64_t>(page) * x.k4.page_stride + static_cast<int64_t>(h) * x.k4.head_stride +
                           static_cast<int64_t>(slot) * x.k4.token_stride;
           const char* sc = x.k4.scales + static_cast<int64_t>(page) * x.k4.s_page + static_cast<int64_t>(h) * x.k4.s_head +
@@ -149,68 +185,65 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
 #pragma unroll
             for (uint32_t e = 0; e < 4; ++e) {
               const uint32_t i = g * 4 + e;
+              const uint32_t y0 = quad::decode<F16, 0>(u[e], p, magic), y1 = quad::decode<F16, 1>(u[e], p, magic);
+              const uint32_t y2 = quad::decode<F16, 2>(u[e], p, magic), y3 = quad::decode<F16, 3>(u[e], p, magic);
               *reinterpret_cast<uint4*>(dst + (i / 8) * S::kPanel + (((i & 7u) ^ (r & 7u)) << 4)) =
-                  make_uint4(quad::decode<F16, 0>(u[e], p, magic), quad::decode<F16, 1>(u[e], p, magic),
-                             quad::decode<F16, 2>(u[e], p, magic), quad::decode<F16, 3>(u[e], p, magic));
+                  make_uint4(__byte_perm(y0, y1, 0x5410), __byte_perm(y2, y3, 0x5410), __byte_perm(y0, y1, 0x7632), __byte_perm(y2, y3, 0x7632));
             }
           }
         } else {
-          const char* c = a.k.data + static_cast<int64_t>(page) * a.k.page_stride + static_cast<int64_t>(h) * a.k.head_stride +
-                          static_cast<int64_t>(slot) * a.k.token_stride;
-          uint4 u[DP / 8];
-#pragma unroll
-          for (uint32_t i = 0; i < DP / 8; ++i) u[i] = there && i * 8 < a.dim ? __ldg(reinterpret_cast<const uint4*>(c + i * 16)) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (uint32_t i = 0; i < DP / 8; ++i) *reinterpret_cast<uint4*>(dst + (i / 8) * S::kPanel + (((i & 7u) ^ (r & 7u)) << 4)) = u[i];
+          const int64_t off = there ? static_cast<int64_t>(page) * a.k.page_stride + static_cast<int64_t>(slot) * a.k.token_stride : kWtNone;
+          wt_rows<DP>(k_sm + m * S::kTile, r & 96u, a.k.data + static_cast<int64_t>(h) * a.k.head_stride, off, a.dim, true);
         }
       }
+      cp_commit();
+      cp_wait<0>();
       tc::fence_async();
       tc::bar_arrive(tc::s32(&sh.k_full));
-      // Blocks of queries: the next one is read while the ring has no room for this one.
-      uint4 u[DP / 8];
-      float back;
-      auto read = [&](uint32_t j) {
-        const uint32_t row = (part + j * parts) * 128 + r;
-        const bool on = j < mine && row < rows;
-        const uint32_t t = on ? row / a.group : 0, head = on ? h * a.group + row - t * a.group : 0;
-        const char* q = a.q + static_cast<int64_t>(b) * a.q_seq + static_cast<int64_t>(t) * a.q_token + static_cast<int64_t>(head) * a.q_head;
-#pragma unroll
-        for (uint32_t i = 0; i < DP / 8; ++i) {
-          u[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (on && i * 8 < a.dim) {
-            if (x.q16) {
-              u[i] = __ldg(reinterpret_cast<const uint4*>(q + i * 16));
-            } else {
-              const uint32_t* v = reinterpret_cast<const uint32_t*>(q + i * 16);
-              u[i] = make_uint4(__ldg(v), __ldg(v + 1), __ldg(v + 2), __ldg(v + 3));
-            }
-          }
-        }
-        const float lse = on ? __ldg(x.lse + (static_cast<uint64_t>(b) * a.T + t) * a.kv_heads * a.group + head) : -INFINITY;
-        back = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+      // Blocks of queries, up to kFly on their way; one is handed on when it has landed.
+      constexpr uint32_t kFly = kWtStages - 1;
+      auto hand_on = [&](uint32_t nth) {
+        tc::fence_async();
+        tc::bar_arrive(tc::s32(&sh.q_full[nth % kWtStages]));
       };
-      read(0);
+      auto lse_of = [&](uint32_t j, uint32_t* t, uint32_t* head, bool* on) {
+        const uint32_t row = (part + j * parts) * 128 + r;
+        *on = j < mine && row < rows;
+        *t = *on ? row / a.group : 0, *head = *on ? h * a.group + row - *t * a.group : 0;
+        return *on ? __ldg(x.lse + (static_cast<uint64_t>(b) * a.T + *t) * a.kv_heads * a.group + *head) : -INFINITY;
+      };
+      uint32_t t, head;
+      bool on;
+      float lse = lse_of(0, &t, &head, &on);
 #pragma unroll 1
       for (uint32_t j = 0; j < mine; ++j, ++fill) {
         const uint32_t st = fill % kWtStages;
         ok = tc::bar_wait(tc::s32(&sh.q_empty[st]), (fill / kWtStages & 1u) ^ 1u, stop, w.limit);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        unsigned char* dst = sm + (2 + st) * S::kTile + r * 128;
-#pragma unroll
-        for (uint32_t i = 0; i < DP / 8; ++i) {
-          uint4 v = u[i];
-          if (FOUR)  // dimensions as the decoder has them
-            v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-          *reinterpret_cast<uint4*>(dst + (i / 8) * S::kPanel + (((i & 7u) ^ (r & 7u)) << 4)) = v;
-        }
+        wt_rows<DP>(q_sm + st * S::kTile, r & 96u, a.q + static_cast<int64_t>(b) * a.q_seq,
+                    on ? static_cast<int64_t>(t) * a.q_token + static_cast<int64_t>(head) * a.q_head : kWtNone, a.dim, x.q16);
+        cp_commit();
+        const float back = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
         sh.back[st][r] = back;
         const bool plain = __all_sync(0xFFFFFFFFu, back != -INFINITY);
         if (lane == 0) sh.plain[st][r / 32] = plain;
-        tc::fence_async();
-        tc::bar_arrive(tc::s32(&sh.q_full[st]));
-        read(j + 1);
+        if (partly) {
+          const uint32_t* words = a.mask ? a.mask + (static_cast<uint64_t>(b) * a.T + t) * a.mask_words : nullptr;
+#pragma unroll 1
+          for (uint32_t e = 0; e < 8; ++e)
+            sh.seen[st][e >> 2][e & 3u][r] = on && back != -INFINITY ? seen_bits(a, seg, words, t, static_cast<int32_t>(first + 32 * e)) : 0u;
+        }
+        lse = lse_of(j + 1, &t, &head, &on);
+        if (j >= kFly - 1) {
+          cp_wait<kFly - 1>();
+          hand_on(fill - (kFly - 1));
+        }
       }
+      // the last ones (all of them have been asked for unless a wait gave up)
+      cp_wait<0>();
+      if (ok)
+        for (uint32_t n = mine < kFly ? mine : kFly - 1; n > 0; --n) hand_on(fill - n);
     }
   } else if (warp == 8) {
     // ---- MMA
@@ -261,7 +294,6 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
     // ---- sums: thread of tile m, token r of it
     const uint32_t m = warp / 4, r = tid & 127u;
     const uint32_t lanes = (warp & 3u) << 21;
-    const int32_t pos = static_cast<int32_t>(first + m * 128 + r), at = pos - ctx;
     const bool open = static_cast<int32_t>(first + m * 128 + 128) <= ctx;  // every row sees the whole tile
     const float scale = a.scale_log2;
     float total = 0.f;
@@ -276,7 +308,6 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
         if (!ok) break;
         tc::fence_after();
         const uint32_t col = tmem + lanes + (slot * 2 + m) * 128;
-        const uint32_t row0 = (part + j * parts) * 128;
         float y[2][32];
         tc::ld32(y[0], col);
         float block[4] = {0.f, 0.f, 0.f, 0.f};
@@ -299,17 +330,17 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
               block[2] += tc::ex2(__fmaf_rn(v[i + 2], scale, bk.z));
               block[3] += tc::ex2(__fmaf_rn(v[i + 3], scale, bk.w));
             }
-          } else {
-            uint32_t t = (row0 + 32 * c) / a.group, g = row0 + 32 * c - t * a.group;
+          } else if (open) {
 #pragma unroll
             for (uint32_t i = 0; i < 32; ++i) {
-              const float bk = sh.back[st][32 * c + i];
-              bool on = bk != -INFINITY && pos < all;
-              if (on && at >= 0)
-                on = a.mask ? (__ldg(a.mask + (static_cast<uint64_t>(b) * a.T + t) * a.mask_words + (at >> 5)) >> (at & 31)) & 1u
-                            : static_cast<uint32_t>(at) <= t;
-              if (on) block[i & 3u] += tc::ex2(__fmaf_rn(v[i], scale, bk));
-              if (++g == a.group) g = 0, ++t;
+              const float bk = sh.back[st][32 * c + i], p = tc::ex2(__fmaf_rn(v[i], scale, bk));
+              block[i & 3u] += bk == -INFINITY ? 0.f : p;
+            }
+          } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) {
+              const float p = tc::ex2(__fmaf_rn(v[i], scale, sh.back[st][32 * c + i]));
+              block[i & 3u] += sh.seen[st][m][warp & 3u][32 * c + i] >> lane & 1u ? p : 0.f;
             }
           }
         }
