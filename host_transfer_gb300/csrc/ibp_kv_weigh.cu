@@ -14,100 +14,108 @@
 
 namespace ibp {
 
-constexpr uint32_t kWgWarps = 8;
+constexpr uint32_t kWgWarps = 4;
+constexpr uint32_t kWgTiles = 4;  // of a CTA's warps
 constexpr uint64_t kWgMany = 64;  // rows a kv head from which the tensor cores take over
 
-// Keys of 16 tokens as operands A: [step][register].
-template <uint32_t DP, bool FOUR, bool F16>
-struct WeighKeys {
-  uint32_t f[DP / 16][4];
+// A warp's stage: the keys of 16 MT tokens of a head as the cache has them, the scales
+// of codes, and which of the tokens there are.
+template <uint32_t DP, uint32_t MT, bool FOUR>
+struct WeighStage {
+  static constexpr uint32_t kTokens = 16 * MT;
+  static constexpr uint32_t kRow = FOUR ? DP / 2 : DP * 2;       // bytes of a key
+  static constexpr uint32_t kScale = FOUR ? DP / 16 : 0;         // and of its scales
+  static constexpr uint32_t kKeys = kTokens * kRow;
+  static constexpr uint32_t kBytes = kKeys + kTokens * kScale + 16;
+  static constexpr uint32_t kStages = DP == 256 && !FOUR ? 3 : 4;
 
-  // key rows g and g + 8 of this lane's DP / 4 dimensions
-  __device__ __forceinline__ void load(const WeighArgs& x, const int64_t (&page)[2], const uint32_t (&slot)[2], uint32_t h, uint32_t t) {
-    const AttendArgs& a = x.a;
-    const uint32_t d0 = t * (DP / 4);
-    if constexpr (FOUR) {
-      uint32_t w[2][DP / 32], s[2][DP == 256 ? 2 : 1];
-#pragma unroll
-      for (uint32_t i = 0; i < 2; ++i) {
-        const bool on = page[i] >= 0;
-        const int64_t pg = on ? page[i] : 0;
-        const char* c = x.k4.codes + pg * x.k4.page_stride + static_cast<int64_t>(h) * x.k4.head_stride +
-                        static_cast<int64_t>(slot[i]) * x.k4.token_stride + d0 / 2;
-        const char* sc = x.k4.scales + pg * x.k4.s_page + static_cast<int64_t>(h) * x.k4.s_head +
-                         static_cast<int64_t>(slot[i]) * x.k4.s_token + d0 / kQuadGroup * 2;
-        if constexpr (DP == 256) {
-#pragma unroll
-          for (uint32_t j = 0; j < 2; ++j) {
-            const bool in = on && d0 + 32 * j < a.dim;
-            const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(c + 16 * j)) : make_uint4(0u, 0u, 0u, 0u);
-            w[i][4 * j] = u.x, w[i][4 * j + 1] = u.y, w[i][4 * j + 2] = u.z, w[i][4 * j + 3] = u.w;
-            s[i][j] = in ? __ldg(reinterpret_cast<const uint16_t*>(sc + 2 * j)) : 0u;
-          }
-        } else {
-          const bool in = on && d0 < a.dim;
-          if constexpr (DP == 128) {
-            const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(c)) : make_uint4(0u, 0u, 0u, 0u);
-            w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
-          } else {
-            const uint2 u = in ? __ldg(reinterpret_cast<const uint2*>(c)) : make_uint2(0u, 0u);
-            w[i][0] = u.x, w[i][1] = u.y;
-          }
-          s[i][0] = in ? __ldg(reinterpret_cast<const uint16_t*>(sc)) : 0u;
-        }
-      }
-      const quad::Magic<F16> m;
-#pragma unroll
-      for (uint32_t j = 0; j < DP / 32; ++j) {
-        const uint32_t gi = DP == 256 ? j / 4 : 0;
-        const quad::Pair<F16> p0(s[0][gi] * 0x10001u), p1(s[1][gi] * 0x10001u);
-        f[2 * j][0] = quad::decode<F16, 0>(w[0][j], p0, m), f[2 * j][1] = quad::decode<F16, 0>(w[1][j], p1, m);
-        f[2 * j][2] = quad::decode<F16, 1>(w[0][j], p0, m), f[2 * j][3] = quad::decode<F16, 1>(w[1][j], p1, m);
-        f[2 * j + 1][0] = quad::decode<F16, 2>(w[0][j], p0, m), f[2 * j + 1][1] = quad::decode<F16, 2>(w[1][j], p1, m);
-        f[2 * j + 1][2] = quad::decode<F16, 3>(w[0][j], p0, m), f[2 * j + 1][3] = quad::decode<F16, 3>(w[1][j], p1, m);
-      }
-    } else {
-#pragma unroll
-      for (uint32_t i = 0; i < 2; ++i) {
-        const bool on = page[i] >= 0;
-        const char* c = a.k.data + (on ? page[i] : 0) * a.k.page_stride + static_cast<int64_t>(h) * a.k.head_stride +
-                        static_cast<int64_t>(slot[i]) * a.k.token_stride + d0 * 2;
-#pragma unroll
-        for (uint32_t j = 0; j < DP / 32; ++j) {
-          const uint4 u = on && d0 + 8 * j < a.dim ? __ldg(reinterpret_cast<const uint4*>(c + 16 * j)) : make_uint4(0u, 0u, 0u, 0u);
-          f[2 * j][i] = u.x, f[2 * j][2 + i] = u.y, f[2 * j + 1][i] = u.z, f[2 * j + 1][2 + i] = u.w;
-        }
-      }
+  // Place of 16 bytes of a token's key, so that eight lanes on two rows meet in no bank.
+  static __device__ __forceinline__ uint32_t at(uint32_t tok, uint32_t c) {
+    if (FOUR) {
+      const uint32_t piece = tok * (DP / 32) + c, line = piece >> 3;
+      return (piece ^ (DP == 256 ? line & 7u : 0u)) * 16;
     }
+    const uint32_t turn = DP == 64 ? tok & 1u : (c >> 3) ^ (tok & 1u) << (DP == 128 ? 1 : 2);
+    return tok * kRow + ((c ^ (turn & 7u)) * 16);
   }
 };
 
-// Eight dimensions of a query as the keys' order has them: registers of two steps.
-template <bool FOUR>
-__device__ __forceinline__ void weigh_query(uint32_t (&r)[4], const char* q, bool q16) {
-  uint32_t w[4];
-  if (q16) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(q));
-    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint16_t* h = reinterpret_cast<const uint16_t*>(q) + 2 * i;
-      w[i] = __ldg(h) | static_cast<uint32_t>(__ldg(h + 1)) << 16;
-    }
-  }
-  if (FOUR) {  // elements (0, 4), (1, 5), (2, 6), (3, 7)
-    r[0] = __byte_perm(w[0], w[2], 0x5410), r[1] = __byte_perm(w[0], w[2], 0x7632);
-    r[2] = __byte_perm(w[1], w[3], 0x5410), r[3] = __byte_perm(w[1], w[3], 0x7632);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = w[i];
+// Operands A of two steps (16 dimensions each) from a lane's eight of tokens g and g + 8.
+template <bool FOUR, bool F16>
+__device__ __forceinline__ void weigh_operands(const uint4& x, const uint4& y, uint32_t j, const quad::Pair<F16>& p0, const quad::Pair<F16>& p1,
+                                               const quad::Magic<F16>& m, uint32_t (&lo)[4], uint32_t (&hi)[4]) {
+  if constexpr (FOUR) {  // word j of 32 codes
+    const uint32_t u = j == 0 ? x.x : (j == 1 ? x.y : (j == 2 ? x.z : x.w)), v = j == 0 ? y.x : (j == 1 ? y.y : (j == 2 ? y.z : y.w));
+    lo[0] = quad::decode<F16, 0>(u, p0, m), lo[1] = quad::decode<F16, 0>(v, p1, m);
+    lo[2] = quad::decode<F16, 1>(u, p0, m), lo[3] = quad::decode<F16, 1>(v, p1, m);
+    hi[0] = quad::decode<F16, 2>(u, p0, m), hi[1] = quad::decode<F16, 2>(v, p1, m);
+    hi[2] = quad::decode<F16, 3>(u, p0, m), hi[3] = quad::decode<F16, 3>(v, p1, m);
+  } else {  // eight values
+    lo[0] = x.x, lo[1] = y.x, lo[2] = x.y, lo[3] = y.y;
+    hi[0] = x.z, hi[1] = y.z, hi[2] = x.w, hi[3] = y.w;
   }
 }
 
-template <uint32_t DP, uint32_t MT, bool FOUR, bool F16>
-__global__ void __launch_bounds__(kWgWarps * 32) k_kv_weigh(const WeighArgs x, uint32_t head_warps) {
+// Eight rows of queries of a head and their logarithms of sums.
+template <uint32_t DP>
+struct WeighRows {
+  uint32_t q[DP / 32][4];
+  float lse[2];  // of rows 2t and 2t + 1; -infinity where there is none
+};
+
+// Where a lane's part of a block's queries and its rows' logarithms are in a head.
+struct WeighAt {
+  const char* q;
+  const float* lse[2];  // nullptr: no such row
+};
+
+__device__ __forceinline__ WeighAt weigh_at(const WeighArgs& x, uint32_t b, uint32_t h, uint32_t r0, uint32_t rows, uint32_t d) {
+  const AttendArgs& a = x.a;
+  const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
+  const uint32_t rq = r0 + g < rows ? r0 + g : rows - 1, tq = rq / a.group;  // a row past the end is not counted
+  WeighAt at;
+  at.q = a.q + static_cast<int64_t>(b) * a.q_seq + static_cast<int64_t>(tq) * a.q_token +
+         static_cast<int64_t>(h * a.group + rq - tq * a.group) * a.q_head + d * 2;
+#pragma unroll
+  for (uint32_t e = 0; e < 2; ++e) {
+    const uint32_t r = r0 + 2 * t + e, tr = r / a.group;
+    at.lse[e] = r < rows ? x.lse + (static_cast<uint64_t>(b) * a.T + tr) * a.kv_heads * a.group + h * a.group + r - tr * a.group : nullptr;
+  }
+  return at;
+}
+
+template <uint32_t DP>
+__device__ __forceinline__ void weigh_rows(const WeighArgs& x, const WeighAt& at, uint32_t d, WeighRows<DP>& o) {
+  const AttendArgs& a = x.a;
+  if (x.q16) {
+#pragma unroll
+    for (uint32_t j = 0; j < DP / 32; ++j) {
+      const uint4 u = d + 8 * j < a.dim ? __ldg(reinterpret_cast<const uint4*>(at.q + 16 * j)) : make_uint4(0u, 0u, 0u, 0u);
+      o.q[j][0] = u.x, o.q[j][1] = u.y, o.q[j][2] = u.z, o.q[j][3] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (uint32_t j = 0; j < DP / 32; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint16_t* v = reinterpret_cast<const uint16_t*>(at.q + 16 * j) + 2 * i;
+        o.q[j][i] = d + 8 * j < a.dim ? __ldg(v) | static_cast<uint32_t>(__ldg(v + 1)) << 16 : 0u;
+      }
+  }
+#pragma unroll
+  for (uint32_t e = 0; e < 2; ++e) o.lse[e] = at.lse[e] ? __ldg(at.lse[e]) : -INFINITY;
+}
+
+// 16 MT tokens a warp.  head_warps of a CTA's warps share a run of tokens, each with its
+// own heads; each warp has a ring of stages that asynchronous copies fill some heads
+// ahead, over the ends of tiles.
+// SHARED: at most 8 rows a head, whose queries the CTA lays out in shared memory as the
+// products take them.
+template <uint32_t DP, uint32_t MT, bool FOUR, bool F16, bool SHARED>
+__global__ void __launch_bounds__(kWgWarps * 32, DP == 256 ? 3 : 4) k_kv_weigh(const __grid_constant__ WeighArgs x, uint32_t head_warps, int32_t shift, uint32_t even) {
+  using S = WeighStage<DP, MT, FOUR>;
   __shared__ float sums[kWgWarps][16 * MT];
+  extern __shared__ __align__(128) unsigned char dyn[];  // the rings, then (SHARED) queries and -lse log2 e
   pdl_begin();
   const AttendArgs& a = x.a;
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
@@ -121,77 +129,206 @@ __global__ void __launch_bounds__(kWgWarps * 32) k_kv_weigh(const WeighArgs x, u
   const uint32_t rows = static_cast<uint32_t>(n_live) * a.group;
   const float* was = x.w + static_cast<uint64_t>(b) * x.width;
   float* out = x.w_out + static_cast<uint64_t>(b) * x.width;
-  for (uint32_t first = blockIdx.x * tokens; first < x.width; first += gridDim.x * tokens) {
-    const uint32_t base = first + warp / head_warps * 16 * MT;  // this warp's run
+  const quad::Magic<F16> magic;
+  const uint32_t tiles = len > 0 ? ceil_div(static_cast<uint32_t>(len), tokens) : 0;
+  const uint32_t h0 = warp % head_warps, heads = rows && h0 < a.kv_heads ? ceil_div(a.kv_heads - h0, head_warps) : 0;  // this warp's
+  uint4* sq = reinterpret_cast<uint4*>(dyn + kWgWarps * S::kStages * S::kBytes);  // [head][DP / 32][lane]
+  float* sl = reinterpret_cast<float*>(sq + a.kv_heads * DP);                     // [head][8]
+  if (SHARED && blockIdx.x < tiles && rows) {
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < a.kv_heads * DP; i += kWgWarps * 32) {
+      const uint32_t h = i / DP, j = i / 32 % (DP / 32), l = i & 31u, r = l >> 2, d = (l & 3u) * (DP / 4) + 8 * j;
+      const uint32_t tr = r / a.group;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows && d < a.dim) {
+        const char* q = a.q + static_cast<int64_t>(b) * a.q_seq + static_cast<int64_t>(tr) * a.q_token +
+                        static_cast<int64_t>(h * a.group + r - tr * a.group) * a.q_head + d * 2;
+        if (x.q16) {
+          w = __ldg(reinterpret_cast<const uint4*>(q));
+        } else {
+          const uint16_t* v = reinterpret_cast<const uint16_t*>(q);
+          w = make_uint4(v[0] | static_cast<uint32_t>(v[1]) << 16, v[2] | static_cast<uint32_t>(v[3]) << 16, v[4] | static_cast<uint32_t>(v[5]) << 16,
+                         v[6] | static_cast<uint32_t>(v[7]) << 16);
+        }
+      }
+      if (FOUR)
+        w = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632), __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
+      sq[i] = w;
+    }
+    for (uint32_t i = threadIdx.x; i < a.kv_heads * 8; i += kWgWarps * 32) {
+      const uint32_t h = i / 8, r = i & 7u, tr = r / a.group;
+      const float lse = r < rows ? __ldg(x.lse + (static_cast<uint64_t>(b) * a.T + tr) * a.kv_heads * a.group + h * a.group + r - tr * a.group) : -INFINITY;
+      sl[i] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+    }
+    __syncthreads();
+  }
+  auto base_of = [&](uint32_t tile) { return tile * tokens + warp / head_warps * 16 * MT; };  // this warp's run
+  // The page of this lane's token of a tile, on its way; none past the last.
+  auto page_of = [&](uint32_t tile) -> uint32_t {
+    const uint32_t pos = base_of(tile) + lane;
+    if (!heads || tile >= tiles || lane >= S::kTokens || static_cast<int32_t>(pos) >= len) return 0xFFFFFFFFu;
+    return static_cast<uint32_t>(__ldg(a.table + static_cast<uint64_t>(b) * a.max_pages + (shift >= 0 ? pos >> shift : pos / a.page_tokens)));
+  };
+  const int64_t key_step = (FOUR ? x.k4.head_stride : a.k.head_stride) * static_cast<int64_t>(head_warps);
+  const int64_t scale_step = x.k4.s_head * static_cast<int64_t>(head_warps);
+  unsigned char* const ring_p = dyn + warp * S::kStages * S::kBytes;
+  const uint32_t ring = smem_u32(ring_p);
+  uint32_t read_tile = blockIdx.x, read_left = heads, there = 0;
+  uint32_t ahead = page_of(read_tile);
+  const char *key = nullptr, *scale = nullptr;  // of this lane's token in the head that is read next
+  auto fill = [&](uint32_t slot) {
+    if (read_tile >= tiles || !heads) return;
+    if (read_left == heads) {
+      const uint32_t pos = base_of(read_tile) + lane;
+      uint32_t pg = ahead, at = shift >= 0 ? pos & ((1u << shift) - 1u) : pos % a.page_tokens;
+      const bool on = pg < a.n_pages;
+      if (!on) {  // page 0 is read instead and the score made zero
+        if (lane < S::kTokens && static_cast<int32_t>(pos) < len) kv_status(a.status, IBP_ERANGE);
+        pg = at = 0;
+      }
+      there = __ballot_sync(0xFFFFFFFFu, on);
+      if (FOUR) {
+        key = x.k4.codes + static_cast<int64_t>(pg) * x.k4.page_stride + static_cast<int64_t>(h0) * x.k4.head_stride +
+              static_cast<int64_t>(at) * x.k4.token_stride;
+        scale = x.k4.scales + static_cast<int64_t>(pg) * x.k4.s_page + static_cast<int64_t>(h0) * x.k4.s_head + static_cast<int64_t>(at) * x.k4.s_token;
+      } else {
+        key = a.k.data + static_cast<int64_t>(pg) * a.k.page_stride + static_cast<int64_t>(h0) * a.k.head_stride + static_cast<int64_t>(at) * a.k.token_stride;
+      }
+      ahead = page_of(read_tile + gridDim.x);
+    }
+    constexpr uint32_t kChunks = S::kRow / 16, kPer = 32 / kChunks;
+    const uint32_t c = lane % kChunks, r0 = lane / kChunks, stage = ring + slot * S::kBytes;
+    const bool col = c * (FOUR ? 32 : 8) < a.dim;
+#pragma unroll
+    for (uint32_t i = 0; i < S::kTokens / kPer; ++i) {
+      const char* p = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(key), r0 + i * kPer));
+      cp16(stage + S::at(r0 + i * kPer, c), col ? p + c * 16 : p, col);
+    }
+    if constexpr (FOUR) {
+      if (lane < S::kTokens) {
+        const uint32_t off = S::kKeys + lane * S::kScale;
+        if (even) {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(stage + off), "l"(scale), "n"(S::kScale) : "memory");
+        } else {
+#pragma unroll
+          for (uint32_t j = 0; j < DP / 32; ++j)
+            *reinterpret_cast<uint16_t*>(ring_p + slot * S::kBytes + off + 2 * j) = j * 32 < a.dim ? __ldg(reinterpret_cast<const uint16_t*>(scale) + j) : uint16_t(0);
+        }
+      }
+      scale += scale_step;
+    }
+    if (lane == 0) *reinterpret_cast<uint32_t*>(ring_p + slot * S::kBytes + S::kBytes - 16) = there;
+    key += key_step;
+    if (--read_left == 0) {
+      read_left = heads;
+      read_tile += gridDim.x;
+    }
+  };
+  constexpr uint32_t kAhead = S::kStages - 1;
+#pragma unroll
+  for (uint32_t i = 0; i < kAhead; ++i) {
+    fill(i);
+    cp_commit();
+  }
+  // This lane's places in a stage.
+  constexpr uint32_t kReads = FOUR ? (DP == 256 ? 2 : 1) : DP / 32;  // 16 bytes each (DP 64: 8 of codes)
+  uint32_t k_at[kReads];
+#pragma unroll
+  for (uint32_t i = 0; i < kReads; ++i) k_at[i] = FOUR && DP == 64 ? S::at(g, t / 2) + (t & 1u) * 8 : S::at(g, t * kReads + i);
+  uint32_t slot = 0;
+#pragma unroll 1
+  for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const uint32_t first = tile * tokens, base = base_of(tile);
+    const bool open = static_cast<int32_t>(base + 16 * MT) <= ctx;  // every row sees the whole run
     float sum[MT][2];
 #pragma unroll
     for (uint32_t m = 0; m < MT; ++m) sum[m][0] = sum[m][1] = 0.f;
-    if (static_cast<int32_t>(base) < len) {
-      int64_t page[MT][2];
-      uint32_t slot[MT][2];
+    // f(j): operand B of eight dimensions; back: -lse log2 e, -infinity for a row that sees nothing
+    auto work = [&](const unsigned char* st, auto f, const float (&back)[2], uint32_t r0) {
+      const uint32_t there_now = *reinterpret_cast<const uint32_t*>(st + S::kBytes - 16) >> g;
+      float c[MT][4];
 #pragma unroll
-      for (uint32_t m = 0; m < MT; ++m)
+      for (uint32_t m = 0; m < MT; ++m) {
+        c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
 #pragma unroll
-        for (uint32_t i = 0; i < 2; ++i) {
-          const uint32_t pos = base + 16 * m + g + 8 * i, nth = pos / a.page_tokens;
-          slot[m][i] = pos - nth * a.page_tokens;
-          page[m][i] = -1;
-          if (static_cast<int32_t>(pos) < len) {
-            const uint32_t pg = static_cast<uint32_t>(__ldg(a.table + static_cast<uint64_t>(b) * a.max_pages + nth));
-            if (pg < a.n_pages)
-              page[m][i] = pg;
-            else
-              kv_status(a.status, IBP_ERANGE);
+        for (uint32_t i = 0; i < kReads; ++i) {
+          const unsigned char* k0 = st + k_at[i] + 16 * m * S::kRow;
+          uint4 u, v;
+          if constexpr (FOUR && DP == 64) {
+            const uint2 u2 = *reinterpret_cast<const uint2*>(k0), v2 = *reinterpret_cast<const uint2*>(k0 + 8 * S::kRow);
+            u = make_uint4(u2.x, u2.y, 0u, 0u), v = make_uint4(v2.x, v2.y, 0u, 0u);
+          } else {
+            u = *reinterpret_cast<const uint4*>(k0), v = *reinterpret_cast<const uint4*>(k0 + 8 * S::kRow);
           }
-        }
-      const bool open = static_cast<int32_t>(base + 16 * MT) <= ctx;  // every row sees the whole run
-#pragma unroll 1
-      for (uint32_t h = warp % head_warps; h < a.kv_heads; h += head_warps) {
-        WeighKeys<DP, FOUR, F16> k[MT];
-#pragma unroll
-        for (uint32_t m = 0; m < MT; ++m) k[m].load(x, page[m], slot[m], h, t);
-#pragma unroll 1
-        for (uint32_t r0 = 0; r0 < rows; r0 += 8) {
-          const uint32_t rq = r0 + g < rows ? r0 + g : rows - 1;  // a row past the end is not counted
-          const char* q = a.q + static_cast<int64_t>(b) * a.q_seq + static_cast<int64_t>(rq / a.group) * a.q_token +
-                          static_cast<int64_t>(h * a.group + rq % a.group) * a.q_head + t * (DP / 4) * 2;
-          float c[MT][4];
-#pragma unroll
-          for (uint32_t m = 0; m < MT; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
-#pragma unroll
-          for (uint32_t j = 0; j < DP / 32; ++j) {
-            uint32_t f[4] = {0u, 0u, 0u, 0u};
-            if (t * (DP / 4) + 8 * j < a.dim) weigh_query<FOUR>(f, q + 16 * j, x.q16);
-#pragma unroll
-            for (uint32_t m = 0; m < MT; ++m) {
-              mma16816<F16>(c[m], k[m].f[2 * j], f[0], f[1]);
-              mma16816<F16>(c[m], k[m].f[2 * j + 1], f[2], f[3]);
-            }
+          uint32_t s0 = 0, s1 = 0;
+          if constexpr (FOUR) {
+            const unsigned char* sc = st + S::kKeys + (16 * m + g) * S::kScale + 2 * (DP == 64 ? t / 2 : t * kReads + i);
+            s0 = *reinterpret_cast<const uint16_t*>(sc), s1 = *reinterpret_cast<const uint16_t*>(sc + 8 * S::kScale);
           }
+          const quad::Pair<F16> p0(s0 * 0x10001u), p1(s1 * 0x10001u);
+          constexpr uint32_t kWords = FOUR ? (DP == 64 ? 2 : 4) : 1;
 #pragma unroll
-          for (uint32_t e = 0; e < 2; ++e) {
-            const uint32_t r = r0 + 2 * t + e;
-            if (r >= rows) continue;
-            const uint32_t tq = r / a.group;
-            const float lse = __ldg(x.lse + (static_cast<uint64_t>(b) * a.T + tq) * a.kv_heads * a.group + h * a.group + r % a.group);
-            if (lse == -INFINITY) continue;  // a row that sees nothing
-            const float back = -lse * 1.4426950408889634f;
-#pragma unroll
-            for (uint32_t m = 0; m < MT; ++m)
-#pragma unroll
-              for (uint32_t i = 0; i < 2; ++i) {
-                bool on = true;
-                if (!open) {
-                  const int32_t pos = static_cast<int32_t>(base + 16 * m + g + 8 * i), at = pos - ctx;
-                  on = pos < len && (at < 0 || (a.mask ? (a.mask[(static_cast<uint64_t>(b) * a.T + tq) * a.mask_words + (at >> 5)] >> (at & 31)) & 1u
-                                                      : static_cast<uint32_t>(at) <= tq));
-                }
-                if (on) sum[m][i] += ex2(fmaf(c[m][2 * i + e], a.scale_log2, back));
-              }
+          for (uint32_t j = 0; j < kWords; ++j) {
+            const uint4 w = f(i * kWords + j);
+            uint32_t lo[4], hi[4];
+            weigh_operands<FOUR, F16>(u, v, j, p0, p1, magic, lo, hi);
+            mma16816<F16>(c[m], lo, w.x, w.y);
+            mma16816<F16>(c[m], hi, w.z, w.w);
           }
         }
       }
+#pragma unroll
+      for (uint32_t e = 0; e < 2; ++e) {
+        const uint32_t tq = open ? 0 : (r0 + 2 * t + e) / a.group;
+#pragma unroll
+        for (uint32_t m = 0; m < MT; ++m)
+#pragma unroll
+          for (uint32_t i = 0; i < 2; ++i) {
+            bool on = back[e] != -INFINITY;
+            if (!open && on) {
+              const int32_t pos = static_cast<int32_t>(base + 16 * m + g + 8 * i), at = pos - ctx;
+              on = pos < len && (at < 0 || (a.mask ? (a.mask[(static_cast<uint64_t>(b) * a.T + tq) * a.mask_words + (at >> 5)] >> (at & 31)) & 1u
+                                                  : static_cast<uint32_t>(at) <= tq));
+            }
+            const float p = ex2(fmaf(there_now >> (16 * m + 8 * i) & 1u ? c[m][2 * i + e] : 0.f, a.scale_log2, back[e]));
+            sum[m][i] += on ? p : 0.f;
+          }
+      }
+    };
+    auto head = [&](const unsigned char* k, uint32_t h) {
+      if constexpr (SHARED) {
+        const float2 back = *reinterpret_cast<const float2*>(sl + h * 8 + 2 * t);
+        work(k, [&](uint32_t j) { return sq[h * DP + j * 32 + lane]; }, {back.x, back.y}, 0);
+      } else {
+#pragma unroll 1
+        for (uint32_t r0 = 0; r0 < rows; r0 += 8) {
+          WeighRows<DP> q;
+          weigh_rows<DP>(x, weigh_at(x, b, h, r0, rows, t * (DP / 4)), t * (DP / 4), q);
+          float back[2];
+#pragma unroll
+          for (uint32_t e = 0; e < 2; ++e) back[e] = q.lse[e] == -INFINITY ? -INFINITY : -q.lse[e] * 1.4426950408889634f;
+          work(k, [&](uint32_t j) {
+            const uint32_t(&w)[4] = q.q[j];
+            return FOUR ? make_uint4(__byte_perm(w[0], w[2], 0x5410), __byte_perm(w[0], w[2], 0x7632), __byte_perm(w[1], w[3], 0x5410), __byte_perm(w[1], w[3], 0x7632))
+                        : make_uint4(w[0], w[1], w[2], w[3]);
+          }, back, r0);
+        }
+      }
+    };
+#pragma unroll 1
+    for (uint32_t n = 0, h = h0; n < heads; ++n, h += head_warps) {
+      __syncwarp();  // every lane is done with the stage that is filled next
+      fill(slot == 0 ? kAhead : slot - 1);
+      cp_commit();
+      cp_wait<kAhead>();
+      __syncwarp();
+      head(ring_p + slot * S::kBytes, h);
+      slot = slot == kAhead ? 0 : slot + 1;
     }
+    auto write = [&](uint32_t pos, float s) {
+      const int32_t p = static_cast<int32_t>(pos);
+      if (p < len) out[pos] = p < ctx ? fmaf(x.decay, was[pos], s) : s;
+    };
 #pragma unroll
     for (uint32_t m = 0; m < MT; ++m)
 #pragma unroll
@@ -199,39 +336,84 @@ __global__ void __launch_bounds__(kWgWarps * 32) k_kv_weigh(const WeighArgs x, u
         float s = sum[m][i];
         s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
         s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-        if (t == 0) sums[warp][16 * m + 8 * i + g] = s;
+        if (t == 0) {
+          if (head_warps == 1)
+            write(base + 16 * m + 8 * i + g, s);
+          else
+            sums[warp][16 * m + 8 * i + g] = s;
+        }
       }
+    if (head_warps == 1) continue;
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < tokens; i += kWgWarps * 32) {
-      const uint32_t pos = first + i;
-      if (pos >= x.width) break;
       const uint32_t run = i / (16 * MT);
       float s = 0.f;
       for (uint32_t w = 0; w < head_warps; ++w) s += sums[run * head_warps + w][i % (16 * MT)];
-      const int32_t p = static_cast<int32_t>(pos);
-      out[pos] = p >= len ? was[pos] : (p < ctx ? fmaf(x.decay, was[pos], s) : s);
+      write(first + i, s);
     }
     __syncthreads();
   }
+  // positions without a token keep what they have
+  for (uint64_t i = static_cast<uint32_t>(len > 0 ? len : 0) + static_cast<uint64_t>(blockIdx.x) * kWgWarps * 32 + threadIdx.x; i < x.width;
+       i += static_cast<uint64_t>(gridDim.x) * kWgWarps * 32)
+    out[i] = was[i];
 }
 
 int launch_kv_weigh(const WeighArgs& x, int device, cudaStream_t stream) {
   const AttendArgs& a = x.a;
   if (a.dim <= 128 && static_cast<uint64_t>(a.T) * a.group >= kWgMany) return launch_kv_weigh_tc(x, device, stream);
-  uint32_t head_warps = 1;
-  while (head_warps < kWgWarps && head_warps < a.kv_heads) head_warps *= 2;
   const uint32_t dp = a.dim <= 64 ? 64 : (a.dim <= 128 ? 128 : 256);
-  const uint32_t mt = static_cast<uint64_t>(a.T) * a.group > 8 && dp < 256 ? 2 : 1, tokens = 16 * mt * (kWgWarps / head_warps);
-  const uint64_t want = (static_cast<uint64_t>(x.width) + tokens - 1) / tokens, most = 0x7FFFFFFFull;
-  const dim3 grid(static_cast<unsigned>(want < most ? want : most), a.n_seqs);
-  auto go = [&](auto kern) { return kv_launch("k_kv_weigh", kern, grid, kWgWarps * 32, 0, 1, stream, x, head_warps); };
-  auto typed = [&](auto four, auto f16) {
-    constexpr bool Q = decltype(four)::value, F = decltype(f16)::value;
-    if (dp == 64) return mt == 2 ? go(k_kv_weigh<64, 2, Q, F>) : go(k_kv_weigh<64, 1, Q, F>);
-    if (dp == 128) return mt == 2 ? go(k_kv_weigh<128, 2, Q, F>) : go(k_kv_weigh<128, 1, Q, F>);
-    return go(k_kv_weigh<256, 1, Q, F>);
-  };
   const bool four = x.k4.codes != nullptr;
+  const uint32_t mt = four && dp < 256 ? 2 : 1;
+  // A warp takes all heads of its tokens where there are tokens enough to fill the GPU.
+  const uint64_t all_runs = (static_cast<uint64_t>(x.width) + 16 * mt - 1) / (16 * mt) * a.n_seqs;
+  uint32_t head_warps = 1;
+  while (head_warps < kWgWarps && head_warps < a.kv_heads && all_runs * head_warps < 16ull * sm_count(device)) head_warps *= 2;
+  const uint32_t tokens = 16 * mt * (kWgWarps / head_warps);
+  // A CTA walks a few tiles, so that what it begins with counts less; more would leave ragged
+  // batches uneven.
+  const uint32_t tiles = (x.width + tokens - 1) / tokens, some = kWgTiles < tiles ? kWgTiles : 1;
+  const uint32_t walk = static_cast<uint64_t>(tiles) * a.n_seqs >= 4ull * some * sm_count(device) ? some : 1;
+  const dim3 grid((tiles + walk - 1) / walk, a.n_seqs);
+  int32_t shift = -1;
+  if ((a.page_tokens & (a.page_tokens - 1)) == 0)
+    for (shift = 0; (1u << shift) < a.page_tokens;) ++shift;
+  const uint32_t room = a.kv_heads * (dp * 16 + 32);
+  const bool shared = static_cast<uint64_t>(a.T) * a.group <= 8 && a.kv_heads <= 64 && room <= 40 * 1024;
+  const uint64_t scales = reinterpret_cast<uintptr_t>(x.k4.scales) | static_cast<uint64_t>(x.k4.s_page) | static_cast<uint64_t>(x.k4.s_head) |
+                          static_cast<uint64_t>(x.k4.s_token);
+  const bool even = a.dim == dp && scales % (dp / 16) == 0;
+  auto go = [&](auto kern, uint32_t ring, std::atomic<int>* ready) {
+    if (device < 0 || device >= 64 || !ready[device].load(std::memory_order_acquire)) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+      if (e != cudaSuccess) {
+        set_cuda_error(e, "set-up of k_kv_weigh");
+        cudaGetLastError();
+        return static_cast<int>(IBP_ECUDA);
+      }
+      if (device >= 0 && device < 64) ready[device].store(1, std::memory_order_release);
+    }
+    return kv_launch("k_kv_weigh", kern, grid, kWgWarps * 32, ring + (shared ? room : 0), 1, stream, x, head_warps, shift, even);
+  };
+  auto sized = [&](auto d, auto m, auto quads, auto f16, auto sh) {
+    constexpr uint32_t D = decltype(d)::value, M = decltype(m)::value;
+    constexpr bool Q = decltype(quads)::value, F = decltype(f16)::value, H = decltype(sh)::value;
+    using S = WeighStage<D, M, Q>;
+    static std::atomic<int> ready[64];
+    static_assert(kWgWarps * S::kStages * S::kBytes + 40 * 1024 <= 160 * 1024, "the attribute covers it");
+    return go(k_kv_weigh<D, M, Q, F, H>, kWgWarps * S::kStages * S::kBytes, ready);
+  };
+  auto typed = [&](auto quads, auto f16) {
+    constexpr bool Q = decltype(quads)::value;
+    using One = std::integral_constant<uint32_t, 1>;
+    using Many = std::integral_constant<uint32_t, Q ? 2 : 1>;
+    auto by_dim = [&](auto sh) {
+      if (dp == 64) return sized(std::integral_constant<uint32_t, 64>{}, Many{}, quads, f16, sh);
+      if (dp == 128) return sized(std::integral_constant<uint32_t, 128>{}, Many{}, quads, f16, sh);
+      return sized(std::integral_constant<uint32_t, 256>{}, One{}, quads, f16, sh);
+    };
+    return shared ? by_dim(std::true_type{}) : by_dim(std::false_type{});
+  };
   if (a.f16) return four ? typed(std::true_type{}, std::true_type{}) : typed(std::false_type{}, std::true_type{});
   return four ? typed(std::true_type{}, std::false_type{}) : typed(std::false_type{}, std::false_type{});
 }
