@@ -29,7 +29,7 @@ struct Rows {
     pieces = r.heads * (r.dim / 8);
     width = pieces < kRowThreads ? pieces : kRowThreads;
     at_once = kRowThreads / width;
-    first = blockIdx.x * at_once * kRowFly;
+    first = blockIdx.x * at_once * kRowFly * r.loops;
     b = blockIdx.y, which = blockIdx.z;
     const int32_t raw = r.lens[b], len = clamp_len(raw, r.page_tokens, r.max_pages);
     const int32_t want = r.n_rows ? r.n_rows[b] : static_cast<int32_t>(r.T);
@@ -41,16 +41,32 @@ struct Rows {
     Spot s = {0xFFFFFFFFu, 0u};
     const int32_t pos = base + static_cast<int32_t>(t);
     if (static_cast<int32_t>(t) >= n || pos < 0) return s;
-    const uint32_t nth = static_cast<uint32_t>(pos) / r.page_tokens;
-    const uint32_t page = static_cast<uint32_t>(__ldg(r.table + static_cast<uint64_t>(b) * r.max_pages + nth));
-    if (page >= r.n_pages) {
+    const uint32_t p = static_cast<uint32_t>(pos), nth = r.shift >= 0 ? p >> r.shift : p / r.page_tokens;
+    s.page = static_cast<uint32_t>(__ldg(r.table + static_cast<uint64_t>(b) * r.max_pages + nth));
+    s.slot = r.shift >= 0 ? p & ((1u << r.shift) - 1u) : p - nth * r.page_tokens;
+    if (s.page >= r.n_pages) {
       kv_status(r.status, IBP_ERANGE);
-      return s;
+      s.page = 0xFFFFFFFFu;
     }
-    s.page = page;
-    s.slot = static_cast<uint32_t>(pos) - nth * r.page_tokens;
     return s;
   }
+};
+
+// A thread's piece of token slot 0 of page 0; from there by page and slot.  NARROW:
+// strides of 32 bits.
+template <bool NARROW>
+struct Piece {
+  char *codes, *scale;
+  const Kv4View& v;
+  __device__ __forceinline__ Piece(const Kv4View& v_, uint32_t h, uint32_t c) : v(v_) {
+    codes = const_cast<char*>(v.codes) + static_cast<int64_t>(h) * v.head_stride + c * 4;
+    scale = const_cast<char*>(v.scales) + static_cast<int64_t>(h) * v.s_head + c / 4 * 2;
+  }
+  static __device__ __forceinline__ uint64_t times(uint32_t x, int64_t stride) {
+    return NARROW ? static_cast<uint64_t>(x) * static_cast<uint32_t>(stride) : static_cast<uint64_t>(x) * static_cast<uint64_t>(stride);
+  }
+  __device__ __forceinline__ char* codes_of(const Spot& s) const { return codes + times(s.page, v.page_stride) + times(s.slot, v.token_stride); }
+  __device__ __forceinline__ char* scale_of(const Spot& s) const { return scale + times(s.page, v.s_page) + times(s.slot, v.s_token); }
 };
 
 __device__ __forceinline__ char* codes_at(const Kv4View& v, const Spot& s, uint32_t h, uint32_t c) {
@@ -75,66 +91,81 @@ __device__ __forceinline__ uint32_t scale_of(float a) {
   return __float_as_uint(fminf(s, 0x1p121f)) >> 16;
 }
 
-// 8 + rint(x / s), kept within 1 to 15, in the low bits of a float.  x times the rounded
-// reciprocal is off by 2^-21 at most, while x / s (11 bits by 5) is a tie k + 1/2 or 2^-12 away
-// from one: rounded to multiples of 2^-16 first, ties are exact again and go to
-// even like the quotient's own.
-__device__ __forceinline__ uint32_t code_of(float x, float inv) {
-  const float y = __fadd_rn(__fmaf_rn(x, inv, 192.f), -192.f);
-  return __float_as_uint(__fadd_rn(fmaxf(fminf(y, 7.f), -7.f), 12582920.f)) & 15u;  // 1.5 2^23 + 8
+// 8 + rint(x / s) in the lowest byte, with `edge` kept within 1 to 15.  x times the reciprocal
+// (within 2^-22 of itself) is off by 2^-19 at most, while x / s (11 bits by 5) is a tie
+// k + 1/2 or 2^-12 away from one: rounded to multiples of 2^-16 first, ties are exact again
+// and go to even like the quotient's own.
+__device__ __forceinline__ uint32_t code_of(float x, float inv, bool edge) {
+  float y = __fadd_rn(__fmaf_rn(x, inv, 192.f), -192.f);
+  if (edge) y = fmaxf(fminf(y, 7.f), -7.f);
+  return __float_as_uint(__fadd_rn(y, 12582920.f));  // 1.5 2^23 + 8
 }
 
-template <bool F16>
+// FAST: rows that may be read 16 bytes at a time, and narrow strides.
+template <bool F16, bool FAST>
 __global__ void __launch_bounds__(kRowThreads) k_kv4_store(const Kv4Rows r) {
   pdl_begin();
   const Rows o(r);
-  const Kv4View& p = r.p[o.which];
   const uint32_t mine = threadIdx.x / o.width, chunks = r.dim / 8;
-  const uint32_t quad = 0xFu << (threadIdx.x & 28u);  // threads of a group; they run alike
-  if (mine >= o.at_once) return;
-  for (uint32_t piece = threadIdx.x - mine * o.width; piece < o.pieces; piece += o.width) {
-    const uint32_t h = piece / chunks, c = piece - h * chunks;
-    const char* src = r.x[o.which] + static_cast<int64_t>(o.b) * r.x_seq[o.which] + static_cast<int64_t>(h) * r.x_head[o.which] + c * 16;
-    Spot at[kRowFly];
-    uint32_t w[kRowFly][4];
+  // whole warps go round alike: the four threads of a group exchange their maxima
+  for (uint32_t p0 = 0; p0 < o.pieces; p0 += o.width) {
+    const uint32_t piece = p0 + threadIdx.x - mine * o.width;
+    const bool on = mine < o.at_once && piece < o.pieces;
+    const uint32_t h = on ? piece / chunks : 0, c = on ? piece - h * chunks : 0;
+    const Piece<FAST> to(r.p[o.which], h, c);
+    const char* src = r.x[o.which] + static_cast<int64_t>(o.b) * r.x_seq[o.which] + static_cast<int64_t>(h) * r.x_head[o.which] + c * 16 +
+                      static_cast<int64_t>(o.first + mine) * r.x_token[o.which];
+    const int64_t next = static_cast<int64_t>(o.at_once) * r.x_token[o.which];
+    uint32_t t0 = on ? o.first + mine : 0x40000000u;
+#pragma unroll 1
+    for (uint32_t l = 0; l < r.loops; ++l, t0 += kRowFly * o.at_once, src += kRowFly * next) {
+      if (o.first + l * kRowFly * o.at_once >= static_cast<uint32_t>(o.n)) break;  // the same for the block
+      Spot at[kRowFly];
+      uint32_t w[kRowFly][4];
 #pragma unroll
-    for (uint32_t i = 0; i < kRowFly; ++i) {
-      const uint32_t t = o.first + i * o.at_once + mine;
-      at[i] = o.spot(r, t);
-      w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
-      if (static_cast<int32_t>(t) < o.n) {
-        const char* x = src + static_cast<int64_t>(t) * r.x_token[o.which];
-        if (r.vec) {
-          const uint4 u = __ldg(reinterpret_cast<const uint4*>(x));
-          w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
-        } else {
+      for (uint32_t i = 0; i < kRowFly; ++i) {
+        at[i] = o.spot(r, t0 + i * o.at_once);
+        w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
+        if (static_cast<int32_t>(t0 + i * o.at_once) < o.n) {
+          const char* x = src + i * next;
+          if (FAST) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(x));
+            w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
+          } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[i][j] = *reinterpret_cast<const uint16_t*>(x + 4 * j) | (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(x + 4 * j + 2)) << 16);
+            for (int j = 0; j < 4; ++j)
+              w[i][j] = *reinterpret_cast<const uint16_t*>(x + 4 * j) | (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(x + 4 * j + 2)) << 16);
+          }
         }
       }
-    }
 #pragma unroll
-    for (uint32_t i = 0; i < kRowFly; ++i) {
-      float v[8], a = 0.f, all = 0.f;  // all: NaN where something is not finite
+      for (uint32_t i = 0; i < kRowFly; ++i) {
+        // magnitudes are ordered as whole numbers are, infinities and NaN above all
+        uint32_t top = __vmaxu2(__vmaxu2(w[i][0] & 0x7FFF7FFFu, w[i][1] & 0x7FFF7FFFu), __vmaxu2(w[i][2] & 0x7FFF7FFFu, w[i][3] & 0x7FFF7FFFu));
+        top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        top = max(top & 0xFFFFu, top >> 16);
+        const bool fine = top < (F16 ? 0x7C00u : 0x7F80u);
+        uint32_t sb = fine ? scale_of<F16>(quad::to_float<F16>(top)) : 0u;
+        const float sc = quad::to_float<F16>(sb);
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sc));
+        uint32_t word = 0x88888888u;
+        if (sb) {
+          // only the type's smallest and largest scales leave quotients above 7 1/2
+          const bool edge = F16 ? sb < 0x0400u : sb >= 0x7C00u;
+          uint32_t f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = quad::to_float<F16>(j & 1 ? w[i][j / 2] >> 16 : w[i][j / 2] & 0xFFFFu);
-        a = fmaxf(a, fabsf(v[j]));
-        all = __fmaf_rn(v[j], 0.f, all);
+          for (int j = 0; j < 8; ++j) f[j] = code_of(quad::to_float<F16>(j & 1 ? w[i][j / 2] >> 16 : w[i][j / 2] & 0xFFFFu), inv, edge);
+          const uint32_t low = __byte_perm(__byte_perm(f[0], f[2], 0x0040), __byte_perm(f[4], f[6], 0x0040), 0x5410);
+          const uint32_t high = __byte_perm(__byte_perm(f[1], f[3], 0x0040), __byte_perm(f[5], f[7], 0x0040), 0x5410);
+          word = low | high << 4;
+        }
+        if (!fine) sb = F16 ? 0x7E00u : 0x7FC0u;
+        if (at[i].page == 0xFFFFFFFFu) continue;
+        *reinterpret_cast<uint32_t*>(to.codes_of(at[i])) = word;
+        if ((c & 3u) == 0) *reinterpret_cast<uint16_t*>(to.scale_of(at[i])) = static_cast<uint16_t>(sb);
       }
-      a = fmaxf(a, __shfl_xor_sync(quad, a, 1));
-      a = fmaxf(a, __shfl_xor_sync(quad, a, 2));
-      const bool fine = (__ballot_sync(quad, all == 0.f) & quad) == quad;
-      uint32_t sb = fine ? scale_of<F16>(a) : 0u;
-      const float sc = quad::to_float<F16>(sb), inv = sc > 0.f ? __fdiv_rn(1.f, sc) : 0.f;
-      uint32_t word = 0;
-#pragma unroll
-      for (int j = 7; j >= 0; --j) word = word << 4 | code_of(fine ? v[j] : 0.f, inv);
-      if (!fine) sb = F16 ? 0x7E00u : 0x7FC0u;
-      if (at[i].page == 0xFFFFFFFFu) continue;
-      *reinterpret_cast<uint32_t*>(codes_at(p, at[i], h, c)) = word;
-      if ((c & 3u) == 0) *reinterpret_cast<uint16_t*>(scale_at(p, at[i], h, c)) = static_cast<uint16_t>(sb);
     }
   }
 }
@@ -149,48 +180,79 @@ __device__ __forceinline__ uint4 decode8(uint32_t word, uint32_t scale) {
   return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(c, d, 0x7632));
 }
 
-template <bool F16>
+template <bool F16, bool FAST>
 __global__ void __launch_bounds__(kRowThreads) k_kv4_load(const Kv4Rows r) {
   pdl_begin();
   const Rows o(r);
-  const Kv4View& p = r.p[o.which];
   const uint32_t mine = threadIdx.x / o.width, chunks = r.dim / 8;
   if (mine >= o.at_once) return;
   for (uint32_t piece = threadIdx.x - mine * o.width; piece < o.pieces; piece += o.width) {
     const uint32_t h = piece / chunks, c = piece - h * chunks;
-    char* dst = const_cast<char*>(r.x[o.which]) + static_cast<int64_t>(o.b) * r.x_seq[o.which] + static_cast<int64_t>(h) * r.x_head[o.which] + c * 16;
-    uint32_t word[kRowFly], scale[kRowFly];
+    const Piece<FAST> from(r.p[o.which], h, c);
+    char* dst = const_cast<char*>(r.x[o.which]) + static_cast<int64_t>(o.b) * r.x_seq[o.which] + static_cast<int64_t>(h) * r.x_head[o.which] + c * 16 +
+                static_cast<int64_t>(o.first + mine) * r.x_token[o.which];
+    const int64_t next = static_cast<int64_t>(o.at_once) * r.x_token[o.which];
+    uint32_t t0 = o.first + mine;
+#pragma unroll 1
+    for (uint32_t l = 0; l < r.loops && t0 < r.T; ++l, t0 += kRowFly * o.at_once, dst += kRowFly * next) {
+      uint32_t word[kRowFly], scale[kRowFly];
 #pragma unroll
-    for (uint32_t i = 0; i < kRowFly; ++i) {
-      const Spot s = o.spot(r, o.first + i * o.at_once + mine);
-      word[i] = scale[i] = 0u;  // code 0 times 0
-      if (s.page != 0xFFFFFFFFu) {
-        word[i] = __ldg(reinterpret_cast<const uint32_t*>(codes_at(p, s, h, c)));
-        scale[i] = __ldg(reinterpret_cast<const uint16_t*>(scale_at(p, s, h, c)));
+      for (uint32_t i = 0; i < kRowFly; ++i) {
+        const Spot s = o.spot(r, t0 + i * o.at_once);
+        word[i] = scale[i] = 0u;  // code 0 times 0
+        if (s.page != 0xFFFFFFFFu) {
+          word[i] = __ldg(reinterpret_cast<const uint32_t*>(from.codes_of(s)));
+          scale[i] = __ldg(reinterpret_cast<const uint16_t*>(from.scale_of(s)));
+        }
       }
-    }
 #pragma unroll
-    for (uint32_t i = 0; i < kRowFly; ++i) {
-      const uint32_t t = o.first + i * o.at_once + mine;
-      if (t >= r.T) continue;
-      uint4 u = decode8<F16>(word[i], scale[i]);
-      if (F16 && scale[i] == 0u) u = make_uint4(0u, 0u, 0u, 0u);  // not -0
-      *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(t) * r.x_token[o.which]) = u;
+      for (uint32_t i = 0; i < kRowFly; ++i) {
+        if (t0 + i * o.at_once >= r.T) continue;
+        uint4 u = decode8<F16>(word[i], scale[i]);
+        if (F16 && scale[i] == 0u) u = make_uint4(0u, 0u, 0u, 0u);  // not -0
+        *reinterpret_cast<uint4*>(dst + i * next) = u;
+      }
     }
   }
 }
 
 static dim3 row_grid(const Kv4Rows& r) {
-  const uint32_t pieces = r.heads * (r.dim / 8), at_once = pieces < kRowThreads ? kRowThreads / pieces : 1;
-  return dim3((r.T + at_once * kRowFly - 1) / (at_once * kRowFly), r.n_seqs, 2);
+  const uint64_t pieces = r.heads * (r.dim / 8), at_once = pieces < kRowThreads ? kRowThreads / pieces : 1, each = at_once * kRowFly * r.loops;
+  return dim3(static_cast<unsigned>((r.T + each - 1) / each), r.n_seqs, 2);
 }
 
-int launch_kv4_store(const Kv4Rows& r, int device, cudaStream_t stream) {
-  return kv_launch("k_kv4_store", r.f16 ? k_kv4_store<true> : k_kv4_store<false>, row_grid(r), kRowThreads, 0, 1, stream, r);
+static bool narrow(const Kv4Rows& r) {
+  uint64_t all = 0;
+  for (int i = 0; i < 2; ++i)
+    all |= static_cast<uint64_t>(r.p[i].page_stride) | static_cast<uint64_t>(r.p[i].token_stride) | static_cast<uint64_t>(r.p[i].s_page) |
+           static_cast<uint64_t>(r.p[i].s_token);
+  return all <= 0xFFFFFFFFull;
 }
 
-int launch_kv4_load(const Kv4Rows& r, int device, cudaStream_t stream) {
-  return kv_launch("k_kv4_load", r.f16 ? k_kv4_load<true> : k_kv4_load<false>, row_grid(r), kRowThreads, 0, 1, stream, r);
+// What the kernels go by besides: pages of 2^shift tokens; and several rounds of tokens a
+// block, so that what it begins with counts less, where there are blocks enough.
+static Kv4Rows planned(Kv4Rows r, int device) {
+  r.shift = -1;
+  if ((r.page_tokens & (r.page_tokens - 1)) == 0)
+    for (r.shift = 0; (1u << r.shift) < r.page_tokens;) ++r.shift;
+  r.loops = 1;
+  const dim3 g = row_grid(r);
+  if (static_cast<uint64_t>(g.x) * g.y * 2 >= 32ull * sm_count(device)) r.loops = 4;
+  return r;
+}
+
+int launch_kv4_store(const Kv4Rows& rows, int device, cudaStream_t stream) {
+  const Kv4Rows r = planned(rows, device);
+  const bool fast = r.vec && narrow(r);
+  auto kern = r.f16 ? (fast ? k_kv4_store<true, true> : k_kv4_store<true, false>) : (fast ? k_kv4_store<false, true> : k_kv4_store<false, false>);
+  return kv_launch("k_kv4_store", kern, row_grid(r), kRowThreads, 0, 1, stream, r);
+}
+
+int launch_kv4_load(const Kv4Rows& rows, int device, cudaStream_t stream) {
+  const Kv4Rows r = planned(rows, device);
+  const bool fast = narrow(r);
+  auto kern = r.f16 ? (fast ? k_kv4_load<true, true> : k_kv4_load<true, false>) : (fast ? k_kv4_load<false, true> : k_kv4_load<false, false>);
+  return kv_launch("k_kv4_load", kern, row_grid(r), kRowThreads, 0, 1, stream, r);
 }
 
 // ---------------------------------------------------------------------------

@@ -30,6 +30,8 @@ struct Kv4Rows {  // arguments of the storing and loading kernels
   uint32_t n_seqs, max_pages, n_pages, page_tokens, T, heads, dim;
   uint32_t f16;
   uint32_t vec;           // rows may be read and written 16 bytes at a time
+  int32_t shift;          // set by the launch: pages of 2^shift tokens, or -1
+  uint32_t loops;         // and rounds of tokens a block
   uint32_t* status;
 };
 

@@ -18,10 +18,10 @@ size_t kv4_tree_workspace(uint32_t dim, int device) {
   return align256((n + 1) * sizeof(int4)) + align256(2 * n * kTcTile * sizeof(float2)) + 2 * n * kTcTile * dp * 4;
 }
 
-template <uint32_t DP, bool F16>
+template <uint32_t DP, bool F16, bool EVEN>
 static int launch(TcArgs& t, int device, cudaStream_t stream) {
   using S = TcShape<DP, 1, true>;
-  auto kern = k_kv_tree<DP, 1, F16, true>;
+  auto kern = k_kv_tree<DP, 1, F16, true, EVEN>;
   static std::atomic<int> ready[64];
   if (device < 0 || device >= 64 || !ready[device].load(std::memory_order_acquire)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
@@ -48,6 +48,20 @@ int launch_kv4_tree(const Attend4Args& x, int device, size_t ws_bytes, cudaStrea
   t.a = a;
   t.four[0] = x.k, t.four[1] = x.v;
   t.limit = kv_tree_limit();
+  const uint32_t dp = a.dim <= 64 ? 64 : 128;
+  t.shift = -1;
+  if ((a.page_tokens & (a.page_tokens - 1)) == 0)
+    for (t.shift = 0; (1u << t.shift) < a.page_tokens;) ++t.shift;
+  bool even = a.dim == dp;  // all of the tile's dimensions, a token's scales aligned as one
+  t.narrow = 1;
+  for (int i = 0; i < 2; ++i) {
+    const Kv4View& v = t.four[i];
+    even = even && (reinterpret_cast<uintptr_t>(v.scales) | static_cast<uint64_t>(v.s_page) | static_cast<uint64_t>(v.s_head) |
+                        static_cast<uint64_t>(v.s_token)) % (dp / 16) == 0;
+    const uint64_t wide = static_cast<uint64_t>(v.page_stride) | static_cast<uint64_t>(v.token_stride) | static_cast<uint64_t>(v.s_page) |
+                          static_cast<uint64_t>(v.s_token);
+    t.narrow = t.narrow && wide <= 0xFFFFFFFFull;
+  }
   t.row_pairs = static_cast<uint32_t>((rows + kTcTile - 1) / kTcTile);
   t.q16 = ((reinterpret_cast<uintptr_t>(a.q) | static_cast<uint64_t>(a.q_seq) | static_cast<uint64_t>(a.q_token) |
             static_cast<uint64_t>(a.q_head)) & 15u) == 0;
@@ -62,8 +76,12 @@ int launch_kv4_tree(const Attend4Args& x, int device, size_t ws_bytes, cudaStrea
   t.ml_part = reinterpret_cast<float2*>(w);
   w += align256(2 * n * kTcTile * sizeof(float2));
   t.o_part = reinterpret_cast<float*>(w);
-  if (a.dim <= 64) return a.f16 ? launch<64, true>(t, device, stream) : launch<64, false>(t, device, stream);
-  return a.f16 ? launch<128, true>(t, device, stream) : launch<128, false>(t, device, stream);
+  auto go = [&](auto f16, auto e) {
+    constexpr bool F = decltype(f16)::value, E = decltype(e)::value;
+    return dp == 64 ? launch<64, F, E>(t, device, stream) : launch<128, F, E>(t, device, stream);
+  };
+  if (even) return a.f16 ? go(std::true_type{}, std::true_type{}) : go(std::false_type{}, std::true_type{});
+  return a.f16 ? go(std::true_type{}, std::false_type{}) : go(std::false_type{}, std::false_type{});
 }
 
 }  // namespace ibp

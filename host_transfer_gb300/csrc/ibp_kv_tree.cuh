@@ -71,6 +71,8 @@ struct TcArgs {
   uint32_t n_ctas;
   long long limit;    // clock cycles after which a wait gives up
   Kv4View four[2];    // K and V of a cache in 4 bits
+  int32_t shift;      // its pages hold 2^shift tokens; -1: another number
+  uint32_t narrow;    // strides, and a page's tokens, within 32 bits
 };
 
 namespace tc {
@@ -356,7 +358,8 @@ __device__ __forceinline__ uint32_t seen_bits(const AttendArgs& a, const TcSeg& 
 // tile, one of the second half of every V tile, in the swizzled layout that TMA boxes
 // have, the elements of eight in the decoder's order.  Codes are two tiles ahead of
 // the one that is decoded, pages three.
-template <uint32_t DP, uint32_t MT, bool F16>
+// EVEN: all of DP's dimensions, a token's scales aligned for one read.
+template <uint32_t DP, uint32_t MT, bool F16, bool EVEN>
 __device__ __forceinline__ void tc_load4(const TcArgs& t, TcShared& sh, uint64_t at, uint64_t end, unsigned char* ring_sm, uint32_t thread) {
   using S = TcShape<DP, MT, true>;
   const AttendArgs& a = t.a;
@@ -364,52 +367,82 @@ __device__ __forceinline__ void tc_load4(const TcArgs& t, TcShared& sh, uint64_t
   const Kv4View& v = t.four[kv];
   volatile uint32_t* stop = &sh.stop;
   struct Spot {  // nothing is done with the page here: it is still on its way
-    uint32_t page, slot, h;
+    uint32_t page, slot;
+    const char *codes, *scales;  // of the head
     bool there;
   };
   struct Raw {
     uint4 w[DP / 32];
-    uint32_t s[DP / 32];
+    uint32_t s[DP / 32];  // EVEN: two to a word
+    bool good;
   };
   TcWalk walk(t, sh, at, end);
   TcSeg s;
   bool more = walk.next(&s);
   uint32_t j = 0;
+  const char *codes = v.codes, *scales = v.scales;
+  const int32_t* row = a.table;
   auto next_spot = [&](Spot& sp) {
-    sp.page = sp.slot = sp.h = 0;
+    sp.page = sp.slot = 0;
     sp.there = false;
     if (!more) return;
-    if (j == 0 && thread == 0) {
-      const int32_t raw = a.lens[s.b], n = a.n_live ? a.n_live[s.b] : static_cast<int32_t>(a.T);
-      if (raw != s.len || n != s.n_live || n > s.len) kv_status(a.status, IBP_ERANGE);
+    if (j == 0) {
+      codes = v.codes + static_cast<int64_t>(s.h) * v.head_stride;
+      scales = v.scales + static_cast<int64_t>(s.h) * v.s_head;
+      row = a.table + static_cast<uint64_t>(s.b) * a.max_pages;
+      if (thread == 0) {
+        const int32_t raw = a.lens[s.b], n = a.n_live ? a.n_live[s.b] : static_cast<int32_t>(a.T);
+        if (raw != s.len || n != s.n_live || n > s.len) kv_status(a.status, IBP_ERANGE);
+      }
     }
-    const int32_t p = static_cast<int32_t>((s.tile0 + j) * kTcTile + r);
-    sp.h = s.h;
-    if (p < s.len) {
-      const uint32_t nth = static_cast<uint32_t>(p) / a.page_tokens;
-      sp.slot = static_cast<uint32_t>(p) - nth * a.page_tokens;
+    const uint32_t p = (s.tile0 + j) * kTcTile + r;
+    sp.codes = codes, sp.scales = scales;
+    if (static_cast<int32_t>(p) < s.len) {
+      const uint32_t nth = t.shift >= 0 ? p >> t.shift : p / a.page_tokens;
+      sp.slot = t.shift >= 0 ? p & ((1u << t.shift) - 1u) : p - nth * a.page_tokens;
       sp.there = true;
-      sp.page = static_cast<uint32_t>(__ldg(a.table + static_cast<uint64_t>(s.b) * a.max_pages + nth));
+      sp.page = static_cast<uint32_t>(__ldg(row + nth));
     }
     if (++j == s.tiles) {
       more = walk.next(&s);
       j = 0;
     }
   };
+  // Tokens that are not there read page 0 and become zeros when they are decoded.
   auto fetch = [&](const Spot& sp, Raw& raw) {
-    const bool on = sp.there && sp.page < a.n_pages;
-    if (!on && sp.there) kv_status(a.status, IBP_ERANGE);
-    const char* c = v.codes + static_cast<int64_t>(on ? sp.page : 0) * v.page_stride + static_cast<int64_t>(sp.h) * v.head_stride +
-                    static_cast<int64_t>(on ? sp.slot : 0) * v.token_stride;
-    const char* sc = v.scales + static_cast<int64_t>(on ? sp.page : 0) * v.s_page + static_cast<int64_t>(sp.h) * v.s_head +
-                     static_cast<int64_t>(on ? sp.slot : 0) * v.s_token;
+    raw.good = sp.there && sp.page < a.n_pages;
+    if (!raw.good && sp.there) kv_status(a.status, IBP_ERANGE);
+    const char *c = v.codes, *sc = v.scales;
+    if (raw.good) {
+      if (t.narrow) {
+        c = sp.codes + static_cast<uint64_t>(sp.page) * static_cast<uint32_t>(v.page_stride) + static_cast<uint64_t>(sp.slot) * static_cast<uint32_t>(v.token_stride);
+        sc = sp.scales + static_cast<uint64_t>(sp.page) * static_cast<uint32_t>(v.s_page) + static_cast<uint64_t>(sp.slot) * static_cast<uint32_t>(v.s_token);
+      } else {
+        c = sp.codes + static_cast<int64_t>(sp.page) * v.page_stride + static_cast<int64_t>(sp.slot) * v.token_stride;
+        sc = sp.scales + static_cast<int64_t>(sp.page) * v.s_page + static_cast<int64_t>(sp.slot) * v.s_token;
+      }
+    }
+    if constexpr (EVEN) {
 #pragma unroll
-    for (uint32_t g = 0; g < DP / 32; ++g) {
-      const bool in = on && g * 32 < a.dim;
-      raw.w[g] = in ? __ldg(reinterpret_cast<const uint4*>(c + g * 16)) : make_uint4(0u, 0u, 0u, 0u);
-      raw.s[g] = in ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(sc + g * 2))) : 0u;
+      for (uint32_t g = 0; g < DP / 32; ++g) raw.w[g] = __ldg(reinterpret_cast<const uint4*>(c + g * 16));
+      if constexpr (DP == 128) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(sc));
+        raw.s[0] = x.x, raw.s[1] = x.y;
+      } else {
+        raw.s[0] = __ldg(reinterpret_cast<const uint32_t*>(sc));
+      }
+    } else {
+#pragma unroll
+      for (uint32_t g = 0; g < DP / 32; ++g) {
+        const bool in = g * 32 < a.dim;
+        raw.w[g] = in ? __ldg(reinterpret_cast<const uint4*>(c + g * 16)) : make_uint4(0u, 0u, 0u, 0u);
+        raw.s[g] = in ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(sc + g * 2))) : 0u;
+      }
     }
   };
+  uint32_t turn[8];  // places of a row's pieces of 16 bytes
+#pragma unroll
+  for (uint32_t c = 0; c < 8; ++c) turn[c] = r * 128 + ((c ^ (r & 7u)) << 4);
   const quad::Magic<F16> magic;
   const uint64_t n = end - at;
   Spot spot;
@@ -428,15 +461,15 @@ __device__ __forceinline__ void tc_load4(const TcArgs& t, TcShared& sh, uint64_t
       if (lane == 0) ok = tc::bar_wait(tc::s32(&sh.empty[slot]), (f / S::kSlots & 1u) ^ 1u, stop, t.limit);
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       if (!ok) break;
-      unsigned char* dst = ring_sm + slot * S::kTileBytes + r * 128;
+      unsigned char* dst = ring_sm + slot * S::kTileBytes;
 #pragma unroll
       for (uint32_t g = 0; g < DP / 32; ++g) {
-        const quad::Pair<F16> p(__byte_perm(raw[u].s[g], 0, 0x1010));
+        const quad::Pair<F16> p(EVEN ? __byte_perm(raw[u].s[g / 2], 0, g & 1u ? 0x3232 : 0x1010) : __byte_perm(raw[u].s[g], 0, 0x1010), raw[u].good);
         const uint32_t w[4] = {raw[u].w[g].x, raw[u].w[g].y, raw[u].w[g].z, raw[u].w[g].w};
 #pragma unroll
         for (uint32_t e = 0; e < 4; ++e) {
           const uint32_t c = g * 4 + e;
-          *reinterpret_cast<uint4*>(dst + (c / 8) * S::kPanel + (((c & 7u) ^ (r & 7u)) << 4)) =
+          *reinterpret_cast<uint4*>(dst + (c / 8) * S::kPanel + turn[c & 7u]) =
               make_uint4(quad::decode<F16, 0>(w[e], p, magic), quad::decode<F16, 1>(w[e], p, magic),
                          quad::decode<F16, 2>(w[e], p, magic), quad::decode<F16, 3>(w[e], p, magic));
         }
@@ -453,7 +486,7 @@ __device__ __forceinline__ void tc_load4(const TcArgs& t, TcShared& sh, uint64_t
 __device__ constexpr uint32_t quad_element(uint32_t k) { return (k >> 1) + (k & 1u) * 4; }
 __device__ constexpr uint32_t quad_place(uint32_t e) { return (e & 3u) * 2 + (e >> 2); }
 
-template <uint32_t DP, uint32_t MT, bool F16, bool FOUR = false>
+template <uint32_t DP, uint32_t MT, bool F16, bool FOUR = false, bool EVEN = false>
 __global__ void __launch_bounds__(TcShape<DP, MT, FOUR>::kThreads, 1)
     k_kv_tree(const __grid_constant__ TcArgs t, const __grid_constant__ CUtensorMap map_k,
               const __grid_constant__ CUtensorMap map_v) {
@@ -549,7 +582,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT, FOUR>::kThreads, 1)
 
   if (warp >= S::kLoadWarp && warp < S::kLoadWarp + S::kLoaders) {
     if constexpr (FOUR) {
-      tc_load4<DP, MT, F16>(t, sh, at, end, sm + (kv_sm - base), tid - S::kLoadWarp * 32);
+      tc_load4<DP, MT, F16, EVEN>(t, sh, at, end, sm + (kv_sm - base), tid - S::kLoadWarp * 32);
     } else {
       // ---- producer: one lane issues; all follow the same path
       TcWalk walk(t, sh, at, end);
