@@ -155,8 +155,14 @@ __global__ void __launch_bounds__(kRowThreads) k_kv4_store(const Kv4Rows r) {
           // only the type's smallest and largest scales leave quotients above 7 1/2
           const bool edge = F16 ? sb < 0x0400u : sb >= 0x7C00u;
           uint32_t f[8];
+          auto codes = [&](bool at_edge) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = code_of(quad::to_float<F16>(j & 1 ? w[i][j / 2] >> 16 : w[i][j / 2] & 0xFFFFu), inv, edge);
+            for (int j = 0; j < 8; ++j) f[j] = code_of(quad::to_float<F16>(j & 1 ? w[i][j / 2] >> 16 : w[i][j / 2] & 0xFFFFu), inv, at_edge);
+          };
+          if (edge)
+            codes(true);
+          else
+            codes(false);
           const uint32_t low = __byte_perm(__byte_perm(f[0], f[2], 0x0040), __byte_perm(f[4], f[6], 0x0040), 0x5410);
           const uint32_t high = __byte_perm(__byte_perm(f[1], f[3], 0x0040), __byte_perm(f[5], f[7], 0x0040), 0x5410);
           word = low | high << 4;

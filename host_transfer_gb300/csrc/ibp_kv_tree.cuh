@@ -856,6 +856,15 @@ __global__ void __launch_bounds__(TcShape<DP, MT, FOUR>::kThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc::fence_after();
+        if constexpr (FOUR) {
+          // a warp without a row: what its lanes of TMEM hold reaches no other row
+          if (!__any_sync(0xFFFFFFFFu, live)) {
+            tc::fence_before();
+            tc::bar_arrive(tc::s32(&sh.p_full[slot][0]));
+            tc::bar_arrive(tc::s32(&sh.p_full[slot][1]));
+            continue;
+          }
+        }
         const uint32_t s_col = tmem + lanes + slot * 128;
         const int32_t p0 = static_cast<int32_t>((s.tile0 + j) * kTcTile);
         const bool partly = p0 + static_cast<int32_t>(kTcTile) > s.ctx;  // some row may not see it all

@@ -22,8 +22,10 @@ constexpr float kVfUnit = 17592186044416.f;  // 2^44
 __device__ __forceinline__ float probability(float x) { return fminf(fmaxf(x, 0.f), 1.f); }  // NaN: 0
 
 struct VerifyShared {
-  long long warp[2][kVfWarps];  // sums of the warps' parts of a row, this pass and the one before
-  long long cta[2];             // and of the CTA's
+  // Sums of the warps' parts of a row, and the CTA's.  Three slots: the one that is kept,
+  // the one that was written last (others may still read it), and the next.
+  long long warp[3][kVfWarps];
+  long long cta[3];
   long long part[kVfWarps];
 };
 
@@ -116,7 +118,6 @@ __device__ __forceinline__ long long vf_sum(VerifyShared& sh, uint32_t buf, cons
   long long total = 0;
 #pragma unroll
   for (uint32_t r = 0; r < C; ++r) total += C == 1 ? sh.cta[buf] : remote_ll(&sh.cta[buf], r);
-  vf_sync<C>();  // the slot may be written again
   return total;
 }
 
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) k_kv_verify(const VerifyArgs a)
   const uint32_t from = clip((rank * kVfWarps + warp) * part), to = clip(from + part);
 
   int32_t node = -1;
-  uint32_t count = 0, keep = 0;
+  uint32_t count = 0, keep = 0, last = 0;
   long long total = -1;  // of the weights that a token would be drawn by, in slot `keep`; -1: not known
   Left f = {p, q, scale, gone, 0u};
   for (int32_t t = 0; t < n; ++t) {
@@ -188,9 +189,10 @@ __global__ void __launch_bounds__(kVfThreads, 4) k_kv_verify(const VerifyArgs a)
       if (tid == 0) gone[f.depth] = x;
       __syncthreads();
       ++f.depth;
-      const long long z = vf_sum<C, VEC>(sh, keep ^ 1u, f, from, to);
+      last = keep != last ? 3 - keep - last : (keep + 1) % 3;
+      const long long z = vf_sum<C, VEC>(sh, last, f, from, to);
       if (z > 0) {
-        keep ^= 1u;
+        keep = last;
         total = z;
         if (tid == 0) scale[f.depth - 1] = static_cast<float>(__ddiv_rn(17592186044416.0, static_cast<double>(z)));
         __syncthreads();
@@ -199,7 +201,10 @@ __global__ void __launch_bounds__(kVfThreads, 4) k_kv_verify(const VerifyArgs a)
       }
     }
   }
-  if (total < 0) total = vf_sum<C, VEC>(sh, keep, f, from, to);
+  if (total < 0) {
+    keep = last = keep != last ? 3 - keep - last : (keep + 1) % 3;
+    total = vf_sum<C, VEC>(sh, last, f, from, to);
+  }
   if (rank == 0) {
     for (uint32_t t = count + tid; t < T; t += kVfThreads) a.path[static_cast<uint64_t>(b) * T + t] = -1;
     if (tid == 0) a.n_accept[b] = static_cast<int32_t>(count);
