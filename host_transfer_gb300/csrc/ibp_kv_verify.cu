@@ -11,13 +11,14 @@
 // depend on the order, so neither do the choices.  What is left after several
 // rejections is computed anew from the rows (m subtractions and products an element)
 // and not stored.  Bound by latency for few sequences, by DRAM for many.
+#include <type_traits>
+
 #include "ibp_kv_serve.cuh"
 
 namespace ibp {
 
 constexpr int kVfThreads = 256;
 constexpr uint32_t kVfWarps = kVfThreads / 32;
-constexpr float kVfUnit = 17592186044416.f;  // 2^44
 
 __device__ __forceinline__ float probability(float x) { return fminf(fmaxf(x, 0.f), 1.f); }  // NaN: 0
 
@@ -39,21 +40,38 @@ struct Left {
   __device__ __forceinline__ float drawn(uint32_t i, float qi, uint32_t k) const {
     return q ? qi : (static_cast<int32_t>(i) == x[k] ? 1.f : 0.f);
   }
-  // of element i, whose probabilities are pi and qi
-  __device__ __forceinline__ float operator()(uint32_t i, float pi, float qi) const {
+  // of element i, whose probabilities are pi and qi; DEPTH: what depth is, 2 for more
+  template <uint32_t DEPTH>
+  __device__ __forceinline__ float of(uint32_t i, float pi, float qi) const {
     float v = probability(pi);
-    if (depth == 0) return v;
+    if (DEPTH == 0) return v;
     qi = probability(qi);
     v = fmaxf(__fsub_rn(v, drawn(i, qi, 0)), 0.f);
-    for (uint32_t k = 1; k < depth; ++k) v = fmaxf(__fsub_rn(__fmul_rn(v, scale[k - 1]), drawn(i, qi, k)), 0.f);
+    if (DEPTH > 1)
+      for (uint32_t k = 1; k < depth; ++k) v = fmaxf(__fsub_rn(__fmul_rn(v, scale[k - 1]), drawn(i, qi, k)), 0.f);
     return v;
   }
   __device__ __forceinline__ float operator()(uint32_t i) const {
-    return (*this)(i, __ldg(p + i), q && depth ? __ldg(q + i) : 0.f);
+    const float pi = __ldg(p + i);
+    return depth ? of<2>(i, pi, q ? __ldg(q + i) : 0.f) : of<0>(i, pi, 0.f);
   }
 };
 
-__device__ __forceinline__ long long whole(float w) { return __float2ll_rn(__fmul_rn(w, kVfUnit)); }
+// rint(w 2^44) of a weight in [0, 1] as high 2^23 + low: high = rint(w 2^21), what is left
+// is exact and low its rounding, to even like the whole's since high 2^23 is.  Whole numbers
+// below 2^22 are the last bits of a float of 1.5 2^23 more.  (A conversion to 64 bits
+// goes through the double-precision pipe: 25 % of the kernel's time.)
+__device__ __forceinline__ void whole_parts(float w, int32_t& high, int32_t& low) {
+  const float h = __fmaf_rn(w, 0x1p21f, 12582912.f);
+  const float rest = __fmaf_rn(__fadd_rn(h, -12582912.f), -0x1p-21f, w);
+  high += __float_as_int(h) - 0x4B400000;
+  low += __float_as_int(__fmaf_rn(rest, 0x1p44f, 12582912.f)) - 0x4B400000;
+}
+__device__ __forceinline__ long long whole(float w) {
+  int32_t high = 0, low = 0;
+  whole_parts(w, high, low);
+  return (static_cast<long long>(high) << 23) + low;
+}
 
 __device__ __forceinline__ long long warp_total(long long s) {
 #pragma unroll
@@ -82,31 +100,46 @@ __device__ __forceinline__ void vf_sync() {
 template <uint32_t C, bool VEC>
 __device__ __forceinline__ long long vf_sum(VerifyShared& sh, uint32_t buf, const Left& f, uint32_t from, uint32_t to) {
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-  long long s = 0;
-  if (VEC) {
-    constexpr uint32_t kFly = 4;  // 16-byte reads of each row under way
-    const bool two = f.q && f.depth;
-    for (uint32_t i0 = from + 4 * lane; i0 < to; i0 += 128 * kFly) {
-      float4 x[kFly], y[kFly];
+  // A lane has at most 2^18 / (8 * 256) elements of up to 2^21 and +-2^22: 32 bits hold its sums.
+  static_assert(IBP_VERIFY_MAX_VOCAB / (8 * kVfThreads) <= 256, "");
+  int32_t high = 0, low = 0;
+  auto sum = [&](auto depth) {
+    constexpr uint32_t D = decltype(depth)::value;
+    const bool two = D && f.q;
+    if (VEC) {
+      constexpr uint32_t kFly = 4;  // 16-byte reads of each row under way
+      for (uint32_t i0 = from + 4 * lane; i0 < to; i0 += 128 * kFly) {
+        float4 x[kFly], y[kFly];
 #pragma unroll
-      for (uint32_t u = 0; u < kFly; ++u) {
-        const uint32_t i = i0 + 128 * u;
-        x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < to) {
-          x[u] = __ldg(reinterpret_cast<const float4*>(f.p + i));
-          if (two) y[u] = __ldg(reinterpret_cast<const float4*>(f.q + i));
+        for (uint32_t u = 0; u < kFly; ++u) {
+          const uint32_t i = i0 + 128 * u;
+          x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < to) {
+            x[u] = __ldg(reinterpret_cast<const float4*>(f.p + i));
+            if (two) y[u] = __ldg(reinterpret_cast<const float4*>(f.q + i));
+          }
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < kFly; ++u) {
+          const uint32_t i = i0 + 128 * u;  // past the end all weights are zeros
+          whole_parts(f.template of<D>(i, x[u].x, y[u].x), high, low);
+          whole_parts(f.template of<D>(i + 1, x[u].y, y[u].y), high, low);
+          whole_parts(f.template of<D>(i + 2, x[u].z, y[u].z), high, low);
+          whole_parts(f.template of<D>(i + 3, x[u].w, y[u].w), high, low);
         }
       }
-#pragma unroll
-      for (uint32_t u = 0; u < kFly; ++u) {
-        const uint32_t i = i0 + 128 * u;
-        if (i < to) s += (whole(f(i, x[u].x, y[u].x)) + whole(f(i + 1, x[u].y, y[u].y))) + (whole(f(i + 2, x[u].z, y[u].z)) + whole(f(i + 3, x[u].w, y[u].w)));
-      }
-    }
-  } else {
+    } else {
 #pragma unroll 8
-    for (uint32_t i = from + lane; i < to; i += 32) s += whole(f(i));
-  }
+      for (uint32_t i = from + lane; i < to; i += 32) whole_parts(f.template of<D>(i, __ldg(f.p + i), two ? __ldg(f.q + i) : 0.f), high, low);
+    }
+  };
+  if (f.depth == 0)
+    sum(std::integral_constant<uint32_t, 0>{});
+  else if (f.depth == 1)
+    sum(std::integral_constant<uint32_t, 1>{});
+  else
+    sum(std::integral_constant<uint32_t, 2>{});
+  long long s = (static_cast<long long>(high) << 23) + low;
   s = warp_total(s);
   if (lane == 0) sh.warp[buf][warp] = s;
   __syncthreads();
