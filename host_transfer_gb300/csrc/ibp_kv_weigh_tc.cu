@@ -81,6 +81,24 @@ __device__ __forceinline__ void wt_rows(uint32_t tile, uint32_t first_row, const
   }
 }
 
+// The same with every row and dimension there, lane i's row at `row`: next to nothing to
+// compute, since four warps have a block of 128 rows to keep up with.
+template <uint32_t DP>
+__device__ __forceinline__ void wt_sure_rows(uint32_t tile, uint32_t first_row, const char* row) {
+  constexpr uint32_t kChunks = DP / 8, kPer = 32 / kChunks, kTurns = 8 / kPer;  // instructions after which the order repeats
+  const uint32_t lane = threadIdx.x & 31u, c = lane % kChunks, r0 = lane / kChunks;
+  uint32_t dst[kTurns];
+#pragma unroll
+  for (uint32_t i = 0; i < kTurns; ++i)
+    dst[i] = tile + (c / 8) * 128 * 128 + (first_row + r0 + i * kPer) * 128 + (((c & 7u) ^ ((r0 + i * kPer) & 7u)) << 4);
+  const uint64_t mine = reinterpret_cast<uint64_t>(row);
+#pragma unroll
+  for (uint32_t j = 0; j < kChunks; ++j) {
+    const char* p = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, mine, j * kPer + r0)) + c * 16;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst[j % kTurns] + j / kTurns * 8 * 128), "l"(p) : "memory");
+  }
+}
+
 template <uint32_t DP, bool FOUR, bool F16>
 __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_constant__ WtArgs w) {
   using S = WtShape<DP>;
@@ -221,8 +239,12 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
         ok = tc::bar_wait(tc::s32(&sh.q_empty[st]), (fill / kWtStages & 1u) ^ 1u, stop, w.limit);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        wt_rows<DP>(q_sm + st * S::kTile, r & 96u, a.q + static_cast<int64_t>(b) * a.q_seq,
-                    on ? static_cast<int64_t>(t) * a.q_token + static_cast<int64_t>(head) * a.q_head : kWtNone, a.dim, x.q16);
+        const char* q = a.q + static_cast<int64_t>(b) * a.q_seq;
+        const int64_t off = static_cast<int64_t>(t) * a.q_token + static_cast<int64_t>(head) * a.q_head;
+        if (x.q16 && a.dim == DP)
+          wt_sure_rows<DP>(q_sm + st * S::kTile, r & 96u, q + off);  // rows past the end: the first one, which adds nothing
+        else
+          wt_rows<DP>(q_sm + st * S::kTile, r & 96u, q, on ? off : kWtNone, a.dim, x.q16);
         cp_commit();
         const float back = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
         sh.back[st][r] = back;
@@ -310,7 +332,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
         const uint32_t col = tmem + lanes + (slot * 2 + m) * 128;
         float y[2][32];
         tc::ld32(y[0], col);
-        float block[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t block[2] = {0, 0};  // two sums of two lanes
+        const uint64_t scale2 = tc::two(scale, scale);
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {
           float(&v)[32] = y[c & 1u];
@@ -321,30 +344,42 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
             tc::fence_before();
             tc::bar_arrive(tc::s32(&sh.s_empty[m][slot]));
           }
+          // two rows' exponentials; those that are not wanted are dropped, not multiplied away
+          auto pair = [&](uint32_t i, uint64_t back, bool on0, bool on1) {
+            float p, q;
+            tc::split(tc::fma2(tc::two(v[i], v[i + 1]), scale2, back), p, q);
+            p = tc::ex2(p), q = tc::ex2(q);
+            block[i / 2 & 1u] = tc::add2(block[i / 2 & 1u], tc::two(on0 ? p : 0.f, on1 ? q : 0.f));
+          };
+          const ulonglong2* bk = reinterpret_cast<const ulonglong2*>(&sh.back[st][32 * c]);
           if (open && sh.plain[st][c]) {
 #pragma unroll
             for (uint32_t i = 0; i < 32; i += 4) {
-              const float4 bk = *reinterpret_cast<const float4*>(&sh.back[st][32 * c + i]);
-              block[0] += tc::ex2(__fmaf_rn(v[i], scale, bk.x));
-              block[1] += tc::ex2(__fmaf_rn(v[i + 1], scale, bk.y));
-              block[2] += tc::ex2(__fmaf_rn(v[i + 2], scale, bk.z));
-              block[3] += tc::ex2(__fmaf_rn(v[i + 3], scale, bk.w));
+              const ulonglong2 x4 = bk[i / 4];
+              pair(i, x4.x, true, true);
+              pair(i + 2, x4.y, true, true);
             }
           } else if (open) {
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) {
-              const float bk = sh.back[st][32 * c + i], p = tc::ex2(__fmaf_rn(v[i], scale, bk));
-              block[i & 3u] += bk == -INFINITY ? 0.f : p;
+            for (uint32_t i = 0; i < 32; i += 4) {
+              const ulonglong2 x4 = bk[i / 4];
+              const float* f = &sh.back[st][32 * c + i];
+              pair(i, x4.x, f[0] != -INFINITY, f[1] != -INFINITY);
+              pair(i + 2, x4.y, f[2] != -INFINITY, f[3] != -INFINITY);
             }
           } else {
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) {
-              const float p = tc::ex2(__fmaf_rn(v[i], scale, sh.back[st][32 * c + i]));
-              block[i & 3u] += sh.seen[st][m][warp & 3u][32 * c + i] >> lane & 1u ? p : 0.f;
+            for (uint32_t i = 0; i < 32; i += 4) {
+              const ulonglong2 x4 = bk[i / 4];
+              const uint4 seen = *reinterpret_cast<const uint4*>(&sh.seen[st][m][warp & 3u][32 * c + i]);
+              pair(i, x4.x, seen.x >> lane & 1u, seen.y >> lane & 1u);
+              pair(i + 2, x4.y, seen.z >> lane & 1u, seen.w >> lane & 1u);
             }
           }
         }
-        total += (block[0] + block[1]) + (block[2] + block[3]);
+        float s0, s1;
+        tc::split(tc::add2(block[0], block[1]), s0, s1);
+        total += s0 + s1;
         __syncwarp();
         if (lane == 0) tc::bar_arrive(tc::s32(&sh.q_empty[st]));
       }
