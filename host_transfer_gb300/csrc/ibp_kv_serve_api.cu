@@ -47,7 +47,7 @@ int rows4_of(Kv4Rows* r, const ibp_kv4_pages* k, const ibp_kv4_pages* v, uint32_
   if (rc != IBP_OK) return rc;
   if (dtype > IBP_KV_F16) return refuse("dtype is neither IBP_KV_BF16 nor IBP_KV_F16");
   if (!alike(k, v)) return refuse("k and v pages differ in shape");
-  if (T == 0 || T > 0x7FFFFF00u) return refuse("T outside [1, 2^31 - 256]");
+  if (T == 0 || T > (1u << 30)) return refuse("T outside [1, 2^30]");
   r->table = seqs->table, r->lens = seqs->lens, r->n_rows = n_rows, r->status = status;
   if (!resolve(r->table, device, seqs->max_pages == 0) || !resolve(r->lens, device) ||
       !resolve(r->n_rows, device, true) || !resolve(r->status, device, true))
@@ -95,12 +95,13 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 // 89 / 100 / -, 64 rows 160 / 98 / -, 256 rows 580 / 175 / 217, 512 rows 1120 / 330 /
 // 297, 1024 rows 2230 / 650 / 455; one cache of 65536 tokens: 4 rows 48 / 72, 64 rows 115 /
 // 70; one of 777: 64 rows 17 / 26.
+// Decoding once wants scratch for the whole batch in 16 bits: not beyond 4 GB.
 enum Path { kFew, kCodes, kDecoded };
-constexpr uint64_t kFewRows = 32, kCodesRows = 256;
+constexpr uint64_t kFewRows = 32, kCodesRows = 256, kDecodedBytes = 4ull << 30;
 
 Path path_of(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint64_t tokens, int device) {
   if (rows <= kFewRows || !kv4_tree_takes(n_seqs, kv_heads, rows, dim, tokens, device)) return kFew;
-  return rows <= kCodesRows ? kCodes : kDecoded;
+  return rows <= kCodesRows || kv4_expand_workspace(n_seqs, tokens, kv_heads, dim) > kDecodedBytes ? kCodes : kDecoded;
 }
 
 }  // namespace

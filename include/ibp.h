@@ -767,7 +767,7 @@ typedef struct ibp_kv4_pages {
 
 /*
  * Puts keys and values into the cache: row t < n of sequence b, n = n_new[b]
- * (NULL: T), becomes position lens[b] - n + t, so the lengths count the new tokens
+ * (NULL: T <= 2^30), becomes position lens[b] - n + t, so the lengths count the new tokens
  * already.  The pages that are written must not be shared.  Rows whose position is
  * below 0 or whose page id is out of range are not stored and record IBP_ERANGE, as
  * does an n outside [0, T] (read as the nearer end).
@@ -795,7 +795,7 @@ int ibp_kv4_load(const ibp_kv4_pages* k_pages, const ibp_kv4_pages* v_pages, uin
  *
  * ws       ibp_kv4_attention_workspace bytes.  Large calls of more than 256 rows a
  *          kv head (T * q_heads / kv_heads) and dim <= 128 decode the cache once,
- *          so theirs holds the sequences in 16 bits.
+ *          so theirs holds the sequences in 16 bits where that is at most 4 GB.
  */
 int ibp_kv4_attention(const ibp_kv4_pages* k, const ibp_kv4_pages* v, uint32_t dtype, const ibp_kv_seqs* seqs,
                       const void* q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride, uint32_t T,
