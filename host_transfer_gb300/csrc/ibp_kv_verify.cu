@@ -218,7 +218,9 @@ __global__ void __launch_bounds__(kVfThreads, 4) k_kv_verify(const VerifyArgs a)
       f.depth = 0;
       total = -1;
     } else {
-      // every thread is past the loads of the entry that is written (it is not read before depth grows)
+      // A warp behind may still read entry 0: the test of a token that was accepted behind a
+      // rejection, whose node now rejects its first.
+      __syncthreads();
       if (tid == 0) gone[f.depth] = x;
       __syncthreads();
       ++f.depth;

@@ -436,6 +436,22 @@ def test_verify_many_siblings(V, certain):
     run_verify(p, tokens, u, None if certain else q, parents)
 
 
+@pytest.mark.parametrize("V", [8, 5000, 20000])
+def test_verify_rejections_on_both_sides_of_an_acceptance(V):
+    """A token is accepted behind a rejected one, and then its child with the same token is
+    rejected: the rejected tokens are listed anew while the first list may still be read."""
+    B, T = 40, 12
+    rng = np.random.default_rng(V)
+    p = rng.random((B, T + 1, V)).astype(np.float32) ** 4
+    p /= p.sum(-1, keepdims=True)
+    # four times: a token rejected, one accepted, and that one again behind itself rejected
+    tokens = np.tile(np.array([1, 2, 2, 1, 3, 3], np.int32), (B, T // 6))
+    parents = np.tile(np.array([[-1, -1, 1, 1, 1, 4, 4, 4, 7, 7, 7, 10]], np.int32), (B, 1))
+    u = np.tile(np.array([1, 0, 1], np.float32), (B, T // 3))
+    u = np.concatenate([u, rng.random((B, 1), np.float32)], 1)
+    assert (run_verify(p, tokens, u, None, parents)[1] == 4).all()
+
+
 def test_verify_no_drafts_and_many():
     p, tokens, u, q, _ = draft(3, 5, 100, False, 1)
     for n in ([0, 0, 0], [5, 2, 0], [7, -1, 3]):
