@@ -31,7 +31,17 @@
 // DRAM 1.5 times, not twice.
 //
 // The same kernel serves caches held in 4 bits (tc_load4): codes are decoded on their
-// way into the ring, which the tensor core reads as before.
+// way into the ring, which the tensor core reads as before.  Eight warps do so, since
+// a tile's 32768 elements are 1100 instructions a scheduler for four, with nothing to
+// hide their latencies; more than thirteen warps in all would leave the softmax less than
+// 128 registers a thread.  Measured: the drafts of 13 tokens over 8 caches named at
+// tc_load4, 108 MB of codes and scales, 85 us with cold caches (1.3 TB/s; the same
+// shape in 16 bits, 384 MB, 80 us).  Neither bytes nor products bound it: about 2900 cycles
+// a tile, of which the tensor core works 1030, a loader warp 1500 to 2000 and a softmax
+// warp 2400, each of them waiting for another at times; issue slots are 42 % used.  Two
+// things that did not help: 64 of the 128 lanes of TMEM on each half of a tile's tokens
+// (85 us), and O rescaled only after a growth by 2^8 (85 us, error 1.30 to 1.36 of the
+// result's rounding).
 //
 // Measured on one GB300: 16 ragged caches of up to 32768 tokens, 8 kv heads of 128
 // (1.48 GB): 64 rows a head 233 us (6.4 TB/s, 0.94 of the copy rate), 512 rows
@@ -453,32 +463,37 @@ __device__ __forceinline__ void tc_load4(const TcArgs& t, TcShared& sh, uint64_t
   fetch(spot, raw[1]);
   next_spot(spot);
   bool ok = true;
-  for (uint64_t i = 0; i < n && ok; i += 2) {
+  // One tile a round, the next one's codes moved up: with two rounds written out the
+  // loop and the softmax's do not stay in the instruction cache (104 us against 85 us for
+  // drafts of 13 tokens, 8 ragged caches of up to 16384, 8 kv heads of 4 query heads of 128).
+#pragma unroll 1
+  for (uint64_t i = 0; i < n && ok; ++i) {
+    const uint32_t f = static_cast<uint32_t>(2 * i) + kv, slot = f % S::kSlots;
+    if (lane == 0) ok = tc::bar_wait(tc::s32(&sh.empty[slot]), (f / S::kSlots & 1u) ^ 1u, stop, t.limit);
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    if (!ok) break;
+    unsigned char* dst = ring_sm + slot * S::kTileBytes;
 #pragma unroll
-    for (uint32_t u = 0; u < 2; ++u) {
-      if (i + u >= n) break;
-      const uint32_t f = static_cast<uint32_t>(2 * (i + u)) + kv, slot = f % S::kSlots;
-      if (lane == 0) ok = tc::bar_wait(tc::s32(&sh.empty[slot]), (f / S::kSlots & 1u) ^ 1u, stop, t.limit);
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-      if (!ok) break;
-      unsigned char* dst = ring_sm + slot * S::kTileBytes;
+    for (uint32_t g = 0; g < DP / 32; ++g) {
+      const quad::Pair<F16> p(EVEN ? __byte_perm(raw[0].s[g / 2], 0, g & 1u ? 0x3232 : 0x1010) : __byte_perm(raw[0].s[g], 0, 0x1010), raw[0].good);
+      const uint32_t w[4] = {raw[0].w[g].x, raw[0].w[g].y, raw[0].w[g].z, raw[0].w[g].w};
 #pragma unroll
-      for (uint32_t g = 0; g < DP / 32; ++g) {
-        const quad::Pair<F16> p(EVEN ? __byte_perm(raw[u].s[g / 2], 0, g & 1u ? 0x3232 : 0x1010) : __byte_perm(raw[u].s[g], 0, 0x1010), raw[u].good);
-        const uint32_t w[4] = {raw[u].w[g].x, raw[u].w[g].y, raw[u].w[g].z, raw[u].w[g].w};
-#pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) {
-          const uint32_t c = g * 4 + e;
-          *reinterpret_cast<uint4*>(dst + (c / 8) * S::kPanel + turn[c & 7u]) =
-              make_uint4(quad::decode<F16, 0>(w[e], p, magic), quad::decode<F16, 1>(w[e], p, magic),
-                         quad::decode<F16, 2>(w[e], p, magic), quad::decode<F16, 3>(w[e], p, magic));
-        }
+      for (uint32_t e = 0; e < 4; ++e) {
+        const uint32_t c = g * 4 + e;
+        *reinterpret_cast<uint4*>(dst + (c / 8) * S::kPanel + turn[c & 7u]) =
+            make_uint4(quad::decode<F16, 0>(w[e], p, magic), quad::decode<F16, 1>(w[e], p, magic),
+                       quad::decode<F16, 2>(w[e], p, magic), quad::decode<F16, 3>(w[e], p, magic));
       }
-      tc::fence_async();
-      tc::bar_arrive(tc::s32(&sh.full[slot]));
-      fetch(spot, raw[u]);
-      next_spot(spot);
     }
+    tc::fence_async();
+    tc::bar_arrive(tc::s32(&sh.full[slot]));
+    raw[0] = raw[1];
+    // here and not at the round's end, where it would wait for the codes just asked for
+#pragma unroll
+    for (uint32_t g = 0; g < DP / 32; ++g)
+      asm volatile("" : "+r"(raw[0].w[g].x), "+r"(raw[0].w[g].y), "+r"(raw[0].w[g].z), "+r"(raw[0].w[g].w), "+r"(raw[0].s[EVEN ? g / 2 : g]));
+    fetch(spot, raw[1]);
+    next_spot(spot);
   }
 }
 
