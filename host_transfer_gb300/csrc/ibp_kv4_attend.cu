@@ -20,6 +20,15 @@
 //
 // Decoding is what counts beside the cache's bytes: 12 instructions for 8 elements
 // (a shift, a mask with the exponent put in, one fused multiply-add a pair).
+//
+// Measured on one GB300: 32 ragged caches of up to 32768 tokens, 8 kv heads of 8 query
+// heads of 128, one token each (798 MB): 200 us with cold caches, 4.0 TB/s; the same
+// caches in 16 bits, 3.5 times the bytes, take 422 us.  16 tokens of K and V cost about 440
+// warp instructions, of which 192 decode, 32 are products and most others move operands
+// and find maxima: issue, not DRAM, is what bounds it.  A single cache of 777 tokens: 15 us
+// cold, 9 us warm, the latency of table, codes and a second launch for the join.
+// Stages by bulk copies instead of 16-byte ones were 2 % faster for 8 rows and 6 % slower
+// for 16, and were not kept.
 #include <type_traits>
 
 #include "ibp_kv_tree.cuh"
@@ -36,7 +45,7 @@ template <uint32_t DP, uint32_t NT>
 struct Quad {
   // Tokens of a step: what a step costs besides decoding and products (maxima over the
   // lanes, bookkeeping) is shared by two blocks of 16 where the registers allow it.
-    static constexpr uint32_t kMma = DP == 256 ? 1 : 2;
+  static constexpr uint32_t kMma = DP == 256 ? 1 : 2;
   static constexpr uint32_t kSub = 16 * kMma;
   static constexpr uint32_t kTile = kSub * kQdWarps;       // a step of every warp
   static constexpr uint32_t kRows = 8 * NT;

@@ -90,14 +90,15 @@ int queries_of(AttendArgs* a, uint32_t heads, uint32_t page_tokens, uint64_t n_p
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Which kernel takes a call.  Rows: drafted tokens times query heads of a kv head.
-// Measured (us; few rows / tensor cores on codes / decoded once, then tensor cores),
-// 8 ragged caches of up to 16384 tokens, 8 kv heads of 128: 16 rows 58 / 100 / -, 32 rows
-// 89 / 100 / -, 64 rows 160 / 98 / -, 256 rows 580 / 175 / 217, 512 rows 1120 / 330 /
-// 297, 1024 rows 2230 / 650 / 455; one cache of 65536 tokens: 4 rows 48 / 72, 64 rows 115 /
-// 70; one of 777: 64 rows 17 / 26.
+// Measured (us, cold; few rows / tensor cores on codes / decoded once, then tensor cores),
+// 8 ragged caches of up to 16384 tokens, 8 kv heads of 128: 16 rows 58 / 83 / 195, 24 rows
+// 89 / 83 / 195, 64 rows 159 / 85 / 194, 128 rows 294 / 87 / 196, 256 rows - / 149 / 218, 512
+// rows - / 263 / 298, 1024 rows - / 527 / 456; one cache of 65536 tokens: 16 rows 52 / 67, 24
+// rows 71 / 67, 64 rows 116 / 67; 64 of up to 1024: 16 rows 59 / 95, 24 rows 97 / 97, 48 rows
+// 136 / 95; one of 777: 64 rows 22 / 28.
 // Decoding once wants scratch for the whole batch in 16 bits: not beyond 4 GB.
 enum Path { kFew, kCodes, kDecoded };
-constexpr uint64_t kFewRows = 32, kCodesRows = 256, kDecodedBytes = 4ull << 30;
+constexpr uint64_t kFewRows = 16, kCodesRows = 512, kDecodedBytes = 4ull << 30;
 
 Path path_of(uint32_t n_seqs, uint32_t kv_heads, uint64_t rows, uint32_t dim, uint64_t tokens, int device) {
   if (rows <= kFewRows || !kv4_tree_takes(n_seqs, kv_heads, rows, dim, tokens, device)) return kFew;

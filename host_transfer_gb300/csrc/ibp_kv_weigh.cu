@@ -6,8 +6,12 @@
 // tokens, where there are fewer heads than warps) and add up their rows in registers;
 // the warps' sums are added in a fixed order, so results do not depend on how threads
 // run.  S^T = K Q^T as in the attention kernels: a lane holds neighbouring dimensions
-// of a token's key, and queries are laid out to match.  Bound by the keys' bytes for
-// single tokens, by products and exponentials for prompts.
+// of a token's key, and queries are laid out to match.
+//
+// Measured on one GB300: 32 ragged caches of up to 16384 tokens in 4 bits, 8 kv heads of 4
+// query heads of 128, one token each (202 MB): 91 us with cold caches, 2.2 TB/s.  16
+// tokens of a head cost about 270 warp instructions, of which 96 decode: issue bounds it.
+// Loads straight into registers, without the ring, took 325 us.
 #include <type_traits>
 
 #include "ibp_kv_serve.cuh"
@@ -15,8 +19,12 @@
 namespace ibp {
 
 constexpr uint32_t kWgWarps = 4;
-constexpr uint32_t kWgTiles = 4;  // of a CTA's warps
-constexpr uint64_t kWgMany = 64;  // rows a kv head from which the tensor cores take over
+constexpr uint32_t kWgTiles = 2;  // of a CTA's warps: 93 us for the batch above with 1, 91 with 2, 95 with 4
+// Rows a kv head from which the tensor cores take over (ibp_kv_weigh_tc.cu).  Measured (us, few
+// rows / tensor cores): two caches of up to 8192 tokens in 16 bits, 8 kv heads: 52 rows 44 / 46,
+// 64 rows 48 / 44, 96 rows 65 / 42; eight of up to 16384 in 4 bits, which the few-row kernel
+// reads faster: 52 rows 185 / 259, 64 rows 210 / 251, 96 rows 302 / 235.
+constexpr uint64_t kWgMany = 64, kWgMany4 = 80;
 
 // A warp's stage: the keys of 16 MT tokens of a head as the cache has them, the scales
 // of codes, and which of the tokens there are.
@@ -361,14 +369,16 @@ __global__ void __launch_bounds__(kWgWarps * 32, DP == 256 ? 3 : 4) k_kv_weigh(c
 
 int launch_kv_weigh(const WeighArgs& x, int device, cudaStream_t stream) {
   const AttendArgs& a = x.a;
-  if (a.dim <= 128 && static_cast<uint64_t>(a.T) * a.group >= kWgMany) return launch_kv_weigh_tc(x, device, stream);
+  if (a.dim <= 128 && static_cast<uint64_t>(a.T) * a.group >= (x.k4.codes ? kWgMany4 : kWgMany)) return launch_kv_weigh_tc(x, device, stream);
   const uint32_t dp = a.dim <= 64 ? 64 : (a.dim <= 128 ? 128 : 256);
   const bool four = x.k4.codes != nullptr;
   const uint32_t mt = four && dp < 256 ? 2 : 1;
-  // A warp takes all heads of its tokens where there are tokens enough to fill the GPU.
+  // A warp takes all heads of its tokens where there are tokens enough to fill the GPU (4-bit
+  // caches of up to 8192 tokens, 8 kv heads, 1 / 2 / 4 warps: one cache 20 / 17 / 15 us, four
+  // 22 / 20 / 26 us; 32 of up to 16384 95 / 95 / 112 us).
   const uint64_t all_runs = (static_cast<uint64_t>(x.width) + 16 * mt - 1) / (16 * mt) * a.n_seqs;
   uint32_t head_warps = 1;
-  while (head_warps < kWgWarps && head_warps < a.kv_heads && all_runs * head_warps < 16ull * sm_count(device)) head_warps *= 2;
+  while (head_warps < kWgWarps && head_warps < a.kv_heads && all_runs * head_warps < 8ull * sm_count(device)) head_warps *= 2;
   const uint32_t tokens = 16 * mt * (kWgWarps / head_warps);
   // A CTA walks a few tiles, so that what it begins with counts less; more would leave ragged
   // batches uneven.

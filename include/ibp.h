@@ -793,7 +793,7 @@ int ibp_kv4_load(const ibp_kv4_pages* k_pages, const ibp_kv4_pages* v_pages, uin
  * rules, with what the codes stand for as keys and values.  A position whose page id
  * is out of range reads as a zero key and value and records IBP_ERANGE.
  *
- * ws       ibp_kv4_attention_workspace bytes.  Large calls of more than 256 rows a
+ * ws       ibp_kv4_attention_workspace bytes.  Large calls of more than 512 rows a
  *          kv head (T * q_heads / kv_heads) and dim <= 128 decode the cache once,
  *          so theirs holds the sequences in 16 bits where that is at most 4 GB.
  */

@@ -259,10 +259,11 @@ def test_attention_over_long_caches(lens, T, hk, G, page, D, dt):
     ([300, 290] * 3, 17, 2, 8, 64, 128, True), ([200, 141, 141, 150] * 2, 141, 3, 1, 7, 64, False),
     ([170] * 12, 130, 2, 1, 16, 96, True), ([90, 700, 41] * 4, 40, 4, 1, 24, 32, True),
     ([300, 290] * 2, 40, 2, 8, 64, 128, True), ([310, 305, 301], 300, 2, 1, 5, 64, True),
-    ([150, 160, 100], 37, 3, 8, 16, 96, False),
+    ([150, 160, 100], 37, 3, 8, 16, 96, False), ([300, 290], 66, 2, 8, 64, 128, True),
+    ([600, 641], 600, 1, 1, 7, 64, False), ([310, 305, 301], 130, 2, 4, 5, 96, True), ([170] * 40, 9, 2, 2, 16, 128, True),
 ])
 def test_attention_of_many_rows(lens, T, hk, G, page, D, mask, dt):
-    """Calls for the tensor cores: on codes, and (above 256 rows) decoded once."""
+    """Calls for the tensor cores: on codes, and (above 512 rows) decoded once."""
     c = Cache(lens, T, hk, G, page, D, dt, seed=T, mask=mask)
     B = len(lens)
     assert -(-max(lens) // 128) * B * hk * -(-T * G // 16) >= 304, "work enough for the tensor cores"
@@ -883,10 +884,10 @@ def test_a_gradient_is_an_error():
         out.sum().backward()
 
 
-@pytest.mark.parametrize("T", [40, 300])
-def test_waits_that_run_out(T):
+@pytest.mark.parametrize("T,hk,G", [(40, 8, 2), (300, 4, 1), (300, 4, 2)])
+def test_waits_that_run_out(T, hk, G):
     """Every wait of the tensor-core kernels gives up: the status says so, and the next call is whole."""
-    c = Cache([300, 310, 333], T, 8 if T == 40 else 4, 2 if T == 40 else 1, 16, 64, seed=5)
+    c = Cache([300, 310, 333], T, hk, G, 16, 64, seed=5)
     want = c.attend()
     torch.cuda.synchronize()
     before = kv.ibp_kv_set_wait_limit(0)

@@ -46,8 +46,8 @@ def test_scratch_sizes(lib):
     assert size(1, 4, 16, 1, 8, 2, 64) < 1 << 16  # a part of each of a few blocks
     assert size(64, 1024, 64, 1, 64, 8, 128) < 1 << 30  # parts of the blocks that the GPU holds at once
     # many rows decode the cache once, but not one of more than 4 GB
-    assert size(4, 256, 64, 512, 8, 8, 128) > 4 * 256 * 64 * 8 * 128 * 4
-    assert size(64, 4096, 64, 512, 8, 8, 128) < 1 << 30
+    assert size(4, 256, 64, 1024, 8, 8, 128) > 4 * 256 * 64 * 8 * 128 * 4
+    assert size(64, 4096, 64, 1024, 8, 8, 128) < 1 << 30
 
 
 def test_refusals_without_gpu(lib):
