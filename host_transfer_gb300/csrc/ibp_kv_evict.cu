@@ -9,7 +9,7 @@
 //
 // Measured on one GB300: 8 sequences of 2063 positions 17 us, 32 of 65521 down to 8192 36 us
 // with cold caches (12.7 MB, 2 us at the copy rate).  Bound by latency: three digits of a
-// histogram, its joining and a cluster barrier each, then the placing.  A CTA's lanes hold
+// histogram, its joining and two cluster barriers each, then the placing.  A CTA's lanes hold
 // up to 8192 positions in registers, a cluster of eight 65536; what is longer is read again for
 // every digit.  One CTA or eight, us: 8192 positions 32 sequences 24 / 22, 256 30 / 93;
 // 16384 positions 32 sequences 46 / 24, 256 65 / 106; 32768 positions 32 sequences 85 / 28,

@@ -16,7 +16,7 @@
 // sequences over 131072 tokens 63 us with cold caches (46 to 49 us where the
 // probabilities have just been written), of which the rows that cannot be left out are 10.  Each
 // rejection is a walk over two rows that the next step waits for, and a cluster's row comes
-// out of few SMs: latency of the walks bounds it, about 3 us each.
+// out of few SMs: latency of the walks bounds it.
 //
 // CTAs of a sequence: 1 up to a vocabulary of 4096, 4 up to 16384, 8 beyond (64 trees of 15,
 // us with 1 / 4 / 8: 4096 20 / 24 / 24, 8192 28 / 24 / 26, 16384 40 / 26 / 26, 32768
