@@ -33,7 +33,8 @@ results and scratch are allocated for that stream.  Data errors go to a status
 word: the caller's own (``status``, an int32 device tensor) or the device's,
 read by ``ibp_kv_get_status`` (call it once before the first call is captured
 in a graph: it makes the word).  Nothing here has a backward pass: one that
-reaches an attention call raises an error.
+reaches an attention call, loaded keys and values or accumulated weights raises an
+error.
 """
 
 from __future__ import annotations
@@ -451,6 +452,25 @@ def _results(name: str, out: torch.Tensor, lse: torch.Tensor, q: torch.Tensor, k
     return out, lse
 
 
+class _NoBackwardOfOne(torch.autograd.Function):
+    """The same for a single result."""
+
+    @staticmethod
+    def forward(ctx, name, out, *inputs):
+        ctx.name = name
+        return out.view_as(out)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name} has no backward pass: detach its inputs, or call it under torch.no_grad()")
+
+
+def _result(name: str, out: torch.Tensor, *inputs: torch.Tensor):
+    if any(t.requires_grad for t in inputs) and torch.is_grad_enabled():
+        return _NoBackwardOfOne.apply(name, out, *inputs)
+    return out
+
+
 def _heads(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
     """(k pages, v pages, dtype, sequences) of an attention call."""
     kp, vp = _as_pages("k", k), _as_pages("v", v)
@@ -685,7 +705,7 @@ def ibp_kv4_load(k4, v4, table: torch.Tensor, lens: torch.Tensor, T: int, n_load
         seqs.table, seqs.lens = table.data_ptr(), lens.data_ptr()
         _check(lib.ibp_kv4_load(kp, vp, dt, seqs, T, None if n_load is None else n_load.data_ptr(), k.data_ptr(),
                                 v.data_ptr(), _status(status, device), handle), "ibp_kv4_load")
-    return k, v
+    return _results("ibp_kv4_load", k, v, k4[1], v4[1], v4[1])
 
 
 def _queries(q: torch.Tensor, seqs: _Seqs, dim: int, dtype, mask, n_draft):
@@ -825,6 +845,8 @@ def ibp_kv_weigh(q: torch.Tensor, k, table: torch.Tensor, lens: torch.Tensor, ls
         _floats("weights", weights, seqs.n_seqs, *weights.shape[1:2])
         return kp, _dtype(kind), seqs, rows, weights.shape[1], 1.0 / math.sqrt(kp.dim)
 
+    if inplace and weights.requires_grad and torch.is_grad_enabled():
+        raise ValueError("weights that require a gradient cannot be written in place")
     key = ("weigh", _form(q), _form4(k) if four else _form(k), _form(table), _form(lens), _form(lse), _form(weights),
            _form(mask), _form(n_draft))
     device = lse.device
@@ -841,7 +863,7 @@ def ibp_kv_weigh(q: torch.Tensor, k, table: torch.Tensor, lens: torch.Tensor, ls
         _check(call(kp, dt, seqs, q.data_ptr(), *rows, None if n_draft is None else n_draft.data_ptr(),
                     None if mask is None else mask.data_ptr(), usual if scale is None else scale, lse.data_ptr(),
                     weights.data_ptr(), out.data_ptr(), width, decay, _status(status, device), handle), "ibp_kv_weigh")
-    return out
+    return _result("ibp_kv_weigh", out, q, k[1] if four else k, lse, weights)
 
 
 def ibp_kv_evict(weights: torch.Tensor, lens: torch.Tensor, budget: int, keep_first: int = 0, keep_last: int = 0,
@@ -872,4 +894,4 @@ def ibp_kv_evict(weights: torch.Tensor, lens: torch.Tensor, budget: int, keep_fi
         _check(lib.ibp_kv_evict(weights.data_ptr(), width, lens.data_ptr(), n, budget, keep_first, keep_last,
                                 path.data_ptr(), n_draft.data_ptr(), n_keep.data_ptr(), out.data_ptr(),
                                 _status(status, device), handle), "ibp_kv_evict")
-    return path, n_draft, n_keep, out
+    return path, n_draft, n_keep, _result("ibp_kv_evict", out, weights)

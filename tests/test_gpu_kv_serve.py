@@ -528,6 +528,9 @@ def check_weigh(got, want, top, lse, rows, was, decay):
     # the tensor cores: fewer heads than CTAs, more, a head's blocks shared out
     ([300, 90], 70, 3, 1, 16, 64, False), ([700], 40, 1, 8, 24, 128, True), ([120, 300], 17, 10, 4, 7, 96, True),
     ([0, 600], 64, 8, 1, 64, 128, False), ([260], 130, 2, 2, 16, 32, True),
+    # work for clusters of two and of four
+    ([250, 0, 190, 97] * 5, 21, 1, 4, 16, 64, True), ([120, 260] * 5, 90, 3, 1, 16, 128, False),
+    ([180, 256, 33] * 6, 35, 1, 4, 16, 64, False), ([270, 140] * 5, 70, 5, 2, 24, 128, True),
 ])
 def test_weigh(lens, T, hk, G, page, D, mask, dt, four, inplace):
     c = Cache(lens, T, hk, G, page, D, dt, seed=D + T, mask=mask)
@@ -882,6 +885,20 @@ def test_a_gradient_is_an_error():
     out, lse = c.attend()
     with pytest.raises(RuntimeError, match="no backward"):
         out.sum().backward()
+    w = torch.ones((1, 50), device="cuda")
+    got = kv.ibp_kv_weigh(c.q, c.k, c.table, c.lens, lse.detach(), w)
+    with torch.no_grad():
+        assert torch.equal(got, kv.ibp_kv_weigh(c.q, c.k, c.table, c.lens, lse, w))
+    with pytest.raises(RuntimeError, match="no backward"):
+        got.sum().backward()
+    w.requires_grad_()
+    with pytest.raises(RuntimeError, match="no backward"):
+        kv.ibp_kv_evict(w, c.lens, 10)[3].sum().backward()
+    with pytest.raises(ValueError, match="in place"):
+        kv.ibp_kv_weigh(c.q.detach(), c.k, c.table, c.lens, lse.detach(), w, inplace=True)
+    scales = c.k[1].detach().requires_grad_()
+    with pytest.raises(RuntimeError, match="no backward"):
+        kv.ibp_kv4_load((c.k[0], scales), c.v, c.table, c.lens, 4)[0].sum().backward()
 
 
 @pytest.mark.parametrize("T,hk,G", [(40, 8, 2), (300, 4, 1), (300, 4, 2)])
