@@ -1,7 +1,7 @@
 // ibp_kv_weigh_tc.cu - the attention weight of cached tokens on the tensor cores
 // (tcgen05), for calls of many rows (prompts, large drafts).
 //
-// A cluster of eight CTAs takes 256 tokens of a sequence and shares out the kv heads, and
+// A cluster of CTAs takes 256 tokens of a sequence and shares out the kv heads, and
 // the row blocks where there are fewer heads than CTAs.  In a CTA
 //   four loader warps   write two tiles of 128 keys (once a head) and blocks of 128 queries
 //                       with the rows' logarithms of sums into shared memory;
@@ -14,13 +14,13 @@
 // finite in it needs no care.  Bound by the exponentials and the products, about alike:
 // 32768 and 4.2 million multiply-adds for 128 rows and 256 tokens, of 1024 cycles each.
 //
-// 256 tokens a CTA share a block of queries, which is what moves most; a cluster of eight
+// 256 tokens a CTA share a block of queries, which is what moves most; a cluster
 // shares the heads, so that the sum over heads needs no scratch and no atomics.
 //
 // Measured on one GB300: 511 queries a sequence, 32 heads on 8 kv heads of 128, two caches of
-// up to 8192 tokens in 16 bits: 126 us with cold caches, 0.41 PFLOP/s of products; the few-row
-// kernel takes 960 us.  128 rows of a CTA take about 3300 cycles; 15 clusters of eight
-// fit beside one another, so 120 of the 152 SMs work.
+// up to 8192 tokens in 16 bits: 132 us with cold caches, 0.39 PFLOP/s of products; the few-row
+// kernel takes 960 us.  128 rows of a CTA take about 4000 cycles, what a CTA begins and ends with
+// 13 us.
 //
 // Every wait has a limit, as in ibp_kv_tree.cuh.
 #include "ibp_kv_serve.cuh"
@@ -29,12 +29,12 @@
 namespace ibp {
 
 constexpr uint32_t kWtTokens = 256;   // of a CTA
-constexpr uint32_t kWtCluster = 8;
 constexpr uint32_t kWtStages = 4;     // blocks of queries in flight
 constexpr uint32_t kWtThreads = 256 + 32 + 128;
 
 struct WtArgs {
   WeighArgs x;
+  uint32_t cluster;        // CTAs
   uint32_t heads_at_once;  // CTAs of a cluster on different heads; the others share out row blocks
   long long limit;
 };
@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
   WtShared& sh = *reinterpret_cast<WtShared*>(sm + S::kBytes);
   static_assert(sizeof(WtShared) <= 20480, "shared");
   const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
-  const uint32_t rank = blockIdx.x % kWtCluster, first = blockIdx.x / kWtCluster * kWtTokens, b = blockIdx.y;
+  const uint32_t rank = blockIdx.x % w.cluster, first = blockIdx.x / w.cluster * kWtTokens, b = blockIdx.y;
+  const uint32_t share = kWtTokens / w.cluster;  // tokens that a CTA adds up at the end
   pdl_begin();
   const int32_t raw = a.lens[b], all = clamp_len(raw, a.page_tokens, a.max_pages);
   const int32_t len = all < static_cast<int32_t>(x.width) ? all : static_cast<int32_t>(x.width);  // weighed positions
@@ -130,8 +131,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
   const float* was = x.w + static_cast<uint64_t>(b) * x.width;
   float* out = x.w_out + static_cast<uint64_t>(b) * x.width;
   if (static_cast<int32_t>(first) >= len) {  // the same for the whole cluster
-    for (uint32_t i = rank * 32 + tid; tid < 32 && i < kWtTokens; i += 256)
-      if (first + i < x.width) out[first + i] = was[first + i];
+    const uint32_t i = first + rank * share + tid;
+    if (tid < share && i < x.width) out[i] = was[i];
     return;
   }
   if (tid == 0) {
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
   tc::fence_after();
   const uint32_t tmem = sh.tmem;
   volatile uint32_t* stop = &sh.stop;
-  const uint32_t head0 = rank % w.heads_at_once, part = rank / w.heads_at_once, parts = kWtCluster / w.heads_at_once;
+  const uint32_t head0 = rank % w.heads_at_once, part = rank / w.heads_at_once, parts = w.cluster / w.heads_at_once;
   const uint32_t blocks = (rows + 127) / 128, mine = blocks > part ? (blocks - part + parts - 1) / parts : 0;
   const uint32_t k_sm = base, q_sm = base + 2 * S::kTile;
 
@@ -400,13 +401,12 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
     tc::fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
-  // The cluster's CTAs each add up 32 tokens, in the CTAs' order.
+  // The cluster's CTAs each add up their share of the tokens, in the CTAs' order.
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (tid < 32) {
-    const uint32_t i = rank * 32 + tid;
+  if (tid < share) {
+    const uint32_t i = rank * share + tid;
     float s = 0.f;
-#pragma unroll
-    for (uint32_t c = 0; c < kWtCluster; ++c) {
+    for (uint32_t c = 0; c < w.cluster; ++c) {
       uint32_t addr = tc::s32(&sh.sums[i]);
       float v;
       asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(addr) : "r"(c));
@@ -434,14 +434,21 @@ static int launch(const WtArgs& w, int device, cudaStream_t stream) {
     if (device >= 0 && device < 64) ready[device].store(1, std::memory_order_release);
   }
   const uint32_t tiles = (w.x.width + kWtTokens - 1) / kWtTokens;
-  return kv_launch("k_kv_weigh_tc", kern, dim3(tiles * kWtCluster, w.x.a.n_seqs), kWtThreads, S::kSmem, kWtCluster, stream, w);
+  return kv_launch("k_kv_weigh_tc", kern, dim3(tiles * w.cluster, w.x.a.n_seqs), kWtThreads, S::kSmem, w.cluster, stream, w);
 }
 
 int launch_kv_weigh_tc(const WeighArgs& x, int device, cudaStream_t stream) {
   WtArgs w;
   w.x = x;
+  // Eight CTAs where all clusters of eight run at once (15 fit), else four, which leave fewer
+  // SMs idle and begin fewer times; two for a single block of rows, where beginning counts most.
+  // Measured (us with 2 / 4 / 8), 511 queries of 4 heads on 8 kv heads: one cache of 1024 tokens
+  // 153 / 83 / 48, one of 8192 153 / 83 / 99, two 155 / 132 / 126, eight 337 / 323 / 370, three of
+  // 16384 335 / 276 / 306; 16 queries: two of 8192 30 / 36 / 44, sixteen 114 / 149 / 230.
+  const uint64_t rows = static_cast<uint64_t>(x.a.T) * x.a.group, clusters = (x.width + kWtTokens - 1ull) / kWtTokens * x.a.n_seqs;
+  w.cluster = clusters * 10 <= static_cast<uint64_t>(sm_count(device)) ? 8 : (rows <= 128 ? 2 : 4);
   w.heads_at_once = 1;
-  while (w.heads_at_once < kWtCluster && 2 * w.heads_at_once <= x.a.kv_heads) w.heads_at_once *= 2;
+  while (w.heads_at_once < w.cluster && 2 * w.heads_at_once <= x.a.kv_heads) w.heads_at_once *= 2;
   w.limit = kv_tree_limit();
   const bool four = x.k4.codes != nullptr, f16 = x.a.f16;
   if (x.a.dim <= 64) {
