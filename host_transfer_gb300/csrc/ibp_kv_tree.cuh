@@ -31,10 +31,9 @@
 // DRAM 1.5 times, not twice.
 //
 // The same kernel serves caches held in 4 bits (tc_load4): codes are decoded on their
-// way into the ring, which the tensor core reads as before.  Eight warps do so, since
-// a tile's 32768 elements are 1100 instructions a scheduler for four, with nothing to
-// hide their latencies; more than thirteen warps in all would leave the softmax less than
-// 128 registers a thread.  Measured: the drafts of 13 tokens over 8 caches named at
+// way into the ring, which the tensor core reads as before.  Eight warps do so, a thread
+// for each token of K and of V, which makes thirteen in all and leaves the softmax 128
+// registers a thread (more than sixteen would leave it fewer).  Measured: the drafts of 13 tokens over 8 caches named at
 // tc_load4, 108 MB of codes and scales, 85 us with cold caches (1.3 TB/s; the same
 // shape in 16 bits, 384 MB, 80 us).  Neither bytes nor products bound it: about 2900 cycles
 // a tile, of which the tensor core works 1030, a loader warp 1500 to 2000 and a softmax

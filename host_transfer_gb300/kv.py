@@ -466,8 +466,9 @@ class _NoBackwardOfOne(torch.autograd.Function):
 
 
 def _result(name: str, out: torch.Tensor, *inputs: torch.Tensor):
-    if any(t.requires_grad for t in inputs) and torch.is_grad_enabled():
-        return _NoBackwardOfOne.apply(name, out, *inputs)
+    for t in inputs:
+        if t.requires_grad and torch.is_grad_enabled():
+            return _NoBackwardOfOne.apply(name, out, *inputs)
     return out
 
 
