@@ -79,7 +79,9 @@ __global__ void __launch_bounds__(kEvThreads) k_kv_evict(const EvictArgs a) {
   const float* w = a.w + static_cast<uint64_t>(b) * a.width;
   float* out = a.w_out + static_cast<uint64_t>(b) * a.width;
   int32_t* path = a.path + static_cast<uint64_t>(b) * a.budget;
-  const bool over = len > a.budget;
+  // A sequence longer than its weights is left alone: the path would name positions of the
+  // part that has weights, and ibp_kv_accept goes by the whole length.
+  const bool over = len > a.budget && raw == static_cast<int32_t>(len);
   if (rank == 0 && tid == 0) {
     a.n_draft[b] = over ? static_cast<int32_t>(len) : 0;
     a.n_keep[b] = over ? static_cast<int32_t>(a.budget) : 0;

@@ -876,7 +876,8 @@ int ibp_kv4_weigh(const ibp_kv4_pages* k, uint32_t dtype, const ibp_kv_seqs* seq
  * pool and frees the pages behind.  Sequences within the budget get n_draft =
  * n_keep = 0, which ibp_kv_accept leaves alone.  w_out[b] has the weights of the
  * tokens that stay at their new positions and 0 behind.  Lengths outside [0,
- * width] are cut to it and record IBP_ERANGE.
+ * width] record IBP_ERANGE and leave the sequence alone: n_draft = n_keep = 0, and
+ * w_out[b] is w[b] (0 for a length below 0).
  *
  * w, w_out  n_seqs x width floats, not overlapping.
  * path      n_seqs x budget, unused entries -1; n_draft, n_keep  per sequence.

@@ -173,6 +173,9 @@ def evict(w, lens, budget, keep_first, keep_last):
     out = np.zeros_like(w)
     for b in range(B):
         n = int(lens[b])
+        if not 0 <= n <= width:  # left alone
+            out[b] = w[b] if n > width else 0
+            continue
         kept = list(range(n))
         if n > budget:
             forced = [i for i in kept if i < keep_first or i >= n - keep_last]
