@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kAtWarps * 32)
   if (!a.cluster) return;
   // The splits of an item are a cluster: each CTA joins every a.splits-th row out
   // of the others' shared memory.
-  cluster_sync();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   for (uint32_t r = split + a.splits * warp; r < it.rows; r += a.splits * WPI) {
     auto remote = [&](uint32_t rank, uint32_t at) {
       uint32_t addr = smem_u32(sp + r * (DP + 2) + at);
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kAtWarps * 32)
     if (lane == 0 && a.lse) a.lse[orow] = row_lse<F16>(top, sum);
   }
   // no CTA leaves while another reads its shared memory
-  cluster_sync();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Joins the partial sums of split items: a warp per row.

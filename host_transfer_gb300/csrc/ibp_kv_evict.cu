@@ -64,7 +64,7 @@ __device__ __forceinline__ void ev_sync() {
   if (C == 1)
     __syncthreads();
   else
-    cluster_sync();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <uint32_t C>

@@ -17,15 +17,6 @@ __device__ __forceinline__ void pdl_begin() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// All threads of the cluster; shared and global writes before it are visible to them after it.
-// The instruction wants whole warps, which the compiler does not know of inline assembly: without
-// the warp's own barrier it may copy the instruction into both sides of a branch on the lane
-// before it, and then lanes pass while the one that writes has not yet written.
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 template <typename... P, typename... A>
 int kv_launch(const char* name, void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
               cudaStream_t stream, A&&... args) {

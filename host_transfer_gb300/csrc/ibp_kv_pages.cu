@@ -34,7 +34,7 @@ __device__ __forceinline__ void cl_sync() {
     return;
   }
   __threadfence();
-  cluster_sync();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // *p of CTA `rank` of the cluster, p in shared memory.

@@ -102,7 +102,7 @@ __device__ __forceinline__ void vf_sync() {
   if (C == 1)
     __syncthreads();
   else
-    cluster_sync();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Sums of the weights, in slot `buf`: every warp's, the CTA's, and the row's (returned).

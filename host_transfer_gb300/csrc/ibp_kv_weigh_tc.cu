@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
   // The cluster's CTAs each add up their share of the tokens, in the CTAs' order.
-  cluster_sync();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (tid < share) {
     const uint32_t i = rank * share + tid;
     float s = 0.f;
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_kv_weigh_tc(const __grid_cons
     const int32_t p = static_cast<int32_t>(first + i);
     if (static_cast<uint32_t>(p) < x.width) out[p] = p >= len ? was[p] : (p < ctx ? fmaf(x.decay, was[p], s) : s);
   }
-  cluster_sync();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <uint32_t DP, bool FOUR, bool F16>

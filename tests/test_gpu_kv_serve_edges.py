@@ -50,42 +50,3 @@ def test_a_sequence_longer_than_its_weights_is_left_alone(width, budget):
     assert np.array_equal(host(pages), moved[0])
     assert all(np.array_equal(host(x), y) for x, y in zip(after, moved[1:]))
     assert host(after[1])[0] == width + 1 and host(after[1])[2] == width + 33
-
-
-# ---------------------------------------------------------------------------
-# Clusters
-
-
-def test_calls_of_clusters_agree_with_the_oracle_every_time():
-    """What one lane of a CTA writes before the cluster's barrier is there for all behind it."""
-    rng = np.random.default_rng(11)
-    B, width, budget, V, T = 12, 20001, 700, 20000, 5
-    w = np.round(rng.random((B, width)) * 50).astype(np.float32)  # many equal weights: every count is used
-    lens = rng.integers(budget, width + 1, B).astype(np.int32)
-    evicted = ref.evict(w, lens, budget, 3, 90)
-    p, q = (rng.random((B, T + i, V)).astype(np.float32) ** 6 for i in (1, 0))
-    p, q = p / p.sum(-1, keepdims=True), q / q.sum(-1, keepdims=True)
-    tokens = rng.integers(0, V, (B, T)).astype(np.int32)
-    parents = np.maximum(np.arange(T) - rng.integers(1, 4, (B, T)), -1).astype(np.int32)
-    u = rng.random((B, T + 1)).astype(np.float32)
-    verified = ref.verify(p, tokens, u, q, parents)[:3]
-    # 200 sequences: the bookkeeping of an acceptance is a cluster's
-    page, draft = 8, 20
-    n = rng.integers(draft, 60, 200).astype(np.int32)
-    table, refs = tables(n, page, 2000, 8, rng)
-    count = rng.integers(0, draft + 1, 200).astype(np.int32)
-    path = np.stack([np.sort(rng.permutation(draft)) for _ in n]).astype(np.int32)
-    for b, c in enumerate(count):
-        path[b, :c] = np.sort(rng.permutation(draft)[:c])
-    pages = torch.randn((2000, 2, page, 16), device="cuda", generator=gen(3)).bfloat16()
-    accepted = kv_ref.accept(host(pages), table, n, refs, np.full(200, draft), path, count)
-    args = dev(w, torch.float32), dev(lens)
-    drafts = dev(p, torch.float32), dev(tokens), dev(u, torch.float32), dev(q, torch.float32), dev(parents)
-    rows = [dev(x) for x in (table, n, refs, np.full(200, draft), path, count)]
-    for _ in range(20):
-        got = kv.ibp_kv_evict(*args, budget, keep_first=3, keep_last=90)
-        assert all(np.array_equal(host(x), y) for x, y in zip(got, evicted))
-        assert all(np.array_equal(host(x), y) for x, y in zip(kv.ibp_kv_verify(*drafts), verified))
-        x = pages.clone()
-        got = kv.ibp_kv_accept(x, *rows)
-        assert np.array_equal(host(x), accepted[0]) and all(np.array_equal(host(x), y) for x, y in zip(got, accepted[1:]))
