@@ -412,29 +412,60 @@ __global__ void __launch_bounds__(kCpThreads) k_kv_copy(const KvRuns r, const in
 }
 
 // Number of entries of path[b] that count: up to n_accept, ascending and below
-// n_draft.  One warp.
+// n_draft; *still: how many of them, from the first on, stay where they are.  One warp.
 __device__ uint32_t valid_path(const int32_t* path, int32_t n_accept, uint32_t max_accept, int32_t n_draft,
-                               bool* bad) {
+                               bool* bad, uint32_t* still) {
   const uint32_t lane = threadIdx.x & 31u;
-  const uint32_t n = n_accept < 0 ? 0 : (static_cast<uint32_t>(n_accept) < max_accept ? n_accept : max_accept);
+  uint32_t n = n_accept < 0 ? 0 : (static_cast<uint32_t>(n_accept) < max_accept ? n_accept : max_accept);
   *bad = n_accept < 0 || static_cast<uint32_t>(n_accept) > max_accept;
+  *still = 0xFFFFFFFFu;
   for (uint32_t a = 0; a < n; a += 32) {
     const uint32_t j = a + lane;
-    const bool wrong = j < n && (path[j] < 0 || path[j] >= n_draft || (j > 0 && path[j] <= path[j - 1]));
-    const uint32_t w = __ballot_sync(0xFFFFFFFFu, wrong);
+    const int32_t x = j < n ? path[j] : 0;
+    const bool wrong = j < n && (x < 0 || x >= n_draft || (j > 0 && x <= path[j - 1]));
+    const uint32_t w = __ballot_sync(0xFFFFFFFFu, wrong), moved = __ballot_sync(0xFFFFFFFFu, j < n && x != static_cast<int32_t>(j));
+    if (moved && *still == 0xFFFFFFFFu) *still = a + __ffs(moved) - 1;
     if (w) {
       *bad = true;
-      return a + __ffs(w) - 1;
+      n = a + __ffs(w) - 1;
     }
   }
+  if (*still > n) *still = n;
   return n;
 }
+
+// Whether a page onto which a token of a draft moves is another sequence's, too.  Thread
+// `nth` of `step` looks at every step-th page of the draft; the first is on its way while the
+// path is read.
+struct DraftPages {
+  const KvMeta& m;
+  uint64_t row;
+  uint32_t page, step, id;
+  __device__ __forceinline__ DraftPages(const KvMeta& m_, uint32_t b, int64_t ctx, int32_t len, uint32_t nth, uint32_t step_)
+      : m(m_), row(static_cast<uint64_t>(b) * m_.max_pages), step(step_), id(0xFFFFFFFFu) {
+    page = ctx < 0 ? 0xFFFFFFFFu : static_cast<uint32_t>(ctx) / m.page_tokens + nth;
+    if (ctx >= 0 && static_cast<uint64_t>(page) * m.page_tokens < static_cast<uint64_t>(len)) id = static_cast<uint32_t>(m.table[row + page]);
+  }
+  __device__ __forceinline__ bool shared() const { return id < m.n_pages && m.refs[id] > 1; }
+  // Of the pages of tokens from to `to` - 1 of the sequence; `one`: shared() of the first.
+  __device__ __forceinline__ bool written(int64_t from, int64_t to, bool one) {
+    if (from < 0 || from >= to) return false;
+    const uint32_t lo = static_cast<uint32_t>(from) / m.page_tokens, hi = static_cast<uint32_t>(to - 1) / m.page_tokens;
+    bool r = one && page >= lo && page <= hi;
+    for (uint32_t p = page + step; p <= hi && p > page; p += step) {
+      id = static_cast<uint32_t>(m.table[row + p]);
+      r = r || (p >= lo && shared());
+    }
+    return r;
+  }
+};
 
 // The CTAs of a sequence move the rows of its accepted tokens.  A thread takes
 // one access-wide column of one run in one pool after another, four
 // tokens of it at a time: it loads them all before it stores any.  Sources ascend and
 // never lie below their targets, so a row is always read before it is
-// overwritten, and only by the thread that overwrites it.  Bound by the latency
+// overwritten, and only by the thread that overwrites it.  A sequence that would write a page
+// which another holds as well is left alone.  Bound by the latency
 // of two dependent accesses for short paths, by DRAM sectors for long ones.
 template <typename V>
 __global__ void __launch_bounds__(kCpThreads, 6) k_kv_accept_move(const KvRuns r, const KvMeta m,
@@ -443,20 +474,26 @@ __global__ void __launch_bounds__(kCpThreads, 6) k_kv_accept_move(const KvRuns r
                                                                const int32_t* __restrict__ n_accept,
                                                                uint32_t max_accept) {
   __shared__ int64_t from[32], into[32];
-  __shared__ uint32_t n_sh;
+  __shared__ uint32_t n_sh, still_sh;
   pdl_begin();
   const uint32_t b = blockIdx.y, t = threadIdx.x;
   const int32_t len = clamp_len(m.lens[b], m.page_tokens, m.max_pages), nd = n_draft[b];
   const int64_t ctx = static_cast<int64_t>(len) - nd;
   const int32_t* pb = path + static_cast<uint64_t>(b) * max_accept;
+  DraftPages pages(m, b, t < 32 ? -1 : ctx, len, t - 32, kCpThreads - 32);  // by the warps that do not read the path
+  bool one = false;
   if (t < 32) {
     bool bad;
-    uint32_t n = valid_path(pb, n_accept[b], max_accept, nd, &bad);
+    uint32_t still, n = valid_path(pb, n_accept[b], max_accept, nd, &bad, &still);
     if (nd < 0 || ctx < 0) n = 0;
-    if (t == 0) n_sh = n;
+    if (t == 0) n_sh = n, still_sh = still;
+  } else {
+    one = pages.shared();
   }
   __syncthreads();
   const uint32_t n = n_sh;
+  // every CTA of the sequence, and the bookkeeping, come to the same answer from the same counts
+  if (__syncthreads_or(t >= 32 && pages.written(ctx + still_sh, ctx + n, one))) return;
   const uint32_t cols = r.row_bytes / sizeof(V);
   const uint64_t columns = r.n_pools * r.outer * cols;
   for (uint32_t a = 0; a < n; a += 32) {
@@ -497,20 +534,35 @@ __global__ void __launch_bounds__(kMt) k_kv_accept_meta(const KvMeta m, const in
                                                         const int32_t* __restrict__ path,
                                                         const int32_t* __restrict__ n_accept, uint32_t max_accept) {
   pdl_begin();
+  // What is left of each of a warp's sequences, found before any reference is given up:
+  // the counts that say whether a page is shared may be the ones that are changed.
+  constexpr uint32_t kWarps = kMt / 32, kEach = kCl == 1 ? 1 : (65535 + kCl * kWarps - 1) / (kCl * kWarps);
+  __shared__ int32_t left[kWarps][kEach];
   const uint32_t t = threadIdx.x, gt = (kCl == 1 ? 0 : cl_rank()) * kMt + t, lane = t & 31u;
-  const uint32_t gw = gt >> 5, n_warps = kCl * kMt / 32, P = m.max_pages;
+  const uint32_t gw = gt >> 5, n_warps = kCl * kWarps, P = m.max_pages;
   carry<kCl>(m.refs_out, m.refs, m.n_pages, gt);
-  cl_sync<kCl>();
-  for (uint32_t b = gw; b < m.n_seqs; b += n_warps) {
+  for (uint32_t b = gw, i = 0; b < m.n_seqs; b += n_warps, ++i) {
     const int32_t raw = m.lens[b], len = clamp_len(raw, m.page_tokens, P), nd = n_draft[b];
+    DraftPages pages(m, b, static_cast<int64_t>(len) - nd, len, lane, 32);
     bool bad;
-    uint32_t n = valid_path(path + static_cast<uint64_t>(b) * max_accept, n_accept[b], max_accept, nd, &bad);
+    uint32_t still, n = valid_path(path + static_cast<uint64_t>(b) * max_accept, n_accept[b], max_accept, nd, &bad, &still);
     int32_t kept = len - nd + static_cast<int32_t>(n);
     if (nd < 0 || nd > len) {
       bad = true;
       kept = len;
+    } else if (__any_sync(0xFFFFFFFFu, pages.written(static_cast<int64_t>(len) - nd + still, kept, pages.shared()))) {
+      if (lane == 0) kv_status(m.status, IBP_EINVAL);
+      kept = len;
     }
     if ((bad || raw != len) && lane == 0) kv_status(m.status, IBP_ERANGE);
+    if (lane == 0) left[t >> 5][i] = kept;
+  }
+  cl_sync<kCl>();
+  for (uint32_t b = gw, i = 0; b < m.n_seqs; b += n_warps, ++i) {
+    const int32_t len = clamp_len(m.lens[b], m.page_tokens, P);
+    // Lane 0 reads what it has written.  With the whole warp reading it the others got 0 (code of
+    // nvcc 13.0.88, behind any barrier).
+    const int32_t kept = __shfl_sync(0xFFFFFFFFu, lane == 0 ? left[t >> 5][i] : 0, 0);
     const uint32_t was = held_pages(len, m.page_tokens, P), now = held_pages(kept, m.page_tokens, P);
     for (uint32_t p = lane; p < P; p += 32) {
       const uint64_t at = static_cast<uint64_t>(b) * P + p;

@@ -398,8 +398,9 @@ def ibp_kv_accept(pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, 
                   n_draft: torch.Tensor, path: torch.Tensor, n_accept: torch.Tensor, inplace: bool = False,
                   status: torch.Tensor | None = None, stream=None):
     """Keeps the accepted tokens of each sequence's draft (its last n_draft[b]
-    tokens): path[b][: n_accept[b]] move to the draft's front in every pool.
-    Returns (table, lens, refs)."""
+    tokens): path[b][: n_accept[b]] move to the draft's front in every pool.  A
+    sequence with a page of several references among those that tokens move onto is
+    left alone (status IBP_EINVAL).  Returns (table, lens, refs)."""
     lib = _load()
 
     def check():
@@ -874,7 +875,9 @@ def ibp_kv_evict(weights: torch.Tensor, lens: torch.Tensor, budget: int, keep_fi
 
     Returns (path [n_seqs, budget], n_draft [n_seqs], n_keep [n_seqs], weights): the
     first three make ibp_kv_accept(pool, table, lens, refs, n_draft, path, n_keep) move
-    what stays to the front; the weights have moved already."""
+    what stays to the front; the weights have moved already.  The move rewrites the
+    sequence's pages: one that shares them with a fork is left alone by it (status
+    IBP_EINVAL), one longer than its weights by this call (status IBP_ERANGE)."""
     lib = _load()
 
     def check():

@@ -631,7 +631,11 @@ int ibp_kv_copy(const ibp_kv_pages* pages, const int32_t* moves, const int32_t* 
  * j < n_accept[b], in every pool, the length becomes that of the kept tokens,
  * and pages behind it lose a reference.  path[b] ascends; at its first entry
  * that does not, or that is not below n_draft[b], the sequence's list ends and
- * IBP_ERANGE is recorded.  The draft's pages must not be shared.
+ * IBP_ERANGE is recorded.  Pages onto which a token moves must not be shared: a
+ * sequence that has one of more than one reference among them is left alone, and
+ * IBP_EINVAL is recorded.  (A kept token that is at its place already does not move, so
+ * a draft may follow on a shared prefix.)  Several pools of their own calls are given
+ * the same table, lengths and references, and so agree.
  *
  * pages    every pool; seqs, refs, table_out, lens_out, refs_out as for
  *          ibp_kv_free (the outputs may be the inputs).
@@ -748,9 +752,9 @@ size_t ibp_sparse_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint3
  * half-precision ones give (c - 8) s rounded to half precision.
  *
  * Codes and scales are pages of elem_bytes 1 and 2 to ibp_kv_copy and
- * ibp_kv_accept (one call each; the second with the table, lengths and references
- * that the first was given), so forks, compaction, acceptance and eviction serve
- * these caches too.
+ * ibp_kv_accept (one call each, all with the table, lengths and references that the
+ * first was given), so forks, compaction and acceptance serve these caches too,
+ * and eviction those of their sequences that share no page it rewrites.
  */
 #define IBP_KV4_GROUP 32u
 
@@ -873,8 +877,11 @@ int ibp_kv4_weigh(const ibp_kv4_pages* k, uint32_t dtype, const ibp_kv_seqs* seq
  * first when equal (NaN is below everything), up to `budget` in all.
  * path[b] lists them ascending, n_keep[b] = budget, n_draft[b] = lens[b]: the
  * arguments with which ibp_kv_accept moves them to the front of the sequence in every
- * pool and frees the pages behind.  Sequences within the budget get n_draft =
- * n_keep = 0, which ibp_kv_accept leaves alone.  w_out[b] has the weights of the
+ * pool and frees the pages behind.  That rewrites the sequence's pages from the first
+ * token that moves on: ibp_kv_accept leaves a sequence alone that shares one of them
+ * (with a fork of it, or a prefix cache): it needs copies of its own first, and
+ * until then w[b] stays what goes with it.
+ * Sequences within the budget get n_draft = n_keep = 0, which ibp_kv_accept leaves alone.  w_out[b] has the weights of the
  * tokens that stay at their new positions and 0 behind.  Lengths outside [0,
  * width] record IBP_ERANGE and leave the sequence alone: n_draft = n_keep = 0, and
  * w_out[b] is w[b] (0 for a length below 0).

@@ -85,11 +85,13 @@ def copy(pool, moves):
 
 
 def accept(pool, table, lens, refs, n_draft, path, n_accept):
-    """(pool, table, lens, refs)"""
-    page = pool.shape[-2]
+    """(pool, table, lens, refs); a sequence that would write a shared page stays as it is"""
+    page, held_by = pool.shape[-2], refs
     new, table, lens, refs = pool.copy(), table.copy(), lens.copy(), refs.copy()
     for b in range(len(lens)):
         ctx = int(lens[b] - n_draft[b])
+        if any(held_by[table[b, (ctx + j) // page]] > 1 for j in range(n_accept[b]) if path[b, j] != j):
+            continue
         for j in range(n_accept[b]):
             s, d = ctx + int(path[b, j]), ctx + j
             new[..., table[b, d // page], :, d % page, :] = pool[..., table[b, s // page], :, s % page, :]

@@ -8,7 +8,7 @@ import torch
 from host_transfer_gb300 import ibp, kv
 from oracle import kv_ref, kv_serve_ref as ref
 from tests.kv_util import dev, host, tables
-from tests.test_gpu_kv_serve import gen
+from tests.test_gpu_kv_serve import Cache, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,147 @@ def test_a_sequence_longer_than_its_weights_is_left_alone(width, budget):
     assert np.array_equal(host(pages), moved[0])
     assert all(np.array_equal(host(x), y) for x, y in zip(after, moved[1:]))
     assert host(after[1])[0] == width + 1 and host(after[1])[2] == width + 33
+
+
+def forked(lens, page, seed=0, extra=2):
+    """Sequences, and a fork of each: (table, lens, refs) with the full pages shared."""
+    rng = np.random.default_rng(seed)
+    n = len(lens)
+    lens = np.array(lens, np.int32)
+    width = -(-int(lens.max()) // page) + 1
+    table, refs = tables(lens, page, int((-(-lens // page)).sum()) + n + extra, width, rng)
+    pages = torch.randn((len(refs), 2, page, 16), device="cuda", generator=gen(seed)).bfloat16()
+    got = kv.ibp_kv_fork(dev(table), dev(lens), dev(refs), dev(np.repeat(np.arange(n), 2)), page)
+    kv.ibp_kv_copy(pages, *got[3:])
+    return pages, *got[:3]
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("evicted", [(0,), (0, 1), (1, 2, 3)])
+def test_evicting_a_fork_leaves_its_sibling_alone(evicted, inplace):
+    """Moving a fork's tokens to the front would overwrite pages that another sequence holds:
+    a sequence of whose targets one is shared stays as it is, and the status says so."""
+    page, budget = 16, 40
+    pages, table, lens, refs = forked([100, 64], page, extra=4)
+    # a sequence of its own beside them, which moves
+    own = np.flatnonzero(host(refs) == 0)[:4].astype(np.int32)
+    assert len(own) == 4 or pytest.fail("no pages left")
+    row = np.full((1, table.shape[1]), -1, np.int32)
+    row[0, :4] = own
+    table, lens = torch.cat([table, dev(row)]), torch.cat([lens, dev(np.array([60]))])
+    refs[torch.from_numpy(own).cuda().long()] = 1
+    rng = np.random.default_rng(5)
+    w = rng.random((5, 112)).astype(np.float32)
+    path, n_draft, n_keep, _ = kv.ibp_kv_evict(dev(w, torch.float32), lens, budget, keep_first=2, keep_last=3)
+    others = [b for b in range(4) if b not in evicted]
+    n_draft[others] = 0
+    n_keep[others] = 0
+    before = host(pages).copy()
+    want = kv_ref.accept(before, *map(host, (table, lens, refs, n_draft, path, n_keep)))
+    got = kv.ibp_kv_accept(pages, table, lens, refs, n_draft, path, n_keep, inplace=inplace)
+    err(ibp.IBP_EINVAL)
+    assert np.array_equal(host(pages), want[0])
+    assert all(np.array_equal(host(x), y) for x, y in zip(got, want[1:]))
+    assert host(got[1]).tolist() == [100, 100, 64, 64, budget]
+    changed = (want[0] != before).any((1, 2, 3))
+    assert set(np.flatnonzero(changed)) <= set(own.tolist()) and changed.any()
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+def test_sharing_is_judged_before_any_page_is_freed(inplace):
+    """One row gives a shared page up while another wants to write it: both in one call."""
+    page = 8
+    # rows 0 and 1 share pages 0 and 1; row 2 is on its own
+    table, lens = np.array([[0, 1, -1], [0, 1, 2], [3, 4, -1]], np.int32), np.array([16, 20, 16], np.int32)
+    refs = np.array([2, 2, 1, 1, 1, 0], np.int32)
+    n_draft, n_keep = np.array([16, 20, 16], np.int32), np.array([3, 12, 10], np.int32)
+    path = np.full((3, 12), -1, np.int32)
+    path[0, :3] = [0, 1, 2]  # nothing moves, page 1 is given up
+    path[1] = np.arange(8, 20)  # writes pages 0 and 1
+    path[2, :10] = np.arange(6, 16)
+    pages = torch.arange(6 * page * 4, device="cuda", dtype=torch.float32).reshape(6, 1, page, 4)
+    want = kv_ref.accept(host(pages), table, lens, refs, n_draft, path, n_keep)
+    got = kv.ibp_kv_accept(pages, *map(dev, (table, lens, refs, n_draft, path, n_keep)), inplace=inplace)
+    err(ibp.IBP_EINVAL)
+    assert np.array_equal(host(pages), want[0])
+    assert all(np.array_equal(host(x), y) for x, y in zip(got, want[1:]))
+    assert host(got[1]).tolist() == [3, 20, 10] and host(got[2]).tolist() == [2, 1, 1, 1, 1, 0]
+
+
+def test_a_draft_behind_a_shared_prefix_is_accepted():
+    """Only the pages that are written have to be a sequence's own."""
+    page, T = 16, 9
+    rng = np.random.default_rng(3)
+    pages, table, lens, refs = forked([77, 64, 40], page, seed=3, extra=12)
+    free = iter(np.flatnonzero(host(refs) == 0))
+    t, r, n = host(table).copy(), host(refs).copy(), host(lens) + T
+    for b in range(6):
+        for p in range(-(-int(n[b] - T) // page), -(-int(n[b]) // page)):
+            t[b, p] = next(free)
+            r[t[b, p]] = 1
+    n_draft, n_accept = np.full(6, T, np.int32), np.array([3, 9, 0, 5, 4, 1], np.int32)
+    path = np.full((6, T), -1, np.int32)
+    for b in range(6):
+        path[b, : n_accept[b]] = np.sort(rng.permutation(T)[: n_accept[b]])
+    assert (r > 1).any()
+    want = kv_ref.accept(host(pages), t, n, r, n_draft, path, n_accept)
+    got = kv.ibp_kv_accept(pages, *map(dev, (t, n, r, n_draft, path, n_accept)))
+    assert np.array_equal(host(pages), want[0]) and host(got[1]).tolist() == (n - T + n_accept).tolist()
+    assert all(np.array_equal(host(x), y) for x, y in zip(got, want[1:]))
+
+
+@pytest.mark.parametrize("page", [16, 24])
+def test_a_long_eviction_and_its_move(page):
+    """A budget of 8192 tokens over several sequences, codes and scales, the lengths and references once."""
+    lens, budget, dim = [20000, 8192, 12345, 9000], 8192, 64
+    c = Cache(lens, 1, 2, 1, page, dim, seed=9)
+    rng = np.random.default_rng(9)
+    w = rng.random((4, 20480)).astype(np.float32)
+    path, n_draft, n_keep, left = kv.ibp_kv_evict(dev(w, torch.float32), c.lens, budget, keep_first=4, keep_last=1024)
+    want = ref.evict(w, lens, budget, 4, 1024)
+    assert all(np.array_equal(host(x), y) for x, y in zip((path, n_draft, n_keep, left), want))
+    for x in (*c.k, *c.v):
+        bits = x.view(torch.int16) if x.dtype != torch.uint8 else x  # NaN where no token is
+        moved = kv_ref.accept(host(bits), c.np_table, c.np_lens, c.np_refs, want[1], want[0], want[2])
+        got = kv.ibp_kv_accept(x, c.table, c.lens, c.refs, n_draft, path, n_keep)
+        assert np.array_equal(host(bits), moved[0])
+        assert all(np.array_equal(host(a), b) for a, b in zip(got, moved[1:]))
+
+
+# ---------------------------------------------------------------------------
+# Clusters
+
+
+def test_calls_of_clusters_agree_with_the_oracle_every_time():
+    """What one lane of a CTA writes before the cluster's barrier is there for all behind it."""
+    rng = np.random.default_rng(11)
+    B, width, budget, V, T = 12, 20001, 700, 20000, 5
+    w = np.round(rng.random((B, width)) * 50).astype(np.float32)  # many equal weights: every count is used
+    lens = rng.integers(budget, width + 1, B).astype(np.int32)
+    evicted = ref.evict(w, lens, budget, 3, 90)
+    p, q = (rng.random((B, T + i, V)).astype(np.float32) ** 6 for i in (1, 0))
+    p, q = p / p.sum(-1, keepdims=True), q / q.sum(-1, keepdims=True)
+    tokens = rng.integers(0, V, (B, T)).astype(np.int32)
+    parents = np.maximum(np.arange(T) - rng.integers(1, 4, (B, T)), -1).astype(np.int32)
+    u = rng.random((B, T + 1)).astype(np.float32)
+    verified = ref.verify(p, tokens, u, q, parents)[:3]
+    # 200 sequences: the bookkeeping of an acceptance is a cluster's
+    page, draft = 8, 20
+    n = rng.integers(draft, 60, 200).astype(np.int32)
+    table, refs = tables(n, page, 2000, 8, rng)
+    count = rng.integers(0, draft + 1, 200).astype(np.int32)
+    path = np.stack([np.sort(rng.permutation(draft)) for _ in n]).astype(np.int32)
+    for b, c in enumerate(count):
+        path[b, :c] = np.sort(rng.permutation(draft)[:c])
+    pages = torch.randn((2000, 2, page, 16), device="cuda", generator=gen(3)).bfloat16()
+    accepted = kv_ref.accept(host(pages), table, n, refs, np.full(200, draft), path, count)
+    args = dev(w, torch.float32), dev(lens)
+    drafts = dev(p, torch.float32), dev(tokens), dev(u, torch.float32), dev(q, torch.float32), dev(parents)
+    rows = [dev(x) for x in (table, n, refs, np.full(200, draft), path, count)]
+    for _ in range(20):
+        got = kv.ibp_kv_evict(*args, budget, keep_first=3, keep_last=90)
+        assert all(np.array_equal(host(x), y) for x, y in zip(got, evicted))
+        assert all(np.array_equal(host(x), y) for x, y in zip(kv.ibp_kv_verify(*drafts), verified))
+        x = pages.clone()
+        got = kv.ibp_kv_accept(x, *rows)
+        assert np.array_equal(host(x), accepted[0]) and all(np.array_equal(host(x), y) for x, y in zip(got, accepted[1:]))
