@@ -473,6 +473,13 @@ def _result(name: str, out: torch.Tensor, *inputs: torch.Tensor):
     return out
 
 
+def _no_gradients(name: str, *inputs: torch.Tensor):
+    """For calls that write into tensors of the caller's, which cannot carry the error to a backward."""
+    if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
+        raise ValueError(f"{name} writes in place, which a gradient does not follow: detach its inputs, or call it "
+                         "under torch.no_grad()")
+
+
 def _heads(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
     """(k pages, v pages, dtype, sequences) of an attention call."""
     kp, vp = _as_pages("k", k), _as_pages("v", v)
@@ -655,8 +662,11 @@ def _caches4(k4, v4, table: torch.Tensor, lens: torch.Tensor):
 def ibp_kv4_store(k: torch.Tensor, v: torch.Tensor, k4, v4, table: torch.Tensor, lens: torch.Tensor,
                   n_new: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
     """Puts k and v [n_seqs, T, heads, dim], the last T (or n_new[b]) tokens of each
-    sequence, into caches in 4 bits, (codes, scales) each, in place.  Returns (k4, v4)."""
+    sequence, into caches in 4 bits, (codes, scales) each, in place.  Returns (k4, v4).
+    The cache carries no gradient: tensors that require one are refused where gradients are
+    enabled."""
     lib = _load()
+    _no_gradients("ibp_kv4_store", k, v, k4[1], v4[1])
 
     def check():
         kp, vp, dt, seqs = _caches4(k4, v4, table, lens)

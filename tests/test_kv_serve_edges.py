@@ -2,7 +2,10 @@
 no GPU."""
 
 import numpy as np
+import pytest
+import torch
 
+from host_transfer_gb300 import kv
 from oracle import kv_ref, kv_serve_ref as ref
 
 
@@ -24,3 +27,49 @@ def test_acceptance_leaves_a_sequence_that_would_write_a_shared_page():
     new, table, lens, refs = kv_ref.accept(pages, *args, [8, 4], np.array([[0, 3, 5], [1, 2, -1]]), [3, 2])
     assert table.tolist() == args[0].tolist() and lens.tolist() == [8, 10] and refs.tolist() == [2, 2, 1]
     assert np.array_equal(new[:2], pages[:2]) and new[2].ravel().tolist() == [9, 10, 10, 11]
+
+
+# ---------------------------------------------------------------------------
+# Binding
+
+
+class Library:
+    """Stands for the library: notes what was called."""
+
+    def __init__(self):
+        self.called = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.called.append(name) or 0
+
+
+@pytest.fixture
+def library(monkeypatch):
+    """Calls on CPU tensors, up to the library."""
+    lib = Library()
+    for name, stub in (("_load", lambda: lib), ("_for", lambda stream, device: (0, torch.enable_grad())),
+                       ("_status", lambda status, device: 0), ("_on_device", lambda name, t: None), ("_checked", kv._Checked())):
+        monkeypatch.setattr(kv, name, stub)
+    return lib
+
+
+def cache():
+    return torch.zeros((4, 2, 16, 32), dtype=torch.uint8), torch.zeros((4, 2, 16, 2), dtype=torch.bfloat16)
+
+
+TABLE, LENS = torch.zeros((2, 2), dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("which", ["k", "v", "k4", "v4"])
+def test_a_store_refuses_what_requires_a_gradient(library, which):
+    """What is read back from the cache would be attached to nothing, and no error reach the backward."""
+    args = dict(k=torch.zeros((2, 1, 2, 64), dtype=torch.bfloat16), v=torch.zeros((2, 1, 2, 64), dtype=torch.bfloat16),
+                k4=cache(), v4=cache())
+    kv.ibp_kv4_store(**args, table=TABLE, lens=LENS)
+    (args[which][1] if "4" in which else args[which]).requires_grad_()
+    with pytest.raises(ValueError, match="ibp_kv4_store.*detach"):
+        kv.ibp_kv4_store(**args, table=TABLE, lens=LENS)
+    assert library.called == ["ibp_kv4_store"]
+    with torch.no_grad():
+        kv.ibp_kv4_store(**args, table=TABLE, lens=LENS)
+    assert library.called == ["ibp_kv4_store"] * 2
