@@ -476,7 +476,7 @@ def _result(name: str, out: torch.Tensor, *inputs: torch.Tensor):
 def _no_gradients(name: str, *inputs: torch.Tensor):
     """For calls that write into tensors of the caller's, which cannot carry the error to a backward."""
     if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
-        raise ValueError(f"{name} writes in place, which a gradient does not follow: detach its inputs, or call it "
+        raise ValueError(f"{name}: what is written in place carries no gradient: detach its inputs, or call it "
                          "under torch.no_grad()")
 
 
@@ -844,7 +844,8 @@ def ibp_kv_weigh(q: torch.Tensor, k, table: torch.Tensor, lens: torch.Tensor, ls
 
     k        pages of 16 bits, or a cache in 4 bits (codes, scales).
     weights  float32 [n_seqs, width], width at least the longest length.
-    Returns the new weights (`weights` itself with `inplace`)."""
+    Returns the new weights; with `inplace` these are `weights` itself, and tensors that
+    require a gradient are refused where gradients are enabled."""
     lib = _load()
     four = isinstance(k, (tuple, list))
 
@@ -857,8 +858,8 @@ def ibp_kv_weigh(q: torch.Tensor, k, table: torch.Tensor, lens: torch.Tensor, ls
         _floats("weights", weights, seqs.n_seqs, *weights.shape[1:2])
         return kp, _dtype(kind), seqs, rows, weights.shape[1], 1.0 / math.sqrt(kp.dim)
 
-    if inplace and weights.requires_grad and torch.is_grad_enabled():
-        raise ValueError("weights that require a gradient cannot be written in place")
+    if inplace:
+        _no_gradients("ibp_kv_weigh", q, k[1] if four else k, lse, weights)
     key = ("weigh", _form(q), _form4(k) if four else _form(k), _form(table), _form(lens), _form(lse), _form(weights),
            _form(mask), _form(n_draft))
     device = lse.device

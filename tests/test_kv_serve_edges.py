@@ -73,3 +73,23 @@ def test_a_store_refuses_what_requires_a_gradient(library, which):
     with torch.no_grad():
         kv.ibp_kv4_store(**args, table=TABLE, lens=LENS)
     assert library.called == ["ibp_kv4_store"] * 2
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("which", ["q", "k", "lse", "weights"])
+def test_weighing_in_place_refuses_what_requires_a_gradient(library, which, four):
+    """It gives `weights` itself, not a view that the next step in place would refuse."""
+    args = dict(q=torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16), k=cache() if four else torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16),
+                lse=torch.zeros((2, 1, 4)), weights=torch.zeros((2, 32)))
+    call = lambda inplace: kv.ibp_kv_weigh(**args, table=TABLE, lens=LENS, inplace=inplace)  # noqa: E731
+    assert call(True) is args["weights"]
+    (args[which][1] if isinstance(args[which], tuple) else args[which]).requires_grad_()
+    n = len(library.called)
+    with pytest.raises(ValueError, match="in place.*detach"):
+        call(True)
+    assert len(library.called) == n
+    with torch.no_grad():
+        assert call(True) is args["weights"]
+    got = call(False)
+    with pytest.raises(RuntimeError, match="no backward"):
+        got.sum().backward()
