@@ -774,9 +774,11 @@ def ibp_kv4_attention(q: torch.Tensor, k4, v4, table: torch.Tensor, lens: torch.
 
 
 def _floats(name: str, t: torch.Tensor, *shape):
+    """shape: the wanted sizes, None where any will do."""
     _on_device(name, t)
-    if t.dtype != torch.float32 or not t.is_contiguous() or t.shape != shape:
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {list(shape)}")
+    if (t.dtype != torch.float32 or not t.is_contiguous() or t.dim() != len(shape)
+            or any(want is not None and have != want for have, want in zip(t.shape, shape))):
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {[w if w is not None else 'any' for w in shape]}")
 
 
 def _probabilities(name: str, t: torch.Tensor, *shape):
@@ -855,7 +857,7 @@ def ibp_kv_weigh(q: torch.Tensor, k, table: torch.Tensor, lens: torch.Tensor, ls
         kind = k[1] if four else k
         rows = _queries(q, seqs, kp.dim, kind.dtype, mask, n_draft)
         _floats("lse", lse, *q.shape[:3])
-        _floats("weights", weights, seqs.n_seqs, *weights.shape[1:2])
+        _floats("weights", weights, seqs.n_seqs, None)
         return kp, _dtype(kind), seqs, rows, weights.shape[1], 1.0 / math.sqrt(kp.dim)
 
     if inplace:
@@ -894,7 +896,7 @@ def ibp_kv_evict(weights: torch.Tensor, lens: torch.Tensor, budget: int, keep_fi
     def check():
         _on_device("lens", lens)
         _ints("lens", lens, None)
-        _floats("weights", weights, lens.shape[0], *weights.shape[1:2])
+        _floats("weights", weights, lens.shape[0], None)
         return weights.shape
 
     if not 1 <= budget < 1 << 31 or keep_first < 0 or keep_last < 0 or keep_first + keep_last > budget:

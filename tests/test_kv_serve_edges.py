@@ -93,3 +93,15 @@ def test_weighing_in_place_refuses_what_requires_a_gradient(library, which, four
     got = call(False)
     with pytest.raises(RuntimeError, match="no backward"):
         got.sum().backward()
+
+
+@pytest.mark.parametrize("shape", [(2,), (2, 4, 8), (3, 32), ()])
+def test_weights_of_another_shape_are_named(library, shape):
+    """One dimension as long as the batch among them."""
+    w = torch.zeros(shape)
+    q, lse = torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16), torch.zeros((2, 1, 4))
+    for call in (lambda: kv.ibp_kv_weigh(q, cache(), TABLE, LENS, lse, w), lambda: kv.ibp_kv_evict(w, LENS, 4)):
+        with pytest.raises(ValueError, match="weights must be a contiguous float32 tensor of shape .2, 'any'."):
+            call()
+    assert not library.called
+    kv.ibp_kv_evict(torch.zeros((2, 32)), LENS, 4)
