@@ -7,8 +7,8 @@ import torch
 
 from host_transfer_gb300 import ibp, kv
 from oracle import kv_ref, kv_serve_ref as ref
-from tests.kv_util import dev, host, tables
-from tests.test_gpu_kv_serve import Cache, gen
+from tests.kv_util import DTYPES, check_attention, dev, host, pool, tables
+from tests.test_gpu_kv_serve import Cache, check_weigh, gen, unheld
 
 pytestmark = pytest.mark.gpu
 
@@ -155,6 +155,83 @@ def test_a_long_eviction_and_its_move(page):
         got = kv.ibp_kv_accept(x, c.table, c.lens, c.refs, n_draft, path, n_keep)
         assert np.array_equal(host(bits), moved[0])
         assert all(np.array_equal(host(a), b) for a, b in zip(got, moved[1:]))
+
+
+# ---------------------------------------------------------------------------
+# Layouts
+
+
+def loose(q):
+    """The same queries with a base and strides that are multiples of 4 bytes only."""
+    B, T, H, D = q.shape
+    wide = torch.full((B, T, H, D + 6), float("nan"), dtype=q.dtype, device="cuda")
+    wide[..., 2 : D + 2] = q
+    return wide[..., 2 : D + 2]
+
+
+@pytest.mark.parametrize("layout,strided", [("hnd", True), ("nhd", False), ("padded", True), ("padded", False)])
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("lens,T,hk,G,page,D", [
+    ([70, 0, 33], 1, 2, 4, 16, 64), ([300, 17], 1, 8, 1, 7, 128), ([60, 90], 2, 3, 2, 24, 256),  # 8 rows at most
+    ([100, 64, 80], 5, 3, 2, 24, 96), ([90, 41], 20, 2, 2, 16, 128), ([50, 41], 30, 1, 3, 64, 256),  # few rows
+    ([300, 90], 70, 3, 1, 16, 64), ([700], 40, 1, 8, 24, 128), ([300, 120], 17, 4, 5, 7, 96),  # tensor cores
+])
+def test_weigh_in_every_layout(lens, T, hk, G, page, D, dt, four, layout, strided):
+    c = Cache(lens, T, hk, G, page, D, dt, layout, seed=D + T)
+    n_draft = np.array([max(0, min(T - i, n)) for i, n in enumerate(lens)], np.int32)
+    keys = c.k
+    if not four:
+        keys = pool(c.np_k.shape, DTYPES[dt], layout, gen(1), fill=float("nan"))
+        keys.copy_(torch.from_numpy(c.np_k).to("cuda"))
+        keys.masked_fill_(unheld(c.np_table, c.np_lens, keys.shape[0], page), float("nan"))
+    lse = c.want(n_draft)[1].astype(np.float32)
+    width = c.np_table.shape[1] * page + 3
+    was = np.random.default_rng(1).random((len(lens), width)).astype(np.float32)
+    want, top = ref.weigh(host(c.q), c.np_k, c.np_table, c.np_lens, lse, was, None, n_draft, decay=0.75)
+    got = kv.ibp_kv_weigh(loose(c.q) if strided else c.q, keys, c.table, c.lens, dev(lse, torch.float32), dev(was, torch.float32),
+                          n_draft=dev(n_draft), decay=0.75)
+    check_weigh(got, want, top, lse, T * hk * G, was, 0.75)
+
+
+MANY = [  # (sequences, drafted tokens, kv heads, heads of each, page, dim): tensor cores on codes
+    ([300, 290] * 3, 17, 2, 8, 64, 128), ([200, 141, 150] * 3, 100, 3, 1, 7, 64), ([170] * 12, 130, 2, 1, 16, 96),
+    ([310, 305, 301], 100, 2, 5, 24, 128),
+    # more than 512 rows: decoded once
+    ([310, 305, 301], 130, 2, 4, 16, 128), ([600, 641], 600, 1, 1, 7, 64), ([310, 303], 260, 2, 3, 24, 96),
+]
+
+
+@pytest.mark.parametrize("layout,strided", [("hnd", True), ("nhd", False), ("padded", True), ("padded", False)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("lens,T,hk,G,page,D", MANY)
+def test_attention_of_many_rows_in_every_layout(lens, T, hk, G, page, D, dt, layout, strided):
+    """Scratch begins as NaN: what a call does not write there must not matter."""
+    c = Cache(lens, T, hk, G, page, D, dt, layout, seed=T, mask=True)
+    assert -(-max(lens) // 128) * len(lens) * hk * -(-T * G // 16) >= 304, "work enough for the tensor cores"
+    live = np.array([T - (i % 3) for i in range(len(lens))], np.int32)
+    size = kv._load().ibp_kv4_attention_workspace(len(lens), c.np_table.shape[1], page, T, hk * G, hk, D)
+    want = c.want(live)
+    if strided:
+        c.q = loose(c.q)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    check_attention(*c.attend(n_draft=dev(live), workspace=ws), *want, dt)
+
+
+@pytest.mark.parametrize("layout", ["hnd", "padded"])
+@pytest.mark.parametrize("T,hk,G,D", [(260, 2, 3, 128), (100, 1, 12, 64)])
+def test_many_rows_over_a_table_too_wide_to_decode(T, hk, G, D, layout):
+    """Scratch goes by the table's width; where the decoded cache would pass 4 GB there, calls
+    of more than 512 rows read codes too."""
+    c = Cache([700, T, 500], T, hk, G, 64, D, "bf16", layout, seed=T, mask=True)
+    live = np.array([T, T - 1, T - 2], np.int32)
+    want = c.want(live)
+    wide = torch.full((3, 120000), -1, dtype=torch.int32, device="cuda")
+    wide[:, : c.table.shape[1]] = c.table
+    size = kv._load().ibp_kv4_attention_workspace(3, 120000, 64, T, hk * G, hk, D)
+    assert size < 1 << 30 < 3 * 120000 * 64 * hk * D * 4 // 4
+    c.table = wide
+    check_attention(*c.attend(n_draft=dev(live), workspace=torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")), *want, "bf16")
 
 
 # ---------------------------------------------------------------------------
