@@ -235,6 +235,39 @@ def test_many_rows_over_a_table_too_wide_to_decode(T, hk, G, D, layout):
 
 
 # ---------------------------------------------------------------------------
+# Values past the type's range
+
+
+@pytest.mark.parametrize("T,hk,G,page", [(3, 1, 2, 16), (7, 2, 1, 24), (13, 1, 4, 16), (70, 8, 4, 16)])
+def test_half_precision_values_past_its_range_are_infinite(T, hk, G, page):
+    """Scale 9000 stands for 0 (code 8) and -infinity (code 0: -72000): a row that sees such a
+    value has the infinity there and its ordinary output beside it."""
+    lens = [T + 30, T + 900, T]
+    c = Cache(lens, T, hk, G, page, 64, "f16", seed=T)
+    odd = T - 2
+    sees = np.random.default_rng(7).random((3, T, T)) < 0.5
+    sees[:, :, odd] = np.arange(T) % 2 == 1
+    bits = np.zeros((3, T, -(-T // 32)), np.uint32)
+    for t in range(T):
+        for i in range(T):
+            bits[:, t, i // 32] |= (sees[:, t, i].astype(np.uint32) << np.uint32(i % 32)).astype(np.uint32)
+    c.np_mask, c.mask = bits, dev(bits.view(np.int32))
+    for b in range(3):
+        pos = lens[b] - T + odd
+        at = int(c.np_table[b, pos // page]), hk - 1, pos % page
+        c.v[0][at], c.v[1][at] = 0x08, 9000.0
+        c.np_v[at] = 0.0  # what the even elements stand for
+    out, lse = c.attend()
+    want, want_lse, mean, top = c.want()
+    seen = torch.from_numpy(sees[:, :, odd]).cuda()
+    last = out[:, :, (hk - 1) * G :]
+    assert (last[seen][..., 1::2] == -float("inf")).all()
+    got = out.clone()
+    got[:, :, (hk - 1) * G :][..., 1::2][seen] = torch.from_numpy(want).cuda()[:, :, (hk - 1) * G :][..., 1::2][seen].half()
+    check_attention(got, lse, want, want_lse, mean, top, "f16")
+
+
+# ---------------------------------------------------------------------------
 # Clusters
 
 
