@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT, FOUR>::kThreads, 1)
           }
           const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, have));
           const uint32_t bytes = n * t.box * 128 * S::kHalves;
-  #pragma unroll
+#pragma unroll
           for (uint32_t kv = 0; kv < 2; ++kv, ++f) {
             ok = tc::bar_wait(tc::s32(&sh.empty[ring(f)]), ring_phase(f) ^ 1u, stop, t.limit);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(TcShape<DP, MT, FOUR>::kThreads, 1)
             if (lane == 0) tc::bar_expect(bar, bytes);
             __syncwarp();
             if (have)
-  #pragma unroll
+#pragma unroll
               for (uint32_t hf = 0; hf < S::kHalves; ++hf)
                 tc::tma_box(dst + hf * S::kPanel, kv ? &map_v : &map_k, hf * 64, slot, s.h, page, bar);
           }

@@ -10,8 +10,16 @@
 //
 // Measured on one GB300: 32 ragged caches of up to 16384 tokens in 4 bits, 8 kv heads of 4
 // query heads of 128, one token each (202 MB): 91 us with cold caches, 2.2 TB/s.  16
-// tokens of a head cost about 270 warp instructions, of which 96 decode: issue bounds it.
-// Loads straight into registers, without the ring, took 325 us.
+// tokens of a head cost about 270 warp instructions, of which 96 decode.  Issue slots are 56 %
+// used, DRAM 31 %: with 3.7 warps a scheduler, loads and the chain of products into one
+// accumulator are waited for.  The same caches in 16 bits (712 MB) 183 us, 3.9 TB/s, issue slots
+// 27 % used: two warps a scheduler wait for their loads.  Loads straight into registers, without the
+// ring, took 325 us (4 bits).
+//
+// Heads of 136 to 256 come here with any number of rows, eight at a time, for each of which the
+// keys are read from shared memory anew: 8 caches of up to 8192 tokens in 4 bits, 8 kv heads of
+// 256, 64 rows 289 us, 256 rows 1127 us, 1024 rows 4353 us (16 bits: 332, 1237, 4711), where
+// heads of 128 take 142, 105 and 201 us.
 #include <type_traits>
 
 #include "ibp_kv_serve.cuh"

@@ -11,16 +11,19 @@
 //                       S^T in a register.
 // With tokens as TMEM lanes no sum crosses threads until the cluster's CTAs are added up
 // at the end, in a fixed order.  A token's key reaches its own sum alone, so what is not
-// finite in it needs no care.  Bound by the exponentials and the products, about alike:
-// 32768 and 4.2 million multiply-adds for 128 rows and 256 tokens, of 1024 cycles each.
+// finite in it needs no care.  128 rows by 256 tokens are 32768 exponentials and 4.2 million
+// multiply-adds, of 1024 cycles each on their pipes.
 //
 // 256 tokens a CTA share a block of queries, which is what moves most; a cluster
 // shares the heads, so that the sum over heads needs no scratch and no atomics.
 //
 // Measured on one GB300: 511 queries a sequence, 32 heads on 8 kv heads of 128, two caches of
-// up to 8192 tokens in 16 bits: 132 us with cold caches, 0.39 PFLOP/s of products; the few-row
-// kernel takes 960 us.  128 rows of a CTA take about 4000 cycles, what a CTA begins and ends with
-// 13 us.
+// up to 8192 tokens in 16 bits: 130 us with cold caches, 0.40 PFLOP/s of products; the few-row
+// kernel takes 960 us.  128 rows of a CTA take 3300 to 4000 cycles, what a CTA begins and ends
+// with 13 us.  Two things bound it.  In a CTA the roles wait for one another: exponentials and
+// products each keep their pipe 33 % busy, issue slots are 38 % used.  And CTAs of fixed size do not
+// fill the SMs evenly: 204 of them here, one a SM, so two rounds, and the SMs work for 54 % of
+// the time.
 //
 // Every wait has a limit, as in ibp_kv_tree.cuh.
 #include "ibp_kv_serve.cuh"

@@ -799,7 +799,8 @@ int ibp_kv4_load(const ibp_kv4_pages* k_pages, const ibp_kv4_pages* v_pages, uin
  *
  * ws       ibp_kv4_attention_workspace bytes.  Large calls of more than 512 rows a
  *          kv head (T * q_heads / kv_heads) and dim <= 128 decode the cache once,
- *          so theirs holds the sequences in 16 bits where that is at most 4 GB.
+ *          so theirs holds the sequences in 16 bits where that is at most 4 GB.  With
+ *          dim > 128 the cache is decoded anew for every 8 rows: many are slow.
  */
 int ibp_kv4_attention(const ibp_kv4_pages* k, const ibp_kv4_pages* v, uint32_t dtype, const ibp_kv_seqs* seqs,
                       const void* q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride, uint32_t T,
@@ -826,7 +827,8 @@ size_t ibp_kv4_attention_workspace(uint32_t n_seqs, uint32_t max_pages, uint32_t
  * With q NULL every drafted token was certain (q_x = 1, all others 0).  The next
  * token is drawn from the rest of the last rejection that left something behind the
  * last node, or from its row of p: the first token whose running sum of
- * rint(w * 2^44) is above floor(u[b][T] * total).  These sums are of whole numbers, so the results are the same on every run.
+ * rint(w * 2^44) is above floor(u[b][T] * total) (in double precision).  These sums
+ * are of whole numbers, so the results are the same on every run.
  * Tokens out of range and parents that are not an earlier token or -1 are passed
  * over and record IBP_ERANGE; where nothing has a probability the token is -1 and
  * IBP_ERANGE is recorded.  A u of 1 or more draws the last token with a weight; one
@@ -858,6 +860,9 @@ int ibp_kv_verify(const float* p, int64_t p_seq_stride, int64_t p_row_stride, co
  * A row with lse -infinity adds nothing.  Positions whose page id is out of range
  * count as zero keys and record IBP_ERANGE, as lengths above width do (positions from
  * width on are not weighed).
+ *
+ * Weights do not follow ibp_kv_accept: a program that weighs a draft's queries and
+ * then accepts a part of it moves the draft's weights itself, by the same path.
  *
  * w, w_out  n_seqs x width floats; w_out may be w.
  * The rest as for ibp_tree_attention; ibp_kv4_weigh reads keys in 4 bits.
